@@ -277,6 +277,115 @@ int sptg_plan_square(int64_t M, int64_t N, int64_t K, sptg_dtype dtype, int sm_c
 int sptg_plan(int64_t M, int64_t N, int64_t K, sptg_dtype dtype, int sm_count,
               const sptg_config* cfg, int* out);
 
+/*
+ * ------------------------------------------------------------------------
+ * The operators around the products of a language model's layer. All are
+ * asynchronous on `stream`, allocate nothing, copy nothing to the host and
+ * may be captured in a CUDA graph. They keep all sums in fp32 and give the
+ * same bits for the same inputs on every call.
+ */
+
+/* Element types of these operators. */
+typedef enum {
+  SPTG_T_F16 = 0,   /* binary16 */
+  SPTG_T_BF16 = 1,  /* bfloat16 */
+  SPTG_T_S8 = 2,    /* int8; quantised values are -127 ... 127 */
+  SPTG_T_E4M3 = 3,  /* 8-bit float, 4 exponent and 3 fraction bits, largest 448 */
+  SPTG_T_RANGE_MIN_ = -2147483647 - 1, /* as for sptg_dtype: any int is rejected cleanly */
+  SPTG_T_RANGE_MAX_ = 2147483647
+} sptg_type;
+
+/*
+ * Residual addition and root-mean-square norm of each row, with the next
+ * product's operand as output:
+ *
+ *   t = x + residual                            (fp32)
+ *   h = t rounded to the rows' type             (the new residual stream)
+ *   v = t * weight / sqrt(mean(t^2) + eps)      (fp32; mean over the row)
+ *   y = v rounded to the rows' type             (out_type == in_type), or
+ *   scale = max|v| / Q,  y = v / scale rounded to nearest even
+ *                                               (out_type SPTG_T_S8, Q = 127,
+ *                                                or SPTG_T_E4M3, Q = 448)
+ *
+ * so that y * scale stands for v. scales holds one fp32 for each row (unused,
+ * may be NULL, for 16-bit outputs). A row of zeros gives y = 0, scale = 0, as
+ * does one whose max|t * weight| is below about 1e-36 or whose sum of squares
+ * passes the fp32 range. A row holding an infinity or a NaN gives y = 0, scale
+ * = NaN.
+ *
+ * x, residual, h: rows x cols of in_type (SPTG_T_F16 or SPTG_T_BF16) with row
+ * pitches ldx, ldr, ldh; weight: cols of in_type; y: rows x cols of out_type
+ * with row pitch ldy (pitches in elements, >= cols). h may be x or residual
+ * itself (same pointer and pitch); nothing else may overlap. Any cols, pitch
+ * and element-aligned pointers are taken; rows are read in 16-byte pieces when
+ * cols and every pitch are multiples of 8 and every pointer is 16-byte aligned
+ * (an 8-bit y: 8-byte). eps > 0. rows == 0 or cols == 0: nothing is done.
+ */
+int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type out_type,
+                      const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                      const void* weight, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
+                      float* scales, void* stream);
+
+/*
+ * Product with 4-bit weights and group scales:
+ *
+ *   Y[m, n] = x_scales[m] * sum_g scales[n, g] *
+ *             sum_{k in group g} X[m, k] * (code[n, k] - zeros[n, g])
+ *
+ *   X         M x K of x_type, row pitch ldx elements. SPTG_T_F16 or
+ *             SPTG_T_BF16 (out_type must be the same; x_scales NULL), or
+ *             SPTG_T_S8 or SPTG_T_E4M3 with x_scales, one fp32 for each row,
+ *             as sptg_add_rms_norm writes them
+ *   codes     N rows of K / 2 bytes, row pitch ldw bytes: byte j of a row holds
+ *             column 2j in its low half and column 2j + 1 in its high half
+ *   scales    N x (K / group) of out_type, dense
+ *   zeros     N x (K / group) bytes 0 ... 15 (the low four bits count), dense;
+ *             NULL: 8 everywhere
+ *   Y         M x N of out_type (SPTG_T_F16 or SPTG_T_BF16), row pitch ldy
+ *
+ * Products and sums are exact to fp32 accumulation; Y is rounded once.
+ * group is 32, 64 or 128 and divides K. X and codes are 16-byte aligned with
+ * row pitches of a multiple of 16 bytes (SPTG_ERR_ALIGN); N, M and ldy are
+ * free. Up to 64 rows of X share one pass over the weights; more rows take
+ * ceil(M / 64) passes. M == 0 or N == 0: nothing is done. K == 0: Y is zero.
+ */
+int sptg_gemm_w4(int64_t M, int64_t N, int64_t K, int group, sptg_type x_type, sptg_type out_type,
+                 const void* X, int64_t ldx, const float* x_scales, const uint8_t* codes,
+                 int64_t ldw, const void* scales, const uint8_t* zeros, void* Y, int64_t ldy,
+                 void* stream);
+
+/*
+ * Products grouped by expert with ragged sizes, and their gradients. Rows
+ * offsets[e] ... offsets[e + 1] - 1 of the T rows belong to expert e:
+ *
+ *   sptg_grouped_gemm      Y[t, n]     = sum_k X[t, k]  * W[e, n, k]
+ *   sptg_grouped_gemm_dx   dX[t, k]    = sum_n dY[t, n] * W[e, n, k]
+ *   sptg_grouped_gemm_dw   dW[e, n, k] = sum_t dY[t, n] * X[t, k]
+ *
+ * offsets: E + 1 int32 in device memory, not decreasing, 0 <= offsets[0],
+ * offsets[E] <= T (read by the kernel: the host never waits for them). An
+ * expert may have no rows (its dW is zero). Rows of Y and dX that belong to no
+ * expert are set to zero. Offsets that break these rules are clamped to
+ * [0, T] and to not decreasing; results are then unspecified, but nothing
+ * outside the given arrays is touched.
+ *
+ * X, Y, dY, dX: T rows with row pitches in elements; W and dW: E x N x K,
+ * dense (N rows of K for each expert, as the weights of sptg_gemm are stored).
+ * dtype: a float pair of sptg_dtype; its first type is that of X, W and dY, its
+ * second that of the output. Alignment as for sptg_gemm: 16-byte aligned
+ * bases; N and K, and each pitch, a multiple of 16 bytes in the types they
+ * count. E <= 1024.
+ */
+int sptg_grouped_gemm(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype dtype,
+                      const int32_t* offsets, const void* X, int64_t ldx, const void* W, void* Y,
+                      int64_t ldy, void* stream);
+int sptg_grouped_gemm_dx(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype dtype,
+                         const int32_t* offsets, const void* dY, int64_t lddy, const void* W,
+                         void* dX, int64_t lddx, void* stream);
+int sptg_grouped_gemm_dw(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype dtype,
+                         const int32_t* offsets, const void* dY, int64_t lddy, const void* X,
+                         int64_t ldx, void* dW, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

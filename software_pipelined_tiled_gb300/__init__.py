@@ -23,6 +23,7 @@ __all__ = ["DTYPES", "SptgError", "Config", "load", "gemm", "gemm_host", "gemm_r
            "gemm_strided_raw",
            "gemm_skinny_noalloc_raw",
            "stream_scale",
+           "add_rms_norm", "gemm_w4", "grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw",
            "last_config",
            "last_error", "device_error", "status_string", "LIB_PATH", "build"]
 
@@ -38,7 +39,8 @@ KERNELS = {"auto": 0, "square": 1, "skinny": 2, "skinny_cluster": 3, "skinny_row
 EXPORTS = ("sptg_gemm", "sptg_gemm_ex", "sptg_gemm_strided", "sptg_gemm_host",
            "sptg_plan_square", "sptg_plan", "sptg_status_string", "sptg_last_error",
            "sptg_last_config", "sptg_device_error", "sptg_version", "sptg_gemm_skinny_noalloc",
-           "sptg_stream_scale", "sptg_stream_scale_ex")
+           "sptg_stream_scale", "sptg_stream_scale_ex", "sptg_add_rms_norm", "sptg_gemm_w4",
+           "sptg_grouped_gemm", "sptg_grouped_gemm_dx", "sptg_grouped_gemm_dw")
 
 
 class SptgError(RuntimeError):
@@ -103,6 +105,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.sptg_plan.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.c_int,
                                   ctypes.POINTER(Config), ctypes.POINTER(ctypes.c_int)]
         lib.sptg_plan.restype = ctypes.c_int
+        lib.sptg_add_rms_norm.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int, vp, i64, vp, i64,
+                                          vp, ctypes.c_float, vp, i64, vp, i64, vp, vp]
+        lib.sptg_gemm_w4.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp,
+                                     i64, vp, vp, i64, vp, vp, vp, i64, vp]
+        lib.sptg_grouped_gemm.argtypes = [i64, i64, i64, i64, ctypes.c_int, vp, vp, i64, vp, vp,
+                                          i64, vp]
+        lib.sptg_grouped_gemm_dx.argtypes = lib.sptg_grouped_gemm.argtypes
+        lib.sptg_grouped_gemm_dw.argtypes = [i64, i64, i64, i64, ctypes.c_int, vp, vp, i64, vp,
+                                             i64, vp, vp]
+        for f in (lib.sptg_add_rms_norm, lib.sptg_gemm_w4, lib.sptg_grouped_gemm,
+                  lib.sptg_grouped_gemm_dx, lib.sptg_grouped_gemm_dw):
+            f.restype = ctypes.c_int
         lib.sptg_version.argtypes = []
         lib.sptg_version.restype = ctypes.c_int
         if path is None:
@@ -319,3 +333,17 @@ def stream_scale(x, alpha: float, out=None, stream=None, config: Config | None =
 def device_error(stream=None) -> int:
     """Synchronizes the stream and returns (and clears) the device error status."""
     return int(load().sptg_device_error(_stream_handle(stream)))
+
+
+# The operators around the products live in layers.py, which imports PyTorch;
+# they are looked up on first use, so that importing the package stays light.
+_LAYERS = ("add_rms_norm", "gemm_w4", "grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw")
+
+
+def __getattr__(name: str):
+    if name not in _LAYERS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layers
+    for n in _LAYERS:
+        globals()[n] = getattr(layers, n)
+    return globals()[name]

@@ -1,0 +1,589 @@
+// grouped_gemm.cuh -- products grouped by expert with ragged sizes, and their
+// gradients, on CTA pairs with the 2-SM tensor-core instruction.
+//
+// Rows offsets[e] ... offsets[e + 1] - 1 of X (and of Y, dY, dX) belong to
+// expert e, whose weights are W[e] (N x K):
+//
+//   GROUPED_Y    Y[t, n]     = sum_k X[t, k]  W[e, n, k]
+//   GROUPED_DX   dX[t, k]    = sum_n dY[t, n] W[e, n, k]
+//   GROUPED_DW   dW[e, n, k] = sum_t dY[t, n] X[t, k]     (t over e's rows)
+//
+// The offsets are read on the device, so a caller never waits for the GPU to
+// learn the sizes: the grid is fixed (persistent CTA pairs) and every CTA works
+// out the same list of tiles from the offsets.
+//
+// Orientation: the ragged side is the MMA's N side. The MMA's M side (256 over
+// a pair: 128 of each CTA) covers "features" -- rows n of W (Y), columns k of
+// W (dX), columns n of dY (dW) -- which are wide and regular; its N side
+// covers up to TT rows of an expert (Y, dX), whose width the instruction takes
+// in steps of 16. An expert with few rows so pays for few rows, and its weights
+// stream through the fixed 128-row side; on the other orientation it would pay
+// for 128 or 256 rows. For dW the N side covers 256 columns k and the ragged
+// side is the sum.
+//
+// Operands as they lie in memory, no transposed copies: the tensor core reads
+// K-major tiles (rows contiguous along the sum: W and X for Y, dY for dX) and
+// MN-major tiles (rows contiguous along the features: W for dX, both operands
+// of dW), both 128-byte swizzled as the tensor-copy engine writes them.
+//
+// Bounds: rows of X past an expert's end that a tile's copy brings along only
+// reach accumulator columns that are never stored. W is a 3-D tensor, so that
+// a tile past its N or K reads zeros, not the next expert's weights. For dW
+// the sum itself is ragged: the last chunk of an expert's rows is cut at a
+// multiple of 16 rows, and a fixer warp in each CTA zeroes the rows between
+// the expert's end and that multiple in both operands (0 times another
+// expert's infinity would be NaN) before the chunk goes to the MMA.
+//
+// Roles of a CTA: warp 0 producer, warp 1 MMA issuer (leader CTA only), warps
+// 2-5 epilogue, warp 6 fixer (dW only). Two accumulators of up to 256 columns,
+// so a tile's epilogue overlaps the next tile's K-loop.
+//
+// The epilogue of Y and dX writes the transpose of the accumulator: a lane
+// holds one feature, its columns are rows of the output. Each warp turns
+// blocks of 32 x 32 in shared memory and stores rows of 32 features.
+#pragma once
+
+#include "common.cuh"
+#include "variants.h"
+
+namespace sptg {
+
+enum GroupedMode : int { GROUPED_Y = 0, GROUPED_DX = 1, GROUPED_DW = 2 };
+
+constexpr int GROUPED_MAX_EXPERTS = 1024;
+constexpr int GROUPED_THREADS = 224;
+
+struct GroupedParams {
+  int experts;
+  int T;   // rows of X
+  int F;   // features (M side): N (Y, dW) or K (dX)
+  int C;   // Y, dX: length of the sum (K, N); dW: columns of the output (K)
+  const int32_t* offsets;  // experts + 1
+  void* out;
+  int64_t ldo;             // elements between output rows
+  int64_t expert_pitch;    // dW: elements between experts
+  int keep_weights;        // 1: W is read by several tiles; 0: once (evict first)
+  unsigned int* error_word;
+  uint64_t timeout_ns;
+};
+
+// TT: widest N side of a tile (256, or 64 for experts of few rows: the ring
+// then holds nine or ten stages of weights instead of six).
+template <int TT, int OBYTES>
+struct GroupedLayout {
+  static constexpr int A_STAGE = 128 * 128;         // 128 features x 64 of the sum
+  static constexpr int B_STAGE = TT / 2 * 128;      // this CTA's half of the N side
+  static constexpr int STAGE = A_STAGE + B_STAGE;
+  static constexpr int STAGES = TT == 256 ? 6 : OBYTES == 4 ? 9 : 10;
+  static constexpr int EPI_PITCH = 32 * OBYTES + 16;
+  static constexpr int EPI_BUF = 32 * EPI_PITCH;    // one 32 x 32 block per epilogue warp
+  static constexpr int OFF_EPI = STAGES * STAGE;
+  static constexpr int OFF_BAR = OFF_EPI + 4 * EPI_BUF;
+  static constexpr int NUM_BARS = 3 * STAGES + 5;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int OFF_GROUPS = OFF_MISC + 16;
+  // first row and first tile of each expert, of the rows before the first
+  // expert and after the last (written as zeros), and of the end
+  static constexpr int GROUP_SLOTS = GROUPED_MAX_EXPERTS + 3;
+  static constexpr int BYTES_USED = OFF_GROUPS + 3 * GROUP_SLOTS * 4;
+  static constexpr int SMEM_BYTES = BYTES_USED + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget exceeded");
+};
+
+// Matrix descriptor of an MN-major operand tile: lines of 64 elements (128
+// bytes, swizzled) along the M or N side, one line for each step of the sum,
+// 8-line groups 1024 bytes apart, the next 64 elements `atom` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn_major_sw128(uint32_t saddr, uint32_t atom) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(atom >> 4) << 16;   // leading byte offset: next 64 elements
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;  // stride byte offset: next 8 of the sum
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// The MMA's N side for `n` rows or columns: steps of 32, and of 16 past 96
+// (the widths of 112 and more that the square kernel's pair tiles use).
+__host__ __device__ constexpr int grouped_mma_n(int n) {
+  return n <= 96 ? (n + 31) & ~31 : (n + 15) & ~15;
+}
+
+// One tile of work.
+struct GroupedTile {
+  int e;       // expert
+  int f0;      // first feature
+  int t0;      // Y, dX: first row of the tile; dW: the expert's first row
+  int rows;    // Y, dX: rows of the tile; dW: rows of the expert
+  int c0;      // dW: first column
+  int n;       // width of the MMA's N side
+  int chunks;  // 64-long pieces of the sum (0: the tile is zeros)
+};
+
+template <int MODE, int TT>
+struct GroupedSchedule {
+  const int* first;  // in shared memory: first row
+  const int* count;  // rows
+  const int* cum;    // tiles before the group
+  int groups, nf, F, C;
+  int g = 0;
+
+  __device__ __forceinline__ int total() const { return cum[groups]; }
+
+  // `tile` never decreases from call to call
+  __device__ __forceinline__ GroupedTile at(int tile) {
+    while (tile >= cum[g + 1]) ++g;
+    GroupedTile w;
+    const int i = tile - cum[g];
+    const int first_g = first[g], count_g = count[g];
+    w.e = g;
+    if constexpr (MODE == GROUPED_DW) {
+      const int nc = (C + 255) >> 8;
+      int ft, ct;
+      tile_coords(i, nf, nc, 8, ft, ct);
+      w.f0 = ft * 256;
+      w.c0 = ct * 256;
+      w.t0 = first_g;
+      w.rows = count_g;
+      w.n = grouped_mma_n(min(256, C - w.c0));
+      w.chunks = (count_g + 63) >> 6;
+    } else {
+      const int nt = (count_g + TT - 1) / TT;
+      // the expert's rows in tiles of equal width (a multiple of 16)
+      const int width = ((count_g + nt - 1) / nt + 15) & ~15;
+      int tt, ft;
+      tile_coords(i, nt, nf, 8, tt, ft);
+      w.f0 = ft * 256;
+      w.c0 = 0;
+      w.t0 = first_g + tt * width;
+      w.rows = max(0, min(width, first_g + count_g - w.t0));
+      w.n = grouped_mma_n(w.rows);
+      // groups past the experts are rows that belong to none
+      w.chunks = (g < groups - 2 && w.rows > 0) ? (C + 63) >> 6 : 0;
+    }
+    return w;
+  }
+};
+
+template <int MODE, int TT, bool BF16, int OUT>
+__global__ void __launch_bounds__(GROUPED_THREADS, 1)
+    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,   // the features' operand
+                        const __grid_constant__ CUtensorMap tmB,   // the N side, boxes of 32 rows
+                        const __grid_constant__ CUtensorMap tmB4,  // the N side, boxes of 128 rows
+                        const GroupedParams p) {
+  constexpr int OBYTES = OutTraits<OUT>::bytes;
+  using L = GroupedLayout<TT, OBYTES>;
+  constexpr int STAGES = L::STAGES;
+  constexpr bool A_MN = MODE != GROUPED_Y, B_MN = MODE == GROUPED_DW;
+  static_assert(MODE != GROUPED_DW || TT == 256, "dW tiles are 256 columns wide");
+  constexpr uint32_t IDESC0 = idesc_f16_f32acc(BF16, 256, 0) | (A_MN ? 1u << 15 : 0u) |
+                              (B_MN ? 1u << 16 : 0u);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_addr(smem);
+  auto stage_a = [&](int s) { return sbase + s * L::STAGE; };
+  auto stage_b = [&](int s) { return sbase + s * L::STAGE + L::A_STAGE; };
+  const uint32_t bar0 = sbase + L::OFF_BAR;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // dW: own copies of a tail
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  int* g_first = reinterpret_cast<int*>(smem + L::OFF_GROUPS);
+  int* g_count = g_first + L::GROUP_SLOTS;
+  int* g_cum = g_count + L::GROUP_SLOTS;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int worker = static_cast<int>(blockIdx.x >> 1);
+  const int workers = static_cast<int>(gridDim.x >> 1);
+  // dW: a stage is complete when both CTAs' parts are (two arrivals: the
+  // leader's producer makes both, or each CTA's fixer one)
+  constexpr uint32_t FULL_COUNT = MODE == GROUPED_DW ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), FULL_COUNT);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(tail_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 8);  // four epilogue warps of each CTA
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensor_map(&tmA);
+    prefetch_tensor_map(&tmB);
+    prefetch_tensor_map(&tmB4);
+  }
+  if (warp == 1) {
+    tmem_alloc_g<true>(smem_addr(tmem_slot), 512);
+    tmem_relinquish_g<true>();
+  }
+  grid_dependency_wait();
+  // The list of groups: experts 0 ... experts - 1, then the rows before the
+  // first and after the last. Offsets outside [0, T] or decreasing are
+  // clamped, so that no tile leaves the rows of X.
+  const int groups = MODE == GROUPED_DW ? p.experts : p.experts + 2;
+  const int nf = (p.F + 255) >> 8;
+  if (warp == 2) {
+    const int lo = min(max(p.offsets[0], 0), p.T);
+    const int hi = min(max(p.offsets[p.experts], lo), p.T);
+    int base = 0;
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+      const int g = g0 + lane;
+      int a = 0, n = 0, tiles = 0;
+      if (g < groups) {
+        if (g < p.experts) {
+          a = min(max(p.offsets[g], 0), p.T);
+          n = min(max(p.offsets[g + 1], a), p.T) - a;
+        } else if (g == p.experts) {
+          n = lo;
+        } else {
+          a = hi;
+          n = p.T - hi;
+        }
+        tiles = MODE == GROUPED_DW ? nf * ((p.C + 255) >> 8) : (n + TT - 1) / TT * nf;
+      }
+      int sum = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      if (g < groups) {
+        g_first[g] = a;
+        g_count[g] = n;
+        g_cum[g] = base + sum - tiles;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) g_cum[groups] = base;
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  GroupedSchedule<MODE, TT> sched{g_first, g_count, g_cum, groups, nf, p.F, p.C};
+  const int total = sched.total();
+  const WaitCtl ctl{p.timeout_ns, p.error_word, abort_flag};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one_sync();
+    const uint64_t pol_a = p.keep_weights ? policy_evict_last() : policy_evict_first();
+    const uint64_t pol_b = policy_evict_last();
+    int s = 0;
+    uint32_t round = 0;
+    uint32_t tail_used = 0, tail_parity = 0;  // bit s: of stage s's tail barrier
+    uint32_t last_tail = 0;                   // bit s: the stage's last copies went to it
+    int issued = 0;
+    bool ok = true;
+    for (int tile = worker; ok && tile < total; tile += workers) {
+      const GroupedTile w = sched.at(tile);
+      const int half = w.n >> 1;
+      const int n_first = static_cast<int>(rank) * half;  // this CTA's part of the N side
+      // boxes of the N side and the bytes of one stage (both CTAs)
+      const int boxes = MODE == GROUPED_DW ? (half + 63) >> 6 : (half + 31) >> 5;
+      const uint32_t own_tx =
+          L::A_STAGE + static_cast<uint32_t>(boxes) * (MODE == GROUPED_DW ? 8192u : 4096u);
+      const int f = w.f0 + 128 * static_cast<int>(rank);
+      for (int c = 0; c < w.chunks; ++c) {
+        if (round > 0 && !__all_sync(0xffffffffu, wait_bounded(empty_bar(s), (round & 1u) ^ 1u,
+                                                                ctl, WAIT_PRODUCER_EMPTY))) {
+          ok = false;
+          break;
+        }
+        ++issued;
+        if (leader) {
+          const uint32_t a = stage_a(s), b = stage_b(s);
+          if constexpr (MODE == GROUPED_DW) {
+            const int t = w.t0 + 64 * c;
+            const bool tail = c == w.chunks - 1 && (w.rows & 63) != 0;
+            if (tail) {
+              // own copies complete on this CTA's tail barrier; its fixer
+              // then hands the stage to the MMA issuer
+              mbar_arrive_expect_tx(tail_bar(s), own_tx);
+              for (int j = 0; j < 2; ++j)
+                tma_load_2d(a + j * 8192, &tmA, tail_bar(s), f + 64 * j, t, pol_b);
+              for (int j = 0; j < boxes; ++j)
+                tma_load_2d(b + j * 8192, &tmB, tail_bar(s), w.c0 + n_first + 64 * j, t, pol_b);
+              tail_parity ^= (tail_used >> s & 1u) << s;
+              tail_used |= 1u << s;
+              last_tail |= 1u << s;
+            } else {
+              last_tail &= ~(1u << s);
+              if (rank == 0) {
+                mbar_arrive_expect_tx(full_bar(s), 2 * own_tx);
+                mbar_arrive(full_bar(s));
+              }
+              const uint32_t full = map_to_cta(full_bar(s), 0u);
+              for (int j = 0; j < 2; ++j)
+                tma_load_2d_pair(a + j * 8192, &tmA, full, f + 64 * j, t, pol_b);
+              for (int j = 0; j < boxes; ++j)
+                tma_load_2d_pair(b + j * 8192, &tmB, full, w.c0 + n_first + 64 * j, t, pol_b);
+            }
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * own_tx);
+            const uint32_t full = map_to_cta(full_bar(s), 0u);
+            if constexpr (MODE == GROUPED_Y) {
+              tma_load_3d_pair(a, &tmA, full, 64 * c, f, w.e, pol_a);
+            } else {
+              for (int j = 0; j < 2; ++j)
+                tma_load_3d_pair(a + j * 8192, &tmA, full, f + 64 * j, 64 * c, w.e, pol_a);
+            }
+            if (boxes == 4) {
+              tma_load_2d_pair(b, &tmB4, full, 64 * c, w.t0 + n_first, pol_b);
+            } else {
+              for (int j = 0; j < boxes; ++j)
+                tma_load_2d_pair(b + j * 4096, &tmB, full, 64 * c, w.t0 + n_first + 32 * j, pol_b);
+            }
+          }
+        }
+        if (++s == STAGES) {
+          s = 0;
+          ++round;
+        }
+      }
+    }
+    grid_launch_dependents();
+    if (!ok) {
+      // let every copy already issued land before the CTA can exit
+      if (leader && rank == 0) {
+        for (int i = max(0, issued - STAGES); i < issued; ++i) {
+          const int st = i % STAGES;
+          const bool in_tail = last_tail >> st & 1u;
+          const uint32_t bar = in_tail ? tail_bar(st) : full_bar(st);
+          const uint32_t par = in_tail ? tail_parity >> st & 1u
+                                       : static_cast<uint32_t>(i / STAGES) & 1u;
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_try_wait(bar, par) && global_timer_ns() - t0 < ctl.timeout_ns) {
+          }
+        }
+      }
+      __syncwarp();
+      if (rank != 0) {
+        // copies that complete on the leader's barriers, which this CTA
+        // cannot wait on: give them a fixed 100 us to land
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 100000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      const bool leader = elect_one_sync();
+      int s = 0;
+      uint32_t phase = 0, unit = 0;
+      bool ok = true;
+      for (int tile = worker; ok && tile < total; tile += workers) {
+        const GroupedTile w = sched.at(tile);
+        if (w.chunks == 0) continue;
+        const uint32_t b = unit & 1u;
+        if (!__all_sync(0xffffffffu, wait_bounded(tempty_bar(b), ((unit >> 1) & 1u) ^ 1u, ctl,
+                                                  WAIT_MMA_TMEM_EMPTY))) {
+          ok = false;
+          break;
+        }
+        ++unit;
+        tc_fence_after();
+        const uint32_t d = tmem_base + b * 256;
+        const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
+        for (int c = 0; c < w.chunks; ++c) {
+          if (!__all_sync(0xffffffffu, wait_bounded(full_bar(s), phase, ctl, WAIT_MMA_FULL))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (leader) {
+            const uint64_t ad = A_MN ? sdesc_mn_major_sw128(stage_a(s), 8192)
+                                     : sdesc_k_major_sw128(stage_a(s));
+            const uint64_t bd = B_MN ? sdesc_mn_major_sw128(stage_b(s), 8192)
+                                     : sdesc_k_major_sw128(stage_b(s));
+            // one step of 16 along the sum: 32 bytes of a K-major row, 16
+            // lines of an MN-major tile (in units of 16 bytes)
+            constexpr uint64_t ADV_A = A_MN ? 128 : 2, ADV_B = B_MN ? 128 : 2;
+            if (MODE == GROUPED_DW && c == w.chunks - 1 && (w.rows & 63) != 0) {
+              const int steps = ((w.rows & 63) + 15) >> 4;
+              for (int k = 0; k < steps; ++k)
+                mma_f16_g<true>(d, ad + ADV_A * k, bd + ADV_B * k, idesc, (c > 0 || k > 0) ? 1u : 0u);
+            } else {
+              mma_f16_g<true>(d, ad, bd, idesc, c > 0 ? 1u : 0u);
+#pragma unroll
+              for (int k = 1; k < 4; ++k)
+                mma_f16_g<true>(d, ad + ADV_A * k, bd + ADV_B * k, idesc, 1u);
+            }
+            mma_commit_g<true>(empty_bar(s));
+          }
+          __syncwarp();
+          if (++s == STAGES) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok && leader) mma_commit_g<true>(tfull_bar(b));
+        __syncwarp();
+      }
+      if (leader) mma_commit_local_g<true>(drain_bar);
+      __syncwarp();
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < ctl.timeout_ns) {
+      }
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // tensor-memory lanes 32q ... 32q + 31
+    uint8_t* buf = smem + L::OFF_EPI + (warp - 2) * L::EPI_BUF;
+    constexpr int PITCH = L::EPI_PITCH;
+    constexpr int VEC = 16 / OBYTES;            // outputs in 16 bytes
+    constexpr int VPR = 32 / VEC;               // 16-byte pieces of a row of 32
+    constexpr int RPI = 32 / VPR;               // rows a warp stores at a time
+    const int vr = lane / VPR, vc = lane % VPR;
+    uint32_t unit = 0;
+    for (int tile = worker; tile < total; tile += workers) {
+      const GroupedTile w = sched.at(tile);
+      const uint32_t b = unit & 1u;
+      const bool zeros = w.chunks == 0;
+      if (!zeros) {
+        if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(b), (unit >> 1) & 1u, ctl,
+                                                  WAIT_EPI_TMEM_FULL)))
+          break;
+        ++unit;
+        tc_fence_after();
+      }
+      const int f = w.f0 + 128 * static_cast<int>(rank) + 32 * q;  // this warp's first feature
+      const uint32_t t_acc = tmem_base + b * 256 + (static_cast<uint32_t>(32 * q) << 16);
+      if (f < p.F) {
+        for (int cb = 0; cb < w.n; cb += 32) {
+          uint32_t r[32];
+          if (!zeros) {
+            tmem_ld_32x32b_x32(t_acc + cb, r);
+            tmem_wait_ld_regs(r);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0;
+          }
+          __syncwarp();  // the block before this one has been read
+          if constexpr (MODE == GROUPED_DW) {
+            // rows of the output are features: a lane's own row
+            if constexpr (OBYTES == 4) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(buf + lane * PITCH + 16 * j) =
+                    make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  o[i] = pack2<OUT>(__uint_as_float(r[8 * j + 2 * i]),
+                                    __uint_as_float(r[8 * j + 2 * i + 1]));
+                *reinterpret_cast<uint4*>(buf + lane * PITCH + 16 * j) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          } else {
+            // rows of the output are accumulator columns
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              store_out<OUT>(buf + i * PITCH, lane, __uint_as_float(r[i]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32; i += RPI) {
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + (i + vr) * PITCH + 16 * vc);
+            int64_t at;
+            bool in;
+            if constexpr (MODE == GROUPED_DW) {
+              const int row = f + i + vr, col = w.c0 + cb + vc * VEC;
+              in = row < p.F && col < p.C;
+              at = w.e * p.expert_pitch + row * p.ldo + col;
+            } else {
+              const int row = cb + i + vr, col = f + vc * VEC;
+              in = row < w.rows && col < p.F;
+              at = static_cast<int64_t>(w.t0 + row) * p.ldo + col;
+            }
+            if (in)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at * OBYTES) = v;
+          }
+        }
+      }
+      if (!zeros) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(b), 0u));
+      }
+    }
+  } else if constexpr (MODE == GROUPED_DW) {
+    // --------------------------------------------------------------- fixer
+    // Zeroes the rows past an expert's end in the last chunk of its rows, up
+    // to the next multiple of 16 (the MMA reads no further), then hands the
+    // stage to the MMA issuer.
+    int s = 0;
+    uint32_t used = 0, parity = 0;
+    for (int tile = worker; tile < total; tile += workers) {
+      const GroupedTile w = sched.at(tile);
+      if (w.chunks == 0) continue;
+      const int tail = w.rows & 63;
+      s = (s + w.chunks - 1) % STAGES;  // the last chunk's stage
+      if (tail != 0) {
+        parity ^= (used >> s & 1u) << s;
+        used |= 1u << s;
+        if (!__all_sync(0xffffffffu,
+                        wait_bounded(tail_bar(s), parity >> s & 1u, ctl, WAIT_MMA_FULL)))
+          break;
+        const int end = (tail + 15) & ~15;
+        const int boxes = 2 + (((w.n >> 1) + 63) >> 6);
+        uint8_t* base = smem + s * L::STAGE;
+        // box j of the stage (the features' two, then the N side's) is 64
+        // lines of 128 bytes; a line keeps its place under the swizzle
+        for (int j = 0; j < boxes; ++j)
+          for (int i = tail * 8 + lane; i < end * 8; i += 32)
+            *reinterpret_cast<uint4*>(base + j * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_cta(full_bar(s), 0u));
+      }
+      s = s + 1 == STAGES ? 0 : s + 1;
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the pair's MMAs may still read it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_g<true>(tmem_base, 512);
+  }
+}
+
+template <int MODE, int TT, bool BF16, int OUT>
+KernelVariant grouped_variant_at() {
+  using L = GroupedLayout<TT, OutTraits<OUT>::bytes>;
+  return {reinterpret_cast<const void*>(&grouped_gemm_kernel<MODE, TT, BF16, OUT>), TT, L::STAGES,
+          L::SMEM_BYTES, true, GROUPED_THREADS};
+}
+
+// The variants of one mode and operand type (a translation unit each): output
+// in the operands' type OUT16 or in fp32, tiles up to tt = 64 or 256 wide.
+template <int MODE, bool BF16, int OUT16>
+KernelVariant grouped_variant_of(int out_kind, int tt) {
+  if constexpr (MODE != GROUPED_DW) {
+    if (tt == 64)
+      return out_kind == OUT_F32 ? grouped_variant_at<MODE, 64, BF16, OUT_F32>()
+                                 : grouped_variant_at<MODE, 64, BF16, OUT16>();
+  }
+  return out_kind == OUT_F32 ? grouped_variant_at<MODE, 256, BF16, OUT_F32>()
+                             : grouped_variant_at<MODE, 256, BF16, OUT16>();
+}
+
+}  // namespace sptg

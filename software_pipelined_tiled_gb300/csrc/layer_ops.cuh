@@ -1,0 +1,422 @@
+// layer_ops.cuh -- the C ABI of the operators around the dense products:
+// residual addition with norm, products with 4-bit weights, products grouped
+// by expert. Argument checks, kernel choice and launch; part of sptgemm.cu,
+// whose device state, tensor maps and error texts it shares.
+#pragma once
+
+namespace {
+
+struct TypeInfo {
+  int bytes;
+  const char* name;
+  CUtensorMapDataType tma;
+};
+
+bool type_info(int type, TypeInfo& t) {
+  switch (type) {
+    case SPTG_T_F16: t = {2, "f16", CU_TENSOR_MAP_DATA_TYPE_FLOAT16}; return true;
+    case SPTG_T_BF16: t = {2, "bf16", CU_TENSOR_MAP_DATA_TYPE_BFLOAT16}; return true;
+    case SPTG_T_S8: t = {1, "s8", CU_TENSOR_MAP_DATA_TYPE_UINT8}; return true;
+    case SPTG_T_E4M3: t = {1, "e4m3", CU_TENSOR_MAP_DATA_TYPE_UINT8}; return true;
+    default: return false;
+  }
+}
+
+int refuse(int status, const char* why) {
+  t_last_error = why;
+  return status;
+}
+
+bool multiple16(int64_t elements, int bytes) { return (elements * bytes) % 16 == 0; }
+
+// A 3-D map: `inner` contiguous elements, rows `pitch` and planes `plane`
+// bytes apart. Cached like the 2-D maps.
+struct Map3dEntry {
+  const void* base = nullptr;
+  uint64_t dims[3] = {}, strides[2] = {};
+  uint32_t box[3] = {};
+  int dt = -1, swizzle = -1;
+  CUtensorMap map;
+};
+constexpr int kMap3dCache = 32;
+thread_local Map3dEntry t_maps3d[kMap3dCache];
+thread_local int t_map3d_next = 0;
+
+int make_map_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
+                uint64_t rows, uint64_t planes, uint64_t pitch, uint64_t plane, uint32_t box_inner,
+                uint32_t box_rows, uint32_t box_planes, CUtensorMapSwizzle swizzle) {
+  for (const Map3dEntry& e : t_maps3d) {
+    if (e.base == base && e.dims[0] == inner && e.dims[1] == rows && e.dims[2] == planes &&
+        e.strides[0] == pitch && e.strides[1] == plane && e.box[0] == box_inner &&
+        e.box[1] == box_rows && e.box[2] == box_planes && e.dt == static_cast<int>(dt) &&
+        e.swizzle == static_cast<int>(swizzle)) {
+      *map = e.map;
+      return SPTG_OK;
+    }
+  }
+  auto enc = tensor_map_encoder();
+  if (!enc) return refuse(SPTG_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available from the driver");
+  Map3dEntry n;
+  n.base = base;
+  n.dims[0] = inner;
+  n.dims[1] = rows;
+  n.dims[2] = planes;
+  n.strides[0] = pitch;
+  n.strides[1] = plane;
+  n.box[0] = box_inner;
+  n.box[1] = box_rows;
+  n.box[2] = box_planes;
+  n.dt = static_cast<int>(dt);
+  n.swizzle = static_cast<int>(swizzle);
+  const cuuint64_t dims[3] = {inner, rows, planes}, strides[2] = {pitch, plane};
+  const cuuint32_t box[3] = {box_inner, box_rows, box_planes}, estr[3] = {1, 1, 1};
+  const CUresult r = enc(&n.map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char b[160];
+    snprintf(b, sizeof(b), "cuTensorMapEncodeTiled failed (%d) for %llux%llux%llu", (int)r,
+             (unsigned long long)planes, (unsigned long long)rows, (unsigned long long)inner);
+    return refuse(SPTG_ERR_ARG, b);
+  }
+  *map = n.map;
+  t_maps3d[t_map3d_next] = n;
+  t_map3d_next = (t_map3d_next + 1) % kMap3dCache;
+  return SPTG_OK;
+}
+
+// Launches with programmatic overlap (the kernels wait for the previous one
+// before they touch memory), in clusters of `cluster` CTAs along x.
+cudaError_t launch_op(const void* fn, dim3 grid, int threads, int smem, int cluster,
+                      cudaStream_t stream, void** args) {
+  cudaLaunchConfig_t lc;
+  memset(&lc, 0, sizeof(lc));
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
+  lc.attrs = attr;
+  lc.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
+  ++t_launches;
+  return e;
+}
+
+// No C++ exception leaves a C entry point (the tables and texts allocate).
+template <typename F>
+int guarded(F&& body) {
+  try {
+    t_launches = 0;
+    return body();
+  } catch (const std::bad_alloc&) {
+    return SPTG_ERR_NOMEM;
+  } catch (...) {
+    return SPTG_ERR_LAUNCH;
+  }
+}
+
+constexpr uint64_t kOpTimeoutNs = 2000ull * 1000000ull;
+
+// ------------------------------------------------------- residual and norm
+int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const void* x, int64_t ldx,
+                 const void* r, int64_t ldr, const void* w, float eps, void* h, int64_t ldh,
+                 void* y, int64_t ldy, float* scales, cudaStream_t stream) {
+  TypeInfo in, out;
+  if ((in_type != SPTG_T_F16 && in_type != SPTG_T_BF16) || !type_info(in_type, in) ||
+      !type_info(out_type, out) || (out.bytes == 2 && out_type != in_type))
+    return refuse(SPTG_ERR_ARG, "rows are f16 or bf16, outputs s8, e4m3 or the rows' own type");
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX)
+    return refuse(SPTG_ERR_ARG, "dimensions must be in [0, 2^31)");
+  if (!(eps > 0.0f) || !(eps < INFINITY)) return refuse(SPTG_ERR_ARG, "eps must be positive and finite");
+  if (rows == 0 || cols == 0) {
+    set_config("kernel=none type=%s (empty output)", in.name, {});
+    return SPTG_OK;
+  }
+  const bool quantised = out.bytes == 1;
+  if (!x || !r || !w || !h || !y || (quantised && !scales)) return refuse(SPTG_ERR_ARG, "null pointer");
+  if (ldx < cols || ldr < cols || ldh < cols || ldy < cols)
+    return refuse(SPTG_ERR_ARG, "row pitches must be at least cols");
+  const auto off = [](const void* p, unsigned bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+  };
+  if (off(x, 2) || off(r, 2) || off(w, 2) || off(h, 2) || off(y, out.bytes) ||
+      (quantised && off(scales, 4)))
+    return refuse(SPTG_ERR_ALIGN, "a pointer is not aligned to its element type");
+  int dev = 0;
+  DeviceInfo di;
+  const int rc = device_info(di, dev);
+  if (rc) return rc;
+  const bool vectors = cols % 8 == 0 && ldx % 8 == 0 && ldr % 8 == 0 && ldh % 8 == 0 &&
+                       ldy % 8 == 0 && !off(x, 16) && !off(r, 16) && !off(w, 16) && !off(h, 16) &&
+                       !off(y, 8 * out.bytes);
+  const int out_kind = out_type == SPTG_T_S8 ? NORM_S8 : out_type == SPTG_T_E4M3 ? NORM_E4M3 : NORM_16;
+  const NormVariant v = norm_variant(in_type == SPTG_T_BF16, out_kind, static_cast<int>(cols), vectors);
+  NormParams p{x, r, w, h, y, scales, ldx, ldr, ldh, ldy, rows, static_cast<int>(cols), eps};
+  const int64_t grid = (rows + v.rows_per_block - 1) / v.rows_per_block;
+  void* args[] = {&p};
+  const cudaError_t e = launch_op(v.fn, dim3(static_cast<unsigned>(grid)), v.threads, 0, 1, stream, args);
+  if (e != cudaSuccess) return cuda_fail(e, "add_rms_norm launch");
+  set_config("kernel=add_rms_norm type=%s out_bytes=%lld threads=%lld rows_per_block=%lld grid=%lld "
+             "vectors=%lld",
+             in.name, {out.bytes, v.threads, v.rows_per_block, grid, vectors});
+  return SPTG_OK;
+}
+
+// ---------------------------------------------------------- 4-bit weights
+// CTAs sharing K (a cluster): as many as keep every CTA at least two ring
+// stages of K, until the CTAs fill the GPU about twice.
+int w4_splits(int64_t n_tiles, int64_t k_stages, int64_t m_blocks, int sm_count) {
+  int splits = 1;
+  while (splits < 8 && n_tiles * m_blocks * splits < 2 * sm_count && k_stages >= 4 * splits) splits *= 2;
+  return splits;
+}
+
+int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type, const void* X,
+            int64_t ldx, const float* x_scales, const uint8_t* codes, int64_t ldw,
+            const void* scales, const uint8_t* zeros, void* Y, int64_t ldy, cudaStream_t stream) {
+  TypeInfo xt, ot;
+  if (!type_info(x_type, xt) || !type_info(out_type, ot) || ot.bytes != 2 ||
+      (xt.bytes == 2 && x_type != out_type))
+    return refuse(SPTG_ERR_ARG, "x is f16 or bf16 (and so is Y), or s8 or e4m3 (Y f16 or bf16)");
+  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+    return refuse(SPTG_ERR_ARG, "dimensions must be in [0, 2^31)");
+  if (group != 32 && group != 64 && group != 128)
+    return refuse(SPTG_ERR_ARG, "groups of 32, 64 or 128 columns");
+  if (K % group != 0) return refuse(SPTG_ERR_ARG, "K must be a multiple of the group");
+  if (M == 0 || N == 0) {
+    set_config("kernel=none type=%s (empty output)", xt.name, {});
+    return SPTG_OK;
+  }
+  if (!Y || (K > 0 && (!X || !codes || !scales))) return refuse(SPTG_ERR_ARG, "null pointer");
+  if (xt.bytes == 1 && !x_scales) return refuse(SPTG_ERR_ARG, "8-bit rows need their scales");
+  if (xt.bytes == 2 && x_scales) return refuse(SPTG_ERR_ARG, "16-bit rows take no scales");
+  if (ldy < N || (K > 0 && (ldx < K || ldw < K / 2)) || ldx > INT32_MAX || ldw > INT32_MAX)
+    return refuse(SPTG_ERR_ARG, "row pitches must satisfy ldx >= K, ldw >= K / 2, ldy >= N (< 2^31)");
+  if ((reinterpret_cast<uintptr_t>(Y) & 1u) || (reinterpret_cast<uintptr_t>(scales) & 1u) ||
+      (reinterpret_cast<uintptr_t>(x_scales) & 3u))
+    return refuse(SPTG_ERR_ALIGN, "a pointer is not aligned to its element type");
+  if (K > 0 && (!aligned16(X) || !aligned16(codes) || !multiple16(ldx, xt.bytes) || ldw % 16 != 0))
+    return refuse(SPTG_ERR_ALIGN, "x and the codes need 16-byte aligned bases and row pitches");
+  int dev = 0;
+  DeviceInfo di;
+  int rc = device_info(di, dev);
+  if (rc) return rc;
+  if (K == 0) {  // the empty sum
+    const cudaError_t e = cudaMemset2DAsync(Y, static_cast<size_t>(ldy) * 2, 0,
+                                            static_cast<size_t>(N) * 2, M, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset2DAsync");
+    set_config("kernel=zero-fill type=%s", xt.name, {});
+    return SPTG_OK;
+  }
+  // rows of x in a CTA: 8, 16, 32 or 64; more rows go in blocks of 64, each
+  // passing over the weights
+  const int nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
+  const int64_t m_blocks = (M + 8 * nt - 1) / (8 * nt);
+  if (m_blocks > 65535) return refuse(SPTG_ERR_ARG, "at most 64 * 65535 rows of x");
+  int xk;
+  const void* fn;
+  switch (x_type) {
+    case SPTG_T_BF16: xk = W4_BF16; fn = w4_kernel_bf16(nt, group); break;
+    case SPTG_T_F16: xk = W4_F16; fn = w4_kernel_f16(nt, group); break;
+    case SPTG_T_S8: xk = W4_S8; fn = w4_kernel_s8(nt, group); break;
+    default: xk = W4_E4M3; fn = w4_kernel_e4m3(nt, group); break;
+  }
+  const int64_t n_tiles = (N + W4_ROWS - 1) / W4_ROWS;
+  const int64_t k_stages = (K + W4_STAGE_K - 1) / W4_STAGE_K;
+  const int splits = w4_splits(n_tiles, k_stages, m_blocks, di.sm_count);
+  if (n_tiles * splits > INT32_MAX) return refuse(SPTG_ERR_ARG, "too many columns");
+  // two CTAs to an SM: rings of up to 96 KB
+  const int stages = std::max(2, std::min(W4_MAX_STAGES, (96 << 10) / w4_stage_bytes(xk, nt)));
+  const int smem = w4_smem(xk, nt, stages);
+  CUtensorMap mw, mx;
+  rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, K / 2, N, W4_STAGE_K / 2, W4_ROWS,
+                   CU_TENSOR_MAP_SWIZZLE_128B, ldw);
+  if (rc) return rc;
+  rc = make_map_3d(&mx, xt.tma, X, 32, M, K / 32, static_cast<uint64_t>(ldx) * xt.bytes,
+                   32 * xt.bytes, 32, 8 * nt, W4_UNITS, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (rc) return rc;
+  rc = ensure_smem(dev, fn, smem);
+  if (rc) return rc;
+  W4Params p;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.stages = stages;
+  p.splits = splits;
+  p.scales = static_cast<const uint16_t*>(scales);
+  p.zeros = zeros;
+  p.x_scales = x_scales;
+  p.out = static_cast<uint16_t*>(Y);
+  p.ldo = ldy;
+  p.out_bf16 = out_type == SPTG_T_BF16;
+  p.error_word = di.error_word;
+  p.timeout_ns = kOpTimeoutNs;
+  void* args[] = {&mw, &mx, &p};
+  const cudaError_t e =
+      launch_op(fn, dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_blocks)),
+                W4_THREADS, smem, splits, stream, args);
+  if (e != cudaSuccess) return cuda_fail(e, "gemm_w4 launch");
+  set_config("kernel=w4 type=%s rows=%lld group=%lld splits=%lld stages=%lld grid=%lld m_blocks=%lld "
+             "smem=%lld",
+             xt.name, {8 * nt, group, splits, stages, n_tiles * splits, m_blocks, smem});
+  return SPTG_OK;
+}
+
+// -------------------------------------------------------- grouped products
+// One of the three grouped products. `a` is the features' operand (W, or dY
+// for dW), `b` the ragged side's (X or dY; X for dW).
+int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, const int32_t* offsets,
+            const void* a, int64_t lda, const void* b, int64_t ldb, void* out, int64_t ldo,
+            cudaStream_t stream) {
+  DtypeInfo d;
+  if (!dtype_info(dtype, d) || d.is_int8) return refuse(SPTG_ERR_ARG, "grouped products take the float dtypes");
+  if (E < 0 || T < 0 || N < 0 || K < 0 || T > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+    return refuse(SPTG_ERR_ARG, "dimensions must be in [0, 2^31)");
+  if (E > GROUPED_MAX_EXPERTS) return refuse(SPTG_ERR_ARG, "at most 1024 experts");
+  // columns of the output and length of the sum (dW: the rows)
+  const int64_t cols = mode == GROUPED_Y ? N : K;
+  const int64_t sum = mode == GROUPED_Y ? K : N;
+  const bool dw = mode == GROUPED_DW;
+  if ((dw ? E * N * K : T * cols) == 0) {
+    set_config("kernel=none dtype=%s (empty output)", d.name, {});
+    return SPTG_OK;
+  }
+  if (!out) return refuse(SPTG_ERR_ARG, "null pointer");
+  const int64_t b_cols = dw ? K : sum;
+  const bool nothing = dw ? T == 0 : (sum == 0 || E == 0);
+  if (!nothing && (!a || !b || !offsets)) return refuse(SPTG_ERR_ARG, "null pointer");
+  if (ldo < cols || ldo > INT32_MAX || (!nothing && (ldb < b_cols || ldb > INT32_MAX || (dw && (lda < N || lda > INT32_MAX)))))
+    return refuse(SPTG_ERR_ARG, "row pitches must be at least the row lengths (< 2^31)");
+  if (!aligned16(out) || !multiple16(cols, d.out_bytes) || !multiple16(ldo, d.out_bytes) ||
+      !multiple16(N, d.in_bytes) || !multiple16(K, d.in_bytes) ||
+      (!nothing && (!aligned16(a) || !aligned16(b) || !multiple16(ldb, d.in_bytes) ||
+                    (dw && !multiple16(lda, d.in_bytes)))))
+    return refuse(SPTG_ERR_ALIGN, "TMA needs 16-byte aligned bases and row pitches");
+  if (!nothing && (reinterpret_cast<uintptr_t>(offsets) & 3u))
+    return refuse(SPTG_ERR_ALIGN, "offsets not aligned to their type");
+  int dev = 0;
+  DeviceInfo di;
+  int rc = device_info(di, dev);
+  if (rc) return rc;
+  if (nothing) {  // empty sums
+    const int64_t rows = dw ? E * N : T;
+    const cudaError_t e = cudaMemset2DAsync(out, static_cast<size_t>(ldo) * d.out_bytes, 0,
+                                            static_cast<size_t>(cols) * d.out_bytes, rows, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset2DAsync");
+    set_config("kernel=zero-fill dtype=%s", d.name, {});
+    return SPTG_OK;
+  }
+  // Tiles up to 64 rows wide (and a deeper ring of weights) where the experts
+  // have few rows on average.
+  const int tt = (!dw && T <= 32 * E) ? 64 : 256;
+  const int64_t F = mode == GROUPED_DX ? K : N;
+  const int64_t nf = (F + 255) / 256;
+  const int64_t tiles = dw ? E * nf * ((K + 255) / 256) : nf * (T / tt + E + 2);
+  if (tiles > INT32_MAX / 2) return refuse(SPTG_ERR_ARG, "too many tiles");
+  KernelVariant v;
+  if (mode == GROUPED_Y)
+    v = d.in_bf16 ? grouped_variant_y_bf16(d.out_kind, tt) : grouped_variant_y_f16(d.out_kind, tt);
+  else if (mode == GROUPED_DX)
+    v = d.in_bf16 ? grouped_variant_dx_bf16(d.out_kind, tt) : grouped_variant_dx_f16(d.out_kind, tt);
+  else
+    v = d.in_bf16 ? grouped_variant_dw_bf16(d.out_kind, tt) : grouped_variant_dw_f16(d.out_kind, tt);
+  CUtensorMap ma, mb, mb4;
+  if (dw) {
+    rc = make_map_2d(&ma, d.in_tma, 2, a, N, T, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, lda);
+    if (!rc) rc = make_map_2d(&mb, d.in_tma, 2, b, K, T, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, ldb);
+    mb4 = mb;
+  } else {
+    rc = make_map_3d(&ma, d.in_tma, a, K, N, E, K * 2, N * K * 2, 64, mode == GROUPED_Y ? 128 : 64, 1,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!rc) rc = make_map_2d(&mb, d.in_tma, 2, b, sum, T, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, ldb);
+    if (!rc) rc = make_map_2d(&mb4, d.in_tma, 2, b, sum, T, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, ldb);
+  }
+  if (rc) return rc;
+  rc = ensure_smem(dev, v.fn, v.smem);
+  if (rc) return rc;
+  GroupedParams p;
+  p.experts = static_cast<int>(E);
+  p.T = static_cast<int>(T);
+  p.F = static_cast<int>(F);
+  p.C = static_cast<int>(dw ? K : sum);
+  p.offsets = offsets;
+  p.out = out;
+  p.ldo = ldo;
+  p.expert_pitch = N * K;
+  p.keep_weights = tt == 256;
+  p.error_word = di.error_word;
+  p.timeout_ns = kOpTimeoutNs;
+  const int64_t pairs = std::min<int64_t>(tiles, pair_slots(dev, v, di.sm_count));
+  void* args[] = {&ma, &mb, &mb4, &p};
+  const cudaError_t e =
+      launch_op(v.fn, dim3(static_cast<unsigned>(2 * pairs)), v.threads, v.smem, 2, stream, args);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
+  set_config("kernel=grouped dtype=%s mode=%lld experts=%lld tile_n=%lld stages=%lld grid=%lld smem=%lld",
+             d.name, {mode, E, tt, v.stages, 2 * pairs, v.smem});
+  return SPTG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type out_type,
+                      const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                      const void* weight, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
+                      float* scales, void* stream) {
+  return guarded([&] {
+    return add_rms_norm(rows, cols, in_type, out_type, x, ldx, residual, ldr, weight, eps, h, ldh,
+                        y, ldy, scales, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int sptg_gemm_w4(int64_t M, int64_t N, int64_t K, int group, sptg_type x_type, sptg_type out_type,
+                 const void* X, int64_t ldx, const float* x_scales, const uint8_t* codes,
+                 int64_t ldw, const void* scales, const uint8_t* zeros, void* Y, int64_t ldy,
+                 void* stream) {
+  return guarded([&] {
+    return gemm_w4(M, N, K, group, x_type, out_type, X, ldx, x_scales, codes, ldw, scales, zeros, Y,
+                   ldy, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int sptg_grouped_gemm(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype dtype,
+                      const int32_t* offsets, const void* X, int64_t ldx, const void* W, void* Y,
+                      int64_t ldy, void* stream) {
+  return guarded([&] {
+    return grouped(GROUPED_Y, E, T, N, K, dtype, offsets, W, 0, X, ldx, Y, ldy,
+                   static_cast<cudaStream_t>(stream));
+  });
+}
+
+int sptg_grouped_gemm_dx(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype dtype,
+                         const int32_t* offsets, const void* dY, int64_t lddy, const void* W,
+                         void* dX, int64_t lddx, void* stream) {
+  return guarded([&] {
+    return grouped(GROUPED_DX, E, T, N, K, dtype, offsets, W, 0, dY, lddy, dX, lddx,
+                   static_cast<cudaStream_t>(stream));
+  });
+}
+
+int sptg_grouped_gemm_dw(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype dtype,
+                         const int32_t* offsets, const void* dY, int64_t lddy, const void* X,
+                         int64_t ldx, void* dW, void* stream) {
+  return guarded([&] {
+    return grouped(GROUPED_DW, E, T, N, K, dtype, offsets, dY, lddy, X, ldx, dW, K,
+                   static_cast<cudaStream_t>(stream));
+  });
+}
+
+}  // extern "C"

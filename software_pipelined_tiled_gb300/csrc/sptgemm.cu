@@ -22,6 +22,8 @@
 
 #include "sptgemm.h"
 
+#include "add_rms_norm.cuh"  // NormParams
+#include "grouped_gemm.cuh"  // GroupedParams
 #include "skinny_cluster_gemm.cuh"  // SkinnyClusterParams
 #include "skinny_gemm.cuh"  // SkinnyParams
 #include "skinny_pair_gemm.cuh"  // SkinnyPairParams
@@ -29,6 +31,7 @@
 #include "square_gemm.cuh"  // SquareParams
 #include "stream_scale.cuh"  // StreamParams
 #include "variants.h"
+#include "w4_gemm.cuh"  // W4Params
 
 // Device error word: a timed-out bounded wait ors its site code in here.
 __device__ unsigned int g_sptg_error_word;
@@ -1790,3 +1793,6 @@ int sptg_gemm_skinny_noalloc(int64_t M, int64_t N, int64_t K, sptg_dtype dtype, 
 }
 
 }  // extern "C"
+
+// The operators around the dense products (their own entry points).
+#include "layer_ops.cuh"

@@ -52,4 +52,30 @@ cudaError_t launch_s8_to_f16(const void* srcA, int64_t lda, int64_t rows_a, cons
                              int64_t ldb, int64_t rows_b, int64_t K, void* dstA, void* dstB,
                              int blocks, cudaStream_t stream, bool overlap_previous);
 
+// The residual-addition and norm kernel for rows of `cols` elements (out_kind:
+// NormOut); `vectors`: every row starts 16-byte aligned (8-bit outputs 8-byte)
+// and cols is a multiple of 8.
+struct NormVariant {
+  const void* fn;
+  int threads;
+  int rows_per_block;
+};
+NormVariant norm_variant(bool bf16, int out_kind, int cols, bool vectors);
+
+// The 4-bit-weight kernel for up to 8 * nt rows of x (nt = 1, 2, 4 or 8) and
+// groups of 32, 64 or 128 columns, by the type of x.
+const void* w4_kernel_bf16(int nt, int group);
+const void* w4_kernel_f16(int nt, int group);
+const void* w4_kernel_s8(int nt, int group);
+const void* w4_kernel_e4m3(int nt, int group);
+
+// Grouped products (Y, dX, dW) with tiles up to tt = 64 or 256 wide on the
+// ragged side (dW: 256).
+KernelVariant grouped_variant_y_bf16(int out_kind, int tt);
+KernelVariant grouped_variant_y_f16(int out_kind, int tt);
+KernelVariant grouped_variant_dx_bf16(int out_kind, int tt);
+KernelVariant grouped_variant_dx_f16(int out_kind, int tt);
+KernelVariant grouped_variant_dw_bf16(int out_kind, int tt);
+KernelVariant grouped_variant_dw_f16(int out_kind, int tt);
+
 }  // namespace sptg
