@@ -175,12 +175,73 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
 }
 
 // ---------------------------------------------------------- 4-bit weights
-// CTAs sharing K (a cluster): as many as keep every CTA at least two ring
-// stages of K, until the CTAs fill the GPU about twice.
-int w4_splits(int64_t n_tiles, int64_t k_stages, int64_t m_blocks, int sm_count) {
-  int splits = 1;
-  while (splits < 8 && n_tiles * m_blocks * splits < 2 * sm_count && k_stages >= 4 * splits) splits *= 2;
-  return splits;
+// Rows of weights per CTA and CTAs sharing K (a cluster). For each cluster
+// size the rows are cut so that the CTAs fill the GPU's slots once to four
+// times (fewer in clusters of 4 and 8, which have to find their SMs in one
+// processing cluster), within `least` to `most`; the choice with the least
+// time of its busiest slot wins, counted in bytes of codes with 32 KB for
+// starting a CTA and 16 KB for a cluster's exchange.
+struct W4Shape {
+  int rows, splits;
+};
+
+W4Shape w4_shape(int64_t N, int64_t k_stages, int64_t least, int64_t most, int64_t m_blocks,
+                 const int* slots) {
+  constexpr int64_t step = 16;
+  W4Shape best{static_cast<int>(most), 1};
+  double best_t = 1e300;
+  for (int i = 0; i < 4 && (1 << i) <= k_stages; ++i) {
+    const int splits = 1 << i;
+    for (int64_t waves = 1; waves <= 4; ++waves) {
+      const int64_t fit = (N * splits * m_blocks + slots[i] * waves - 1) / (slots[i] * waves);
+      const int64_t rows = std::min(most, std::max(least, (fit + step - 1) / step * step));
+      const int64_t ctas = (N + rows - 1) / rows * splits * m_blocks;
+      const double rounds = static_cast<double>((ctas + slots[i] - 1) / slots[i]);
+      const double t = rounds * (static_cast<double>((k_stages + splits - 1) / splits) * rows * 128 +
+                                 32768 + (splits > 1 ? 16384 : 0));
+      if (t < best_t * 0.999) {
+        best_t = t;
+        best = {static_cast<int>(rows), splits};
+      }
+    }
+  }
+  return best;
+}
+
+// CTAs resident at once in clusters of 1, 2, 4 and 8, by device and kernel.
+struct W4Slots {
+  int n[4];
+};
+std::map<std::pair<int, const void*>, W4Slots> g_w4_slots;
+
+W4Slots w4_slots(int dev, const void* fn, int per_sm, int threads, int sm_count) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  const auto it = g_w4_slots.find({dev, fn});
+  if (it != g_w4_slots.end()) return it->second;
+  W4Slots w;
+  w.n[0] = per_sm * sm_count;
+  for (int i = 1; i < 4; ++i) {
+    cudaLaunchConfig_t lc;
+    memset(&lc, 0, sizeof(lc));
+    lc.gridDim = dim3(static_cast<unsigned>(sm_count >> i << i), 1, 1);
+    lc.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    lc.dynamicSmemBytes = 225 * 1024 / per_sm;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &lc) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = w.n[0] >> i;
+    }
+    w.n[i] = std::min(w.n[0], n << i);
+  }
+  g_w4_slots[{dev, fn}] = w;
+  return w;
 }
 
 int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type, const void* X,
@@ -220,40 +281,84 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
     set_config("kernel=zero-fill type=%s", xt.name, {});
     return SPTG_OK;
   }
-  // rows of x in a CTA: 8, 16, 32 or 64; more rows go in blocks of 64, each
-  // passing over the weights
-  const int nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
-  const int64_t m_blocks = (M + 8 * nt - 1) / (8 * nt);
+  // Up to 8 rows of x: the streaming kernel. More: the tensor-core tile kernel
+  // with 16, 32 or 64 rows, in blocks of 64 that each pass over the weights.
+  const bool tile = M > 8;
+  const int nt = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int64_t m_blocks = (M + nt - 1) / nt;
   if (m_blocks > 65535) return refuse(SPTG_ERR_ARG, "at most 64 * 65535 rows of x");
   int xk;
   const void* fn;
   switch (x_type) {
-    case SPTG_T_BF16: xk = W4_BF16; fn = w4_kernel_bf16(nt, group); break;
-    case SPTG_T_F16: xk = W4_F16; fn = w4_kernel_f16(nt, group); break;
-    case SPTG_T_S8: xk = W4_S8; fn = w4_kernel_s8(nt, group); break;
-    default: xk = W4_E4M3; fn = w4_kernel_e4m3(nt, group); break;
+    case SPTG_T_BF16:
+      xk = W4_BF16;
+      fn = tile ? w4_tile_kernel_bf16(nt, group) : w4_kernel_bf16(group);
+      break;
+    case SPTG_T_F16:
+      xk = W4_F16;
+      fn = tile ? w4_tile_kernel_f16(nt, group) : w4_kernel_f16(group);
+      break;
+    case SPTG_T_S8:
+      xk = W4_S8;
+      fn = tile ? w4_tile_kernel_s8(nt, group) : w4_kernel_s8(group);
+      break;
+    default:
+      xk = W4_E4M3;
+      fn = tile ? w4_tile_kernel_e4m3(nt, group) : w4_kernel_e4m3(group);
+      break;
   }
-  const int64_t n_tiles = (N + W4_ROWS - 1) / W4_ROWS;
   const int64_t k_stages = (K + W4_STAGE_K - 1) / W4_STAGE_K;
-  const int splits = w4_splits(n_tiles, k_stages, m_blocks, di.sm_count);
+  rc = ensure_smem(dev, fn, 232448);  // the ring's size differs from call to call
+  if (rc) return rc;
+  const int threads = tile ? w4t_threads(nt) : 32 * W4_MAX_WARPS;
+  const W4Slots slots = w4_slots(dev, fn, tile ? 1 : W4_CTAS_PER_SM, threads, di.sm_count);
+  const W4Shape shape = w4_shape(N, k_stages, 64, tile ? W4T_MAX_ROWS : W4_MAX_ROWS,
+                                 m_blocks, slots.n);
+  const int rows = shape.rows, splits = shape.splits;
+  const int64_t n_tiles = (N + rows - 1) / rows;
   if (n_tiles * splits > INT32_MAX) return refuse(SPTG_ERR_ARG, "too many columns");
-  // two CTAs to an SM: rings of up to 96 KB
-  const int stages = std::max(2, std::min(W4_MAX_STAGES, (96 << 10) / w4_stage_bytes(xk, nt)));
-  const int smem = w4_smem(xk, nt, stages);
-  CUtensorMap mw, mx;
-  rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, K / 2, N, W4_STAGE_K / 2, W4_ROWS,
-                   CU_TENSOR_MAP_SWIZZLE_128B, ldw);
-  if (rc) return rc;
-  rc = make_map_3d(&mx, xt.tma, X, 32, M, K / 32, static_cast<uint64_t>(ldx) * xt.bytes,
-                   32 * xt.bytes, 32, 8 * nt, W4_UNITS, CU_TENSOR_MAP_SWIZZLE_NONE);
-  if (rc) return rc;
-  rc = ensure_smem(dev, fn, smem);
-  if (rc) return rc;
   W4Params p;
+  int smem, launch_threads = threads;
+  if (tile) {
+    // as many stages of codes as fit beside two to four of x
+    p.segment = nt == 64 ? 2 : W4T_MAX_X_STAGES;
+    p.stages = W4T_MAX_STAGES;
+    while (p.stages > 2 && w4t_smem(xk, nt, rows, p.stages, p.segment) > 232448) --p.stages;
+    smem = w4t_smem(xk, nt, rows, p.stages, p.segment);
+  } else {
+    // Shared memory: rings of at least two stages, x of a segment in at most
+    // two fifths of the rest (a segment is a multiple of the parts of K that
+    // warps take), the rings with what is left.
+    const int budget = (224 << 10) / W4_CTAS_PER_SM - 1024;
+    const int live_m = static_cast<int>(M);
+    const int kw = W4_KW;
+    const int slice = static_cast<int>((k_stages + splits - 1) / splits);
+    const int x_stage = live_m * W4_STAGE_K * 2 + W4_STAGE_K / group * 8 * 4;
+    p.segment = std::max(kw, (budget * 2 / 5) / x_stage / kw * kw);
+    p.segment = std::min(p.segment, (slice + kw - 1) / kw * kw);
+    p.stages = W4_MAX_STAGES;
+    while (p.stages > 2 && w4_layout(group, rows, p.stages, p.segment, live_m).total > budget)
+      --p.stages;
+    const W4Layout lay = w4_layout(group, rows, p.stages, p.segment, live_m);
+    smem = lay.total + 1024;
+    launch_threads = 32 * lay.warps;
+  }
+  CUtensorMap mw, mx;
+  rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, K / 2, N, W4_STAGE_K / 2,
+                   tile ? rows : W4_WARP_ROWS, CU_TENSOR_MAP_SWIZZLE_128B, ldw);
+  if (!rc && tile) {
+    if (xt.bytes == 1)
+      rc = make_map_2d(&mx, xt.tma, 1, X, K, M, W4_STAGE_K, nt, CU_TENSOR_MAP_SWIZZLE_NONE, ldx);
+    else
+      rc = make_map_2d(&mx, xt.tma, 2, X, K, M, 64, nt, CU_TENSOR_MAP_SWIZZLE_128B, ldx);
+  }
+  if (rc) return rc;
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
-  p.stages = stages;
+  p.x = X;
+  p.ldx = ldx;
+  p.rows = rows;
   p.splits = splits;
   p.scales = static_cast<const uint16_t*>(scales);
   p.zeros = zeros;
@@ -261,16 +366,23 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   p.out = static_cast<uint16_t*>(Y);
   p.ldo = ldy;
   p.out_bf16 = out_type == SPTG_T_BF16;
+  // a lane's groups are one load of up to 8 bytes of scales and 4 of zeros
+  p.wide = K % W4_STAGE_K == 0 && aligned16(scales) && (reinterpret_cast<uintptr_t>(zeros) & 7u) == 0;
+  p.mask_lo = 0x000f000fu;
+  p.mask_hi = 0x00f000f0u;
+  p.magic = x_type == SPTG_T_BF16 ? 0x43004300u : 0x64006400u;
   p.error_word = di.error_word;
   p.timeout_ns = kOpTimeoutNs;
-  void* args[] = {&mw, &mx, &p};
+  void* tile_args[] = {&mw, &mx, &p};
+  void* stream_args[] = {&mw, &p};
   const cudaError_t e =
       launch_op(fn, dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_blocks)),
-                W4_THREADS, smem, splits, stream, args);
+                launch_threads, smem, splits, stream, tile ? tile_args : stream_args);
   if (e != cudaSuccess) return cuda_fail(e, "gemm_w4 launch");
-  set_config("kernel=w4 type=%s rows=%lld group=%lld splits=%lld stages=%lld grid=%lld m_blocks=%lld "
-             "smem=%lld",
-             xt.name, {8 * nt, group, splits, stages, n_tiles * splits, m_blocks, smem});
+  set_config("kernel=w4 type=%s x_rows=%lld group=%lld rows=%lld splits=%lld stages=%lld grid=%lld "
+             "m_blocks=%lld threads=%lld segment=%lld smem=%lld",
+             xt.name, {nt, group, rows, splits, p.stages, n_tiles * splits, m_blocks, launch_threads,
+                       p.segment, smem});
   return SPTG_OK;
 }
 

@@ -32,6 +32,7 @@
 #include "stream_scale.cuh"  // StreamParams
 #include "variants.h"
 #include "w4_gemm.cuh"  // W4Params
+#include "w4_tile_gemm.cuh"
 
 // Device error word: a timed-out bounded wait ors its site code in here.
 __device__ unsigned int g_sptg_error_word;

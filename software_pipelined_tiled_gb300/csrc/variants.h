@@ -62,12 +62,17 @@ struct NormVariant {
 };
 NormVariant norm_variant(bool bf16, int out_kind, int cols, bool vectors);
 
-// The 4-bit-weight kernel for up to 8 * nt rows of x (nt = 1, 2, 4 or 8) and
-// groups of 32, 64 or 128 columns, by the type of x.
-const void* w4_kernel_bf16(int nt, int group);
-const void* w4_kernel_f16(int nt, int group);
-const void* w4_kernel_s8(int nt, int group);
-const void* w4_kernel_e4m3(int nt, int group);
+// The 4-bit-weight kernel for up to 8 rows of x and groups of 32, 64 or 128
+// columns, by the type of x.
+const void* w4_kernel_bf16(int group);
+const void* w4_kernel_f16(int group);
+const void* w4_kernel_s8(int group);
+const void* w4_kernel_e4m3(int group);
+// The one for 9 to 64 rows of x (ntok = 16, 32 or 64).
+const void* w4_tile_kernel_bf16(int ntok, int group);
+const void* w4_tile_kernel_f16(int ntok, int group);
+const void* w4_tile_kernel_s8(int ntok, int group);
+const void* w4_tile_kernel_e4m3(int ntok, int group);
 
 // Grouped products (Y, dX, dW) with tiles up to tt = 64 or 256 wide on the
 // ragged side (dW: 256).

@@ -1,4 +1,4 @@
-// w4_gemm.cuh -- products of a few rows with 4-bit weights and group scales.
+// w4_gemm.cuh -- products of up to 8 rows with 4-bit weights and group scales.
 //
 //   Y[m, n] = xs[m] * sum_g s[n, g] * sum_{k in group g} x[m, k] * (w[n, k] - z[n, g])
 //
@@ -7,35 +7,45 @@
 // 128 columns; z: a zero point 0 ... 15 for each group, or 8 everywhere; x: 16
 // bits, or 8 bits (int8, e4m3) with a 32-bit scale xs for each row.
 //
-// Exactness: w - z is an integer of magnitude at most 15 and is formed exactly
-// in the 16-bit type (a code under the exponent of 128 in bfloat16, of 1024 in
-// binary16, less the zero point under the same exponent); 8-bit x is exact in
-// binary16. The tensor core multiplies these and adds in 32 bits; a group's
-// sum is scaled in 32 bits and added to the running sum in 32 bits. The only
-// rounding to 16 bits is that of Y.
+// The zero points come out of the sums: sum x (w - z) = sum x w - z sum x. The
+// codes then need no arithmetic at all before the tensor core, only masks:
+// in binary16 a code in the low bits of a half is the number code * 2^-24 (a
+// subnormal, exact), one in bits 4-7 is 16 times that; in bfloat16 a code under
+// the exponent of 128 is 128 + code. 8-bit x is exact in binary16. The products
+// are exact, the sums are kept in 32 bits for each group, the group's zero
+// point (bfloat16: 128 + z) times the group's sum of x is taken off in 32 bits,
+// and the scaled result is added to the running sum in 32 bits. The only
+// rounding to 16 bits is that of Y. (Subtracting the zero point from every code
+// first costs 8 instructions more for 16 x 32 codes, beside about 24.)
 //
-// Memory-bound for few rows: N * K / 2 bytes of codes, each read once. A CTA
-// takes 128 rows of weights and a range of K; a producer warp streams ring
-// stages of 256 columns (128 rows x 128 bytes of codes, 128-byte swizzled,
-// and the same columns of the 8 * NT rows of x) with the tensor-copy engine;
-// eight consumer warps each hold 16 rows of weights against all rows of x.
-// The range of K may be split over the CTAs of a cluster, whose partial sums
-// meet through distributed shared memory in CTA order (no atomics: the result
-// does not depend on timing).
+// Memory-bound: N * K / 2 bytes of codes, each read once. A CTA takes a block of
+// rows of weights and a range of K (the whole, or a share of it in a cluster of
+// 2, 4 or 8 CTAs, whose partial sums meet through distributed shared memory in
+// CTA order: no atomics, the result does not depend on timing). It keeps its
+// range of x in shared memory, in the order and type the products use; where x
+// is too large for that, it goes through K in segments. Each warp streams the
+// codes of its own 16 rows through a ring of its own with the tensor-copy engine
+// (stages of 256 columns: 128 bytes a row, 128-byte swizzled) and refills a stage
+// when it has read it, so that no warp ever waits for another inside a segment.
+//
+// Measured: one binary16 row through 32768 x 8192, groups of 64 with zero
+// points, 36.4 us (4.0 TB/s; the floor at 6783 GB/s is 21.7 us). The copies
+// alone take 23.4 us; what remains is bound by the issue of about 32
+// instructions for 16 x 32 codes and the scales' own. A ring shared by the CTA,
+// x travelling in its stages, needed two CTA-wide barriers a stage and took
+// 46 us, whatever was taken out of the arithmetic.
 //
 // The multiply is the warp-wide 16 x 8 x 16 instruction, whose operands live
-// in registers: weights are widened in registers and never stored, and with 8
-// rows of x the instruction's rate is far above what memory delivers (a
-// tcgen05 instruction would need the widened weights in shared memory: four
-// times the codes' bytes written and read there).
+// in registers: codes are spread in registers and never stored, and with up to
+// 8 rows of x the instruction's rate (1024 multiply-adds a cycle and SM) is far
+// above what memory delivers. More rows go to w4_tile_gemm.cuh.
 //
 // Order within K: the products' sum does not depend on which columns share an
 // instruction, as long as both operands agree. Lane (g, t) = (lane / 4, lane
 // mod 4) of a warp reads one 32-bit word of codes -- columns 8t ... 8t + 7 of
-// a unit of 32 columns -- for its rows g and g + 8. Masking the word with
-// 0x000f000f after shifts by 0, 4, 8, 12 leaves the column pairs (0, 4),
-// (1, 5), (2, 6), (3, 7), which feed two instructions; x's eight values are
-// paired the same way.
+// a unit of 32 columns -- for its rows g and g + 8. Masking the word after
+// shifts leaves the column pairs (0, 4), (1, 5), (2, 6), (3, 7), which feed two
+// instructions; x's eight values are paired the same way when x is stored.
 #pragma once
 
 #include <cstdint>
@@ -49,312 +59,453 @@ namespace sptg {
 // x in binary16.
 enum W4X : int { W4_BF16 = 0, W4_F16 = 1, W4_S8 = 2, W4_E4M3 = 3 };
 
-constexpr int W4_ROWS = 128;      // rows of weights per CTA
 constexpr int W4_STAGE_K = 256;   // columns per ring stage
 constexpr int W4_UNITS = 8;       // units of 32 columns in a stage
-constexpr int W4_CONSUMERS = 8;   // warps of 16 rows of weights
-constexpr int W4_THREADS = 32 * (W4_CONSUMERS + 1);
-constexpr int W4_CODE_STAGE = W4_ROWS * W4_STAGE_K / 2;
-constexpr int W4_MAX_STAGES = 8;
-constexpr int W4_RED_PITCH = 132;  // 32-bit words between rows of x in the partial sums
-constexpr int W4_BAR_BYTES = 2 * W4_MAX_STAGES * 8 + 16;
+constexpr int W4_MAX_STAGES = 8;  // of a warp's ring
+constexpr int W4_X_ROWS = 8;      // rows of x: the instruction's N side
+constexpr int W4_WARP_ROWS = 16;  // rows of weights of a warp: its M side
+// Two warps share rows of weights, each with half of a segment's K: with one
+// wave of CTAs 14 warps to an SM would otherwise have to hide the latency of
+// their own instructions.
+constexpr int W4_KW = 2;
+// Up to 14 warps to a CTA, two CTAs to an SM with 72 registers a thread.
+constexpr int W4_MAX_WARPS = 14;
+constexpr int W4_CTAS_PER_SM = 2;
+constexpr int W4_MAX_ROWS = W4_WARP_ROWS * W4_MAX_WARPS / W4_KW;
 
 struct W4Params {
   int M, N, K;
-  int stages;          // ring depth
-  int splits;          // CTAs of the cluster, sharing K
+  const void* x;           // M rows of K, ldx elements apart
+  int64_t ldx;
+  int rows;                // rows of weights per CTA, a multiple of 16
+  int stages;              // depth of each warp's ring
+  int splits;              // CTAs of the cluster, sharing K
+  int segment;             // stages of K whose x is held at a time (tile kernel: depth of
+                           // the ring of x)
   const uint16_t* scales;  // N x K / G
   const uint8_t* zeros;    // N x K / G, or null (8)
   const float* x_scales;   // M, or null (1)
   uint16_t* out;           // M rows of N, ldo apart
   int64_t ldo;
   int out_bf16;            // type of scales and out: bfloat16, else binary16
+  int wide;                // scales (and zeros) read a lane's groups at a time
+  uint32_t mask_lo, mask_hi, magic;  // of spread_codes
   unsigned int* error_word;
   uint64_t timeout_ns;
 };
 
 __host__ __device__ constexpr int w4_x_bytes(int xk) { return xk >= W4_S8 ? 1 : 2; }
-__host__ __device__ constexpr int w4_x_stage(int xk, int nt) {
-  return W4_STAGE_K * 8 * nt * w4_x_bytes(xk);
-}
-__host__ __device__ constexpr int w4_stage_bytes(int xk, int nt) {
-  return W4_CODE_STAGE + w4_x_stage(xk, nt);
-}
-__host__ __device__ constexpr int w4_red_bytes(int nt) { return 8 * nt * W4_RED_PITCH * 4; }
-__host__ __device__ constexpr int w4_smem(int xk, int nt, int stages) {
-  const int ring = stages * w4_stage_bytes(xk, nt);
-  const int red = w4_red_bytes(nt);
-  return (ring > red ? ring : red) + W4_BAR_BYTES + 1024;
+
+// Shared memory of a CTA, in this order: the rings, x (16 bits), the sums of x
+// over groups, the scales, the barriers. The partial sums reuse the front.
+struct W4Layout {
+  int warps, ring, x, xsum, table, bars, total;
+};
+__host__ __device__ constexpr int w4_red_pitch(int rows) { return rows + 4; }
+__host__ __device__ constexpr W4Layout w4_layout(int group, int rows, int stages, int segment,
+                                                 int live_m) {
+  W4Layout l{};
+  l.warps = rows / W4_WARP_ROWS * W4_KW;
+  l.ring = 0;
+  l.x = l.warps * stages * W4_WARP_ROWS * (W4_STAGE_K / 2);
+  l.xsum = l.x + segment * live_m * W4_STAGE_K * 2;
+  l.table = l.xsum + segment * (W4_STAGE_K / group) * W4_X_ROWS * 4;
+  l.bars = l.table + l.warps * W4_WARP_ROWS * (W4_STAGE_K / group) * 8;
+  // (the partial sums of all warps take the place of everything before)
+  const int red = W4_KW * W4_X_ROWS * w4_red_pitch(rows) * 4;
+  if (l.bars < red) l.bars = (red + 15) & ~15;
+  l.total = l.bars + W4_MAX_WARPS * W4_MAX_STAGES * 8 + 16;
+  return l;
 }
 
+// d = a b + (first ? 0 : d); a literal zero takes no registers
 template <bool BF>
-__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
+__device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1, bool first) {
+  const float c[4] = {first ? 0.0f : d[0], first ? 0.0f : d[1], first ? 0.0f : d[2],
+                      first ? 0.0f : d[3]};
   if constexpr (BF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+__device__ __forceinline__ float2 lds64f(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+
+// b = 1024 + 128 + a in each half, to a
+__device__ __forceinline__ uint32_t unbias2(uint32_t b) {
+  constexpr uint32_t BIAS = 0x64806480u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&BIAS));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// (w & mask) | magic in one instruction
+__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+  return r;
+}
+
+// The eight codes of a word as column pairs: (0,4), (2,6) in `a`, (1,5), (3,7)
+// in `b`. Binary16: a as code * 2^-24, b as code * 2^-20. bfloat16 has room for
+// a code in the low four bits only: 128 + code everywhere, three shifts.
 template <bool BF>
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ void spread_codes(const W4Params& p, uint32_t w, uint32_t (&a)[2],
+                                             uint32_t (&b)[2]) {
   if constexpr (BF) {
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&d);
+    a[0] = pick(w, p.mask_lo, p.magic);
+    b[0] = pick(w >> 4, p.mask_lo, p.magic);
+    a[1] = pick(w >> 8, p.mask_lo, p.magic);
+    b[1] = pick(w >> 12, p.mask_lo, p.magic);
   } else {
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a),
-                              *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&d);
+    a[0] = w & p.mask_lo;
+    b[0] = w & p.mask_hi;
+    a[1] = (w >> 8) & p.mask_lo;
+    b[1] = (w >> 8) & p.mask_hi;
   }
 }
 
-// The eight codes of a word, less the zero point (given as the pair of
-// magic | z), as the four column pairs (0,4), (1,5), (2,6), (3,7).
-template <bool BF>
-__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t zz, uint32_t (&out)[4]) {
-  constexpr uint32_t MAGIC = BF ? 0x43004300u : 0x64006400u;
-#pragma unroll
-  for (int p = 0; p < 4; ++p) out[p] = sub2<BF>(((w >> (4 * p)) & 0x000f000fu) | MAGIC, zz);
-}
-
-// This lane's eight values of x of one unit, in the same column pairs.
+// One lane's eight values of x of one unit (8-bit: in v.x and v.y), from memory's order to the column
+// pairs of spread_codes, in the type of the product.
 template <int XK>
-__device__ __forceinline__ void load_x(uint32_t addr, uint32_t (&b)[4]) {
+__device__ __forceinline__ uint4 pair_x(const uint4 v) {
   if constexpr (XK == W4_BF16 || XK == W4_F16) {
-    uint32_t v[4];
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(addr));
-    b[0] = __byte_perm(v[0], v[2], 0x5410);
-    b[1] = __byte_perm(v[0], v[2], 0x7632);
-    b[2] = __byte_perm(v[1], v[3], 0x5410);
-    b[3] = __byte_perm(v[1], v[3], 0x7632);
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x7632));
   } else {
-    uint32_t v0, v1;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v0), "=r"(v1) : "r"(addr));
-    const uint32_t lo = __byte_perm(v0, v1, 0x5140);  // bytes 0, 4, 1, 5
-    const uint32_t hi = __byte_perm(v0, v1, 0x7362);  // bytes 2, 6, 3, 7
+    const uint32_t lo = __byte_perm(v.x, v.y, 0x5140);  // bytes 0, 4, 1, 5
+    const uint32_t hi = __byte_perm(v.x, v.y, 0x7362);  // bytes 2, 6, 3, 7
     if constexpr (XK == W4_S8) {
       // a byte with its sign bit flipped is b + 128; under the exponent byte
       // 0x64 it is 1024 + b + 128 in binary16, and 1152 less leaves b
-      constexpr uint32_t E = 0x64646464u, BIAS = 0x64806480u;
+      constexpr uint32_t E = 0x64646464u;
       const uint32_t l = lo ^ 0x80808080u, h = hi ^ 0x80808080u;
-      b[0] = sub2<false>(__byte_perm(l, E, 0x4140), BIAS);
-      b[1] = sub2<false>(__byte_perm(l, E, 0x4342), BIAS);
-      b[2] = sub2<false>(__byte_perm(h, E, 0x4140), BIAS);
-      b[3] = sub2<false>(__byte_perm(h, E, 0x4342), BIAS);
+      return make_uint4(unbias2(__byte_perm(l, E, 0x4140)), unbias2(__byte_perm(h, E, 0x4140)),
+                        unbias2(__byte_perm(l, E, 0x4342)), unbias2(__byte_perm(h, E, 0x4342)));
     } else {
       const uint32_t q[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+      uint32_t b[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __half2_raw r =
             __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q[i]), __NV_E4M3);
         b[i] = static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
       }
+      return make_uint4(b[0], b[2], b[1], b[3]);
     }
   }
 }
 
-template <int XK, int NT, int G>
-__global__ void __launch_bounds__(W4_THREADS)
-    w4_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const W4Params p) {
+template <int XK, int G>
+__global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
+    w4_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const W4Params p) {
   constexpr bool BF = XK == W4_BF16;
   constexpr int XB = w4_x_bytes(XK);
+  constexpr int KW = W4_KW, WR = W4_WARP_ROWS;
   constexpr int GROUPS = W4_STAGE_K / G;      // groups in a stage
   constexpr int UPG = G / 32;                 // units in a group
-  constexpr int SREGS = 2 * GROUPS / 4;       // scale words per lane and stage
-  constexpr int STAGE = w4_stage_bytes(XK, NT);
+  constexpr int STAGE = WR * (W4_STAGE_K / 2);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int S = p.stages;
+  const int R = p.rows;
+  const W4Layout lay = w4_layout(G, R, S, p.segment, p.M);
   const uint32_t sbase = smem_addr(smem);
-  const int ring = S * STAGE > w4_red_bytes(NT) ? S * STAGE : w4_red_bytes(NT);
-  const uint32_t bar0 = sbase + ring;
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (W4_MAX_STAGES + s); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + ring + 2 * W4_MAX_STAGES * 8);
+  volatile int* abort_flag =
+      reinterpret_cast<volatile int*>(smem + lay.bars + W4_MAX_WARPS * W4_MAX_STAGES * 8);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % p.splits;  // = the CTA's rank in its cluster
-  const int n0 = static_cast<int>(blockIdx.x) / p.splits * W4_ROWS;
-  const int m0 = static_cast<int>(blockIdx.y) * 8 * NT;
-  // this CTA's stages of K
+  const int n0 = static_cast<int>(blockIdx.x) / p.splits * R;
+  const int rw = warp / KW, kw = warp % KW;  // block of rows, part of K
+  const int row0 = n0 + WR * rw;
+  const uint32_t ring = sbase + warp * S * STAGE;
+  const uint32_t full0 = sbase + lay.bars + warp * (W4_MAX_STAGES * 8);
+  // this CTA's stages of K, in segments; a warp's part of segment i is
+  // [part_of(i, kw), part_of(i, kw + 1))
   const int KS = (p.K + W4_STAGE_K - 1) / W4_STAGE_K;
   const int ks0 = static_cast<int>(static_cast<int64_t>(KS) * rank / p.splits);
   const int ks1 = static_cast<int>(static_cast<int64_t>(KS) * (rank + 1) / p.splits);
+  const int segments = (ks1 - ks0 + p.segment - 1) / p.segment;
+  auto part_of = [&](int seg, int part) {
+    const int a = ks0 + seg * p.segment, b = min(ks1, a + p.segment);
+    return a + (b - a) * part / KW;
+  };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), W4_CONSUMERS);
-    }
-    *abort_flag = 0;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(full0 + 8 * s, 1);
     fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
     prefetch_tensor_map(&tmW);
-    prefetch_tensor_map(&tmX);
   }
   __syncthreads();
-  // warm L2 with the first stages of codes while the previous kernel drains
-  // (the loads proper wait for it)
-  if (threadIdx.x == 32 * W4_CONSUMERS && m0 == 0)
-    for (int ks = ks0; ks < min(ks1, ks0 + S); ++ks) tma_prefetch_l2_2d(&tmW, ks * (W4_STAGE_K / 2), n0);
   grid_dependency_wait();
   const WaitCtl ctl{p.timeout_ns, p.error_word, abort_flag};
-  float acc[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
 
-  if (warp == W4_CONSUMERS) {
-    // ------------------------------------------------------------ producer
-    const bool leader = elect_one_sync();
-    // codes are read once unless several blocks of rows of x pass over them
-    const uint64_t pol_w = gridDim.y > 1 ? policy_evict_last() : policy_evict_first();
-    const uint64_t pol_x = policy_evict_last();
-    int issued = 0;
-    bool ok = true;
-    int s = 0;
-    uint32_t round = 0;
-    for (int ks = ks0; ks < ks1; ++ks) {
-      if (round > 0 && !__all_sync(0xffffffffu, wait_bounded(empty_bar(s), (round & 1u) ^ 1u, ctl,
-                                                              WAIT_PRODUCER_EMPTY))) {
-        ok = false;
-        break;
+  // The copies run ahead of the products through segments and stages.
+  const bool leader = elect_one_sync();
+  const uint64_t pol = policy_evict_first();  // codes are read once
+  int issued = 0;
+  int next_seg = 0, next_ks = segments > 0 ? part_of(0, kw) : 0;
+  auto issue_next = [&](int s) {
+    while (next_seg < segments && next_ks >= part_of(next_seg, kw + 1)) {
+      ++next_seg;
+      next_ks = part_of(next_seg, kw);
+    }
+    if (next_seg >= segments) return;
+    if (leader) {
+      mbar_arrive_expect_tx(full0 + 8 * s, STAGE);
+      tma_load_2d(ring + s * STAGE, &tmW, full0 + 8 * s, next_ks * (W4_STAGE_K / 2), row0, pol);
+    }
+    ++next_ks;
+    ++issued;
+  };
+  for (int s = 0; s < S; ++s) issue_next(s);
+
+  // Scales and zero points. A lane fetches those of one row for PG groups of
+  // a stage, a stage ahead, and then writes what the products use -- the
+  // factor of a group's sum of products and that of its sum of x, in 32 bits --
+  // into the warp's table of [group][row of the warp]. Rows past N read the
+  // last row's. Where every row's scales fill whole stages and lie aligned
+  // (p.wide), PG of them are one load; elsewhere one by one, with groups past
+  // the end dropped.
+  const int KG = p.K / G;
+  constexpr int PG = GROUPS / 2;
+  const int srow = min(row0 + (lane & 15), p.N - 1);
+  const int sgroup = (lane >> 4) * PG;  // the lane's first group of a stage
+  const uint16_t* my_scales = p.scales + static_cast<int64_t>(srow) * KG + sgroup;
+  const uint8_t* my_zeros =
+      p.zeros ? p.zeros + static_cast<int64_t>(srow) * KG + sgroup : nullptr;
+  float2* table = reinterpret_cast<float2*>(smem + lay.table) + warp * (WR * GROUPS) + sgroup * WR +
+                  (lane & 15);
+  uint32_t next_s[(PG + 1) / 2], next_z[(PG + 3) / 4];  // as they lie in memory
+  auto load_scales = [&](int ks) {
+    const uint16_t* ps = my_scales + ks * GROUPS;
+    const uint8_t* pz = my_zeros + ks * GROUPS;
+    // (rows are far apart: a whole line of each is called into L2 at once)
+    if (p.wide) {
+      if constexpr (PG == 1)
+        asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];" : "=r"(next_s[0]) : "l"(ps));
+      else if constexpr (PG == 2)
+        asm volatile("ld.global.nc.L2::128B.b32 %0, [%1];" : "=r"(next_s[0]) : "l"(ps));
+      else
+        asm volatile("ld.global.nc.L2::128B.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(next_s[0]), "=r"(next_s[PG / 2 - 1])
+                     : "l"(ps));
+      if (p.zeros) {
+        if constexpr (PG == 1)
+          asm volatile("ld.global.nc.L2::128B.u8 %0, [%1];" : "=r"(next_z[0]) : "l"(pz));
+        else if constexpr (PG == 2)
+          asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];" : "=r"(next_z[0]) : "l"(pz));
+        else
+          asm volatile("ld.global.nc.L2::128B.b32 %0, [%1];" : "=r"(next_z[0]) : "l"(pz));
       }
-      if (leader) {
-        mbar_arrive_expect_tx(full_bar(s), STAGE);
-        tma_load_2d(sbase + s * STAGE, &tmW, full_bar(s), ks * (W4_STAGE_K / 2), n0, pol_w);
-        tma_load_3d(sbase + s * STAGE + W4_CODE_STAGE, &tmX, full_bar(s), 0, m0, ks * W4_UNITS,
-                    pol_x);
-      }
-      ++issued;
-      if (++s == S) {
-        s = 0;
-        ++round;
+    } else {
+#pragma unroll
+      for (int i = 0; i < (PG + 1) / 2; ++i) next_s[i] = 0;
+#pragma unroll
+      for (int i = 0; i < (PG + 3) / 4; ++i) next_z[i] = 0;
+#pragma unroll
+      for (int i = 0; i < PG; ++i) {
+        if (ks * GROUPS + sgroup + i < KG) {
+          next_s[i / 2] |= static_cast<uint32_t>(__ldg(ps + i)) << (16 * (i & 1));
+          if (p.zeros) next_z[i / 4] |= static_cast<uint32_t>(__ldg(pz + i)) << (8 * (i & 3));
+        }
       }
     }
-    grid_launch_dependents();
-    if (!ok) {
-      // let every copy already issued land before the CTA can exit
-      for (int i = max(0, issued - S); i < issued; ++i) {
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(full_bar(i % S), static_cast<uint32_t>(i / S) & 1u) &&
-               global_timer_ns() - t0 < ctl.timeout_ns) {
-        }
-      }
+  };
+  auto put_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < PG; ++i) {
+      // (keeps every use of the loads from moving up to them, a stage early)
+      if (i % 2 == 0) asm volatile("" : "+r"(next_s[i / 2]));
+      if (i % 4 == 0) asm volatile("" : "+r"(next_z[i / 4]));
+      const uint32_t h = i % 2 ? next_s[i / 2] >> 16 : next_s[i / 2] & 0xffffu;
+      const bool bf = BF || (XK != W4_F16 && p.out_bf16);
+      const float sc = bf ? __uint_as_float(h << 16)
+                          : __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+      const uint32_t z = p.zeros ? next_z[i / 4] >> (8 * (i % 4)) & 15u : 8u;
+      // 2^23 + z, as a float; bfloat16: -(128 + z), binary16: -z * 2^-24 (both
+      // exact)
+      const float zf = __uint_as_float(z | 0x4b000000u);
+      table[i * WR] = BF ? make_float2(sc, 8388480.0f - zf)
+                         : make_float2(sc * 16777216.0f, fmaf(zf, -1.0f / 16777216.0f, 0.5f));
     }
-  } else {
-    // ----------------------------------------------------------- consumers
-    const int g = lane >> 2, t = lane & 3;
-    const int row = n0 + 16 * warp + g;  // and row + 8
-    const int64_t KG = p.K / G;
-    // Lane t of a quad loads the scales (and zero points) j = t, t + 4, ... of
-    // the stage's 2 * GROUPS: j < GROUPS are row g's, the others row g + 8's.
-    auto load_scales = [&](int ks, uint32_t (&sv)[SREGS]) {
-#pragma unroll
-      for (int i = 0; i < SREGS; ++i) {
-        const int j = 4 * i + t;
-        const int r = row + (j >= GROUPS ? 8 : 0);
-        const int64_t gi = static_cast<int64_t>(ks) * GROUPS + (j % GROUPS);
-        uint32_t v = 8u << 16;
-        if (r < p.N && gi < KG) {
-          const int64_t at = static_cast<int64_t>(r) * KG + gi;
-          const uint32_t z = p.zeros ? (p.zeros[at] & 15u) : 8u;
-          v = p.scales[at] | (z << 16);
+  };
+
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // this lane's row of x in the products' columns; rows past the last read the
+  // last one's values, in columns that are never stored
+  const uint32_t x_row = sbase + lay.x + static_cast<uint32_t>(min(g, p.M - 1) * 64 + t * 16);
+
+  int s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  if (segments > 0) load_scales(part_of(0, kw));
+  for (int seg = 0; seg < segments; ++seg) {
+    // ------------------------------------------------------- x of a segment
+    const int first = ks0 + seg * p.segment;
+    const int units = (min(ks1, first + p.segment) - first) * W4_UNITS;
+    if (seg > 0) __syncthreads();  // every warp is done with the one before
+    // 8 columns of a row of x a thread; G / 8 neighbouring threads a group
+    for (int i = threadIdx.x; i < units * 4 * p.M; i += blockDim.x) {
+      const int m = i / (units * 4), c = i - m * (units * 4);
+      const int k = first * W4_STAGE_K + c * 8;
+      uint4 b = make_uint4(0, 0, 0, 0);
+      float sum = 0.0f;
+      if (k < p.K) {
+        const uint8_t* src = static_cast<const uint8_t*>(p.x) +
+                             (static_cast<int64_t>(m) * p.ldx + k) * XB;
+        uint4 v;
+        if constexpr (XB == 2) {
+          v = *reinterpret_cast<const uint4*>(src);
+        } else {
+          const uint2 e = *reinterpret_cast<const uint2*>(src);
+          v = make_uint4(e.x, e.y, 0, 0);
         }
-        sv[i] = v;
+        b = pair_x<XK>(v);
       }
-    };
-    uint32_t sv[SREGS];
-    if (ks0 < ks1) load_scales(ks0, sv);
-    int s = 0;
-    uint32_t phase = 0;
-    for (int ks = ks0; ks < ks1; ++ks) {
-      uint32_t nv[SREGS];
-      if (ks + 1 < ks1) load_scales(ks + 1, nv);
-      if (!__all_sync(0xffffffffu, wait_bounded(full_bar(s), phase, ctl, WAIT_MMA_FULL))) break;
-      const uint32_t codes = sbase + s * STAGE + (16 * warp + g) * 128 + 4 * t;
-      const uint32_t xs = sbase + s * STAGE + W4_CODE_STAGE + lane * (8 * XB);
-      float part[NT][4];
-      uint32_t zlo = 0, zhi = 0;
-      float slo = 0.0f, shi = 0.0f;
+      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int u = 0; u < W4_UNITS; ++u) {
-        if (u % UPG == 0) {
-          constexpr uint32_t MAGIC = BF ? 0x4300u : 0x6400u;
-          const int jl = u / UPG, jh = GROUPS + u / UPG;
-          const uint32_t vl = __shfl_sync(0xffffffffu, sv[jl / 4], (lane & 28) | (jl & 3));
-          const uint32_t vh = __shfl_sync(0xffffffffu, sv[jh / 4], (lane & 28) | (jh & 3));
-          zlo = (MAGIC | (vl >> 16)) * 0x00010001u;
-          zhi = (MAGIC | (vh >> 16)) * 0x00010001u;
-          const bool bf = BF || (XK != W4_F16 && p.out_bf16);
-          slo = bf ? __uint_as_float(vl << 16) : __half2float(__ushort_as_half(vl & 0xffffu));
-          shi = bf ? __uint_as_float(vh << 16) : __half2float(__ushort_as_half(vh & 0xffffu));
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (BF) {
+          sum += __uint_as_float(w[q] << 16) + __uint_as_float(w[q] & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
+          sum += f.x + f.y;
         }
-        // rows g and g + 8 share their low three bits: the same swizzle
-        const uint32_t off = static_cast<uint32_t>((u ^ g) << 4);
-        uint32_t wl, wh;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(wl) : "r"(codes + off));
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(wh) : "r"(codes + 8 * 128 + off));
-        uint32_t al[4], ah[4];
-        widen_codes<BF>(wl, zlo, al);
-        widen_codes<BF>(wh, zhi, ah);
-        const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]};
-        const uint32_t a1[4] = {al[2], ah[2], al[3], ah[3]};
+      }
+      *reinterpret_cast<uint4*>(smem + lay.x + ((c >> 2) * p.M + m) * 64 + (c & 3) * 16) = b;
+      // the lanes of a group are in the loop together: their number divides
+      // a row's, and the block's
+      const uint32_t mask = (G == 128 ? 0xffffu << (lane & 16) : G == 64 ? 0xffu << (lane & 24)
+                                                                         : 0xfu << (lane & 28));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint32_t b[4];
-          load_x<XK>(xs + (u * NT + j) * (256 * XB), b);
-          mma_m16n8k16<BF>(part[j], a0, b[0], b[1]);
-          mma_m16n8k16<BF>(part[j], a1, b[2], b[3]);
-        }
-        if (u % UPG == UPG - 1) {
+      for (int o = G / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+      if ((c & (G / 8 - 1)) == 0)
+        reinterpret_cast<float*>(smem + lay.xsum)[(c / (G / 8)) * W4_X_ROWS + m] = sum;
+    }
+    __syncthreads();
+    // -------------------------------------------------------------- stages
+    const int end = part_of(seg, kw + 1);
+    for (int ks = part_of(seg, kw); ok && ks < end; ++ks) {
+      put_scales();
+      // (a segment's last stage loads its own scales again where the warp's
+      // next part is not the next stage)
+      const int after = ks + 1 < end ? ks + 1 : seg + 1 < segments ? part_of(seg + 1, kw) : ks;
+      load_scales(after);
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, wait_bounded_lazy(full0 + 8 * s, phase, ctl, WAIT_MMA_FULL));
+      if (!ok) break;
+      const uint32_t codes = ring + s * STAGE + g * 128;
+      const uint32_t swz = static_cast<uint32_t>(g << 4 | t << 2);
+      const uint32_t xu = static_cast<uint32_t>((ks - first) * W4_UNITS * p.M * 64);
+      const uint32_t x_step = static_cast<uint32_t>(p.M * 64);
+      const uint32_t tab = sbase + lay.table + (warp * (WR * GROUPS) + g) * 8;
+      const uint32_t xsums = sbase + lay.xsum + (ks - first) * (GROUPS * W4_X_ROWS * 4) + t * 8;
+      // sums of products over a group; binary16: the pairs of spread_codes'
+      // a and b apart, b's 16 times too large
+      constexpr int PARTS = BF ? 1 : 2;
+      float part[PARTS][4];
+      // (four units at a time: unrolled further, the loads all move to the
+      // front and spill)
+      constexpr int UB = 4;
+#pragma unroll 1
+      for (int u0 = 0; u0 < W4_UNITS; u0 += UB) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            acc[j][0] += slo * part[j][0];
-            acc[j][1] += slo * part[j][1];
-            acc[j][2] += shi * part[j][2];
-            acc[j][3] += shi * part[j][3];
+        for (int ui = 0; ui < UB; ++ui) {
+          const int u = u0 + ui;
+          // rows 8 apart share their low three bits: the same swizzle
+          const uint32_t off = codes + (swz ^ static_cast<uint32_t>(u << 4));
+          uint32_t al[2], bl[2], ah[2], bh[2];
+          spread_codes<BF>(p, lds32(off), al, bl);
+          spread_codes<BF>(p, lds32(off + 1024), ah, bh);
+          const uint32_t a[4] = {al[0], ah[0], al[1], ah[1]};
+          const uint32_t b[4] = {bl[0], bh[0], bl[1], bh[1]};
+          const uint4 x = lds128(x_row + xu + static_cast<uint32_t>(u) * x_step);
+          const bool start = ui % UPG == 0;  // of the group
+          mma_m16n8k16<BF>(part[0], a, x.x, x.y, start);
+          mma_m16n8k16<BF>(part[PARTS - 1], b, x.z, x.w, start && PARTS == 2);
+          if (ui % UPG == UPG - 1) {
+            const int gi = u / UPG;
+            const float2 sx = lds64f(xsums + gi * (W4_X_ROWS * 4));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 f = lds64f(tab + (gi * WR + 8 * h) * 8);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float v = part[0][2 * h + i];
+                if constexpr (!BF) v = fmaf(part[1][2 * h + i], 0.0625f, v);
+                v = fmaf(f.y, i ? sx.y : sx.x, v);
+                acc[2 * h + i] = fmaf(f.x, v, acc[2 * h + i]);
+              }
+            }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty_bar(s));
-#pragma unroll
-      for (int i = 0; i < SREGS; ++i) sv[i] = nv[i];
+      issue_next(s);
       if (++s == S) {
         s = 0;
         phase ^= 1u;
       }
     }
-    // Every stage has been read: the ring becomes the buffer of partial sums.
-    named_barrier_sync(1, 32 * W4_CONSUMERS);
-    float* red = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float* r0 = red + (8 * j + 2 * t) * W4_RED_PITCH + 16 * warp + g;
-      r0[0] = acc[j][0];
-      r0[W4_RED_PITCH] = acc[j][1];
-      r0[8] = acc[j][2];
-      r0[W4_RED_PITCH + 8] = acc[j][3];
+  }
+  grid_launch_dependents();
+  if (!ok) {
+    // a wait ran out: let every copy already issued land before the CTA exits
+    for (int i = max(0, issued - S); i < issued; ++i) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(full0 + 8 * (i % S), static_cast<uint32_t>(i / S) & 1u) &&
+             global_timer_ns() - t0 < ctl.timeout_ns) {
+      }
     }
+  }
+  // Everything has been read: the partial sums take the rings' place.
+  __syncthreads();
+  const int pitch = w4_red_pitch(R);
+  {
+    float* red = reinterpret_cast<float*>(smem) + (kw * W4_X_ROWS + 2 * t) * pitch + WR * rw + g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[(i & 1) * pitch + 8 * (i >> 1)] = acc[i];
   }
   __syncwarp();
   if (p.splits > 1)
@@ -362,29 +513,31 @@ __global__ void __launch_bounds__(W4_THREADS)
   else
     __syncthreads();
   // Each CTA of the cluster adds up its share of the rows of weights, over
-  // the CTAs in order.
-  const int rows = W4_ROWS / p.splits;
-  const int live_m = min(8 * NT, p.M - m0);
-  for (int i = threadIdx.x; i < rows * live_m; i += W4_THREADS) {
+  // the CTAs and parts of K in order.
+  const int rows = R / p.splits;
+  for (int i = threadIdx.x; i < rows * p.M; i += blockDim.x) {
     const int m = i / rows, r = rank * rows + i % rows;
-    const uint32_t at = sbase + static_cast<uint32_t>((m * W4_RED_PITCH + r) * 4);
+    const uint32_t at0 = sbase + static_cast<uint32_t>((m * pitch + r) * 4);
     float v = 0.0f;
     for (int c = 0; c < p.splits; ++c) {
-      float a;
-      if (p.splits > 1)
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(a)
-                     : "r"(map_to_cta(at, static_cast<uint32_t>(c))));
-      else
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(a) : "r"(at));
-      v += a;
+      const uint32_t from = p.splits > 1 ? map_to_cta(at0, static_cast<uint32_t>(c)) : at0;
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        const uint32_t addr = from + static_cast<uint32_t>(k * W4_X_ROWS * pitch * 4);
+        float a;
+        if (p.splits > 1)
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(addr));
+        else
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(a) : "r"(addr));
+        v += a;
+      }
     }
-    if (p.x_scales) v *= p.x_scales[m0 + m];
+    if (p.x_scales) v *= p.x_scales[m];
     if (n0 + r < p.N) {
       if (p.out_bf16)
-        store_out<OUT_BF16>(p.out, static_cast<int64_t>(m0 + m) * p.ldo + n0 + r, v);
+        store_out<OUT_BF16>(p.out, static_cast<int64_t>(m) * p.ldo + n0 + r, v);
       else
-        store_out<OUT_F16>(p.out, static_cast<int64_t>(m0 + m) * p.ldo + n0 + r, v);
+        store_out<OUT_F16>(p.out, static_cast<int64_t>(m) * p.ldo + n0 + r, v);
     }
   }
   __syncwarp();
@@ -393,23 +546,10 @@ __global__ void __launch_bounds__(W4_THREADS)
 
 // The variants of one kind of x (a translation unit each).
 template <int XK>
-const void* w4_kernel_of(int nt, int group) {
-#define SPTG_W4_CASE(NT_, G_) \
-  if (nt == NT_ && group == G_) return reinterpret_cast<const void*>(&w4_gemm_kernel<XK, NT_, G_>)
-  SPTG_W4_CASE(1, 32);
-  SPTG_W4_CASE(1, 64);
-  SPTG_W4_CASE(1, 128);
-  SPTG_W4_CASE(2, 32);
-  SPTG_W4_CASE(2, 64);
-  SPTG_W4_CASE(2, 128);
-  SPTG_W4_CASE(4, 32);
-  SPTG_W4_CASE(4, 64);
-  SPTG_W4_CASE(4, 128);
-  SPTG_W4_CASE(8, 32);
-  SPTG_W4_CASE(8, 64);
-  SPTG_W4_CASE(8, 128);
-#undef SPTG_W4_CASE
-  return nullptr;
+const void* w4_kernel_of(int group) {
+  return group == 32   ? reinterpret_cast<const void*>(&w4_gemm_kernel<XK, 32>)
+         : group == 64 ? reinterpret_cast<const void*>(&w4_gemm_kernel<XK, 64>)
+                       : reinterpret_cast<const void*>(&w4_gemm_kernel<XK, 128>);
 }
 
 }  // namespace sptg

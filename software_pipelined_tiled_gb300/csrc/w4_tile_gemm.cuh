@@ -1,0 +1,499 @@
+// w4_tile_gemm.cuh -- products of 9 to 64 rows with 4-bit weights and group
+// scales, on the fifth-generation tensor cores.
+//
+// The operator is w4_gemm.cuh's. Past 8 rows the warp-wide instruction of that
+// kernel runs out of rate (1024 multiply-adds a cycle and SM: 56 us for the bare
+// products of 64 rows with 32768 x 8192; such a kernel took 121 us), so the
+// weights are widened once, into shared memory, and one tcgen05 instruction
+// multiplies 128 rows of them with all rows of x (swap-AB: the weights' rows are
+// the instruction's M side, NTOK = 16, 32 or 64 rows of x its N side).
+//
+// Measured: 64 bfloat16 rows through 32768 x 8192, 104 us; 61 rows through
+// 5001 x 4128 with groups of 32, 25.5 us; 16 int8 rows through 8192 x 8192,
+// 22 us (floor 5.2). Not bound by any one unit: the copies alone take about half
+// of it, the widening's instructions another third; what bounds it is the chain
+// of hand-overs of each half stage (copy, widen, fence, multiply, sum).
+//
+// A CTA takes up to 128 rows of weights and a range of K (shared in a cluster,
+// as in w4_gemm.cuh). Roles:
+//
+//   16 warps  widen, in two groups, one for each half of a stage's 256
+//             columns: a lane turns 32 bytes of codes of its row (64 columns)
+//             into its row of an operand tile; before that the group pairs up
+//             its half of the stage's x (and widens 8-bit x), once per CTA
+//   4 warps   (8 with 64 rows of x) sums: a lane owns a row of weights; for
+//             each group it reads the group's sums from tensor memory,
+//             multiplies them by its scale and adds them to its own, in 32 bits
+//   2 warps   producers of the two rings, codes and x, by tensor copy
+//   1 warp    MMA issuer: a half's two operand tiles of 64 columns, one
+//             accumulator a group, eight accumulators in turn
+//
+// Each group of widening warps has one set of operand tiles: while it waits for
+// data, its fence or the MMAs, the other computes. A half is handed over at
+// once, because the fence between the warps' writes and the tensor core's
+// reads is slow, and its MMAs are issued without a branch between them. Codes
+// leave their ring as soon as they are in registers, so that ring is all bytes
+// in flight; x stays in its own until it has been multiplied.
+//
+// Exactness: a widened weight is the integer code - zero point, |.| <= 15, in
+// the 16-bit type of the product; products are exact, sums are kept in 32 bits,
+// and the group's scale multiplies the group's 32-bit sum. Y is rounded once.
+// (Scaling the widened weights instead would round each of them.)
+//
+// Order within K: eight columns of a 16-byte piece lie as 0 4 1 5 2 6 3 7, in
+// both operands (a word of codes gives the pairs (0, 4), (1, 5) ... by masks).
+#pragma once
+
+#include "w4_gemm.cuh"
+
+namespace sptg {
+
+constexpr int W4T_MAX_ROWS = 128;
+constexpr int W4T_WIDEN = 16;                      // widening warps
+constexpr int W4T_MAX_STAGES = 10;
+constexpr int W4T_ACCS = 8;
+__host__ __device__ constexpr int w4t_sum_warps(int ntok) { return ntok == 64 ? 8 : 4; }
+__host__ __device__ constexpr int w4t_threads(int ntok) {
+  return 32 * (W4T_WIDEN + w4t_sum_warps(ntok) + 3);
+}
+
+// Shared memory: two sets of two operand tiles (64 columns of the CTA's rows
+// each; the MMA's 128 rows run on into what follows, into sums that are never
+// stored), the ring of codes, the ring of x (in 16 bits, and as copied where
+// that is 8 bits), the barriers.
+__host__ __device__ constexpr int w4t_a_set(int rows) { return 2 * rows * 128; }
+__host__ __device__ constexpr int w4t_code_stage(int rows) { return rows * (W4_STAGE_K / 2); }
+__host__ __device__ constexpr int w4t_x_bytes(int ntok) { return ntok * W4_STAGE_K * 2; }
+__host__ __device__ constexpr int w4t_x_stage(int xk, int ntok) {
+  return w4t_x_bytes(ntok) + (xk >= W4_S8 ? ntok * W4_STAGE_K : 0);
+}
+constexpr int W4T_MAX_X_STAGES = 4;
+constexpr int W4T_BARS = 2 * W4T_MAX_STAGES + 2 * W4T_MAX_X_STAGES + 4 + 2 * W4T_ACCS + 1;
+__host__ __device__ constexpr int w4t_smem(int xk, int ntok, int rows, int stages, int x_stages) {
+  return 2 * w4t_a_set(rows) + stages * w4t_code_stage(rows) + x_stages * w4t_x_stage(xk, ntok) +
+         W4T_BARS * 8 + 16 + 1024;
+}
+
+// The eight codes of a word, less the zero point (exact), as one 16-byte piece
+// of the operand tile. zz: pairs of the zero point under the same exponent;
+// binary16 takes two of the shifts off the integer pipe with a multiply-add
+// ((1024 + 16 code) / 16 - (64 + z)).
+template <bool BF>
+__device__ __forceinline__ uint4 widen_word(const W4Params& p, uint32_t w, uint32_t zz, uint32_t zh) {
+  uint32_t o[4];
+  if constexpr (BF) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = pick(w >> (4 * i), p.mask_lo, p.magic);
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&zz));
+      o[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+  } else {
+    const uint32_t sixteenth = 0x2c002c00u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = pick(w >> (8 * i), p.mask_lo, p.magic);
+      const uint32_t hi = pick(w >> (8 * i), p.mask_hi, p.magic);
+      const __half2 dl = __hsub2(*reinterpret_cast<const __half2*>(&lo),
+                                 *reinterpret_cast<const __half2*>(&zz));
+      const __half2 dh = __hfma2(*reinterpret_cast<const __half2*>(&hi),
+                                 *reinterpret_cast<const __half2*>(&sixteenth),
+                                 *reinterpret_cast<const __half2*>(&zh));
+      o[2 * i] = *reinterpret_cast<const uint32_t*>(&dl);
+      o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&dh);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int XK, int NTOK, int G>
+__global__ void __launch_bounds__(w4t_threads(NTOK), 1)
+    w4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const W4Params p) {
+  constexpr bool BF = XK == W4_BF16;
+  constexpr bool X8 = XK >= W4_S8;
+  constexpr int GROUPS = W4_STAGE_K / G;
+  constexpr uint32_t IDESC = idesc_f16_f32acc(BF, 128, NTOK);
+  constexpr int SUMS = w4t_sum_warps(NTOK);
+  constexpr int PRODUCER = W4T_WIDEN + SUMS, X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
+  constexpr int COLS = NTOK == 64 ? 32 : NTOK;  // rows of x a sums warp holds
+  constexpr uint32_t TMEM_COLS = W4T_ACCS * NTOK;  // 128, 256 or 512
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const int S = p.stages, SX = p.segment, R = p.rows;
+  const int a_set = w4t_a_set(R);
+  const uint32_t ring = sbase + 2 * a_set;
+  const uint32_t x_ring = ring + S * w4t_code_stage(R);
+  constexpr int X_STAGE = w4t_x_stage(XK, NTOK);
+  constexpr int OFF_RAW = w4t_x_bytes(NTOK);  // in a stage of x: x as copied, if 8-bit
+  const int off_bars = 2 * a_set + S * w4t_code_stage(R) + SX * X_STAGE;
+  const uint32_t bar0 = sbase + off_bars;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };  // codes
+  auto empty_bar = [&](int s) { return bar0 + 8u * (W4T_MAX_STAGES + s); };
+  const uint32_t bar1 = bar0 + 8u * (2 * W4T_MAX_STAGES);
+  auto xfull_bar = [&](int s) { return bar1 + 8u * s; };
+  auto xempty_bar = [&](int s) { return bar1 + 8u * (W4T_MAX_X_STAGES + s); };
+  const uint32_t bar2 = bar1 + 8u * (2 * W4T_MAX_X_STAGES);
+  auto ready_bar = [&](int a) { return bar2 + 8u * a; };       // set widened, half of x paired
+  auto used_bar = [&](int a) { return bar2 + 8u * (2 + a); };  // set multiplied
+  auto tfull_bar = [&](int b) { return bar2 + 8u * (4 + b); };
+  auto tempty_bar = [&](int b) { return bar2 + 8u * (4 + W4T_ACCS + b); };
+  const uint32_t drain_bar = bar0 + 8u * (W4T_BARS - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + off_bars + W4T_BARS * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_bars + W4T_BARS * 8 + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % p.splits;
+  const int n0 = static_cast<int>(blockIdx.x) / p.splits * R;
+  const int m0 = static_cast<int>(blockIdx.y) * NTOK;
+  const int KS = (p.K + W4_STAGE_K - 1) / W4_STAGE_K;
+  const int ks0 = static_cast<int>(static_cast<int64_t>(KS) * rank / p.splits);
+  const int ks1 = static_cast<int>(static_cast<int64_t>(KS) * (rank + 1) / p.splits);
+  const int KG = p.K / G;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), W4T_WIDEN);
+    }
+    for (int s = 0; s < SX; ++s) {
+      mbar_init(xfull_bar(s), 1);
+      mbar_init(xempty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(ready_bar(a), W4T_WIDEN / 2);
+      mbar_init(used_bar(a), 1);
+    }
+    for (int b = 0; b < W4T_ACCS; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), SUMS);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensor_map(&tmW);
+    prefetch_tensor_map(&tmX);
+  }
+  if (warp == ISSUER) {
+    tmem_alloc(smem_addr(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_wait();
+  const WaitCtl ctl{p.timeout_ns, p.error_word, abort_flag};
+  // the whole warp waits together
+  auto wait = [&](uint32_t bar, uint32_t parity, unsigned int site) {
+    return __all_sync(0xffffffffu, wait_bounded_lazy(bar, parity, ctl, site));
+  };
+  float acc[COLS];  // sums warps: this lane's row of weights
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
+
+  if (warp < W4T_WIDEN) {
+    // ---------------------------------------------------------------- widen
+    // Thread: half `set` of a stage, row r, operand tile c of the half (columns
+    // 128 set + 64 c ... + 63 of the stage).
+    const int set = warp >> 3, gw = warp & 7;
+    const int r = threadIdx.x & 127, c = (threadIdx.x >> 7) & 1;
+    const bool works = r < R;
+    const uint8_t* zp = p.zeros ? p.zeros + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG : nullptr;
+    constexpr uint32_t ZLO = BF ? 0x4300u : 0x6400u;
+    constexpr int ZS = G == 32 ? 2 : 1;  // zero points of a lane's columns
+    uint32_t next_z[ZS];
+    auto load_zeros = [&](int ks) {
+#pragma unroll
+      for (int i = 0; i < ZS; ++i)
+        next_z[i] =
+            zp ? __ldg(zp + min((ks * W4_STAGE_K + 128 * set + 64 * c) / G + i, KG - 1)) : 8u;
+    };
+    load_zeros(ks0);
+    // places that do not change from stage to stage: this lane's row of codes
+    // and of its operand tile (128-byte aligned; piece i lies at place
+    // i ^ (r & 7)), its piece of x (row m, piece j of the half's 16; then 16
+    // rows on)
+    const uint32_t code0 = static_cast<uint32_t>(r * 128 + (((4 * set + 2 * c) ^ (r & 7)) << 4));
+    const uint32_t dst =
+        sbase + static_cast<uint32_t>(set * a_set + (c * R + r) * 128 + ((r & 7) << 4));
+    const int m = 2 * gw + (lane >> 4), j = lane & 15;
+    const uint32_t piece0 = static_cast<uint32_t>((2 * set + (j >> 3)) * (NTOK * 128) + m * 128 +
+                                                  (((j & 7) ^ (m & 7)) << 4));
+    const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + m * W4_STAGE_K + (16 * set + j) * 8);
+    int s = 0, sx = 0;
+    uint32_t phase = 0, x_phase = 0, used_phase = 1;
+    for (int ks = ks0; ks < ks1; ++ks) {
+      uint32_t z[ZS];
+#pragma unroll
+      for (int i = 0; i < ZS; ++i) {
+        asm volatile("" : "+r"(next_z[i]));  // no use of the loads before this
+        z[i] = next_z[i] & 15u;
+      }
+      load_zeros(min(ks + 1, ks1 - 1));
+      if (!wait(full_bar(s), phase, WAIT_MMA_FULL)) break;
+      const uint32_t st = ring + s * w4t_code_stage(R);
+      uint4 code[2];
+      if (works) {
+        code[0] = lds128(st + code0);
+        code[1] = lds128(st + (code0 ^ 16u));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(s));
+      if (++s == S) {
+        s = 0;
+        phase ^= 1u;
+      }
+      if (!wait(xfull_bar(sx), x_phase, WAIT_MMA_FULL)) break;
+      // pair up x: pieces of 8 columns
+      const uint32_t sxt = x_ring + sx * X_STAGE;
+#pragma unroll
+      for (int i = 0; i < NTOK; i += 16) {
+        uint4 v;
+        if constexpr (X8) {
+          v.x = lds32(sxt + raw0 + i * W4_STAGE_K);
+          v.y = lds32(sxt + raw0 + i * W4_STAGE_K + 4);
+        } else {
+          v = lds128(sxt + piece0 + i * 128);
+        }
+        v = pair_x<XK>(v);  // the pairs (0,4) (2,6) (1,5) (3,7)
+        sts128(sxt + piece0 + i * 128, make_uint4(v.x, v.z, v.y, v.w));
+      }
+      if (++sx == SX) {
+        sx = 0;
+        x_phase ^= 1u;
+      }
+      // the set's last multiplication has ended (there is none the first time)
+      if (!wait(used_bar(set), used_phase, WAIT_PRODUCER_EMPTY)) break;
+      used_phase ^= 1u;
+      if (works) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t zi = z[ZS == 2 ? i : 0];
+          const uint32_t zz = (ZLO | zi) * 0x00010001u;
+          const uint32_t zh = (0xd400u | (zi << 4)) * 0x00010001u;  // -(64 + z), binary16
+          const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sts128(dst ^ static_cast<uint32_t>((4 * i + k) << 4), widen_word<BF>(p, w[k], zz, zh));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready_bar(set));
+    }
+  } else if (warp < PRODUCER) {
+    // ----------------------------------------------------------------- sums
+    const int q = warp & 3;
+    const int r = 32 * q + lane;
+    const int col0 = warp >= W4T_WIDEN + 4 ? COLS : 0;
+    const uint16_t* sp = p.scales + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG;
+    const int g_end = min(ks1 * GROUPS, KG);
+    uint32_t next_s = 0;
+    auto load_scale = [&](int g) {
+      asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];" : "=r"(next_s) : "l"(sp + min(g, KG - 1)));
+    };
+    load_scale(ks0 * GROUPS);
+    int b = 0;
+    uint32_t phase = 0;
+    for (int gi = ks0 * GROUPS; gi < ks1 * GROUPS; ++gi) {
+      asm volatile("" : "+r"(next_s));
+      const bool bf = BF || (XK != W4_F16 && p.out_bf16);
+      float sc = bf ? __uint_as_float(next_s << 16)
+                    : __half2float(__ushort_as_half(static_cast<unsigned short>(next_s)));
+      if (gi >= g_end) sc = 0.0f;  // past K: the sums are zeros
+      load_scale(gi + 1);
+      if (!wait(tfull_bar(b), phase, WAIT_EPI_TMEM_FULL)) break;
+      tc_fence_after();
+      const uint32_t t_acc = tmem_base + b * NTOK + col0 + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll
+      for (int c = 0; c < COLS; c += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(t_acc + c, v);
+        tmem_wait_ld_regs16(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(sc, __uint_as_float(v[i]), acc[c + i]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(b));
+      if (++b == W4T_ACCS) {
+        b = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp == PRODUCER || warp == X_PRODUCER) {
+    // ------------------------------------------------------------ producers
+    const bool leader = elect_one_sync();
+    const bool of_x = warp == X_PRODUCER;
+    const uint64_t pol =
+        of_x || gridDim.y > 1 ? policy_evict_last() : policy_evict_first();
+    const int depth = of_x ? SX : S;
+    auto full = [&](int s) { return of_x ? xfull_bar(s) : full_bar(s); };
+    int issued = 0;
+    bool ok = true;
+    int s = 0;
+    uint32_t phase = 0;
+    for (int ks = ks0; ks < ks1; ++ks) {
+      ok = wait(of_x ? xempty_bar(s) : empty_bar(s), phase ^ 1u, WAIT_PRODUCER_EMPTY);
+      if (!ok) break;
+      if (leader) {
+        if (!of_x) {
+          mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(w4t_code_stage(R)));
+          tma_load_2d(ring + s * w4t_code_stage(R), &tmW, full_bar(s), ks * (W4_STAGE_K / 2), n0, pol);
+        } else {
+          const uint32_t st = x_ring + s * X_STAGE;
+          mbar_arrive_expect_tx(xfull_bar(s), X8 ? NTOK * W4_STAGE_K : w4t_x_bytes(NTOK));
+          if constexpr (X8) {
+            tma_load_2d(st + OFF_RAW, &tmX, xfull_bar(s), ks * W4_STAGE_K, m0, pol);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tma_load_2d(st + c * (NTOK * 128), &tmX, xfull_bar(s), ks * W4_STAGE_K + 64 * c, m0, pol);
+          }
+        }
+      }
+      ++issued;
+      if (++s == depth) {
+        s = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!of_x) grid_launch_dependents();
+    if (!ok) {
+      // let every copy already issued land before the CTA can exit
+      for (int i = max(0, issued - depth); i < issued; ++i) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(full(i % depth), static_cast<uint32_t>(i / depth) & 1u) &&
+               global_timer_ns() - t0 < ctl.timeout_ns) {
+        }
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- MMA issuer
+    const bool leader = elect_one_sync();
+    int sx = 0, b = 0;
+    uint32_t phase = 0, b_phase = 0;
+    bool ok = true;
+    for (int ks = ks0; ok && ks < ks1; ++ks) {
+      // The waits for a half and its groups' accumulators come first, then its
+      // MMAs (steps of 16 columns, 4 an operand tile, G / 16 a group) without a
+      // branch: each stretch that the elected lane runs alone has a cost of
+      // its own.
+      constexpr int AT_ONCE = GROUPS / 2;
+      constexpr int STEPS = G / 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ok = ok && wait(ready_bar(h), phase, WAIT_MMA_FULL);
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+          ok = ok && wait(tempty_bar(b + i), b_phase ^ 1u, WAIT_MMA_TMEM_EMPTY);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ad = sdesc_k_major_sw128(sbase + h * a_set);
+        const uint64_t xd = sdesc_k_major_sw128(x_ring + sx * X_STAGE + 2 * h * (NTOK * 128));
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < AT_ONCE; ++i) {
+#pragma unroll
+            for (int n = 0; n < STEPS; ++n) {
+              const int k = i * STEPS + n;
+              mma_f16(tmem_base + (b + i) * NTOK,
+                      ad + static_cast<uint64_t>((k >> 2) * (R * 128) >> 4) + 2 * (k & 3),
+                      xd + static_cast<uint64_t>((k >> 2) * (NTOK * 128) >> 4) + 2 * (k & 3), IDESC,
+                      n == 0 ? 0u : 1u);
+            }
+            mma_commit(tfull_bar(b + i));
+          }
+          mma_commit(used_bar(h));
+          if (h == 1) mma_commit(xempty_bar(sx));
+        }
+        __syncwarp();
+        b += AT_ONCE;
+        if (b == W4T_ACCS) {
+          b = 0;
+          b_phase ^= 1u;
+        }
+      }
+      phase ^= 1u;
+      if (++sx == SX) sx = 0;
+    }
+    if (leader) mma_commit(drain_bar);
+    __syncwarp();
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < ctl.timeout_ns) {
+    }
+  }
+  // Every MMA and copy has completed: the partial sums take the front of
+  // shared memory.
+  tc_fence_before();
+  __syncthreads();
+  if (warp == ISSUER) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+  const int pitch = W4T_MAX_ROWS + 4;
+  if (warp >= W4T_WIDEN && warp < PRODUCER) {
+    const int col0 = warp >= W4T_WIDEN + 4 ? COLS : 0;
+    float* red = reinterpret_cast<float*>(smem) + col0 * pitch + 32 * (warp & 3) + lane;
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) red[i * pitch] = acc[i];
+  }
+  __syncwarp();
+  if (p.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // Each CTA of the cluster adds up its share of the rows of weights, over
+  // the CTAs in order.
+  const int rows = R / p.splits;
+  const int live_m = min(NTOK, p.M - m0);
+  for (int i = threadIdx.x; i < rows * live_m; i += w4t_threads(NTOK)) {
+    const int m = i / rows, r = rank * rows + i % rows;
+    const uint32_t at = sbase + static_cast<uint32_t>((m * pitch + r) * 4);
+    float v = 0.0f;
+    for (int c = 0; c < p.splits; ++c) {
+      float x;
+      if (p.splits > 1)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(x)
+                     : "r"(map_to_cta(at, static_cast<uint32_t>(c))));
+      else
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+      v += x;
+    }
+    if (p.x_scales) v *= p.x_scales[m0 + m];
+    if (n0 + r < p.N) {
+      if (p.out_bf16)
+        store_out<OUT_BF16>(p.out, static_cast<int64_t>(m0 + m) * p.ldo + n0 + r, v);
+      else
+        store_out<OUT_F16>(p.out, static_cast<int64_t>(m0 + m) * p.ldo + n0 + r, v);
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// The variants of one kind of x (part of its translation unit).
+template <int XK>
+const void* w4_tile_kernel_of(int ntok, int group) {
+#define SPTG_W4T_CASE(NTOK_, G_) \
+  if (ntok == NTOK_ && group == G_) return reinterpret_cast<const void*>(&w4_tile_kernel<XK, NTOK_, G_>)
+  SPTG_W4T_CASE(16, 32);
+  SPTG_W4T_CASE(16, 64);
+  SPTG_W4T_CASE(16, 128);
+  SPTG_W4T_CASE(32, 32);
+  SPTG_W4T_CASE(32, 64);
+  SPTG_W4T_CASE(32, 128);
+  SPTG_W4T_CASE(64, 32);
+  SPTG_W4T_CASE(64, 64);
+  SPTG_W4T_CASE(64, 128);
+#undef SPTG_W4T_CASE
+  return nullptr;
+}
+
+}  // namespace sptg

@@ -3,10 +3,12 @@
 Argument checks and marshalling only, as in the package's ``gemm``: every step
 runs in the library's CUDA kernels.  Outputs that the caller does not pass are
 allocated on the stream that the call runs on.
+
+A decoding step makes these calls for every layer and token, so the checks are
+written for little time: each looks at attributes only, and what a message
+needs is worked out when a check has failed.
 """
 from __future__ import annotations
-
-import contextlib
 
 import torch
 
@@ -18,53 +20,60 @@ TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.int8: 2, torch.float8_e4m3fn
 _PAIRS = {(torch.float16, torch.float16): 1, (torch.float16, torch.float32): 0,
           (torch.bfloat16, torch.bfloat16): 3, (torch.bfloat16, torch.float32): 4}
 _16BIT = (torch.float16, torch.bfloat16)
-_empty = torch.empty
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+
+_lib = _pkg.load()
+_norm, _w4 = _lib.sptg_add_rms_norm, _lib.sptg_gemm_w4
+_y, _dx, _dw = _lib.sptg_grouped_gemm, _lib.sptg_grouped_gemm_dx, _lib.sptg_grouped_gemm_dw
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _pkg._current_stream)
 
 
-def _pitch(t, rows: int, cols: int, dtype, device, name: str) -> int:
+def _refuse(name: str, t, want: str):
+    raise ValueError(f"{name} must be {want}; it is {t.dtype} of shape {tuple(t.shape)} with "
+                     f"strides {t.stride()} on {t.device}")
+
+
+def _pitch(t, rows: int, cols: int, dtype, device: int, name: str) -> int:
     """Elements between the rows of a rows x cols CUDA tensor with contiguous rows."""
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
-    s0, s1 = t.stride()
-    if s1 != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
-    if rows <= 1:
-        return cols  # the stride of a single row says nothing
-    if s0 < cols:
-        raise ValueError(f"the rows of {name} overlap")
-    return s0
+    if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols):
+        s0, s1 = t.stride()
+        if rows <= 1 or not cols:
+            if s1 == 1 or cols <= 1:
+                return cols  # the pitch of one row says nothing
+        elif s0 >= cols and (s1 == 1 or cols == 1):
+            return s0
+    _refuse(name, t, f"a {rows} x {cols} {dtype} tensor with contiguous rows that do not overlap, "
+                     f"on CUDA device {device}")
 
 
-def _dense(t, shape, dtype, device, name: str):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+def _dense(t, shape, dtype, device: int, name: str):
+    if not (t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()):
+        _refuse(name, t, f"a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {device}")
 
 
 def _matrix(t, name: str):
     if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+        _refuse(name, t, "a 2-D CUDA tensor")
 
 
-def _on(stream):
-    """Allocations inside belong to the stream that the call runs on."""
+def _empty(shape, dtype, device, stream):
     if stream is None:
-        return contextlib.nullcontext()
+        return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call(function, device_index: int, stream, *args):
-    handle = (_pkg._current_stream(device_index) if stream is None
-              else _pkg._stream_handle(stream))
-    if device_index == torch.cuda.current_device():
+def _call(function, device: int, stream, *args):
+    handle = _raw_stream(device) if stream is None else _pkg._stream_handle(stream)
+    if device == _current_device():
         rc = function(*args, handle)
     else:
-        with torch.cuda.device(device_index):
+        with torch.cuda.device(device):
             rc = function(*args, handle)
-    if rc != 0:
+    if rc:
         raise _pkg.SptgError(rc, _pkg.last_error() or _pkg.status_string(rc))
 
 
@@ -80,37 +89,34 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None,
     contiguous rows.
     """
     _matrix(x, "x")
-    dtype, device = x.dtype, x.device
-    if dtype not in _16BIT:
-        raise ValueError(f"x must be float16 or bfloat16, not {dtype}")
+    dtype, device, (rows, cols) = x.dtype, x.get_device(), x.shape
     if out_dtype is None:
         out_dtype = dtype if y is None else y.dtype
-    code = TYPES.get(out_dtype)
-    if code is None or (code < 2 and out_dtype != dtype):
-        raise ValueError(f"out_dtype must be int8, float8_e4m3fn or {dtype}, not {out_dtype}")
-    rows, cols = x.shape
+    in_code, code = TYPES.get(dtype, 9), TYPES.get(out_dtype, 9)
+    if in_code > 1 or code > 3 or (code < 2 and code != in_code):
+        raise ValueError(f"x must be float16 or bfloat16 and out_dtype int8, float8_e4m3fn or x's "
+                         f"type, not {dtype} and {out_dtype}")
     ldx = _pitch(x, rows, cols, dtype, device, "x")
     ldr = _pitch(residual, rows, cols, dtype, device, "residual")
     _dense(weight, (cols,), dtype, device, "weight")
-    with _on(stream):
-        if h is None:
-            h, ldh = _empty((rows, cols), dtype=dtype, device=device), cols
-        else:
-            ldh = _pitch(h, rows, cols, dtype, device, "h")
-        if y is None:
-            y, ldy = _empty((rows, cols), dtype=out_dtype, device=device), cols
-        else:
-            ldy = _pitch(y, rows, cols, out_dtype, device, "y")
-        if code < 2:
-            if scales is not None:
-                raise ValueError("a 16-bit y has no scales")
-        elif scales is None:
-            scales = _empty(rows, dtype=torch.float32, device=device)
-        else:
-            _dense(scales, (rows,), torch.float32, device, "scales")
-    _call((_pkg._lib or _pkg.load()).sptg_add_rms_norm, device.index, stream, rows, cols,
-          TYPES[dtype], code, x.data_ptr(), ldx, residual.data_ptr(), ldr, weight.data_ptr(), eps,
-          h.data_ptr(), ldh, y.data_ptr(), ldy, None if scales is None else scales.data_ptr())
+    if h is None:
+        h, ldh = _empty((rows, cols), dtype, x.device, stream), cols
+    else:
+        ldh = _pitch(h, rows, cols, dtype, device, "h")
+    if y is None:
+        y, ldy = _empty((rows, cols), out_dtype, x.device, stream), cols
+    else:
+        ldy = _pitch(y, rows, cols, out_dtype, device, "y")
+    if code < 2:
+        if scales is not None:
+            raise ValueError("a 16-bit y has no scales")
+    elif scales is None:
+        scales = _empty((rows,), _F32, x.device, stream)
+    else:
+        _dense(scales, (rows,), _F32, device, "scales")
+    _call(_norm, device, stream, rows, cols, in_code, code, x.data_ptr(), ldx, residual.data_ptr(),
+          ldr, weight.data_ptr(), eps, h.data_ptr(), ldh, y.data_ptr(), ldy,
+          None if scales is None else scales.data_ptr())
     return h, y, scales
 
 
@@ -127,64 +133,61 @@ def gemm_w4(x, codes, scales, zeros=None, x_scales=None, out=None, stream=None):
     _matrix(x, "x")
     _matrix(codes, "codes")
     _matrix(scales, "scales")
-    device, dtype = x.device, scales.dtype
-    m, k = x.shape
-    n = codes.shape[0]
-    code = TYPES.get(x.dtype)
-    if dtype not in _16BIT or code is None or (code < 2 and x.dtype != dtype):
+    device, dtype, (m, k), n = x.get_device(), scales.dtype, x.shape, codes.shape[0]
+    code, out_code = TYPES.get(x.dtype, 9), TYPES.get(dtype, 9)
+    if out_code > 1 or code > 3 or (code < 2 and code != out_code):
         raise ValueError("x must be of the scales' 16-bit type, int8 or float8_e4m3fn")
     groups = scales.shape[1]
     group = k // groups if groups else 32
-    if k % 2 or (groups and group * groups != k):
+    if k % 2 or group * groups != k:
         raise ValueError(f"{groups} groups do not divide K = {k}")
     ldx = _pitch(x, m, k, x.dtype, device, "x")
-    ldw = _pitch(codes, n, k // 2, torch.uint8, device, "codes")
+    ldw = _pitch(codes, n, k // 2, _U8, device, "codes")
     _dense(scales, (n, groups), dtype, device, "scales")
     if zeros is not None:
-        _dense(zeros, (n, groups), torch.uint8, device, "zeros")
+        _dense(zeros, (n, groups), _U8, device, "zeros")
     if (code < 2) != (x_scales is None):
         raise ValueError("x_scales belong to 8-bit x, and to no other")
     if x_scales is not None:
-        _dense(x_scales, (m,), torch.float32, device, "x_scales")
+        _dense(x_scales, (m,), _F32, device, "x_scales")
     if out is None:
-        with _on(stream):
-            out = _empty((m, n), dtype=dtype, device=device)
-        ldo = n
+        out, ldo = _empty((m, n), dtype, x.device, stream), n
     else:
         ldo = _pitch(out, m, n, dtype, device, "out")
-    _call((_pkg._lib or _pkg.load()).sptg_gemm_w4, device.index, stream, m, n, k, group, code,
-          TYPES[dtype], x.data_ptr(), ldx, None if x_scales is None else x_scales.data_ptr(),
-          codes.data_ptr(), ldw, scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
-          out.data_ptr(), ldo)
+    _call(_w4, device, stream, m, n, k, group, code, out_code, x.data_ptr(), ldx,
+          None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), ldw,
+          scales.data_ptr(), None if zeros is None else zeros.data_ptr(), out.data_ptr(), ldo)
     return out
 
 
-def _experts(W, rows, offsets, name: str):
-    if W.dim() != 3 or not W.is_cuda or W.dtype not in _16BIT:
-        raise ValueError("W must be an experts x N x K CUDA tensor, float16 or bfloat16")
-    _dense(W, tuple(W.shape), W.dtype, W.device, "W")
-    _matrix(rows, name)
-    _dense(offsets, (W.shape[0] + 1,), torch.int32, W.device, "offsets")
-    return W.shape
-
-
-def _grouped(function, rows, W, offsets, width, cols, out, out_dtype, stream, name):
-    e, n, k = W.shape
-    t = rows.shape[0]
-    dtype, device = W.dtype, W.device
-    ld = _pitch(rows, t, width, dtype, device, name)
+def _pair(dtype, out, out_dtype):
+    """The library's dtype pair, and the output's type."""
     if out_dtype is None:
         out_dtype = dtype if out is None else out.dtype
     pair = _PAIRS.get((dtype, out_dtype))
     if pair is None:
-        raise ValueError(f"the output of {dtype} operands is {dtype} or float32, not {out_dtype}")
+        raise ValueError(f"operands are float16 or bfloat16, the output their type or float32, not "
+                         f"{dtype} and {out_dtype}")
+    return pair, out_dtype
+
+
+def _by_rows(function, rows, W, offsets, by_k, out, out_dtype, stream, name):
+    """grouped_gemm and its gradient by X; by_k: the rows' length is K (else N)."""
+    if W.dim() != 3 or not W.is_cuda:
+        _refuse("W", W, "an experts x N x K CUDA tensor")
+    _matrix(rows, name)
+    (e, n, k), t = W.shape, rows.shape[0]
+    width, cols = (k, n) if by_k else (n, k)
+    dtype, device = W.dtype, W.get_device()
+    pair, out_dtype = _pair(dtype, out, out_dtype)
+    _dense(W, (e, n, k), dtype, device, "W")
+    _dense(offsets, (e + 1,), _I32, device, "offsets")
+    ld = _pitch(rows, t, width, dtype, device, name)
     if out is None:
-        with _on(stream):
-            out = _empty((t, cols), dtype=out_dtype, device=device)
-        ldo = cols
+        out, ldo = _empty((t, cols), out_dtype, W.device, stream), cols
     else:
         ldo = _pitch(out, t, cols, out_dtype, device, "out")
-    _call(function, device.index, stream, e, t, n, k, pair, offsets.data_ptr(), rows.data_ptr(), ld,
+    _call(function, device, stream, e, t, n, k, pair, offsets.data_ptr(), rows.data_ptr(), ld,
           W.data_ptr(), out.data_ptr(), ldo)
     return out
 
@@ -197,16 +200,12 @@ def grouped_gemm(X, W, offsets, out=None, out_dtype=None, stream=None):
     (read there: the call does not wait for them).  Rows of no expert get
     zeros.  out_dtype: the operands' type (default) or float32.  Returns Y, T x N.
     """
-    _, n, k = _experts(W, X, offsets, "X")
-    return _grouped((_pkg._lib or _pkg.load()).sptg_grouped_gemm, X, W, offsets, k, n, out,
-                    out_dtype, stream, "X")
+    return _by_rows(_y, X, W, offsets, True, out, out_dtype, stream, "X")
 
 
 def grouped_gemm_dx(dY, W, offsets, out=None, out_dtype=None, stream=None):
     """Gradient of grouped_gemm by X: ``dX[t] = dY[t] @ W[e]``; dY: T x N. Returns dX, T x K."""
-    _, n, k = _experts(W, dY, offsets, "dY")
-    return _grouped((_pkg._lib or _pkg.load()).sptg_grouped_gemm_dx, dY, W, offsets, n, k, out,
-                    out_dtype, stream, "dY")
+    return _by_rows(_dx, dY, W, offsets, False, out, out_dtype, stream, "dY")
 
 
 def grouped_gemm_dw(dY, X, offsets, out=None, out_dtype=None, stream=None):
@@ -217,25 +216,18 @@ def grouped_gemm_dw(dY, X, offsets, out=None, out_dtype=None, stream=None):
     """
     _matrix(X, "X")
     _matrix(dY, "dY")
-    dtype, device = X.dtype, X.device
-    if dtype not in _16BIT:
-        raise ValueError("X and dY must be float16 or bfloat16")
-    t, k = X.shape
-    n = dY.shape[1]
-    e = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
-    _dense(offsets, (max(e, 0) + 1,), torch.int32, device, "offsets")
+    dtype, device, (t, k), n = X.dtype, X.get_device(), X.shape, dY.shape[1]
+    pair, out_dtype = _pair(dtype, out, out_dtype)
+    if offsets.dim() != 1 or not offsets.shape[0]:
+        _refuse("offsets", offsets, "a 1-D tensor of experts + 1 values")
+    e = offsets.shape[0] - 1
+    _dense(offsets, (e + 1,), _I32, device, "offsets")
     ldx = _pitch(X, t, k, dtype, device, "X")
     ldy = _pitch(dY, t, n, dtype, device, "dY")
-    if out_dtype is None:
-        out_dtype = dtype if out is None else out.dtype
-    pair = _PAIRS.get((dtype, out_dtype))
-    if pair is None:
-        raise ValueError(f"the output of {dtype} operands is {dtype} or float32, not {out_dtype}")
     if out is None:
-        with _on(stream):
-            out = _empty((e, n, k), dtype=out_dtype, device=device)
+        out = _empty((e, n, k), out_dtype, X.device, stream)
     else:
         _dense(out, (e, n, k), out_dtype, device, "out")
-    _call((_pkg._lib or _pkg.load()).sptg_grouped_gemm_dw, device.index, stream, e, t, n, k, pair,
-          offsets.data_ptr(), dY.data_ptr(), ldy, X.data_ptr(), ldx, out.data_ptr())
+    _call(_dw, device, stream, e, t, n, k, pair, offsets.data_ptr(), dY.data_ptr(), ldy,
+          X.data_ptr(), ldx, out.data_ptr())
     return out
