@@ -91,23 +91,11 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, cons
   }
 }
 
-// wait_bounded for kernels in which many warps wait at every stage: a try
-// sleeps in hardware for up to 20 us (a waiting warp that polls takes issue
-// slots from the others), and the clock is first read after 64 failed tries.
+// wait_bounded that reads the clock only after 64 failed tries.
 __device__ __forceinline__ bool wait_bounded_lazy(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
                                                   unsigned int site) {
-  for (int i = 0; i < 64; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    if (done) return true;
-    if (*ctl.abort_flag) return false;
-  }
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   return wait_bounded(bar, parity, ctl, site);
 }
 

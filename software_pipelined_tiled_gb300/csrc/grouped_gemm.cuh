@@ -29,18 +29,24 @@
 // Bounds: rows of X past an expert's end that a tile's copy brings along only
 // reach accumulator columns that are never stored. W is a 3-D tensor, so that
 // a tile past its N or K reads zeros, not the next expert's weights. For dW
-// the sum itself is ragged: the last chunk of an expert's rows is cut at a
-// multiple of 16 rows, and a fixer warp in each CTA zeroes the rows between
-// the expert's end and that multiple in both operands (0 times another
-// expert's infinity would be NaN) before the chunk goes to the MMA.
+// the sum itself is ragged: the ring's MMAs stop at a multiple of 16 of an
+// expert's rows, and a warp of its own gathers the up to 15 rows left, zeros
+// below them, into a small operand tile for one last step (0 times another
+// expert's infinity would be NaN, so neither operand may hold its rows). That
+// tile is ready long before the step; clearing the rows in the ring's last
+// stage instead made every tile wait for it (16 experts of 1000 rows, 4096 x
+// 4096: 368 us against 320 with 1024 rows).
 //
 // Roles of a CTA: warp 0 producer, warp 1 MMA issuer (leader CTA only), warps
-// 2-5 epilogue, warp 6 fixer (dW only). Two accumulators of up to 256 columns,
+// 2-9 epilogue, warp 10 the rows left over (dW only). Two accumulators of up to 256 columns,
 // so a tile's epilogue overlaps the next tile's K-loop.
 //
-// The epilogue of Y and dX writes the transpose of the accumulator: a lane
-// holds one feature, its columns are rows of the output. Each warp turns
-// blocks of 32 x 32 in shared memory and stores rows of 32 features.
+// The epilogue reads its whole share of an accumulator into registers and hands
+// it back before it converts and stores. That of Y and dX writes the transpose
+// of the accumulator: a lane holds one feature, its columns are rows of the
+// output. Each warp turns blocks of 32 x 32 in shared memory and stores rows of
+// 32 features (a tensor copy could not stop at an expert's last row). dW's rows
+// are features, so its blocks go out by tensor copy, which clips them at N and K.
 #pragma once
 
 #include "common.cuh"
@@ -51,7 +57,8 @@ namespace sptg {
 enum GroupedMode : int { GROUPED_Y = 0, GROUPED_DX = 1, GROUPED_DW = 2 };
 
 constexpr int GROUPED_MAX_EXPERTS = 1024;
-constexpr int GROUPED_THREADS = 224;
+constexpr int GROUPED_EPI_WARPS = 8;  // two for each quarter of tensor memory's lanes
+constexpr int GROUPED_THREADS = 32 * (2 + GROUPED_EPI_WARPS + 1);
 
 struct GroupedParams {
   int experts;
@@ -59,27 +66,37 @@ struct GroupedParams {
   int F;   // features (M side): N (Y, dW) or K (dX)
   int C;   // Y, dX: length of the sum (K, N); dW: columns of the output (K)
   const int32_t* offsets;  // experts + 1
+  const uint16_t* a;       // dW: dY and X, for the rows left over, and their
+  const uint16_t* b;       // row pitches
+  int64_t lda, ldb;
   void* out;
-  int64_t ldo;             // elements between output rows
-  int64_t expert_pitch;    // dW: elements between experts
+  int64_t ldo;             // elements between output rows (Y, dX)
   int keep_weights;        // 1: W is read by several tiles; 0: once (evict first)
   unsigned int* error_word;
   uint64_t timeout_ns;
 };
 
 // TT: widest N side of a tile (256, or 64 for experts of few rows: the ring
-// then holds nine or ten stages of weights instead of six).
-template <int TT, int OBYTES>
+// then holds eight or nine stages of weights).
+template <int MODE, int TT, int OBYTES>
 struct GroupedLayout {
   static constexpr int A_STAGE = 128 * 128;         // 128 features x 64 of the sum
   static constexpr int B_STAGE = TT / 2 * 128;      // this CTA's half of the N side
   static constexpr int STAGE = A_STAGE + B_STAGE;
-  static constexpr int STAGES = TT == 256 ? 6 : OBYTES == 4 ? 9 : 10;
+  // as many as fit beside the epilogue's blocks
+  static constexpr int STAGES = TT == 64             ? (OBYTES == 4 ? 8 : 9)
+                                : MODE == GROUPED_DW ? 5
+                                                     : (OBYTES == 4 ? 5 : 6);
   static constexpr int EPI_PITCH = 32 * OBYTES + 16;
-  static constexpr int EPI_BUF = 32 * EPI_PITCH;    // one 32 x 32 block per epilogue warp
+  // an epilogue warp's block of 32 x 32; dW: of 32 rows of 128 bytes
+  static constexpr int EPI_BUF = MODE == GROUPED_DW ? 4096 : 32 * EPI_PITCH;
   static constexpr int OFF_EPI = STAGES * STAGE;
-  static constexpr int OFF_BAR = OFF_EPI + 4 * EPI_BUF;
-  static constexpr int NUM_BARS = 3 * STAGES + 5;
+  // dW: two operand tiles of the rows left over, 16 lines of 128 features and
+  // of 128 columns each
+  static constexpr int TAIL = 16 * 128 * 4;
+  static constexpr int OFF_TAIL = OFF_EPI + GROUPED_EPI_WARPS * EPI_BUF;
+  static constexpr int OFF_BAR = OFF_TAIL + (MODE == GROUPED_DW ? 2 * TAIL : 0);
+  static constexpr int NUM_BARS = 2 * STAGES + 9;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_GROUPS = OFF_MISC + 16;
   // first row and first tile of each expert, of the rows before the first
@@ -117,7 +134,10 @@ struct GroupedTile {
   int rows;    // Y, dX: rows of the tile; dW: rows of the expert
   int c0;      // dW: first column
   int n;       // width of the MMA's N side
-  int chunks;  // 64-long pieces of the sum (0: the tile is zeros)
+  int chunks;  // 64-long pieces of the sum in the ring
+  int steps;   // steps of 16 of the last of them
+  int tail;    // dW: rows left over, 0 ... 15
+  __device__ __forceinline__ bool zeros() const { return chunks == 0 && tail == 0; }
 };
 
 template <int MODE, int TT>
@@ -146,7 +166,9 @@ struct GroupedSchedule {
       w.t0 = first_g;
       w.rows = count_g;
       w.n = grouped_mma_n(min(256, C - w.c0));
-      w.chunks = (count_g + 63) >> 6;
+      w.chunks = (count_g + 48) >> 6;  // of the whole steps of 16
+      w.steps = count_g < 16 ? 0 : ((((count_g >> 4) - 1) & 3) + 1);
+      w.tail = count_g & 15;
     } else {
       const int nt = (count_g + TT - 1) / TT;
       // the expert's rows in tiles of equal width (a multiple of 16)
@@ -160,6 +182,8 @@ struct GroupedSchedule {
       w.n = grouped_mma_n(w.rows);
       // groups past the experts are rows that belong to none
       w.chunks = (g < groups - 2 && w.rows > 0) ? (C + 63) >> 6 : 0;
+      w.steps = 4;  // (past C both operands read zeros)
+      w.tail = 0;
     }
     return w;
   }
@@ -169,10 +193,11 @@ template <int MODE, int TT, bool BF16, int OUT>
 __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,   // the features' operand
                         const __grid_constant__ CUtensorMap tmB,   // the N side, boxes of 32 rows
-                        const __grid_constant__ CUtensorMap tmB4,  // the N side, boxes of 128 rows
+                        // the N side in boxes of 128 rows; dW: the output
+                        const __grid_constant__ CUtensorMap tmB4,
                         const GroupedParams p) {
   constexpr int OBYTES = OutTraits<OUT>::bytes;
-  using L = GroupedLayout<TT, OBYTES>;
+  using L = GroupedLayout<MODE, TT, OBYTES>;
   constexpr int STAGES = L::STAGES;
   constexpr bool A_MN = MODE != GROUPED_Y, B_MN = MODE == GROUPED_DW;
   static_assert(MODE != GROUPED_DW || TT == 256, "dW tiles are 256 columns wide");
@@ -188,10 +213,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   const uint32_t bar0 = sbase + L::OFF_BAR;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // dW: own copies of a tail
-  auto tfull_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
-  auto tempty_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+  auto rest_full = [&](int b) { return bar0 + 8u * (2 * STAGES + 4 + b); };   // dW: rows left over
+  auto rest_empty = [&](int b) { return bar0 + 8u * (2 * STAGES + 6 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 8);
+  auto rest_tile = [&](int b) { return sbase + L::OFF_TAIL + b * L::TAIL; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   int* g_first = reinterpret_cast<int*>(smem + L::OFF_GROUPS);
@@ -203,19 +230,16 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const int worker = static_cast<int>(blockIdx.x >> 1);
   const int workers = static_cast<int>(gridDim.x >> 1);
-  // dW: a stage is complete when both CTAs' parts are (two arrivals: the
-  // leader's producer makes both, or each CTA's fixer one)
-  constexpr uint32_t FULL_COUNT = MODE == GROUPED_DW ? 2 : 1;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), FULL_COUNT);
+      mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
-      mbar_init(tail_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 8);  // four epilogue warps of each CTA
+      mbar_init(tempty_bar(b), 2 * GROUPED_EPI_WARPS);  // of both CTAs
+      mbar_init(rest_full(b), 2);                       // both CTAs' halves
+      mbar_init(rest_empty(b), 1);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -283,8 +307,6 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     const uint64_t pol_b = policy_evict_last();
     int s = 0;
     uint32_t round = 0;
-    uint32_t tail_used = 0, tail_parity = 0;  // bit s: of stage s's tail barrier
-    uint32_t last_tail = 0;                   // bit s: the stage's last copies went to it
     int issued = 0;
     bool ok = true;
     for (int tile = worker; ok && tile < total; tile += workers) {
@@ -297,7 +319,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
           L::A_STAGE + static_cast<uint32_t>(boxes) * (MODE == GROUPED_DW ? 8192u : 4096u);
       const int f = w.f0 + 128 * static_cast<int>(rank);
       for (int c = 0; c < w.chunks; ++c) {
-        if (round > 0 && !__all_sync(0xffffffffu, wait_bounded(empty_bar(s), (round & 1u) ^ 1u,
+        if (round > 0 && !__all_sync(0xffffffffu, wait_bounded_lazy(empty_bar(s), (round & 1u) ^ 1u,
                                                                 ctl, WAIT_PRODUCER_EMPTY))) {
           ok = false;
           break;
@@ -307,30 +329,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
           const uint32_t a = stage_a(s), b = stage_b(s);
           if constexpr (MODE == GROUPED_DW) {
             const int t = w.t0 + 64 * c;
-            const bool tail = c == w.chunks - 1 && (w.rows & 63) != 0;
-            if (tail) {
-              // own copies complete on this CTA's tail barrier; its fixer
-              // then hands the stage to the MMA issuer
-              mbar_arrive_expect_tx(tail_bar(s), own_tx);
-              for (int j = 0; j < 2; ++j)
-                tma_load_2d(a + j * 8192, &tmA, tail_bar(s), f + 64 * j, t, pol_b);
-              for (int j = 0; j < boxes; ++j)
-                tma_load_2d(b + j * 8192, &tmB, tail_bar(s), w.c0 + n_first + 64 * j, t, pol_b);
-              tail_parity ^= (tail_used >> s & 1u) << s;
-              tail_used |= 1u << s;
-              last_tail |= 1u << s;
-            } else {
-              last_tail &= ~(1u << s);
-              if (rank == 0) {
-                mbar_arrive_expect_tx(full_bar(s), 2 * own_tx);
-                mbar_arrive(full_bar(s));
-              }
-              const uint32_t full = map_to_cta(full_bar(s), 0u);
-              for (int j = 0; j < 2; ++j)
-                tma_load_2d_pair(a + j * 8192, &tmA, full, f + 64 * j, t, pol_b);
-              for (int j = 0; j < boxes; ++j)
-                tma_load_2d_pair(b + j * 8192, &tmB, full, w.c0 + n_first + 64 * j, t, pol_b);
-            }
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * own_tx);
+            const uint32_t full = map_to_cta(full_bar(s), 0u);
+            for (int j = 0; j < 2; ++j)
+              tma_load_2d_pair(a + j * 8192, &tmA, full, f + 64 * j, t, pol_b);
+            for (int j = 0; j < boxes; ++j)
+              tma_load_2d_pair(b + j * 8192, &tmB, full, w.c0 + n_first + 64 * j, t, pol_b);
           } else {
             if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * own_tx);
             const uint32_t full = map_to_cta(full_bar(s), 0u);
@@ -359,11 +363,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       // let every copy already issued land before the CTA can exit
       if (leader && rank == 0) {
         for (int i = max(0, issued - STAGES); i < issued; ++i) {
-          const int st = i % STAGES;
-          const bool in_tail = last_tail >> st & 1u;
-          const uint32_t bar = in_tail ? tail_bar(st) : full_bar(st);
-          const uint32_t par = in_tail ? tail_parity >> st & 1u
-                                       : static_cast<uint32_t>(i / STAGES) & 1u;
+          const uint32_t bar = full_bar(i % STAGES);
+          const uint32_t par = static_cast<uint32_t>(i / STAGES) & 1u;
           const uint64_t t0 = global_timer_ns();
           while (!mbar_try_wait(bar, par) && global_timer_ns() - t0 < ctl.timeout_ns) {
           }
@@ -383,13 +384,13 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     if (rank == 0) {
       const bool leader = elect_one_sync();
       int s = 0;
-      uint32_t phase = 0, unit = 0;
+      uint32_t phase = 0, unit = 0, rest = 0;
       bool ok = true;
       for (int tile = worker; ok && tile < total; tile += workers) {
         const GroupedTile w = sched.at(tile);
-        if (w.chunks == 0) continue;
+        if (w.zeros()) continue;
         const uint32_t b = unit & 1u;
-        if (!__all_sync(0xffffffffu, wait_bounded(tempty_bar(b), ((unit >> 1) & 1u) ^ 1u, ctl,
+        if (!__all_sync(0xffffffffu, wait_bounded_lazy(tempty_bar(b), ((unit >> 1) & 1u) ^ 1u, ctl,
                                                   WAIT_MMA_TMEM_EMPTY))) {
           ok = false;
           break;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         const uint32_t d = tmem_base + b * 256;
         const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
         for (int c = 0; c < w.chunks; ++c) {
-          if (!__all_sync(0xffffffffu, wait_bounded(full_bar(s), phase, ctl, WAIT_MMA_FULL))) {
+          if (!__all_sync(0xffffffffu, wait_bounded_lazy(full_bar(s), phase, ctl, WAIT_MMA_FULL))) {
             ok = false;
             break;
           }
@@ -412,16 +413,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             // one step of 16 along the sum: 32 bytes of a K-major row, 16
             // lines of an MN-major tile (in units of 16 bytes)
             constexpr uint64_t ADV_A = A_MN ? 128 : 2, ADV_B = B_MN ? 128 : 2;
-            if (MODE == GROUPED_DW && c == w.chunks - 1 && (w.rows & 63) != 0) {
-              const int steps = ((w.rows & 63) + 15) >> 4;
-              for (int k = 0; k < steps; ++k)
-                mma_f16_g<true>(d, ad + ADV_A * k, bd + ADV_B * k, idesc, (c > 0 || k > 0) ? 1u : 0u);
-            } else {
-              mma_f16_g<true>(d, ad, bd, idesc, c > 0 ? 1u : 0u);
+            const int steps = c == w.chunks - 1 ? w.steps : 4;
+            mma_f16_g<true>(d, ad, bd, idesc, c > 0 ? 1u : 0u);
 #pragma unroll
-              for (int k = 1; k < 4; ++k)
+            for (int k = 1; k < 4; ++k)
+              if (MODE != GROUPED_DW || steps > k)
                 mma_f16_g<true>(d, ad + ADV_A * k, bd + ADV_B * k, idesc, 1u);
-            }
             mma_commit_g<true>(empty_bar(s));
           }
           __syncwarp();
@@ -429,6 +426,20 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             s = 0;
             phase ^= 1u;
           }
+        }
+        if (MODE == GROUPED_DW && ok && w.tail != 0) {
+          const uint32_t rb = rest & 1u;
+          ok = __all_sync(0xffffffffu,
+                          wait_bounded_lazy(rest_full(rb), (rest >> 1) & 1u, ctl, WAIT_MMA_FULL));
+          ++rest;
+          tc_fence_after();
+          if (ok && leader) {
+            mma_f16_g<true>(d, sdesc_mn_major_sw128(rest_tile(rb), 2048),
+                            sdesc_mn_major_sw128(rest_tile(rb) + 4096, 2048), idesc,
+                            w.chunks > 0 ? 1u : 0u);
+            mma_commit_g<true>(rest_empty(rb));
+          }
+          __syncwarp();
         }
         if (ok && leader) mma_commit_g<true>(tfull_bar(b));
         __syncwarp();
@@ -439,122 +450,146 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < ctl.timeout_ns) {
       }
     }
-  } else if (warp < 6) {
+  } else if (warp < 2 + GROUPED_EPI_WARPS) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // tensor-memory lanes 32q ... 32q + 31
+    // lanes 32q ... 32q + 31 of tensor memory, every second block of columns
+    const int q = warp & 3, part = (warp - 2) >> 2;
     uint8_t* buf = smem + L::OFF_EPI + (warp - 2) * L::EPI_BUF;
     constexpr int PITCH = L::EPI_PITCH;
     constexpr int VEC = 16 / OBYTES;            // outputs in 16 bytes
     constexpr int VPR = 32 / VEC;               // 16-byte pieces of a row of 32
     constexpr int RPI = 32 / VPR;               // rows a warp stores at a time
     const int vr = lane / VPR, vc = lane % VPR;
+    // this warp's blocks of 32 columns: dW takes two neighbours in turn
+    constexpr int NB = TT / 64;
+    auto block_col = [&](int i) {
+      return MODE == GROUPED_DW ? (i >> 1) * 128 + part * 64 + (i & 1) * 32 : 64 * i + 32 * part;
+    };
     uint32_t unit = 0;
     for (int tile = worker; tile < total; tile += workers) {
       const GroupedTile w = sched.at(tile);
-      const uint32_t b = unit & 1u;
-      const bool zeros = w.chunks == 0;
-      if (!zeros) {
-        if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(b), (unit >> 1) & 1u, ctl,
-                                                  WAIT_EPI_TMEM_FULL)))
+      const int f = w.f0 + 128 * static_cast<int>(rank) + 32 * q;  // this warp's first feature
+      uint32_t r[NB][32];
+      if (!w.zeros()) {
+        const uint32_t b = unit & 1u;
+        if (!__all_sync(0xffffffffu, wait_bounded_lazy(tfull_bar(b), (unit >> 1) & 1u, ctl,
+                                                       WAIT_EPI_TMEM_FULL)))
           break;
         ++unit;
         tc_fence_after();
+        const uint32_t t_acc = tmem_base + b * 256 + (static_cast<uint32_t>(32 * q) << 16);
+        // (columns past the tile's width hold an earlier tile's sums, or
+        // anything: they are not stored)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) tmem_ld_32x32b_x32(t_acc + block_col(i), r[i]);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) tmem_wait_ld_regs(r[i]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(b), 0u));
+      } else {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) r[i][k] = 0;
       }
-      const int f = w.f0 + 128 * static_cast<int>(rank) + 32 * q;  // this warp's first feature
-      const uint32_t t_acc = tmem_base + b * 256 + (static_cast<uint32_t>(32 * q) << 16);
-      if (f < p.F) {
-        for (int cb = 0; cb < w.n; cb += 32) {
-          uint32_t r[32];
-          if (!zeros) {
-            tmem_ld_32x32b_x32(t_acc + cb, r);
-            tmem_wait_ld_regs(r);
-          } else {
+      if (f >= p.F) continue;
+      if constexpr (MODE == GROUPED_DW) {
+        // blocks of 32 features x 128 bytes, in the tensor copy's swizzle
+        constexpr int BLOCKS = 128 / OBYTES / 32;  // of 32 columns in 128 bytes
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = 0;
-          }
-          __syncwarp();  // the block before this one has been read
-          if constexpr (MODE == GROUPED_DW) {
-            // rows of the output are features: a lane's own row
-            if constexpr (OBYTES == 4) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(buf + lane * PITCH + 16 * j) =
-                    make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  o[i] = pack2<OUT>(__uint_as_float(r[8 * j + 2 * i]),
-                                    __uint_as_float(r[8 * j + 2 * i + 1]));
-                *reinterpret_cast<uint4*>(buf + lane * PITCH + 16 * j) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-              }
-            }
-          } else {
-            // rows of the output are accumulator columns
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              store_out<OUT>(buf + i * PITCH, lane, __uint_as_float(r[i]));
-          }
+        for (int i = 0; i < NB; i += BLOCKS) {
+          const int col = w.c0 + block_col(i);
+          if (col >= p.C) break;
+          if (lane == 0) bulk_wait_group_read<0>();  // the block before has been read
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; i += RPI) {
-            const uint4 v = *reinterpret_cast<const uint4*>(buf + (i + vr) * PITCH + 16 * vc);
-            int64_t at;
-            bool in;
-            if constexpr (MODE == GROUPED_DW) {
-              const int row = f + i + vr, col = w.c0 + cb + vc * VEC;
-              in = row < p.F && col < p.C;
-              at = w.e * p.expert_pitch + row * p.ldo + col;
+          for (int j = 0; j < 8; ++j) {
+            uint4 o;
+            if constexpr (OBYTES == 4) {
+              o = make_uint4(r[i][4 * j], r[i][4 * j + 1], r[i][4 * j + 2], r[i][4 * j + 3]);
             } else {
-              const int row = cb + i + vr, col = f + vc * VEC;
-              in = row < w.rows && col < p.F;
-              at = static_cast<int64_t>(w.t0 + row) * p.ldo + col;
+              const uint32_t* v = &r[i + j / 4][8 * (j % 4)];
+              o = make_uint4(pack2<OUT>(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                             pack2<OUT>(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                             pack2<OUT>(__uint_as_float(v[4]), __uint_as_float(v[5])),
+                             pack2<OUT>(__uint_as_float(v[6]), __uint_as_float(v[7])));
             }
-            if (in)
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = o;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmB4, smem_addr(buf), col, f, w.e);
+            bulk_commit_group();
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int cb = block_col(i);
+          if (cb >= w.rows) break;
+          __syncwarp();  // the block before this one has been read
+          // rows of the output are accumulator columns
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            store_out<OUT>(buf + k * PITCH, lane, __uint_as_float(r[i][k]));
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 32; k += RPI) {
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + (k + vr) * PITCH + 16 * vc);
+            const int row = cb + k + vr, col = f + vc * VEC;
+            const int64_t at = static_cast<int64_t>(w.t0 + row) * p.ldo + col;
+            if (row < w.rows && col < p.F)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at * OBYTES) = v;
           }
         }
       }
-      if (!zeros) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(b), 0u));
-      }
     }
+    if (MODE == GROUPED_DW && lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
   } else if constexpr (MODE == GROUPED_DW) {
-    // --------------------------------------------------------------- fixer
-    // Zeroes the rows past an expert's end in the last chunk of its rows, up
-    // to the next multiple of 16 (the MMA reads no further), then hands the
-    // stage to the MMA issuer.
-    int s = 0;
-    uint32_t used = 0, parity = 0;
+    // ------------------------------------------------------ rows left over
+    // Gathers an expert's last rows (past the multiple of 16) for this CTA's
+    // 128 features and its half of the columns: lines of 64 values in the
+    // swizzle of the ring's tiles, zeros past the last row and the tensors.
+    uint32_t rest = 0;
     for (int tile = worker; tile < total; tile += workers) {
       const GroupedTile w = sched.at(tile);
-      if (w.chunks == 0) continue;
-      const int tail = w.rows & 63;
-      s = (s + w.chunks - 1) % STAGES;  // the last chunk's stage
-      if (tail != 0) {
-        parity ^= (used >> s & 1u) << s;
-        used |= 1u << s;
-        if (!__all_sync(0xffffffffu,
-                        wait_bounded(tail_bar(s), parity >> s & 1u, ctl, WAIT_MMA_FULL)))
-          break;
-        const int end = (tail + 15) & ~15;
-        const int boxes = 2 + (((w.n >> 1) + 63) >> 6);
-        uint8_t* base = smem + s * L::STAGE;
-        // box j of the stage (the features' two, then the N side's) is 64
-        // lines of 128 bytes; a line keeps its place under the swizzle
-        for (int j = 0; j < boxes; ++j)
-          for (int i = tail * 8 + lane; i < end * 8; i += 32)
-            *reinterpret_cast<uint4*>(base + j * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_cta(full_bar(s), 0u));
+      if (w.tail == 0) continue;
+      const uint32_t rb = rest & 1u;
+      if (!__all_sync(0xffffffffu, wait_bounded_lazy(rest_empty(rb), ((rest >> 1) & 1u) ^ 1u, ctl,
+                                                     WAIT_PRODUCER_EMPTY)))
+        break;
+      ++rest;
+      const int64_t row0 = w.t0 + w.rows - w.tail;
+      const int half = w.n >> 1;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const uint16_t* src = side == 0 ? p.a : p.b;
+        const int64_t ld = side == 0 ? p.lda : p.ldb;
+        const int col0 = side == 0 ? w.f0 + 128 * static_cast<int>(rank)
+                                   : w.c0 + half * static_cast<int>(rank);
+        const int limit = side == 0 ? p.F : min(p.C, col0 + half);
+        uint4 v[8];
+        // 16 lines of 16 pieces of 8 values: 8 pieces a lane
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int line = 2 * i + (lane >> 4), col = col0 + 8 * (lane & 15);
+          v[i] = line < w.tail && col < limit
+                     ? *reinterpret_cast<const uint4*>(src + (row0 + line) * ld + col)
+                     : make_uint4(0, 0, 0, 0);
+        }
+        uint8_t* dst = smem + L::OFF_TAIL + rb * L::TAIL + side * 4096 + ((lane & 15) >> 3) * 2048;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int line = 2 * i + (lane >> 4);
+          *reinterpret_cast<uint4*>(dst + line * 128 + (((lane & 7) ^ (line & 7)) << 4)) = v[i];
+        }
       }
-      s = s + 1 == STAGES ? 0 : s + 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_cta(rest_full(rb), 0u));
     }
   }
 
@@ -568,7 +603,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
 
 template <int MODE, int TT, bool BF16, int OUT>
 KernelVariant grouped_variant_at() {
-  using L = GroupedLayout<TT, OutTraits<OUT>::bytes>;
+  using L = GroupedLayout<MODE, TT, OutTraits<OUT>::bytes>;
   return {reinterpret_cast<const void*>(&grouped_gemm_kernel<MODE, TT, BF16, OUT>), TT, L::STAGES,
           L::SMEM_BYTES, true, GROUPED_THREADS};
 }

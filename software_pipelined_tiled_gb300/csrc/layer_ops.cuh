@@ -448,7 +448,9 @@ int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, con
   if (dw) {
     rc = make_map_2d(&ma, d.in_tma, 2, a, N, T, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, lda);
     if (!rc) rc = make_map_2d(&mb, d.in_tma, 2, b, K, T, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, ldb);
-    mb4 = mb;
+    if (!rc)  // the output
+      rc = make_map_3d(&mb4, d.out_tma, out, K, N, E, K * d.out_bytes, N * K * d.out_bytes,
+                       128 / d.out_bytes, 32, 1, CU_TENSOR_MAP_SWIZZLE_128B);
   } else {
     rc = make_map_3d(&ma, d.in_tma, a, K, N, E, K * 2, N * K * 2, 64, mode == GROUPED_Y ? 128 : 64, 1,
                      CU_TENSOR_MAP_SWIZZLE_128B);
@@ -464,9 +466,12 @@ int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, con
   p.F = static_cast<int>(F);
   p.C = static_cast<int>(dw ? K : sum);
   p.offsets = offsets;
+  p.a = static_cast<const uint16_t*>(a);
+  p.b = static_cast<const uint16_t*>(b);
+  p.lda = lda;
+  p.ldb = ldb;
   p.out = out;
   p.ldo = ldo;
-  p.expert_pitch = N * K;
   p.keep_weights = tt == 256;
   p.error_word = di.error_word;
   p.timeout_ns = kOpTimeoutNs;
