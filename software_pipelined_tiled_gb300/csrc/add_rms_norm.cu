@@ -5,31 +5,25 @@
 namespace sptg {
 
 template <bool BF16, int OUTK>
-NormVariant norm_variant_of(int cols, bool vectors) {
-  if (!vectors || cols > 32768)
-    return {reinterpret_cast<const void*>(&add_rms_norm_any_kernel<BF16, OUTK>), 512, 1};
-  if (cols <= 1024)
-    return {reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, 32, 128, 4>), 128, 4};
-  if (cols <= 4096)
-    return {reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, 128, 128, 4>), 128, 1};
-  if (cols <= 8192)
-    return {reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, 256, 256, 4>), 256, 1};
-  if (cols <= 16384)
-    return {reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, 512, 512, 4>), 512, 1};
-  return {reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, 1024, 1024, 4>), 1024, 1};
+const void* norm_variant_of(int kind) {
+  switch (kind) {
+    case NORM_WARP_2: return reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, true, 2>);
+    case NORM_WARP_4: return reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, true, 4>);
+    case NORM_BLOCK_2: return reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, false, 2>);
+    case NORM_BLOCK_4: return reinterpret_cast<const void*>(&add_rms_norm_kernel<BF16, OUTK, false, 4>);
+    case NORM_RING_4: return reinterpret_cast<const void*>(&add_rms_norm_ring_kernel<BF16, OUTK, 4, 512>);
+    default: return reinterpret_cast<const void*>(&add_rms_norm_any_kernel<BF16, OUTK>);
+  }
 }
 
-NormVariant norm_variant(bool bf16, int out_kind, int cols, bool vectors) {
+const void* norm_variant(bool bf16, int out_kind, int kind) {
   switch (out_kind) {
     case NORM_S8:
-      return bf16 ? norm_variant_of<true, NORM_S8>(cols, vectors)
-                  : norm_variant_of<false, NORM_S8>(cols, vectors);
+      return bf16 ? norm_variant_of<true, NORM_S8>(kind) : norm_variant_of<false, NORM_S8>(kind);
     case NORM_E4M3:
-      return bf16 ? norm_variant_of<true, NORM_E4M3>(cols, vectors)
-                  : norm_variant_of<false, NORM_E4M3>(cols, vectors);
+      return bf16 ? norm_variant_of<true, NORM_E4M3>(kind) : norm_variant_of<false, NORM_E4M3>(kind);
     default:
-      return bf16 ? norm_variant_of<true, NORM_16>(cols, vectors)
-                  : norm_variant_of<false, NORM_16>(cols, vectors);
+      return bf16 ? norm_variant_of<true, NORM_16>(kind) : norm_variant_of<false, NORM_16>(kind);
   }
 }
 

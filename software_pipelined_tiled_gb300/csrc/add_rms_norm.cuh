@@ -17,8 +17,8 @@
 // kept beside that of |h w| to tell an overflow from an infinity.
 //
 // Memory-bound: 7 bytes an element (x, r in; h, q out) and some ten flops. The
-// row stays in registers between the reduction and the outputs (32 elements a
-// thread), so x and r are read once.
+// row stays in registers between the reduction and the outputs, so x and r are
+// read once.
 #pragma once
 
 #include <cstdint>
@@ -42,6 +42,9 @@ struct NormParams {
   int64_t rows;
   int cols;
   float eps;
+  int stages;  // depth of the ring kernel's ring
+  unsigned int* error_word;
+  uint64_t timeout_ns;
 };
 
 template <bool BF16>
@@ -98,50 +101,97 @@ __device__ __forceinline__ RowScale row_scale(float sumsq, uint2 mx, int cols, f
   return s;
 }
 
-// Sum and maxima over the `TPR` threads of a row, the same for each of them.
-// The order of the sum is fixed: lanes by halves, then warps in turn.
-template <int TPR>
-__device__ __forceinline__ void row_reduce(float& sum, uint2& mx, float* s_sum, uint2* s_max,
-                                           int row_slot) {
+// Sum and maxima over a row's threads, the same for each of them: a warp
+// (WARP_ROW), or the whole block. The order of the sum is fixed: lanes by
+// halves, then warps in turn. s_sum and s_max hold 32 entries.
+template <bool WARP_ROW>
+__device__ __forceinline__ void row_reduce(float& sum, uint2& mx, float* s_sum, uint2* s_max) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   mx.x = __reduce_max_sync(0xffffffffu, mx.x);
   mx.y = __reduce_max_sync(0xffffffffu, mx.y);
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
-    const int warp = threadIdx.x >> 5;
+  if constexpr (!WARP_ROW) {
+    const int warps = static_cast<int>(blockDim.x) >> 5;
     if ((threadIdx.x & 31) == 0) {
-      s_sum[warp] = sum;
-      s_max[warp] = mx;
+      s_sum[threadIdx.x >> 5] = sum;
+      s_max[threadIdx.x >> 5] = mx;
     }
     __syncthreads();
     sum = 0.0f;
     mx = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      sum += s_sum[row_slot * W + i];
-      mx.x = max(mx.x, s_max[row_slot * W + i].x);
-      mx.y = max(mx.y, s_max[row_slot * W + i].y);
+    for (int i = 0; i < warps; ++i) {
+      sum += s_sum[i];
+      mx.x = max(mx.x, s_max[i].x);
+      mx.y = max(mx.y, s_max[i].y);
     }
   }
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Rows of up to TPR * PER * 8 elements held in registers; THREADS / TPR rows
-// to a block. Needs 16-byte aligned rows and cols a multiple of 8.
-template <bool BF16, int OUTK, int TPR, int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS) add_rms_norm_kernel(const NormParams p) {
-  __shared__ float s_sum[THREADS / 32];
-  __shared__ uint2 s_max[THREADS / 32];
-  const int slot = threadIdx.x / TPR;
-  const int lane = threadIdx.x % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / TPR) + slot;
+// 8 elements of x and r to h, with their part of the row's sum and maxima.
+template <bool BF16, int OUTK>
+__device__ __forceinline__ void add_group(const uint4& xv, const uint4& rv, const uint4& wv,
+                                          float (&h)[8], float& sum, uint2& mx) {
+  const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+  const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
+  const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = unpack2<BF16>(xw[j]), b = unpack2<BF16>(rw[j]), c = unpack2<BF16>(ww[j]);
+    const float h0 = a.x + b.x, h1 = a.y + b.y;
+    h[2 * j] = h0;
+    h[2 * j + 1] = h1;
+    sum += h0 * h0;
+    sum += h1 * h1;
+    if constexpr (OUTK != NORM_16) {
+      mx.x = max(mx.x, max(abs_bits(h0 * c.x), abs_bits(h1 * c.y)));
+      mx.y = max(mx.y, max(abs_bits(h0), abs_bits(h1)));
+    }
+  }
+}
+
+// Both outputs of 8 elements, group g of a row.
+template <bool BF16, int OUTK>
+__device__ __forceinline__ void store_group(const NormParams& p, int64_t row, int g, const float* v,
+                                            const uint4& wv, const RowScale& sc) {
+  constexpr int H_OUT = BF16 ? OUT_BF16 : OUT_F16;
+  reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h) + row * p.ldh)[g] =
+      make_uint4(pack2<H_OUT>(v[0], v[1]), pack2<H_OUT>(v[2], v[3]), pack2<H_OUT>(v[4], v[5]),
+                 pack2<H_OUT>(v[6], v[7]));
+  const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 c = unpack2<BF16>(ww[j]);
+    if constexpr (OUTK == NORM_16)
+      o[j] = pack2<H_OUT>(v[2 * j] * sc.rstd * c.x, v[2 * j + 1] * sc.rstd * c.y);
+    else
+      o[j] = sc.zero ? 0u : quant2<OUTK>(v[2 * j] * c.x * sc.qmul, v[2 * j + 1] * c.y * sc.qmul);
+  }
+  if constexpr (OUTK == NORM_16)
+    reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q) + row * p.ldq)[g] =
+        make_uint4(o[0], o[1], o[2], o[3]);
+  else
+    reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q) + row * p.ldq)[g] =
+        make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+}
+
+// One row to a warp (four to a block of 128) or to a block, held in registers:
+// PER groups of 8 elements a thread. Needs 16-byte aligned rows and cols a
+// multiple of 8. The block of a wide row has just the threads that the row
+// needs: with a fixed block, the idle part of it cost up to a third (8192 rows
+// of 5000: 68 us).
+template <bool BF16, int OUTK, bool WARP_ROW, int PER>
+__global__ void __launch_bounds__(WARP_ROW || PER == 4 ? 128 : 1024) add_rms_norm_kernel(const NormParams p) {
+  __shared__ float s_sum[32];
+  __shared__ uint2 s_max[32];
+  const int lanes = WARP_ROW ? 32 : static_cast<int>(blockDim.x);
+  const int lane = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)
+                               : static_cast<int64_t>(blockIdx.x);
   const bool live = row < p.rows;
-  const int groups = p.cols >> 3;  // groups of 8 elements
-  // a block of 1024 threads has 64 registers for each: it reads w a second
-  // time (from L1) instead of keeping it
-  constexpr bool KEEP_W = THREADS < 1024;
+  const int groups = p.cols >> 3;
   grid_dependency_wait();
   uint4 xv[PER], rv[PER], wv[PER];
   const uint4* px = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.ldx);
@@ -149,7 +199,7 @@ __global__ void __launch_bounds__(THREADS) add_rms_norm_kernel(const NormParams 
   const uint4* pw = static_cast<const uint4*>(p.w);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int g = lane + i * TPR;
+    const int g = lane + i * lanes;
     const bool in = live && g < groups;
     xv[i] = in ? __ldcs(px + g) : make_uint4(0, 0, 0, 0);  // read once
     rv[i] = in ? __ldcs(pr + g) : make_uint4(0, 0, 0, 0);
@@ -159,61 +209,103 @@ __global__ void __launch_bounds__(THREADS) add_rms_norm_kernel(const NormParams 
   float sum = 0.0f;
   uint2 mx = make_uint2(0, 0);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
-    const uint32_t rw[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
-    const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = unpack2<BF16>(xw[j]), b = unpack2<BF16>(rw[j]), c = unpack2<BF16>(ww[j]);
-      const float h0 = a.x + b.x, h1 = a.y + b.y;
-      h[i][2 * j] = h0;
-      h[i][2 * j + 1] = h1;
-      sum += h0 * h0;
-      sum += h1 * h1;
-      if constexpr (OUTK != NORM_16) {
-        mx.x = max(mx.x, max(abs_bits(h0 * c.x), abs_bits(h1 * c.y)));
-        mx.y = max(mx.y, max(abs_bits(h0), abs_bits(h1)));
-      }
-    }
-  }
-  row_reduce<TPR>(sum, mx, s_sum, s_max, slot);
+  for (int i = 0; i < PER; ++i) add_group<BF16, OUTK>(xv[i], rv[i], wv[i], h[i], sum, mx);
+  row_reduce<WARP_ROW>(sum, mx, s_sum, s_max);
   grid_launch_dependents();
   if (!live) return;
   const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
-  constexpr int H_OUT = BF16 ? OUT_BF16 : OUT_F16;
-  uint4* ph = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h) + row * p.ldh);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int g = lane + i * TPR;
-    if (g >= groups) continue;
-    const float* v = h[i];
-    ph[g] = make_uint4(pack2<H_OUT>(v[0], v[1]), pack2<H_OUT>(v[2], v[3]),
-                       pack2<H_OUT>(v[4], v[5]), pack2<H_OUT>(v[6], v[7]));
-    const uint4 wi = KEEP_W ? wv[i] : __ldg(pw + g);
-    const uint32_t ww[4] = {wi.x, wi.y, wi.z, wi.w};
-    if constexpr (OUTK == NORM_16) {
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 c = unpack2<BF16>(ww[j]);
-        o[j] = pack2<H_OUT>(v[2 * j] * sc.rstd * c.x, v[2 * j + 1] * sc.rstd * c.y);
-      }
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q) + row * p.ldq)[g] =
-          make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 c = unpack2<BF16>(ww[j]);
-        o[j] = sc.zero ? 0u
-                       : quant2<OUTK>(v[2 * j] * c.x * sc.qmul, v[2 * j + 1] * c.y * sc.qmul);
-      }
-      reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q) + row * p.ldq)[g] =
-          make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
-    }
+    const int g = lane + i * lanes;
+    if (g < groups) store_group<BF16, OUTK>(p, row, g, h[i], wv[i], sc);
   }
   if (OUTK != NORM_16 && lane == 0) p.scales[row] = sc.scale;
+}
+
+// Many wide rows: a fixed number of blocks, each going through every
+// gridDim.x-th row with a ring of rows ahead of it in shared memory, filled by
+// bulk copies. The copies of the next rows run while a row is reduced and
+// stored, whatever the block's size; w stays in registers. PER groups of 8
+// elements a thread.
+constexpr int NORM_MAX_STAGES = 4;
+__host__ __device__ constexpr int norm_row_bytes(int cols) { return (2 * cols + 127) & ~127; }
+__host__ __device__ constexpr int norm_ring_smem(int cols, int stages) {
+  return stages * 2 * norm_row_bytes(cols) + 128;
+}
+
+template <bool BF16, int OUTK, int PER, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const NormParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float s_sum[2][32];
+  __shared__ uint2 s_max[2][32];
+  __shared__ __align__(8) uint64_t bars[NORM_MAX_STAGES];
+  __shared__ int abort_word;
+  const int S = p.stages;
+  const int row_bytes = norm_row_bytes(p.cols);
+  const uint32_t bytes = static_cast<uint32_t>(2 * p.cols);
+  const int groups = p.cols >> 3;
+  const uint32_t bar0 = smem_addr(bars), ring0 = smem_addr(ring);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  const WaitCtl ctl{p.timeout_ns, p.error_word, &abort_word};
+  const uint64_t pol = policy_evict_first();  // read once
+  auto fetch = [&](int64_t row, int s) {
+    const uint32_t bar = bar0 + 8 * s, dst = ring0 + static_cast<uint32_t>(2 * s * row_bytes);
+    mbar_arrive_expect_tx(bar, 2 * bytes);
+    bulk_load_1d(dst, static_cast<const uint16_t*>(p.x) + row * p.ldx, bytes, bar, pol);
+    bulk_load_1d(dst + row_bytes, static_cast<const uint16_t*>(p.r) + row * p.ldr, bytes, bar, pol);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < S; ++s)
+      if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < p.rows)
+        fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+  uint4 wv[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int g = threadIdx.x + i * blockDim.x;
+    wv[i] = g < groups ? __ldg(static_cast<const uint4*>(p.w) + g) : make_uint4(0, 0, 0, 0);
+  }
+  int s = 0;
+  uint32_t phase = 0, odd = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    // (a wait that runs out leaves its rows wrong and says so; the loop and its
+    // barriers go on)
+    wait_bounded_lazy(bar0 + 8 * s, phase, ctl, WAIT_MMA_FULL);
+    const uint4* sx = reinterpret_cast<const uint4*>(ring + 2 * s * row_bytes);
+    const uint4* sr = reinterpret_cast<const uint4*>(ring + (2 * s + 1) * row_bytes);
+    float h[PER][8];
+    float sum = 0.0f;
+    uint2 mx = make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int g = threadIdx.x + i * blockDim.x;
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      add_group<BF16, OUTK>(g < groups ? sx[g] : none, g < groups ? sr[g] : none, wv[i], h[i], sum, mx);
+    }
+    // (its barrier also says that the stage has been read; its buffers
+    // alternate, so a fast warp's next row leaves a slow one's sums alone)
+    row_reduce<false>(sum, mx, s_sum[odd], s_max[odd]);
+    const int64_t next = row + static_cast<int64_t>(S) * gridDim.x;
+    if (threadIdx.x == 0 && next < p.rows) fetch(next, s);
+    const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int g = threadIdx.x + i * blockDim.x;
+      if (g < groups) store_group<BF16, OUTK>(p, row, g, h[i], wv[i], sc);
+    }
+    if (OUTK != NORM_16 && threadIdx.x == 0) p.scales[row] = sc.scale;
+    odd ^= 1u;
+    if (++s == S) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  grid_launch_dependents();
 }
 
 // Rows of any width, alignment and pitch: one block to a row, element by
@@ -222,8 +314,8 @@ __global__ void __launch_bounds__(THREADS) add_rms_norm_kernel(const NormParams 
 // writes it, in both passes.
 template <bool BF16, int OUTK>
 __global__ void __launch_bounds__(512) add_rms_norm_any_kernel(const NormParams p) {
-  __shared__ float s_sum[16];
-  __shared__ uint2 s_max[16];
+  __shared__ float s_sum[32];
+  __shared__ uint2 s_max[32];
   const int64_t row = blockIdx.x;
   grid_dependency_wait();
   const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ldx;
@@ -238,7 +330,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_any_kernel(const NormParams 
       mx.y = max(mx.y, abs_bits(h));
     }
   }
-  row_reduce<512>(sum, mx, s_sum, s_max, 0);
+  row_reduce<false>(sum, mx, s_sum, s_max);
   grid_launch_dependents();
   const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
   constexpr int H_OUT = BF16 ? OUT_BF16 : OUT_F16;

@@ -162,15 +162,53 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
                        ldy % 8 == 0 && !off(x, 16) && !off(r, 16) && !off(w, 16) && !off(h, 16) &&
                        !off(y, 8 * out.bytes);
   const int out_kind = out_type == SPTG_T_S8 ? NORM_S8 : out_type == SPTG_T_E4M3 ? NORM_E4M3 : NORM_16;
-  const NormVariant v = norm_variant(in_type == SPTG_T_BF16, out_kind, static_cast<int>(cols), vectors);
-  NormParams p{x, r, w, h, y, scales, ldx, ldr, ldh, ldy, rows, static_cast<int>(cols), eps};
-  const int64_t grid = (rows + v.rows_per_block - 1) / v.rows_per_block;
+  // Rows up to 1024 elements: one to a warp. Wider ones: one to a block of as
+  // many threads as it needs, or, where there are rows enough to go several
+  // times through the GPU, rows through the ring kernel's blocks. Rows past
+  // 16384 elements take the kernel for any width.
+  const auto round32 = [](int64_t n) { return static_cast<int>((n + 31) / 32 * 32); };
+  int kind = NORM_ANY, threads = 512, smem = 0, stages = 0;
+  int64_t grid = rows;
+  if (vectors && cols <= 1024) {
+    kind = cols <= 512 ? NORM_WARP_2 : NORM_WARP_4;
+    threads = 128;
+    grid = (rows + 3) / 4;
+  } else if (vectors && cols <= 16384) {
+    // two groups of 8 elements a thread; four for rows of 2049 to 4096 elements
+    // where there are rows to fill the GPU with (16384 rows of 4096: 71 us,
+    // with two 75, through the ring 79)
+    const bool four = cols > 2048 && cols <= 4096 && rows >= 4 * di.sm_count;
+    kind = four ? NORM_BLOCK_4 : NORM_BLOCK_2;
+    threads = four ? round32((cols / 8 + 3) / 4) : round32((cols / 8 + 1) / 2);
+    // blocks of the ring kernel: three rows ahead, as many to an SM as its
+    // shared memory and 96 registers a thread allow
+    const int ring_threads = round32((cols / 8 + 3) / 4);
+    const int ring_stages = 3;
+    const int ring_smem = norm_ring_smem(static_cast<int>(cols), ring_stages);
+    const int per_sm = std::max(1, std::min(224 * 1024 / (ring_smem + 2048), 65536 / (96 * ring_threads)));
+    const int64_t blocks = static_cast<int64_t>(per_sm) * di.sm_count;
+    if (cols > 4096 && rows >= 3 * blocks) {
+      kind = NORM_RING_4;
+      threads = ring_threads;
+      stages = ring_stages;
+      smem = ring_smem;
+      grid = blocks;
+    }
+  }
+  const void* fn = norm_variant(in_type == SPTG_T_BF16, out_kind, kind);
+  if (smem) {
+    const int rs = ensure_smem(dev, fn, norm_ring_smem(16384, 3));
+    if (rs) return rs;
+  }
+  NormParams p{x, r, w, h, y, scales, ldx, ldr, ldh, ldy, rows, static_cast<int>(cols), eps,
+               stages, di.error_word, kOpTimeoutNs};
   void* args[] = {&p};
-  const cudaError_t e = launch_op(v.fn, dim3(static_cast<unsigned>(grid)), v.threads, 0, 1, stream, args);
+  const cudaError_t e =
+      launch_op(fn, dim3(static_cast<unsigned>(grid)), threads, smem, 1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "add_rms_norm launch");
-  set_config("kernel=add_rms_norm type=%s out_bytes=%lld threads=%lld rows_per_block=%lld grid=%lld "
-             "vectors=%lld",
-             in.name, {out.bytes, v.threads, v.rows_per_block, grid, vectors});
+  set_config("kernel=add_rms_norm type=%s out_bytes=%lld kind=%lld threads=%lld grid=%lld stages=%lld "
+             "smem=%lld",
+             in.name, {out.bytes, kind, threads, grid, stages, smem});
   return SPTG_OK;
 }
 

@@ -52,15 +52,11 @@ cudaError_t launch_s8_to_f16(const void* srcA, int64_t lda, int64_t rows_a, cons
                              int64_t ldb, int64_t rows_b, int64_t K, void* dstA, void* dstB,
                              int blocks, cudaStream_t stream, bool overlap_previous);
 
-// The residual-addition and norm kernel for rows of `cols` elements (out_kind:
-// NormOut); `vectors`: every row starts 16-byte aligned (8-bit outputs 8-byte)
-// and cols is a multiple of 8.
-struct NormVariant {
-  const void* fn;
-  int threads;
-  int rows_per_block;
-};
-NormVariant norm_variant(bool bf16, int out_kind, int cols, bool vectors);
+// The residual-addition and norm kernels (out_kind: NormOut): a row to a warp or
+// a block, with 2 or 4 groups of 8 elements a thread; rows through a ring; rows
+// of any width and alignment.
+enum NormKind : int { NORM_WARP_2, NORM_WARP_4, NORM_BLOCK_2, NORM_BLOCK_4, NORM_RING_4, NORM_ANY };
+const void* norm_variant(bool bf16, int out_kind, int kind);
 
 // The 4-bit-weight kernel for up to 8 rows of x and groups of 32, 64 or 128
 // columns, by the type of x.

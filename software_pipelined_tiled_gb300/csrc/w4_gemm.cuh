@@ -284,13 +284,14 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
   const bool leader = elect_one_sync();
   const uint64_t pol = policy_evict_first();  // codes are read once
   int issued = 0;
-  int next_seg = 0, next_ks = segments > 0 ? part_of(0, kw) : 0;
+  int next_seg = 0;
+  int next_ks = segments > 0 ? part_of(0, kw) : 0, next_end = segments > 0 ? part_of(0, kw + 1) : 0;
   auto issue_next = [&](int s) {
-    while (next_seg < segments && next_ks >= part_of(next_seg, kw + 1)) {
-      ++next_seg;
+    while (next_ks >= next_end) {  // the next segment in which this warp has a part
+      if (++next_seg >= segments) return;
       next_ks = part_of(next_seg, kw);
+      next_end = part_of(next_seg, kw + 1);
     }
-    if (next_seg >= segments) return;
     if (leader) {
       mbar_arrive_expect_tx(full0 + 8 * s, STAGE);
       tma_load_2d(ring + s * STAGE, &tmW, full0 + 8 * s, next_ks * (W4_STAGE_K / 2), row0, pol);

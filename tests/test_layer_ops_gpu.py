@@ -510,3 +510,16 @@ def test_example_layer():
     for name, ref in (("up", up.grad), ("down", down.grad), ("rows", rows.grad)):
         got = r["grads"][name].float()
         assert float((got - ref).norm() / ref.norm()) < 0.01, name
+
+
+# the choices of kernel that row counts make, at widths that fill and do not fill their threads
+@pytest.mark.parametrize("out_dtype", [S8, E4M3, None])
+@pytest.mark.parametrize("rows,cols", [(700, 4096), (650, 3000), (1400, 4104), (1500, 5000),
+                                       (930, 8192), (460, 16384), (470, 12000), (300, 2048), (33, 520)])
+def test_norm_of_many_rows(rows, cols, out_dtype):
+    g = gen(rows + cols)
+    dtype = BF16 if rows % 2 else F16
+    x, r = rand(g, rows, cols, dtype=dtype), rand(g, rows, cols, dtype=dtype, std=3.0)
+    w = 1 + rand(g, cols, dtype=dtype, std=0.2)
+    check_norm(x, r, w, out_dtype or dtype)
+    check_norm(x, r, w, out_dtype or dtype, h=r)  # in place
