@@ -282,7 +282,8 @@ int sptg_plan(int64_t M, int64_t N, int64_t K, sptg_dtype dtype, int sm_count,
  * The operators around the products of a language model's layer. All are
  * asynchronous on `stream`, allocate nothing, copy nothing to the host and
  * may be captured in a CUDA graph. They keep all sums in fp32 and give the
- * same bits for the same inputs on every call.
+ * same bits for the same inputs on every call. Dimensions are at most
+ * 2^31 - 4096 (SPTG_ERR_ARG).
  */
 
 /* Element types of these operators. */
@@ -343,7 +344,11 @@ int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type o
  *             NULL: 8 everywhere
  *   Y         M x N of out_type (SPTG_T_F16 or SPTG_T_BF16), row pitch ldy
  *
- * Products and sums are exact to fp32 accumulation; Y is rounded once.
+ * Products and sums are exact to fp32 accumulation; Y is rounded once. (For up
+ * to 8 rows the zero points come out of the groups' sums, so a weight equal to
+ * its zero point contributes 0 only to fp32 accuracy, and a row of X that holds
+ * an infinity or a NaN gives NaN; for more rows such a row gives what the
+ * products give. |X| stays below 2^120.)
  * group is 32, 64 or 128 and divides K. X and codes are 16-byte aligned with
  * row pitches of a multiple of 16 bytes (SPTG_ERR_ALIGN); N, M and ldy are
  * free. Up to 64 rows of X share one pass over the weights; more rows take

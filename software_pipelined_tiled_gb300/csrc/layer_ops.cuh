@@ -127,6 +127,11 @@ int guarded(F&& body) {
   }
 }
 
+// Dimensions stop short of 2^31 by more than any tile, so that the kernels'
+// 32-bit coordinates may run past an edge.
+constexpr int64_t kMaxDim = (static_cast<int64_t>(1) << 31) - 4096;
+constexpr const char* kDimText = "dimensions must be in [0, 2^31 - 4096]";
+
 constexpr uint64_t kOpTimeoutNs = 2000ull * 1000000ull;
 
 // ------------------------------------------------------- residual and norm
@@ -137,8 +142,7 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
   if ((in_type != SPTG_T_F16 && in_type != SPTG_T_BF16) || !type_info(in_type, in) ||
       !type_info(out_type, out) || (out.bytes == 2 && out_type != in_type))
     return refuse(SPTG_ERR_ARG, "rows are f16 or bf16, outputs s8, e4m3 or the rows' own type");
-  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX)
-    return refuse(SPTG_ERR_ARG, "dimensions must be in [0, 2^31)");
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return refuse(SPTG_ERR_ARG, kDimText);
   if (!(eps > 0.0f) || !(eps < INFINITY)) return refuse(SPTG_ERR_ARG, "eps must be positive and finite");
   if (rows == 0 || cols == 0) {
     set_config("kernel=none type=%s (empty output)", in.name, {});
@@ -289,8 +293,8 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   if (!type_info(x_type, xt) || !type_info(out_type, ot) || ot.bytes != 2 ||
       (xt.bytes == 2 && x_type != out_type))
     return refuse(SPTG_ERR_ARG, "x is f16 or bf16 (and so is Y), or s8 or e4m3 (Y f16 or bf16)");
-  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
-    return refuse(SPTG_ERR_ARG, "dimensions must be in [0, 2^31)");
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return refuse(SPTG_ERR_ARG, kDimText);
   if (group != 32 && group != 64 && group != 128)
     return refuse(SPTG_ERR_ARG, "groups of 32, 64 or 128 columns");
   if (K % group != 0) return refuse(SPTG_ERR_ARG, "K must be a multiple of the group");
@@ -374,6 +378,8 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
     const int x_stage = live_m * W4_STAGE_K * 2 + W4_STAGE_K / group * 8 * 4;
     p.segment = std::max(kw, (budget * 2 / 5) / x_stage / kw * kw);
     p.segment = std::min(p.segment, (slice + kw - 1) / kw * kw);
+    while (p.segment > kw && w4_layout(group, rows, 2, p.segment, live_m).total > budget)
+      p.segment -= kw;
     p.stages = W4_MAX_STAGES;
     while (p.stages > 2 && w4_layout(group, rows, p.stages, p.segment, live_m).total > budget)
       --p.stages;
@@ -432,8 +438,8 @@ int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, con
             cudaStream_t stream) {
   DtypeInfo d;
   if (!dtype_info(dtype, d) || d.is_int8) return refuse(SPTG_ERR_ARG, "grouped products take the float dtypes");
-  if (E < 0 || T < 0 || N < 0 || K < 0 || T > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
-    return refuse(SPTG_ERR_ARG, "dimensions must be in [0, 2^31)");
+  if (E < 0 || T < 0 || N < 0 || K < 0 || T > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return refuse(SPTG_ERR_ARG, kDimText);
   if (E > GROUPED_MAX_EXPERTS) return refuse(SPTG_ERR_ARG, "at most 1024 experts");
   // columns of the output and length of the sum (dW: the rows)
   const int64_t cols = mode == GROUPED_Y ? N : K;

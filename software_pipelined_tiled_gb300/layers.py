@@ -21,6 +21,7 @@ _PAIRS = {(torch.float16, torch.float16): 1, (torch.float16, torch.float32): 0,
           (torch.bfloat16, torch.bfloat16): 3, (torch.bfloat16, torch.float32): 4}
 _16BIT = (torch.float16, torch.bfloat16)
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_new = torch.empty
 
 _lib = _pkg.load()
 _norm, _w4 = _lib.sptg_add_rms_norm, _lib.sptg_gemm_w4
@@ -37,12 +38,13 @@ def _refuse(name: str, t, want: str):
 def _pitch(t, rows: int, cols: int, dtype, device: int, name: str) -> int:
     """Elements between the rows of a rows x cols CUDA tensor with contiguous rows."""
     if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols):
+        if t.is_contiguous():
+            return cols
         s0, s1 = t.stride()
-        if rows <= 1 or not cols:
-            if s1 == 1 or cols <= 1:
-                return cols  # the pitch of one row says nothing
-        elif s0 >= cols and (s1 == 1 or cols == 1):
+        if s0 >= cols and (s1 == 1 or cols == 1):
             return s0
+        if rows <= 1 and s1 == 1:
+            return cols  # the pitch of one row says nothing
     _refuse(name, t, f"a {rows} x {cols} {dtype} tensor with contiguous rows that do not overlap, "
                      f"on CUDA device {device}")
 
@@ -58,15 +60,16 @@ def _matrix(t, name: str):
 
 
 def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype=dtype, device=device)
 
 
-def _call(function, device: int, stream, *args):
+def _call(function, device: int, stream, args):
     handle = _raw_stream(device) if stream is None else _pkg._stream_handle(stream)
     if device == _current_device():
         rc = function(*args, handle)
@@ -88,35 +91,41 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None,
     in x's type and scales is None.  x, residual, h and y are 2-D with
     contiguous rows.
     """
-    _matrix(x, "x")
-    dtype, device, (rows, cols) = x.dtype, x.get_device(), x.shape
+    if x.dim() != 2 or not x.is_cuda:
+        _refuse("x", x, "a 2-D CUDA tensor")
+    dtype, device, shape = x.dtype, x.get_device(), x.shape
+    rows, cols = shape
     if out_dtype is None:
         out_dtype = dtype if y is None else y.dtype
     in_code, code = TYPES.get(dtype, 9), TYPES.get(out_dtype, 9)
     if in_code > 1 or code > 3 or (code < 2 and code != in_code):
         raise ValueError(f"x must be float16 or bfloat16 and out_dtype int8, float8_e4m3fn or x's "
                          f"type, not {dtype} and {out_dtype}")
-    ldx = _pitch(x, rows, cols, dtype, device, "x")
+    ldx = cols if x.is_contiguous() else _pitch(x, rows, cols, dtype, device, "x")
     ldr = _pitch(residual, rows, cols, dtype, device, "residual")
     _dense(weight, (cols,), dtype, device, "weight")
+    on = x.device
     if h is None:
-        h, ldh = _empty((rows, cols), dtype, x.device, stream), cols
+        h, ldh = _empty(shape, dtype, on, stream), cols
     else:
         ldh = _pitch(h, rows, cols, dtype, device, "h")
     if y is None:
-        y, ldy = _empty((rows, cols), out_dtype, x.device, stream), cols
+        y, ldy = _empty(shape, out_dtype, on, stream), cols
     else:
         ldy = _pitch(y, rows, cols, out_dtype, device, "y")
     if code < 2:
         if scales is not None:
             raise ValueError("a 16-bit y has no scales")
-    elif scales is None:
-        scales = _empty((rows,), _F32, x.device, stream)
+        s = None
     else:
-        _dense(scales, (rows,), _F32, device, "scales")
-    _call(_norm, device, stream, rows, cols, in_code, code, x.data_ptr(), ldx, residual.data_ptr(),
-          ldr, weight.data_ptr(), eps, h.data_ptr(), ldh, y.data_ptr(), ldy,
-          None if scales is None else scales.data_ptr())
+        if scales is None:
+            scales = _empty((rows,), _F32, on, stream)
+        else:
+            _dense(scales, (rows,), _F32, device, "scales")
+        s = scales.data_ptr()
+    _call(_norm, device, stream, (
+        rows, cols, in_code, code, x.data_ptr(), ldx, residual.data_ptr(), ldr, weight.data_ptr(),
+        eps, h.data_ptr(), ldh, y.data_ptr(), ldy, s))
     return h, y, scales
 
 
@@ -130,14 +139,13 @@ def gemm_w4(x, codes, scales, zeros=None, x_scales=None, out=None, stream=None):
     None for 8 everywhere.  x, codes and out are 2-D with contiguous rows.
     Returns out (M x N, of the scales' type).
     """
-    _matrix(x, "x")
-    _matrix(codes, "codes")
-    _matrix(scales, "scales")
-    device, dtype, (m, k), n = x.get_device(), scales.dtype, x.shape, codes.shape[0]
+    if x.dim() != 2 or codes.dim() != 2 or scales.dim() != 2 or not x.is_cuda:
+        for name, t in (("x", x), ("codes", codes), ("scales", scales)):
+            _matrix(t, name)
+    device, dtype, (m, k), (n, groups) = x.get_device(), scales.dtype, x.shape, scales.shape
     code, out_code = TYPES.get(x.dtype, 9), TYPES.get(dtype, 9)
     if out_code > 1 or code > 3 or (code < 2 and code != out_code):
         raise ValueError("x must be of the scales' 16-bit type, int8 or float8_e4m3fn")
-    groups = scales.shape[1]
     group = k // groups if groups else 32
     if k % 2 or group * groups != k:
         raise ValueError(f"{groups} groups do not divide K = {k}")
@@ -154,9 +162,10 @@ def gemm_w4(x, codes, scales, zeros=None, x_scales=None, out=None, stream=None):
         out, ldo = _empty((m, n), dtype, x.device, stream), n
     else:
         ldo = _pitch(out, m, n, dtype, device, "out")
-    _call(_w4, device, stream, m, n, k, group, code, out_code, x.data_ptr(), ldx,
-          None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), ldw,
-          scales.data_ptr(), None if zeros is None else zeros.data_ptr(), out.data_ptr(), ldo)
+    _call(_w4, device, stream, (
+        m, n, k, group, code, out_code, x.data_ptr(), ldx,
+        None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), ldw,
+        scales.data_ptr(), None if zeros is None else zeros.data_ptr(), out.data_ptr(), ldo))
     return out
 
 
@@ -187,8 +196,8 @@ def _by_rows(function, rows, W, offsets, by_k, out, out_dtype, stream, name):
         out, ldo = _empty((t, cols), out_dtype, W.device, stream), cols
     else:
         ldo = _pitch(out, t, cols, out_dtype, device, "out")
-    _call(function, device, stream, e, t, n, k, pair, offsets.data_ptr(), rows.data_ptr(), ld,
-          W.data_ptr(), out.data_ptr(), ldo)
+    _call(function, device, stream, (e, t, n, k, pair, offsets.data_ptr(), rows.data_ptr(), ld,
+                                     W.data_ptr(), out.data_ptr(), ldo))
     return out
 
 
@@ -228,6 +237,6 @@ def grouped_gemm_dw(dY, X, offsets, out=None, out_dtype=None, stream=None):
         out = _empty((e, n, k), out_dtype, X.device, stream)
     else:
         _dense(out, (e, n, k), out_dtype, device, "out")
-    _call(_dw, device, stream, e, t, n, k, pair, offsets.data_ptr(), dY.data_ptr(), ldy,
-          X.data_ptr(), ldx, out.data_ptr())
+    _call(_dw, device, stream, (e, t, n, k, pair, offsets.data_ptr(), dY.data_ptr(), ldy,
+                                X.data_ptr(), ldx, out.data_ptr()))
     return out

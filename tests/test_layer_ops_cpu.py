@@ -21,7 +21,8 @@ def test_norm_refusals(lib):
         return lib.sptg_add_rms_norm(rows, cols, it, ot, x, ldx, r, ldr, w, eps, h, ldh, y, ldy, s, None)
 
     for bad in (dict(it=S8), dict(it=77), dict(ot=F16), dict(ot=-1), dict(rows=-1), dict(cols=-1),
-                dict(rows=1 << 31), dict(eps=0.0), dict(eps=-1e-6), dict(eps=float("nan")),
+                dict(rows=1 << 31), dict(cols=(1 << 31) - 1, ldx=1 << 31, ldr=1 << 31, ldh=1 << 31,
+                                         ldy=1 << 31), dict(eps=0.0), dict(eps=-1e-6), dict(eps=float("nan")),
                 dict(eps=float("inf")), dict(x=None), dict(r=None), dict(w=None), dict(h=None),
                 dict(y=None), dict(s=None), dict(ldx=63), dict(ldr=63), dict(ldh=63), dict(ldy=63)):
         assert call(**bad) == ARG, bad
@@ -37,6 +38,7 @@ def test_w4_refusals(lib):
         return lib.sptg_gemm_w4(M, N, K, g, xt, ot, x, ldx, xs, c, ldw, s, z, y, ldy, None)
 
     for bad in (dict(xt=F16), dict(ot=S8), dict(ot=9), dict(xt=9), dict(M=-1), dict(N=1 << 31),
+                dict(N=(1 << 31) - 128, ldy=1 << 31),
                 dict(K=-128), dict(g=16), dict(g=0), dict(K=160, ldx=160, ldw=80), dict(x=None),
                 dict(c=None), dict(s=None), dict(y=None), dict(xt=S8, xs=None), dict(xs=OK),
                 dict(ldx=127), dict(ldw=63), dict(ldy=7)):
@@ -59,6 +61,7 @@ def test_grouped_refusals(lib):
 
     for f in (y, dx, dw):
         for bad in (dict(d=2), dict(d=50), dict(E=-1), dict(T=-1), dict(N=-8), dict(K=1 << 31),
+                    dict(T=(1 << 31) - 1),
                     dict(E=1025), dict(o=None), dict(x=None), dict(w=None), dict(out=None),
                     dict(ldx=8)):
             assert f(**bad) == ARG, (f.__name__, bad)
