@@ -324,9 +324,10 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
     return SPTG_OK;
   }
   // Up to 8 rows of x: the streaming kernel. More: the tensor-core tile kernel
-  // with 16, 32 or 64 rows, in blocks of 64 that each pass over the weights.
+  // with 16, 32 or 64 rows, in blocks of 64 (groups of 32 columns: of 32) that
+  // each pass over the weights.
   const bool tile = M > 8;
-  const int nt = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int nt = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : w4t_max_ntok(group);
   const int64_t m_blocks = (M + nt - 1) / nt;
   if (m_blocks > 65535) return refuse(SPTG_ERR_ARG, "at most 64 * 65535 rows of x");
   int xk;
@@ -354,7 +355,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   if (rc) return rc;
   const int threads = tile ? w4t_threads(nt) : 32 * W4_MAX_WARPS;
   const W4Slots slots = w4_slots(dev, fn, tile ? 1 : W4_CTAS_PER_SM, threads, di.sm_count);
-  const W4Shape shape = w4_shape(N, k_stages, 64, tile ? W4T_MAX_ROWS : W4_MAX_ROWS,
+  const W4Shape shape = w4_shape(N, k_stages, 64, tile ? w4t_max_rows(xk, nt) : W4_MAX_ROWS,
                                  m_blocks, slots.n);
   const int rows = shape.rows, splits = shape.splits;
   const int64_t n_tiles = (N + rows - 1) / rows;
@@ -363,7 +364,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   int smem, launch_threads = threads;
   if (tile) {
     // as many stages of codes as fit beside two to four of x
-    p.segment = nt == 64 ? 2 : W4T_MAX_X_STAGES;
+    p.segment = nt == 16 ? W4T_MAX_X_STAGES : 2;
     p.stages = W4T_MAX_STAGES;
     while (p.stages > 2 && w4t_smem(xk, nt, rows, p.stages, p.segment) > 232448) --p.stages;
     smem = w4t_smem(xk, nt, rows, p.stages, p.segment);

@@ -17,23 +17,25 @@
 // A CTA takes up to 128 rows of weights and a range of K (shared in a cluster,
 // as in w4_gemm.cuh). Roles:
 //
-//   16 warps  widen, in two groups, one for each half of a stage's 256
-//             columns: a lane turns 32 bytes of codes of its row (64 columns)
-//             into its row of an operand tile; before that the group pairs up
-//             its half of the stage's x (and widens 8-bit x), once per CTA
-//   4 warps   (8 with 64 rows of x) sums: a lane owns a row of weights; for
-//             each group it reads the group's sums from tensor memory,
-//             multiplies them by its scale and adds them to its own, in 32 bits
-//   2 warps   producers of the two rings, codes and x, by tensor copy
-//   1 warp    MMA issuer: a half's two operand tiles of 64 columns, one
-//             accumulator a group, eight accumulators in turn
+//   8 warps  widen: a lane turns 64 bytes of codes of its row (128 of a stage's
+//            256 columns) into its row of two operand tiles; before that the
+//            warps pair up the stage's x (and widen 8-bit x), once per CTA
+//   4 warps  (8 with 64 rows of x) sums: a lane owns a row of weights; for each
+//            group it reads the group's sums from tensor memory, multiplies them
+//            by its scale and adds them to its own, in 32 bits
+//   2 warps  producers of the two rings, codes and x, by tensor copy
+//   1 warp   MMA issuer: a stage's four operand tiles of 64 columns, one
+//            accumulator a group
 //
-// Each group of widening warps has one set of operand tiles: while it waits for
-// data, its fence or the MMAs, the other computes. A half is handed over at
-// once, because the fence between the warps' writes and the tensor core's
-// reads is slow, and its MMAs are issued without a branch between them. Codes
-// leave their ring as soon as they are in registers, so that ring is all bytes
-// in flight; x stays in its own until it has been multiplied.
+// Hand-overs are what a stage costs besides its work, so there are few: the
+// issuer waits once for a stage's operands and once for its accumulators, issues
+// the stage's MMAs without a branch and commits once, on a barrier that the
+// widening warps (their tiles are free), the producer of x (its stage is) and
+// the sums (theirs are ready) all wait on. With a commit for each group and
+// half stage, the bare chain of waits took 58 us on 32768 x 8192. Two sets of
+// operand tiles and of accumulators alternate from stage to stage. Codes leave
+// their ring as soon as they are in registers, so that ring is all bytes in
+// flight; x stays in its own until it has been multiplied.
 //
 // Exactness: a widened weight is the integer code - zero point, |.| <= 15, in
 // the 16-bit type of the product; products are exact, sums are kept in 32 bits,
@@ -49,29 +51,39 @@
 namespace sptg {
 
 constexpr int W4T_MAX_ROWS = 128;
-constexpr int W4T_WIDEN = 16;                      // widening warps
+constexpr int W4T_WIDEN = 8;                       // widening warps
 constexpr int W4T_MAX_STAGES = 10;
-constexpr int W4T_ACCS = 8;
 __host__ __device__ constexpr int w4t_sum_warps(int ntok) { return ntok == 64 ? 8 : 4; }
 __host__ __device__ constexpr int w4t_threads(int ntok) {
   return 32 * (W4T_WIDEN + w4t_sum_warps(ntok) + 3);
 }
 
-// Shared memory: two sets of two operand tiles (64 columns of the CTA's rows
+// Two sets of a stage's accumulators fill tensor memory: groups of 32 columns
+// leave room for 32 rows of x.
+__host__ __device__ constexpr int w4t_max_ntok(int group) { return group == 32 ? 32 : 64; }
+
+// Shared memory: two sets of four operand tiles (64 columns of the CTA's rows
 // each; the MMA's 128 rows run on into what follows, into sums that are never
 // stored), the ring of codes, the ring of x (in 16 bits, and as copied where
 // that is 8 bits), the barriers.
-__host__ __device__ constexpr int w4t_a_set(int rows) { return 2 * rows * 128; }
+__host__ __device__ constexpr int w4t_a_set(int rows) { return 4 * rows * 128; }
 __host__ __device__ constexpr int w4t_code_stage(int rows) { return rows * (W4_STAGE_K / 2); }
 __host__ __device__ constexpr int w4t_x_bytes(int ntok) { return ntok * W4_STAGE_K * 2; }
 __host__ __device__ constexpr int w4t_x_stage(int xk, int ntok) {
   return w4t_x_bytes(ntok) + (xk >= W4_S8 ? ntok * W4_STAGE_K : 0);
 }
 constexpr int W4T_MAX_X_STAGES = 4;
-constexpr int W4T_BARS = 2 * W4T_MAX_STAGES + 2 * W4T_MAX_X_STAGES + 4 + 2 * W4T_ACCS + 1;
+constexpr int W4T_BARS = 2 * W4T_MAX_STAGES + W4T_MAX_X_STAGES + 4 + 2 + 2 + 1;
 __host__ __device__ constexpr int w4t_smem(int xk, int ntok, int rows, int stages, int x_stages) {
   return 2 * w4t_a_set(rows) + stages * w4t_code_stage(rows) + x_stages * w4t_x_stage(xk, ntok) +
          W4T_BARS * 8 + 16 + 1024;
+}
+
+// most rows of weights beside two stages of each ring
+__host__ __device__ constexpr int w4t_max_rows(int xk, int ntok) {
+  int rows = W4T_MAX_ROWS;
+  while (w4t_smem(xk, ntok, rows, 2, 2) > 232448) rows -= 16;
+  return rows;
 }
 
 // The eight codes of a word, less the zero point (exact), as one 16-byte piece
@@ -118,7 +130,9 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   constexpr int SUMS = w4t_sum_warps(NTOK);
   constexpr int PRODUCER = W4T_WIDEN + SUMS, X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
   constexpr int COLS = NTOK == 64 ? 32 : NTOK;  // rows of x a sums warp holds
-  constexpr uint32_t TMEM_COLS = W4T_ACCS * NTOK;  // 128, 256 or 512
+  constexpr int ACC_SET = GROUPS * NTOK;           // columns of a stage's accumulators
+  constexpr uint32_t TMEM_COLS = 2 * ACC_SET;      // a power of two, 64 to 512
+  static_assert(TMEM_COLS <= 512, "accumulators exceed tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -135,12 +149,12 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (W4T_MAX_STAGES + s); };
   const uint32_t bar1 = bar0 + 8u * (2 * W4T_MAX_STAGES);
   auto xfull_bar = [&](int s) { return bar1 + 8u * s; };
-  auto xempty_bar = [&](int s) { return bar1 + 8u * (W4T_MAX_X_STAGES + s); };
-  const uint32_t bar2 = bar1 + 8u * (2 * W4T_MAX_X_STAGES);
-  auto ready_bar = [&](int a) { return bar2 + 8u * a; };       // set widened, half of x paired
-  auto used_bar = [&](int a) { return bar2 + 8u * (2 + a); };  // set multiplied
-  auto tfull_bar = [&](int b) { return bar2 + 8u * (4 + b); };
-  auto tempty_bar = [&](int b) { return bar2 + 8u * (4 + W4T_ACCS + b); };
+  const uint32_t bar2 = bar1 + 8u * W4T_MAX_X_STAGES;
+  auto done_bar = [&](int it) { return bar2 + 8u * (it & 3); };         // stage multiplied
+  auto done_parity = [](int it) { return static_cast<uint32_t>(it >> 2) & 1u; };
+  auto ready_bar = [&](int it) { return bar2 + 8u * (4 + (it & 1)); };  // widened, x paired
+  auto tempty_bar = [&](int it) { return bar2 + 8u * (6 + (it & 1)); };  // sums read
+  auto pair_parity = [](int it) { return static_cast<uint32_t>(it >> 1) & 1u; };
   const uint32_t drain_bar = bar0 + 8u * (W4T_BARS - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + off_bars + W4T_BARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_bars + W4T_BARS * 8 + 4);
@@ -153,6 +167,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   const int KS = (p.K + W4_STAGE_K - 1) / W4_STAGE_K;
   const int ks0 = static_cast<int>(static_cast<int64_t>(KS) * rank / p.splits);
   const int ks1 = static_cast<int>(static_cast<int64_t>(KS) * (rank + 1) / p.splits);
+  const int stages = ks1 - ks0;
   const int KG = p.K / G;
 
   if (threadIdx.x == 0) {
@@ -160,17 +175,11 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), W4T_WIDEN);
     }
-    for (int s = 0; s < SX; ++s) {
-      mbar_init(xfull_bar(s), 1);
-      mbar_init(xempty_bar(s), 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(ready_bar(a), W4T_WIDEN / 2);
-      mbar_init(used_bar(a), 1);
-    }
-    for (int b = 0; b < W4T_ACCS; ++b) {
-      mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), SUMS);
+    for (int s = 0; s < SX; ++s) mbar_init(xfull_bar(s), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(done_bar(i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(ready_bar(i), W4T_WIDEN);
+      mbar_init(tempty_bar(i), SUMS);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -198,49 +207,48 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
 
   if (warp < W4T_WIDEN) {
     // ---------------------------------------------------------------- widen
-    // Thread: half `set` of a stage, row r, operand tile c of the half (columns
-    // 128 set + 64 c ... + 63 of the stage).
-    const int set = warp >> 3, gw = warp & 7;
-    const int r = threadIdx.x & 127, c = (threadIdx.x >> 7) & 1;
+    // Thread: row r, operand tiles 2 c and 2 c + 1 (columns 128 c ... + 127 of a
+    // stage).
+    const int r = threadIdx.x & 127, c = threadIdx.x >> 7;
     const bool works = r < R;
     const uint8_t* zp = p.zeros ? p.zeros + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG : nullptr;
     constexpr uint32_t ZLO = BF ? 0x4300u : 0x6400u;
-    constexpr int ZS = G == 32 ? 2 : 1;  // zero points of a lane's columns
+    constexpr int ZS = 128 / G;  // zero points of a lane's columns
     uint32_t next_z[ZS];
-    auto load_zeros = [&](int ks) {
 #pragma unroll
-      for (int i = 0; i < ZS; ++i)
-        next_z[i] =
-            zp ? __ldg(zp + min((ks * W4_STAGE_K + 128 * set + 64 * c) / G + i, KG - 1)) : 8u;
+    for (int i = 0; i < ZS; ++i) next_z[i] = 8u;
+    auto load_zeros = [&](int ks) {
+      if (zp) {
+#pragma unroll
+        for (int i = 0; i < ZS; ++i)
+          next_z[i] = __ldg(zp + min((ks * W4_STAGE_K + 128 * c) / G + i, KG - 1));
+      }
     };
     load_zeros(ks0);
     // places that do not change from stage to stage: this lane's row of codes
-    // and of its operand tile (128-byte aligned; piece i lies at place
-    // i ^ (r & 7)), its piece of x (row m, piece j of the half's 16; then 16
-    // rows on)
-    const uint32_t code0 = static_cast<uint32_t>(r * 128 + (((4 * set + 2 * c) ^ (r & 7)) << 4));
-    const uint32_t dst =
-        sbase + static_cast<uint32_t>(set * a_set + (c * R + r) * 128 + ((r & 7) << 4));
-    const int m = 2 * gw + (lane >> 4), j = lane & 15;
-    const uint32_t piece0 = static_cast<uint32_t>((2 * set + (j >> 3)) * (NTOK * 128) + m * 128 +
-                                                  (((j & 7) ^ (m & 7)) << 4));
-    const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + m * W4_STAGE_K + (16 * set + j) * 8);
+    // and of its operand tiles (128-byte aligned; piece i lies at place
+    // i ^ (r & 7)), its piece of x (row warp, piece lane of 32; then 8 rows on)
+    const uint32_t code0 = static_cast<uint32_t>(r * 128 + (((4 * c) ^ (r & 7)) << 4));
+    const uint32_t dst0 = sbase + static_cast<uint32_t>((2 * c * R + r) * 128 + ((r & 7) << 4));
+    const uint32_t piece0 = static_cast<uint32_t>((lane >> 3) * (NTOK * 128) + warp * 128 +
+                                                  (((lane & 7) ^ warp) << 4));
+    const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + warp * W4_STAGE_K + lane * 8);
     int s = 0, sx = 0;
-    uint32_t phase = 0, x_phase = 0, used_phase = 1;
-    for (int ks = ks0; ks < ks1; ++ks) {
+    uint32_t phase = 0, x_phase = 0;
+    for (int it = 0; it < stages; ++it) {
       uint32_t z[ZS];
 #pragma unroll
       for (int i = 0; i < ZS; ++i) {
         asm volatile("" : "+r"(next_z[i]));  // no use of the loads before this
         z[i] = next_z[i] & 15u;
       }
-      load_zeros(min(ks + 1, ks1 - 1));
+      load_zeros(min(ks0 + it + 1, ks1 - 1));
       if (!wait(full_bar(s), phase, WAIT_MMA_FULL)) break;
       const uint32_t st = ring + s * w4t_code_stage(R);
-      uint4 code[2];
+      uint4 code[4];
       if (works) {
-        code[0] = lds128(st + code0);
-        code[1] = lds128(st + (code0 ^ 16u));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = lds128(st + (code0 ^ static_cast<uint32_t>(i << 4)));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(s));
@@ -252,7 +260,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
       // pair up x: pieces of 8 columns
       const uint32_t sxt = x_ring + sx * X_STAGE;
 #pragma unroll
-      for (int i = 0; i < NTOK; i += 16) {
+      for (int i = 0; i < NTOK; i += W4T_WIDEN) {
         uint4 v;
         if constexpr (X8) {
           v.x = lds32(sxt + raw0 + i * W4_STAGE_K);
@@ -267,24 +275,24 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
         sx = 0;
         x_phase ^= 1u;
       }
-      // the set's last multiplication has ended (there is none the first time)
-      if (!wait(used_bar(set), used_phase, WAIT_PRODUCER_EMPTY)) break;
-      used_phase ^= 1u;
+      // the set's last multiplication, two stages ago, has ended
+      if (it >= 2 && !wait(done_bar(it - 2), done_parity(it - 2), WAIT_PRODUCER_EMPTY)) break;
       if (works) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t zi = z[ZS == 2 ? i : 0];
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t zi = z[i * ZS / 4];
           const uint32_t zz = (ZLO | zi) * 0x00010001u;
           const uint32_t zh = (0xd400u | (zi << 4)) * 0x00010001u;  // -(64 + z), binary16
           const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+          const uint32_t to = dst0 + (it & 1) * a_set + (i >> 1) * (R * 128);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            sts128(dst ^ static_cast<uint32_t>((4 * i + k) << 4), widen_word<BF>(p, w[k], zz, zh));
+            sts128(to ^ static_cast<uint32_t>((4 * (i & 1) + k) << 4), widen_word<BF>(p, w[k], zz, zh));
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ready_bar(set));
+      if (lane == 0) mbar_arrive(ready_bar(it));
     }
   } else if (warp < PRODUCER) {
     // ----------------------------------------------------------------- sums
@@ -292,38 +300,52 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     const int r = 32 * q + lane;
     const int col0 = warp >= W4T_WIDEN + 4 ? COLS : 0;
     const uint16_t* sp = p.scales + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG;
-    const int g_end = min(ks1 * GROUPS, KG);
-    uint32_t next_s = 0;
-    auto load_scale = [&](int g) {
-      asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];" : "=r"(next_s) : "l"(sp + min(g, KG - 1)));
+    // A stage's scales, a stage ahead. Groups past K have no sums but zeros.
+    uint32_t next_s[GROUPS];
+    auto load_scales = [&](int ks) {
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i)
+        asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];"
+                     : "=r"(next_s[i])
+                     : "l"(sp + min(ks * GROUPS + i, KG - 1)));
     };
-    load_scale(ks0 * GROUPS);
-    int b = 0;
-    uint32_t phase = 0;
-    for (int gi = ks0 * GROUPS; gi < ks1 * GROUPS; ++gi) {
-      asm volatile("" : "+r"(next_s));
+    load_scales(ks0);
+    for (int it = 0; it < stages; ++it) {
+      float sc[GROUPS];
       const bool bf = BF || (XK != W4_F16 && p.out_bf16);
-      float sc = bf ? __uint_as_float(next_s << 16)
-                    : __half2float(__ushort_as_half(static_cast<unsigned short>(next_s)));
-      if (gi >= g_end) sc = 0.0f;  // past K: the sums are zeros
-      load_scale(gi + 1);
-      if (!wait(tfull_bar(b), phase, WAIT_EPI_TMEM_FULL)) break;
-      tc_fence_after();
-      const uint32_t t_acc = tmem_base + b * NTOK + col0 + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll
-      for (int c = 0; c < COLS; c += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(t_acc + c, v);
-        tmem_wait_ld_regs16(v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(sc, __uint_as_float(v[i]), acc[c + i]);
+      for (int i = 0; i < GROUPS; ++i) {
+        asm volatile("" : "+r"(next_s[i]));  // no use of the loads before this
+        sc[i] = bf ? __uint_as_float(next_s[i] << 16)
+                   : __half2float(__ushort_as_half(static_cast<unsigned short>(next_s[i])));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty_bar(b));
-      if (++b == W4T_ACCS) {
-        b = 0;
-        phase ^= 1u;
+      load_scales(min(ks0 + it + 1, ks1 - 1));
+      if (!wait(done_bar(it), done_parity(it), WAIT_EPI_TMEM_FULL)) break;
+      tc_fence_after();
+      const uint32_t t_acc =
+          tmem_base + (it & 1) * ACC_SET + col0 + (static_cast<uint32_t>(32 * q) << 16);
+      // 32 sums at a time
+      constexpr int GS = COLS == 16 ? 2 : 1;  // groups
+#pragma unroll
+      for (int g = 0; g < GROUPS; g += GS) {
+        uint32_t v[2][16];
+        const int c1 = GS == 2 ? NTOK : 16;
+        tmem_ld_32x32b_x16(t_acc + g * NTOK, v[0]);
+        tmem_ld_32x32b_x16(t_acc + g * NTOK + c1, v[1]);
+        tmem_wait_ld_regs16(v[0]);
+        tmem_wait_ld_regs16(v[1]);
+        if (g + GS == GROUPS) {  // all have been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty_bar(it));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float& a = acc[GS == 2 ? i : 16 * h + i];
+            a = fmaf(sc[GS == 2 ? g + h : g], __uint_as_float(v[h][i]), a);
+          }
       }
     }
   } else if (warp == PRODUCER || warp == X_PRODUCER) {
@@ -339,7 +361,11 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     int s = 0;
     uint32_t phase = 0;
     for (int ks = ks0; ks < ks1; ++ks) {
-      ok = wait(of_x ? xempty_bar(s) : empty_bar(s), phase ^ 1u, WAIT_PRODUCER_EMPTY);
+      const int it = ks - ks0;
+      if (!of_x)
+        ok = wait(empty_bar(s), phase ^ 1u, WAIT_PRODUCER_EMPTY);
+      else if (it >= SX)
+        ok = wait(done_bar(it - SX), done_parity(it - SX), WAIT_PRODUCER_EMPTY);
       if (!ok) break;
       if (leader) {
         if (!of_x) {
@@ -376,50 +402,25 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   } else {
     // ----------------------------------------------------------- MMA issuer
     const bool leader = elect_one_sync();
-    int sx = 0, b = 0;
-    uint32_t phase = 0, b_phase = 0;
-    bool ok = true;
-    for (int ks = ks0; ok && ks < ks1; ++ks) {
-      // The waits for a half and its groups' accumulators come first, then its
-      // MMAs (steps of 16 columns, 4 an operand tile, G / 16 a group) without a
-      // branch: each stretch that the elected lane runs alone has a cost of
-      // its own.
-      constexpr int AT_ONCE = GROUPS / 2;
-      constexpr int STEPS = G / 16;
+    int sx = 0;
+    for (int it = 0; it < stages; ++it) {
+      if (!wait(ready_bar(it), pair_parity(it), WAIT_MMA_FULL)) break;
+      if (it >= 2 && !wait(tempty_bar(it), pair_parity(it) ^ 1u, WAIT_MMA_TMEM_EMPTY)) break;
+      tc_fence_after();
+      const uint64_t ad = sdesc_k_major_sw128(sbase + (it & 1) * a_set);
+      const uint64_t xd = sdesc_k_major_sw128(x_ring + sx * X_STAGE);
+      const uint32_t d = tmem_base + (it & 1) * ACC_SET;
+      if (leader) {
+        // steps of 16 columns, 4 an operand tile, G / 16 a group
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ok = ok && wait(ready_bar(h), phase, WAIT_MMA_FULL);
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i)
-          ok = ok && wait(tempty_bar(b + i), b_phase ^ 1u, WAIT_MMA_TMEM_EMPTY);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t ad = sdesc_k_major_sw128(sbase + h * a_set);
-        const uint64_t xd = sdesc_k_major_sw128(x_ring + sx * X_STAGE + 2 * h * (NTOK * 128));
-        if (leader) {
-#pragma unroll
-          for (int i = 0; i < AT_ONCE; ++i) {
-#pragma unroll
-            for (int n = 0; n < STEPS; ++n) {
-              const int k = i * STEPS + n;
-              mma_f16(tmem_base + (b + i) * NTOK,
-                      ad + static_cast<uint64_t>((k >> 2) * (R * 128) >> 4) + 2 * (k & 3),
-                      xd + static_cast<uint64_t>((k >> 2) * (NTOK * 128) >> 4) + 2 * (k & 3), IDESC,
-                      n == 0 ? 0u : 1u);
-            }
-            mma_commit(tfull_bar(b + i));
-          }
-          mma_commit(used_bar(h));
-          if (h == 1) mma_commit(xempty_bar(sx));
-        }
-        __syncwarp();
-        b += AT_ONCE;
-        if (b == W4T_ACCS) {
-          b = 0;
-          b_phase ^= 1u;
-        }
+        for (int k = 0; k < W4_STAGE_K / 16; ++k)
+          mma_f16(d + k / (G / 16) * NTOK,
+                  ad + static_cast<uint64_t>((k >> 2) * (R * 128) >> 4) + 2 * (k & 3),
+                  xd + static_cast<uint64_t>((k >> 2) * (NTOK * 128) >> 4) + 2 * (k & 3), IDESC,
+                  k % (G / 16) == 0 ? 0u : 1u);
+        mma_commit(done_bar(it));
       }
-      phase ^= 1u;
+      __syncwarp();
       if (++sx == SX) sx = 0;
     }
     if (leader) mma_commit(drain_bar);
@@ -489,7 +490,6 @@ const void* w4_tile_kernel_of(int ntok, int group) {
   SPTG_W4T_CASE(32, 32);
   SPTG_W4T_CASE(32, 64);
   SPTG_W4T_CASE(32, 128);
-  SPTG_W4T_CASE(64, 32);
   SPTG_W4T_CASE(64, 64);
   SPTG_W4T_CASE(64, 128);
 #undef SPTG_W4T_CASE
