@@ -355,7 +355,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   if (rc) return rc;
   const int threads = tile ? w4t_threads(nt) : 32 * W4_MAX_WARPS;
   const W4Slots slots = w4_slots(dev, fn, tile ? 1 : W4_CTAS_PER_SM, threads, di.sm_count);
-  const W4Shape shape = w4_shape(N, k_stages, 64, tile ? w4t_max_rows(xk, nt) : W4_MAX_ROWS,
+  const W4Shape shape = w4_shape(N, k_stages, 64, tile ? W4T_MAX_ROWS : W4_MAX_ROWS,
                                  m_blocks, slots.n);
   const int rows = shape.rows, splits = shape.splits;
   const int64_t n_tiles = (N + rows - 1) / rows;
@@ -364,7 +364,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   int smem, launch_threads = threads;
   if (tile) {
     // as many stages of codes as fit beside two to four of x
-    p.segment = nt == 16 ? W4T_MAX_X_STAGES : 2;
+    p.segment = nt == 64 ? 3 : W4T_MAX_X_STAGES;
     p.stages = W4T_MAX_STAGES;
     while (p.stages > 2 && w4t_smem(xk, nt, rows, p.stages, p.segment) > 232448) --p.stages;
     smem = w4t_smem(xk, nt, rows, p.stages, p.segment);

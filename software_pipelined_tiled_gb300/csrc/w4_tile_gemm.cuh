@@ -4,38 +4,34 @@
 // The operator is w4_gemm.cuh's. Past 8 rows the warp-wide instruction of that
 // kernel runs out of rate (1024 multiply-adds a cycle and SM: 56 us for the bare
 // products of 64 rows with 32768 x 8192; such a kernel took 121 us), so the
-// weights are widened once, into shared memory, and one tcgen05 instruction
+// weights are widened once, into tensor memory, and one tcgen05 instruction
 // multiplies 128 rows of them with all rows of x (swap-AB: the weights' rows are
-// the instruction's M side, NTOK = 16, 32 or 64 rows of x its N side).
-//
-// Measured: 64 bfloat16 rows through 32768 x 8192, 104 us; 61 rows through
-// 5001 x 4128 with groups of 32, 25.5 us; 16 int8 rows through 8192 x 8192,
-// 22 us (floor 5.2). Not bound by any one unit: the copies alone take about half
-// of it, the widening's instructions another third; what bounds it is the chain
-// of hand-overs of each half stage (copy, widen, fence, multiply, sum).
+// the instruction's M side, NTOK = 16, 32 or 64 rows of x its N side). Widened
+// into shared memory instead, they are written and read there once each, four
+// bytes a weight: 16 rows through 32768 x 8192 took 77 us, whatever else was
+// changed.
 //
 // A CTA takes up to 128 rows of weights and a range of K (shared in a cluster,
 // as in w4_gemm.cuh). Roles:
 //
 //   8 warps  widen: a lane turns 64 bytes of codes of its row (128 of a stage's
-//            256 columns) into its row of two operand tiles; before that the
-//            warps pair up the stage's x (and widen 8-bit x), once per CTA
+//            256 columns) into its lane of the operand in tensor memory; before
+//            that the warps pair up the stage's x (and widen 8-bit x) in place
 //   4 warps  (8 with 64 rows of x) sums: a lane owns a row of weights; for each
 //            group it reads the group's sums from tensor memory, multiplies them
 //            by its scale and adds them to its own, in 32 bits
 //   2 warps  producers of the two rings, codes and x, by tensor copy
-//   1 warp   MMA issuer: a stage's four operand tiles of 64 columns, one
-//            accumulator a group
+//   1 warp   MMA issuer: a stage's 16 steps of 16 columns, one accumulator a
+//            group
 //
 // Hand-overs are what a stage costs besides its work, so there are few: the
 // issuer waits once for a stage's operands and once for its accumulators, issues
 // the stage's MMAs without a branch and commits once, on a barrier that the
-// widening warps (their tiles are free), the producer of x (its stage is) and
-// the sums (theirs are ready) all wait on. With a commit for each group and
-// half stage, the bare chain of waits took 58 us on 32768 x 8192. Two sets of
-// operand tiles and of accumulators alternate from stage to stage. Codes leave
-// their ring as soon as they are in registers, so that ring is all bytes in
-// flight; x stays in its own until it has been multiplied.
+// widening warps (their operand is free), the producer of x (its stage is) and
+// the sums (theirs are ready) all wait on. Two operands, and two sets of
+// accumulators where they fit, alternate from stage to stage. Codes leave their
+// ring as soon as they are in registers, so that ring is all bytes in flight; x
+// stays in its own until it has been multiplied.
 //
 // Exactness: a widened weight is the integer code - zero point, |.| <= 15, in
 // the 16-bit type of the product; products are exact, sums are kept in 32 bits,
@@ -58,15 +54,13 @@ __host__ __device__ constexpr int w4t_threads(int ntok) {
   return 32 * (W4T_WIDEN + w4t_sum_warps(ntok) + 3);
 }
 
-// Two sets of a stage's accumulators fill tensor memory: groups of 32 columns
-// leave room for 32 rows of x.
+// Tensor memory: 256 columns of accumulators, one for each group of a stage and
+// row of x, then two operands of 128 columns (256 values of K).
+constexpr int W4T_ACC_COLS = 256;
 __host__ __device__ constexpr int w4t_max_ntok(int group) { return group == 32 ? 32 : 64; }
 
-// Shared memory: two sets of four operand tiles (64 columns of the CTA's rows
-// each; the MMA's 128 rows run on into what follows, into sums that are never
-// stored), the ring of codes, the ring of x (in 16 bits, and as copied where
-// that is 8 bits), the barriers.
-__host__ __device__ constexpr int w4t_a_set(int rows) { return 4 * rows * 128; }
+// Shared memory: the ring of codes, the ring of x (in 16 bits, and as copied
+// where that is 8 bits), the barriers. The partial sums reuse the front.
 __host__ __device__ constexpr int w4t_code_stage(int rows) { return rows * (W4_STAGE_K / 2); }
 __host__ __device__ constexpr int w4t_x_bytes(int ntok) { return ntok * W4_STAGE_K * 2; }
 __host__ __device__ constexpr int w4t_x_stage(int xk, int ntok) {
@@ -74,25 +68,22 @@ __host__ __device__ constexpr int w4t_x_stage(int xk, int ntok) {
 }
 constexpr int W4T_MAX_X_STAGES = 4;
 constexpr int W4T_BARS = 2 * W4T_MAX_STAGES + W4T_MAX_X_STAGES + 4 + 2 + 2 + 1;
+__host__ __device__ constexpr int w4t_bars_at(int xk, int ntok, int rows, int stages, int x_stages) {
+  const int rings = stages * w4t_code_stage(rows) + x_stages * w4t_x_stage(xk, ntok);
+  const int red = ntok * (W4T_MAX_ROWS + 4) * 4;
+  return rings > red ? rings : red;
+}
 __host__ __device__ constexpr int w4t_smem(int xk, int ntok, int rows, int stages, int x_stages) {
-  return 2 * w4t_a_set(rows) + stages * w4t_code_stage(rows) + x_stages * w4t_x_stage(xk, ntok) +
-         W4T_BARS * 8 + 16 + 1024;
+  return w4t_bars_at(xk, ntok, rows, stages, x_stages) + W4T_BARS * 8 + 16 + 1024;
 }
 
-// most rows of weights beside two stages of each ring
-__host__ __device__ constexpr int w4t_max_rows(int xk, int ntok) {
-  int rows = W4T_MAX_ROWS;
-  while (w4t_smem(xk, ntok, rows, 2, 2) > 232448) rows -= 16;
-  return rows;
-}
-
-// The eight codes of a word, less the zero point (exact), as one 16-byte piece
-// of the operand tile. zz: pairs of the zero point under the same exponent;
+// The eight codes of a word, less the zero point (exact), as four columns of the
+// operand. zz: pairs of the zero point under the same exponent;
 // binary16 takes two of the shifts off the integer pipe with a multiply-add
 // ((1024 + 16 code) / 16 - (64 + z)).
 template <bool BF>
-__device__ __forceinline__ uint4 widen_word(const W4Params& p, uint32_t w, uint32_t zz, uint32_t zh) {
-  uint32_t o[4];
+__device__ __forceinline__ void widen_word(const W4Params& p, uint32_t w, uint32_t zz, uint32_t zh,
+                                           uint32_t* o) {
   if constexpr (BF) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -116,7 +107,6 @@ __device__ __forceinline__ uint4 widen_word(const W4Params& p, uint32_t w, uint3
       o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&dh);
     }
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int XK, int NTOK, int G>
@@ -130,20 +120,19 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   constexpr int SUMS = w4t_sum_warps(NTOK);
   constexpr int PRODUCER = W4T_WIDEN + SUMS, X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
   constexpr int COLS = NTOK == 64 ? 32 : NTOK;  // rows of x a sums warp holds
-  constexpr int ACC_SET = GROUPS * NTOK;           // columns of a stage's accumulators
-  constexpr uint32_t TMEM_COLS = 2 * ACC_SET;      // a power of two, 64 to 512
-  static_assert(TMEM_COLS <= 512, "accumulators exceed tensor memory");
+  constexpr int ACC_SET = GROUPS * NTOK;  // columns of a stage's accumulators
+  constexpr int SETS = 2 * ACC_SET <= W4T_ACC_COLS ? 2 : 1;
+  static_assert(ACC_SET <= W4T_ACC_COLS, "accumulators exceed their part of tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_addr(smem);
   const int S = p.stages, SX = p.segment, R = p.rows;
-  const int a_set = w4t_a_set(R);
-  const uint32_t ring = sbase + 2 * a_set;
+  const uint32_t ring = sbase;
   const uint32_t x_ring = ring + S * w4t_code_stage(R);
   constexpr int X_STAGE = w4t_x_stage(XK, NTOK);
   constexpr int OFF_RAW = w4t_x_bytes(NTOK);  // in a stage of x: x as copied, if 8-bit
-  const int off_bars = 2 * a_set + S * w4t_code_stage(R) + SX * X_STAGE;
+  const int off_bars = w4t_bars_at(XK, NTOK, R, S, SX);
   const uint32_t bar0 = sbase + off_bars;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };  // codes
   auto empty_bar = [&](int s) { return bar0 + 8u * (W4T_MAX_STAGES + s); };
@@ -153,7 +142,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   auto done_bar = [&](int it) { return bar2 + 8u * (it & 3); };         // stage multiplied
   auto done_parity = [](int it) { return static_cast<uint32_t>(it >> 2) & 1u; };
   auto ready_bar = [&](int it) { return bar2 + 8u * (4 + (it & 1)); };  // widened, x paired
-  auto tempty_bar = [&](int it) { return bar2 + 8u * (6 + (it & 1)); };  // sums read
+  auto tempty_bar = [&](int it) { return bar2 + 8u * (6 + it % SETS); };  // sums read
   auto pair_parity = [](int it) { return static_cast<uint32_t>(it >> 1) & 1u; };
   const uint32_t drain_bar = bar0 + 8u * (W4T_BARS - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + off_bars + W4T_BARS * 8);
@@ -188,7 +177,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     prefetch_tensor_map(&tmX);
   }
   if (warp == ISSUER) {
-    tmem_alloc(smem_addr(tmem_slot), TMEM_COLS);
+    tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -207,8 +196,8 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
 
   if (warp < W4T_WIDEN) {
     // ---------------------------------------------------------------- widen
-    // Thread: row r, operand tiles 2 c and 2 c + 1 (columns 128 c ... + 127 of a
-    // stage).
+    // Thread: row r (= its lane of tensor memory), columns 128 c ... + 127 of a
+    // stage.
     const int r = threadIdx.x & 127, c = threadIdx.x >> 7;
     const bool works = r < R;
     const uint8_t* zp = p.zeros ? p.zeros + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG : nullptr;
@@ -226,10 +215,10 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     };
     load_zeros(ks0);
     // places that do not change from stage to stage: this lane's row of codes
-    // and of its operand tiles (128-byte aligned; piece i lies at place
-    // i ^ (r & 7)), its piece of x (row warp, piece lane of 32; then 8 rows on)
+    // (128-byte aligned; piece i lies at place i ^ (r & 7)), its columns of the
+    // operand, its piece of x (row warp, piece lane of 32; then 8 rows on)
     const uint32_t code0 = static_cast<uint32_t>(r * 128 + (((4 * c) ^ (r & 7)) << 4));
-    const uint32_t dst0 = sbase + static_cast<uint32_t>((2 * c * R + r) * 128 + ((r & 7) << 4));
+    const uint32_t dst0 = tmem_base + W4T_ACC_COLS + 64 * c + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t piece0 = static_cast<uint32_t>((lane >> 3) * (NTOK * 128) + warp * 128 +
                                                   (((lane & 7) ^ warp) << 4));
     const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + warp * W4_STAGE_K + lane * 8);
@@ -246,10 +235,9 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
       if (!wait(full_bar(s), phase, WAIT_MMA_FULL)) break;
       const uint32_t st = ring + s * w4t_code_stage(R);
       uint4 code[4];
-      if (works) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = lds128(st + (code0 ^ static_cast<uint32_t>(i << 4)));
-      }
+      for (int i = 0; i < 4; ++i)
+        code[i] = works ? lds128(st + (code0 ^ static_cast<uint32_t>(i << 4))) : make_uint4(0, 0, 0, 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(s));
       if (++s == S) {
@@ -275,22 +263,28 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
         sx = 0;
         x_phase ^= 1u;
       }
-      // the set's last multiplication, two stages ago, has ended
-      if (it >= 2 && !wait(done_bar(it - 2), done_parity(it - 2), WAIT_PRODUCER_EMPTY)) break;
-      if (works) {
+      fence_proxy_async_smem();  // x, for the MMAs
+      // the operand's last multiplication, two stages ago, has ended
+      if (it >= 2) {
+        if (!wait(done_bar(it - 2), done_parity(it - 2), WAIT_PRODUCER_EMPTY)) break;
+        tc_fence_after();
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t zi = z[i * ZS / 4];
+      for (int i = 0; i < 4; i += 2) {
+        uint32_t o[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t zi = z[(i + h) * ZS / 4];
           const uint32_t zz = (ZLO | zi) * 0x00010001u;
           const uint32_t zh = (0xd400u | (zi << 4)) * 0x00010001u;  // -(64 + z), binary16
-          const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-          const uint32_t to = dst0 + (it & 1) * a_set + (i >> 1) * (R * 128);
+          const uint32_t w[4] = {code[i + h].x, code[i + h].y, code[i + h].z, code[i + h].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            sts128(to ^ static_cast<uint32_t>((4 * (i & 1) + k) << 4), widen_word<BF>(p, w[k], zz, zh));
+          for (int k = 0; k < 4; ++k) widen_word<BF>(p, w[k], zz, zh, o + 16 * h + 4 * k);
         }
+        tmem_st_32x32b_x32(dst0 + (it & 1) * 128 + 16 * i, o);
       }
-      fence_proxy_async_smem();
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ready_bar(it));
     }
@@ -323,7 +317,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
       if (!wait(done_bar(it), done_parity(it), WAIT_EPI_TMEM_FULL)) break;
       tc_fence_after();
       const uint32_t t_acc =
-          tmem_base + (it & 1) * ACC_SET + col0 + (static_cast<uint32_t>(32 * q) << 16);
+          tmem_base + it % SETS * ACC_SET + col0 + (static_cast<uint32_t>(32 * q) << 16);
       // 32 sums at a time
       constexpr int GS = COLS == 16 ? 2 : 1;  // groups
 #pragma unroll
@@ -405,18 +399,19 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     int sx = 0;
     for (int it = 0; it < stages; ++it) {
       if (!wait(ready_bar(it), pair_parity(it), WAIT_MMA_FULL)) break;
-      if (it >= 2 && !wait(tempty_bar(it), pair_parity(it) ^ 1u, WAIT_MMA_TMEM_EMPTY)) break;
+      if (it >= SETS &&
+          !wait(tempty_bar(it), (static_cast<uint32_t>(it / SETS) & 1u) ^ 1u, WAIT_MMA_TMEM_EMPTY))
+        break;
       tc_fence_after();
-      const uint64_t ad = sdesc_k_major_sw128(sbase + (it & 1) * a_set);
+      const uint32_t at = tmem_base + W4T_ACC_COLS + (it & 1) * 128;
       const uint64_t xd = sdesc_k_major_sw128(x_ring + sx * X_STAGE);
-      const uint32_t d = tmem_base + (it & 1) * ACC_SET;
+      const uint32_t d = tmem_base + it % SETS * ACC_SET;
       if (leader) {
-        // steps of 16 columns, 4 an operand tile, G / 16 a group
+        // steps of 16 columns (8 of tensor memory), G / 16 a group
 #pragma unroll
         for (int k = 0; k < W4_STAGE_K / 16; ++k)
-          mma_f16(d + k / (G / 16) * NTOK,
-                  ad + static_cast<uint64_t>((k >> 2) * (R * 128) >> 4) + 2 * (k & 3),
-                  xd + static_cast<uint64_t>((k >> 2) * (NTOK * 128) >> 4) + 2 * (k & 3), IDESC,
+          mma_f16_ts(d + k / (G / 16) * NTOK, at + 8 * k,
+                     xd + static_cast<uint64_t>((k >> 2) * (NTOK * 128) >> 4) + 2 * (k & 3), IDESC,
                   k % (G / 16) == 0 ? 0u : 1u);
         mma_commit(done_bar(it));
       }
@@ -435,7 +430,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   __syncthreads();
   if (warp == ISSUER) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    tmem_dealloc(tmem_base, 512);
   }
   const int pitch = W4T_MAX_ROWS + 4;
   if (warp >= W4T_WIDEN && warp < PRODUCER) {
