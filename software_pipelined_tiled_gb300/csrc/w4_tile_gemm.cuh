@@ -14,12 +14,14 @@
 // A CTA takes up to 128 rows of weights and a range of K (shared in a cluster,
 // as in w4_gemm.cuh). Roles:
 //
-//   8 warps  widen: a lane turns 64 bytes of codes of its row (128 of a stage's
-//            256 columns) into its lane of the operand in tensor memory; before
-//            that the warps pair up the stage's x (and widen 8-bit x) in place
+//   16 warps widen, in two groups that take the stages in turn (8 past 16 rows of
+//            x, for want of registers): a lane turns 64 bytes of codes of its
+//            row (128 of a stage's 256 columns) into its lane of the operand
 //   4 warps  (8 with 64 rows of x) sums: a lane owns a row of weights; for each
 //            group it reads the group's sums from tensor memory, multiplies them
 //            by its scale and adds them to its own, in 32 bits
+//   4 warps  pair up a stage's x (and widen 8-bit x) in place, ahead of the others
+//            (the fence between their writes and the MMAs' reads is slow)
 //   2 warps  producers of the two rings, codes and x, by tensor copy
 //   1 warp   MMA issuer: a stage's 16 steps of 16 columns, one accumulator a
 //            group
@@ -47,11 +49,12 @@
 namespace sptg {
 
 constexpr int W4T_MAX_ROWS = 128;
-constexpr int W4T_WIDEN = 8;                       // widening warps
+constexpr int W4T_PAIR = 4;  // warps that pair up x
+__host__ __device__ constexpr int w4t_widen(int ntok) { return ntok == 16 ? 16 : 8; }
 constexpr int W4T_MAX_STAGES = 10;
 __host__ __device__ constexpr int w4t_sum_warps(int ntok) { return ntok == 64 ? 8 : 4; }
 __host__ __device__ constexpr int w4t_threads(int ntok) {
-  return 32 * (W4T_WIDEN + w4t_sum_warps(ntok) + 3);
+  return 32 * (w4t_widen(ntok) + w4t_sum_warps(ntok) + W4T_PAIR + 3);
 }
 
 // Tensor memory: 256 columns of accumulators, one for each group of a stage and
@@ -67,7 +70,7 @@ __host__ __device__ constexpr int w4t_x_stage(int xk, int ntok) {
   return w4t_x_bytes(ntok) + (xk >= W4_S8 ? ntok * W4_STAGE_K : 0);
 }
 constexpr int W4T_MAX_X_STAGES = 4;
-constexpr int W4T_BARS = 2 * W4T_MAX_STAGES + W4T_MAX_X_STAGES + 4 + 2 + 2 + 1;
+constexpr int W4T_BARS = 2 * W4T_MAX_STAGES + 2 * W4T_MAX_X_STAGES + 4 + 2 + 2 + 1;
 __host__ __device__ constexpr int w4t_bars_at(int xk, int ntok, int rows, int stages, int x_stages) {
   const int rings = stages * w4t_code_stage(rows) + x_stages * w4t_x_stage(xk, ntok);
   const int red = ntok * (W4T_MAX_ROWS + 4) * 4;
@@ -118,7 +121,9 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   constexpr int GROUPS = W4_STAGE_K / G;
   constexpr uint32_t IDESC = idesc_f16_f32acc(BF, 128, NTOK);
   constexpr int SUMS = w4t_sum_warps(NTOK);
-  constexpr int PRODUCER = W4T_WIDEN + SUMS, X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
+  constexpr int WIDEN = w4t_widen(NTOK);
+  constexpr int PAIR = WIDEN + SUMS, PRODUCER = PAIR + W4T_PAIR;  // first warps of the roles
+  constexpr int X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
   constexpr int COLS = NTOK == 64 ? 32 : NTOK;  // rows of x a sums warp holds
   constexpr int ACC_SET = GROUPS * NTOK;  // columns of a stage's accumulators
   constexpr int SETS = 2 * ACC_SET <= W4T_ACC_COLS ? 2 : 1;
@@ -138,10 +143,11 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (W4T_MAX_STAGES + s); };
   const uint32_t bar1 = bar0 + 8u * (2 * W4T_MAX_STAGES);
   auto xfull_bar = [&](int s) { return bar1 + 8u * s; };
-  const uint32_t bar2 = bar1 + 8u * W4T_MAX_X_STAGES;
+  auto xready_bar = [&](int s) { return bar1 + 8u * (W4T_MAX_X_STAGES + s); };  // paired
+  const uint32_t bar2 = bar1 + 8u * (2 * W4T_MAX_X_STAGES);
   auto done_bar = [&](int it) { return bar2 + 8u * (it & 3); };         // stage multiplied
   auto done_parity = [](int it) { return static_cast<uint32_t>(it >> 2) & 1u; };
-  auto ready_bar = [&](int it) { return bar2 + 8u * (4 + (it & 1)); };  // widened, x paired
+  auto ready_bar = [&](int it) { return bar2 + 8u * (4 + (it & 1)); };  // widened
   auto tempty_bar = [&](int it) { return bar2 + 8u * (6 + it % SETS); };  // sums read
   auto pair_parity = [](int it) { return static_cast<uint32_t>(it >> 1) & 1u; };
   const uint32_t drain_bar = bar0 + 8u * (W4T_BARS - 1);
@@ -162,12 +168,15 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), W4T_WIDEN);
+      mbar_init(empty_bar(s), 8);  // a group of widening warps
     }
-    for (int s = 0; s < SX; ++s) mbar_init(xfull_bar(s), 1);
+    for (int s = 0; s < SX; ++s) {
+      mbar_init(xfull_bar(s), 1);
+      mbar_init(xready_bar(s), W4T_PAIR);
+    }
     for (int i = 0; i < 4; ++i) mbar_init(done_bar(i), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(ready_bar(i), W4T_WIDEN);
+      mbar_init(ready_bar(i), 8);
       mbar_init(tempty_bar(i), SUMS);
     }
     mbar_init(drain_bar, 1);
@@ -194,11 +203,13 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
 #pragma unroll
   for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
 
-  if (warp < W4T_WIDEN) {
+  if (warp < WIDEN) {
     // ---------------------------------------------------------------- widen
     // Thread: row r (= its lane of tensor memory), columns 128 c ... + 127 of a
     // stage.
-    const int r = threadIdx.x & 127, c = threadIdx.x >> 7;
+    constexpr int GRPS = WIDEN / 8;
+    const int group = warp >> 3;
+    const int r = threadIdx.x & 127, c = (threadIdx.x >> 7) & 1;
     const bool works = r < R;
     const uint8_t* zp = p.zeros ? p.zeros + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG : nullptr;
     constexpr uint32_t ZLO = BF ? 0x4300u : 0x6400u;
@@ -213,25 +224,22 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
           next_z[i] = __ldg(zp + min((ks * W4_STAGE_K + 128 * c) / G + i, KG - 1));
       }
     };
-    load_zeros(ks0);
+    load_zeros(min(ks0 + group, ks1 - 1));
     // places that do not change from stage to stage: this lane's row of codes
-    // (128-byte aligned; piece i lies at place i ^ (r & 7)), its columns of the
-    // operand, its piece of x (row warp, piece lane of 32; then 8 rows on)
+    // (128-byte aligned; piece i lies at place i ^ (r & 7)) and its columns of
+    // the operand
     const uint32_t code0 = static_cast<uint32_t>(r * 128 + (((4 * c) ^ (r & 7)) << 4));
     const uint32_t dst0 = tmem_base + W4T_ACC_COLS + 64 * c + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t piece0 = static_cast<uint32_t>((lane >> 3) * (NTOK * 128) + warp * 128 +
-                                                  (((lane & 7) ^ warp) << 4));
-    const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + warp * W4_STAGE_K + lane * 8);
-    int s = 0, sx = 0;
-    uint32_t phase = 0, x_phase = 0;
-    for (int it = 0; it < stages; ++it) {
+    int s = group;  // (at least two stages)
+    uint32_t phase = 0;
+    for (int it = group; it < stages; it += GRPS) {
       uint32_t z[ZS];
 #pragma unroll
       for (int i = 0; i < ZS; ++i) {
         asm volatile("" : "+r"(next_z[i]));  // no use of the loads before this
         z[i] = next_z[i] & 15u;
       }
-      load_zeros(min(ks0 + it + 1, ks1 - 1));
+      load_zeros(min(ks0 + it + GRPS, ks1 - 1));
       if (!wait(full_bar(s), phase, WAIT_MMA_FULL)) break;
       const uint32_t st = ring + s * w4t_code_stage(R);
       uint4 code[4];
@@ -240,59 +248,37 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
         code[i] = works ? lds128(st + (code0 ^ static_cast<uint32_t>(i << 4))) : make_uint4(0, 0, 0, 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(s));
-      if (++s == S) {
-        s = 0;
+      s += GRPS;
+      if (s >= S) {
+        s -= S;
         phase ^= 1u;
       }
-      if (!wait(xfull_bar(sx), x_phase, WAIT_MMA_FULL)) break;
-      // pair up x: pieces of 8 columns
-      const uint32_t sxt = x_ring + sx * X_STAGE;
-#pragma unroll
-      for (int i = 0; i < NTOK; i += W4T_WIDEN) {
-        uint4 v;
-        if constexpr (X8) {
-          v.x = lds32(sxt + raw0 + i * W4_STAGE_K);
-          v.y = lds32(sxt + raw0 + i * W4_STAGE_K + 4);
-        } else {
-          v = lds128(sxt + piece0 + i * 128);
-        }
-        v = pair_x<XK>(v);  // the pairs (0,4) (2,6) (1,5) (3,7)
-        sts128(sxt + piece0 + i * 128, make_uint4(v.x, v.z, v.y, v.w));
-      }
-      if (++sx == SX) {
-        sx = 0;
-        x_phase ^= 1u;
-      }
-      fence_proxy_async_smem();  // x, for the MMAs
       // the operand's last multiplication, two stages ago, has ended
       if (it >= 2) {
         if (!wait(done_bar(it - 2), done_parity(it - 2), WAIT_PRODUCER_EMPTY)) break;
         tc_fence_after();
       }
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        uint32_t o[32];
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t zi = z[i * ZS / 4];
+        const uint32_t zz = (ZLO | zi) * 0x00010001u;
+        const uint32_t zh = (0xd400u | (zi << 4)) * 0x00010001u;  // -(64 + z), binary16
+        const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+        uint32_t o[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t zi = z[(i + h) * ZS / 4];
-          const uint32_t zz = (ZLO | zi) * 0x00010001u;
-          const uint32_t zh = (0xd400u | (zi << 4)) * 0x00010001u;  // -(64 + z), binary16
-          const uint32_t w[4] = {code[i + h].x, code[i + h].y, code[i + h].z, code[i + h].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) widen_word<BF>(p, w[k], zz, zh, o + 16 * h + 4 * k);
-        }
-        tmem_st_32x32b_x32(dst0 + (it & 1) * 128 + 16 * i, o);
+        for (int k = 0; k < 4; ++k) widen_word<BF>(p, w[k], zz, zh, o + 4 * k);
+        tmem_st_32x32b_x16(dst0 + (it & 1) * 128 + 16 * i, o);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ready_bar(it));
     }
-  } else if (warp < PRODUCER) {
+  } else if (warp < PAIR) {
     // ----------------------------------------------------------------- sums
     const int q = warp & 3;
     const int r = 32 * q + lane;
-    const int col0 = warp >= W4T_WIDEN + 4 ? COLS : 0;
+    const int col0 = warp >= WIDEN + 4 ? COLS : 0;
     const uint16_t* sp = p.scales + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG;
     // A stage's scales, a stage ahead. Groups past K have no sums but zeros.
     uint32_t next_s[GROUPS];
@@ -340,6 +326,41 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
             float& a = acc[GS == 2 ? i : 16 * h + i];
             a = fmaf(sc[GS == 2 ? g + h : g], __uint_as_float(v[h][i]), a);
           }
+      }
+    }
+  } else if (warp < PRODUCER) {
+    // ----------------------------------------------------------------- pair
+    // Pieces of 8 columns: this lane's first (row pw of x, piece lane of a
+    // stage's 32; then 4 rows on, whose place under the swizzle differs in one
+    // bit).
+    const int pw = warp - PAIR;
+    const uint32_t piece0 = static_cast<uint32_t>((lane >> 3) * (NTOK * 128) + pw * 128 +
+                                                  (((lane & 7) ^ pw) << 4));
+    const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + pw * W4_STAGE_K + lane * 8);
+    int sx = 0;
+    uint32_t phase = 0;
+    for (int it = 0; it < stages; ++it) {
+      if (!wait(xfull_bar(sx), phase, WAIT_MMA_FULL)) break;
+      const uint32_t st = x_ring + sx * X_STAGE;
+#pragma unroll
+      for (int m = 0; m < NTOK; m += W4T_PAIR) {
+        const uint32_t piece = (st + piece0 + m * 128) ^ ((m & 4) << 4);
+        uint4 v;
+        if constexpr (X8) {
+          v.x = lds32(st + raw0 + m * W4_STAGE_K);
+          v.y = lds32(st + raw0 + m * W4_STAGE_K + 4);
+        } else {
+          v = lds128(piece);
+        }
+        v = pair_x<XK>(v);  // the pairs (0,4) (2,6) (1,5) (3,7)
+        sts128(piece, make_uint4(v.x, v.z, v.y, v.w));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xready_bar(sx));
+      if (++sx == SX) {
+        sx = 0;
+        phase ^= 1u;
       }
     }
   } else if (warp == PRODUCER || warp == X_PRODUCER) {
@@ -397,7 +418,9 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     // ----------------------------------------------------------- MMA issuer
     const bool leader = elect_one_sync();
     int sx = 0;
+    uint32_t x_phase = 0;
     for (int it = 0; it < stages; ++it) {
+      if (!wait(xready_bar(sx), x_phase, WAIT_MMA_FULL)) break;
       if (!wait(ready_bar(it), pair_parity(it), WAIT_MMA_FULL)) break;
       if (it >= SETS &&
           !wait(tempty_bar(it), (static_cast<uint32_t>(it / SETS) & 1u) ^ 1u, WAIT_MMA_TMEM_EMPTY))
@@ -416,7 +439,10 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
         mma_commit(done_bar(it));
       }
       __syncwarp();
-      if (++sx == SX) sx = 0;
+      if (++sx == SX) {
+        sx = 0;
+        x_phase ^= 1u;
+      }
     }
     if (leader) mma_commit(drain_bar);
     __syncwarp();
@@ -433,8 +459,8 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     tmem_dealloc(tmem_base, 512);
   }
   const int pitch = W4T_MAX_ROWS + 4;
-  if (warp >= W4T_WIDEN && warp < PRODUCER) {
-    const int col0 = warp >= W4T_WIDEN + 4 ? COLS : 0;
+  if (warp >= WIDEN && warp < PAIR) {
+    const int col0 = warp >= WIDEN + 4 ? COLS : 0;
     float* red = reinterpret_cast<float*>(smem) + col0 * pitch + 32 * (warp & 3) + lane;
 #pragma unroll
     for (int i = 0; i < COLS; ++i) red[i * pitch] = acc[i];
