@@ -353,7 +353,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   const int64_t k_stages = (K + W4_STAGE_K - 1) / W4_STAGE_K;
   rc = ensure_smem(dev, fn, 232448);  // the ring's size differs from call to call
   if (rc) return rc;
-  const int threads = tile ? w4t_threads(nt) : 32 * W4_MAX_WARPS;
+  const int threads = tile ? w4t_threads(xk, nt) : 32 * W4_MAX_WARPS;
   const W4Slots slots = w4_slots(dev, fn, tile ? 1 : W4_CTAS_PER_SM, threads, di.sm_count);
   const W4Shape shape = w4_shape(N, k_stages, 64, tile ? W4T_MAX_ROWS : W4_MAX_ROWS,
                                  m_blocks, slots.n);
@@ -415,6 +415,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   p.wide = K % W4_STAGE_K == 0 && aligned16(scales) && (reinterpret_cast<uintptr_t>(zeros) & 7u) == 0;
   p.mask_lo = 0x000f000fu;
   p.mask_hi = 0x00f000f0u;
+  p.mask_tile = x_type == SPTG_T_BF16 ? p.mask_lo : 0x00f0000fu;
   p.magic = x_type == SPTG_T_BF16 ? 0x43004300u : 0x64006400u;
   p.error_word = di.error_word;
   p.timeout_ns = kOpTimeoutNs;

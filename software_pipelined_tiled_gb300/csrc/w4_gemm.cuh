@@ -90,6 +90,7 @@ struct W4Params {
   int out_bf16;            // type of scales and out: bfloat16, else binary16
   int wide;                // scales (and zeros) read a lane's groups at a time
   uint32_t mask_lo, mask_hi, magic;  // of spread_codes
+  uint32_t mask_tile;                // of widen_word
   unsigned int* error_word;
   uint64_t timeout_ns;
 };

@@ -20,8 +20,8 @@
 //   4 warps  (8 with 64 rows of x) sums: a lane owns a row of weights; for each
 //            group it reads the group's sums from tensor memory, multiplies them
 //            by its scale and adds them to its own, in 32 bits
-//   4 warps  pair up a stage's x (and widen 8-bit x) in place, ahead of the others
-//            (the fence between their writes and the MMAs' reads is slow)
+//   4 warps  widen a stage's x where it is 8-bit, ahead of the others (the fence
+//            between their writes and the MMAs' reads is slow)
 //   2 warps  producers of the two rings, codes and x, by tensor copy
 //   1 warp   MMA issuer: a stage's 16 steps of 16 columns, one accumulator a
 //            group
@@ -39,9 +39,6 @@
 // the 16-bit type of the product; products are exact, sums are kept in 32 bits,
 // and the group's scale multiplies the group's 32-bit sum. Y is rounded once.
 // (Scaling the widened weights instead would round each of them.)
-//
-// Order within K: eight columns of a 16-byte piece lie as 0 4 1 5 2 6 3 7, in
-// both operands (a word of codes gives the pairs (0, 4), (1, 5) ... by masks).
 #pragma once
 
 #include "w4_gemm.cuh"
@@ -49,12 +46,13 @@
 namespace sptg {
 
 constexpr int W4T_MAX_ROWS = 128;
-constexpr int W4T_PAIR = 4;  // warps that pair up x
 __host__ __device__ constexpr int w4t_widen(int ntok) { return ntok == 16 ? 16 : 8; }
+// warps that widen x, where it is 8-bit
+__host__ __device__ constexpr int w4t_widen_x(int xk) { return xk >= W4_S8 ? 4 : 0; }
 constexpr int W4T_MAX_STAGES = 10;
 __host__ __device__ constexpr int w4t_sum_warps(int ntok) { return ntok == 64 ? 8 : 4; }
-__host__ __device__ constexpr int w4t_threads(int ntok) {
-  return 32 * (w4t_widen(ntok) + w4t_sum_warps(ntok) + W4T_PAIR + 3);
+__host__ __device__ constexpr int w4t_threads(int xk, int ntok) {
+  return 32 * (w4t_widen(ntok) + w4t_sum_warps(ntok) + w4t_widen_x(xk) + 3);
 }
 
 // Tensor memory: 256 columns of accumulators, one for each group of a stage and
@@ -80,40 +78,57 @@ __host__ __device__ constexpr int w4t_smem(int xk, int ntok, int rows, int stage
   return w4t_bars_at(xk, ntok, rows, stages, x_stages) + W4T_BARS * 8 + 16 + 1024;
 }
 
-// The eight codes of a word, less the zero point (exact), as four columns of the
-// operand. zz: pairs of the zero point under the same exponent;
-// binary16 takes two of the shifts off the integer pipe with a multiply-add
-// ((1024 + 16 code) / 16 - (64 + z)).
+// The eight codes of a word in order, less the zero point (exact), as four
+// columns of the operand: a byte permutation brings two neighbours to the low
+// byte of either half, a mask and the exponent's bits make numbers of them.
+// bfloat16 has room for a code in the low four bits only (128 + code; the odd
+// ones come from the word moved down four bits); binary16 takes the odd ones
+// where they are, as 1024 + 16 code, and a multiply-add makes (1, 1 / 16) of
+// them. zz: what to take off, (-)(bias + zero point) in either half.
 template <bool BF>
-__device__ __forceinline__ void widen_word(const W4Params& p, uint32_t w, uint32_t zz, uint32_t zh,
-                                           uint32_t* o) {
-  if constexpr (BF) {
+__device__ __forceinline__ void widen_word(const W4Params& p, uint32_t w, uint32_t zz, uint32_t* o) {
+  const uint32_t odd = BF ? w >> 4 : w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = pick(w >> (4 * i), p.mask_lo, p.magic);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = pick(__byte_perm(w, odd, (4 + i) << 8 | i), p.mask_tile, p.magic);
+    if constexpr (BF) {
       const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
                                        *reinterpret_cast<const __nv_bfloat162*>(&zz));
       o[i] = *reinterpret_cast<const uint32_t*>(&d);
-    }
-  } else {
-    const uint32_t sixteenth = 0x2c002c00u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t lo = pick(w >> (8 * i), p.mask_lo, p.magic);
-      const uint32_t hi = pick(w >> (8 * i), p.mask_hi, p.magic);
-      const __half2 dl = __hsub2(*reinterpret_cast<const __half2*>(&lo),
-                                 *reinterpret_cast<const __half2*>(&zz));
-      const __half2 dh = __hfma2(*reinterpret_cast<const __half2*>(&hi),
-                                 *reinterpret_cast<const __half2*>(&sixteenth),
-                                 *reinterpret_cast<const __half2*>(&zh));
-      o[2 * i] = *reinterpret_cast<const uint32_t*>(&dl);
-      o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&dh);
+    } else {
+      const uint32_t one_sixteenth = 0x2c003c00u;
+      const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v),
+                                *reinterpret_cast<const __half2*>(&one_sixteenth),
+                                *reinterpret_cast<const __half2*>(&zz));
+      o[i] = *reinterpret_cast<const uint32_t*>(&d);
     }
   }
 }
 
+// Eight 8-bit values of x, widened to binary16 in order.
+template <int XK>
+__device__ __forceinline__ uint4 widen_x(uint32_t lo, uint32_t hi) {
+  uint32_t o[4];
+  if constexpr (XK == W4_S8) {
+    // as in pair_x: 1024 + b + 128, less 1152
+    const uint32_t b[2] = {lo ^ 0x80808080u, hi ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = unbias2(__byte_perm(b[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t q = (i & 2 ? hi : lo) >> (16 * (i & 1));
+      const __half2_raw r =
+          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q & 0xffffu), __NV_E4M3);
+      o[i] = static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 template <int XK, int NTOK, int G>
-__global__ void __launch_bounds__(w4t_threads(NTOK), 1)
+__global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
     w4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const W4Params p) {
   constexpr bool BF = XK == W4_BF16;
@@ -122,7 +137,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   constexpr uint32_t IDESC = idesc_f16_f32acc(BF, 128, NTOK);
   constexpr int SUMS = w4t_sum_warps(NTOK);
   constexpr int WIDEN = w4t_widen(NTOK);
-  constexpr int PAIR = WIDEN + SUMS, PRODUCER = PAIR + W4T_PAIR;  // first warps of the roles
+  constexpr int WIDEN_X = WIDEN + SUMS, PRODUCER = WIDEN_X + w4t_widen_x(XK);  // first warps of the roles
   constexpr int X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
   constexpr int COLS = NTOK == 64 ? 32 : NTOK;  // rows of x a sums warp holds
   constexpr int ACC_SET = GROUPS * NTOK;  // columns of a stage's accumulators
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (W4T_MAX_STAGES + s); };
   const uint32_t bar1 = bar0 + 8u * (2 * W4T_MAX_STAGES);
   auto xfull_bar = [&](int s) { return bar1 + 8u * s; };
-  auto xready_bar = [&](int s) { return bar1 + 8u * (W4T_MAX_X_STAGES + s); };  // paired
+  auto xready_bar = [&](int s) { return bar1 + 8u * (W4T_MAX_X_STAGES + s); };  // widened
   const uint32_t bar2 = bar1 + 8u * (2 * W4T_MAX_X_STAGES);
   auto done_bar = [&](int it) { return bar2 + 8u * (it & 3); };         // stage multiplied
   auto done_parity = [](int it) { return static_cast<uint32_t>(it >> 2) & 1u; };
@@ -172,7 +187,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     }
     for (int s = 0; s < SX; ++s) {
       mbar_init(xfull_bar(s), 1);
-      mbar_init(xready_bar(s), W4T_PAIR);
+      if (X8) mbar_init(xready_bar(s), w4t_widen_x(XK));
     }
     for (int i = 0; i < 4; ++i) mbar_init(done_bar(i), 1);
     for (int i = 0; i < 2; ++i) {
@@ -212,7 +227,6 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     const int r = threadIdx.x & 127, c = (threadIdx.x >> 7) & 1;
     const bool works = r < R;
     const uint8_t* zp = p.zeros ? p.zeros + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG : nullptr;
-    constexpr uint32_t ZLO = BF ? 0x4300u : 0x6400u;
     constexpr int ZS = 128 / G;  // zero points of a lane's columns
     uint32_t next_z[ZS];
 #pragma unroll
@@ -261,12 +275,12 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t zi = z[i * ZS / 4];
-        const uint32_t zz = (ZLO | zi) * 0x00010001u;
-        const uint32_t zh = (0xd400u | (zi << 4)) * 0x00010001u;  // -(64 + z), binary16
+        // 128 + z twice; or -(1024 + z) and -(64 + z)
+        const uint32_t zz = BF ? (0x4300u | zi) * 0x00010001u : 0xd400e400u | zi | zi << 20;
         const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
         uint32_t o[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) widen_word<BF>(p, w[k], zz, zh, o + 4 * k);
+        for (int k = 0; k < 4; ++k) widen_word<BF>(p, w[k], zz, o + 4 * k);
         tmem_st_32x32b_x16(dst0 + (it & 1) * 128 + 16 * i, o);
       }
       tmem_wait_st();
@@ -274,7 +288,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ready_bar(it));
     }
-  } else if (warp < PAIR) {
+  } else if (warp < WIDEN_X) {
     // ----------------------------------------------------------------- sums
     const int q = warp & 3;
     const int r = 32 * q + lane;
@@ -329,38 +343,31 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
       }
     }
   } else if (warp < PRODUCER) {
-    // ----------------------------------------------------------------- pair
-    // Pieces of 8 columns: this lane's first (row pw of x, piece lane of a
-    // stage's 32; then 4 rows on, whose place under the swizzle differs in one
-    // bit).
-    const int pw = warp - PAIR;
-    const uint32_t piece0 = static_cast<uint32_t>((lane >> 3) * (NTOK * 128) + pw * 128 +
-                                                  (((lane & 7) ^ pw) << 4));
-    const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + pw * W4_STAGE_K + lane * 8);
-    int sx = 0;
-    uint32_t phase = 0;
-    for (int it = 0; it < stages; ++it) {
-      if (!wait(xfull_bar(sx), phase, WAIT_MMA_FULL)) break;
-      const uint32_t st = x_ring + sx * X_STAGE;
+    // -------------------------------------------------------------- widen x
+    if constexpr (X8) {
+      // Pieces of 8 columns: this lane's first (row pw of x, piece lane of a
+      // stage's 32; then 4 rows on, whose place under the swizzle differs in
+      // one bit).
+      const int pw = warp - WIDEN_X;
+      const uint32_t piece0 = static_cast<uint32_t>((lane >> 3) * (NTOK * 128) + pw * 128 +
+                                                    (((lane & 7) ^ pw) << 4));
+      const uint32_t raw0 = static_cast<uint32_t>(OFF_RAW + pw * W4_STAGE_K + lane * 8);
+      int sx = 0;
+      uint32_t phase = 0;
+      for (int it = 0; it < stages; ++it) {
+        if (!wait(xfull_bar(sx), phase, WAIT_MMA_FULL)) break;
+        const uint32_t st = x_ring + sx * X_STAGE;
 #pragma unroll
-      for (int m = 0; m < NTOK; m += W4T_PAIR) {
-        const uint32_t piece = (st + piece0 + m * 128) ^ ((m & 4) << 4);
-        uint4 v;
-        if constexpr (X8) {
-          v.x = lds32(st + raw0 + m * W4_STAGE_K);
-          v.y = lds32(st + raw0 + m * W4_STAGE_K + 4);
-        } else {
-          v = lds128(piece);
+        for (int m = 0; m < NTOK; m += 4)
+          sts128((st + piece0 + m * 128) ^ ((m & 4) << 4),
+                 widen_x<XK>(lds32(st + raw0 + m * W4_STAGE_K), lds32(st + raw0 + m * W4_STAGE_K + 4)));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xready_bar(sx));
+        if (++sx == SX) {
+          sx = 0;
+          phase ^= 1u;
         }
-        v = pair_x<XK>(v);  // the pairs (0,4) (2,6) (1,5) (3,7)
-        sts128(piece, make_uint4(v.x, v.z, v.y, v.w));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(xready_bar(sx));
-      if (++sx == SX) {
-        sx = 0;
-        phase ^= 1u;
       }
     }
   } else if (warp == PRODUCER || warp == X_PRODUCER) {
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     int sx = 0;
     uint32_t x_phase = 0;
     for (int it = 0; it < stages; ++it) {
-      if (!wait(xready_bar(sx), x_phase, WAIT_MMA_FULL)) break;
+      if (!wait(X8 ? xready_bar(sx) : xfull_bar(sx), x_phase, WAIT_MMA_FULL)) break;
       if (!wait(ready_bar(it), pair_parity(it), WAIT_MMA_FULL)) break;
       if (it >= SETS &&
           !wait(tempty_bar(it), (static_cast<uint32_t>(it / SETS) & 1u) ^ 1u, WAIT_MMA_TMEM_EMPTY))
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
     tmem_dealloc(tmem_base, 512);
   }
   const int pitch = W4T_MAX_ROWS + 4;
-  if (warp >= WIDEN && warp < PAIR) {
+  if (warp >= WIDEN && warp < WIDEN_X) {
     const int col0 = warp >= WIDEN + 4 ? COLS : 0;
     float* red = reinterpret_cast<float*>(smem) + col0 * pitch + 32 * (warp & 3) + lane;
 #pragma unroll
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(w4t_threads(NTOK), 1)
   // the CTAs in order.
   const int rows = R / p.splits;
   const int live_m = min(NTOK, p.M - m0);
-  for (int i = threadIdx.x; i < rows * live_m; i += w4t_threads(NTOK)) {
+  for (int i = threadIdx.x; i < rows * live_m; i += w4t_threads(XK, NTOK)) {
     const int m = i / rows, r = rank * rows + i % rows;
     const uint32_t at = sbase + static_cast<uint32_t>((m * pitch + r) * 4);
     float v = 0.0f;
