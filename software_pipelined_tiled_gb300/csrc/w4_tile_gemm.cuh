@@ -46,13 +46,17 @@
 namespace sptg {
 
 constexpr int W4T_MAX_ROWS = 128;
-__host__ __device__ constexpr int w4t_widen(int ntok) { return ntok == 16 ? 16 : 8; }
+// Warps that widen the weights: 16, but 8 where other warps leave them too few
+// registers (32 rows and more, with x in 8 bits or groups of 32).
+__host__ __device__ constexpr int w4t_widen(int xk, int ntok, int group) {
+  return ntok > 16 && (xk >= W4_S8 || group == 32) ? 8 : 16;
+}
 // warps that widen x, where it is 8-bit
 __host__ __device__ constexpr int w4t_widen_x(int xk) { return xk >= W4_S8 ? 4 : 0; }
 constexpr int W4T_MAX_STAGES = 10;
 __host__ __device__ constexpr int w4t_sum_warps(int ntok) { return ntok == 64 ? 8 : 4; }
-__host__ __device__ constexpr int w4t_threads(int xk, int ntok) {
-  return 32 * (w4t_widen(ntok) + w4t_sum_warps(ntok) + w4t_widen_x(xk) + 3);
+__host__ __device__ constexpr int w4t_threads(int xk, int ntok, int group) {
+  return 32 * (w4t_widen(xk, ntok, group) + w4t_sum_warps(ntok) + w4t_widen_x(xk) + 3);
 }
 
 // Tensor memory: 256 columns of accumulators, one for each group of a stage and
@@ -128,7 +132,7 @@ __device__ __forceinline__ uint4 widen_x(uint32_t lo, uint32_t hi) {
 }
 
 template <int XK, int NTOK, int G>
-__global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
+__global__ void __launch_bounds__(w4t_threads(XK, NTOK, G), 1)
     w4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const W4Params p) {
   constexpr bool BF = XK == W4_BF16;
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
   constexpr int GROUPS = W4_STAGE_K / G;
   constexpr uint32_t IDESC = idesc_f16_f32acc(BF, 128, NTOK);
   constexpr int SUMS = w4t_sum_warps(NTOK);
-  constexpr int WIDEN = w4t_widen(NTOK);
+  constexpr int WIDEN = w4t_widen(XK, NTOK, G);
   constexpr int WIDEN_X = WIDEN + SUMS, PRODUCER = WIDEN_X + w4t_widen_x(XK);  // first warps of the roles
   constexpr int X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
   constexpr int COLS = NTOK == 64 ? 32 : NTOK;  // rows of x a sums warp holds
@@ -318,29 +322,22 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
       tc_fence_after();
       const uint32_t t_acc =
           tmem_base + it % SETS * ACC_SET + col0 + (static_cast<uint32_t>(32 * q) << 16);
-      // 32 sums at a time
-      constexpr int GS = COLS == 16 ? 2 : 1;  // groups
+      // 16 sums at a time: with 32 in flight the registers would not do
 #pragma unroll
-      for (int g = 0; g < GROUPS; g += GS) {
-        uint32_t v[2][16];
-        const int c1 = GS == 2 ? NTOK : 16;
-        tmem_ld_32x32b_x16(t_acc + g * NTOK, v[0]);
-        tmem_ld_32x32b_x16(t_acc + g * NTOK + c1, v[1]);
-        tmem_wait_ld_regs16(v[0]);
-        tmem_wait_ld_regs16(v[1]);
-        if (g + GS == GROUPS) {  // all have been read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tempty_bar(it));
-        }
+      for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float& a = acc[GS == 2 ? i : 16 * h + i];
-            a = fmaf(sc[GS == 2 ? g + h : g], __uint_as_float(v[h][i]), a);
+        for (int h = 0; h < COLS; h += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(t_acc + g * NTOK + h, v);
+          tmem_wait_ld_regs16(v);
+          if (g == GROUPS - 1 && h == COLS - 16) {  // all have been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(it));
           }
-      }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[h + i] = fmaf(sc[g], __uint_as_float(v[i]), acc[h + i]);
+        }
     }
   } else if (warp < PRODUCER) {
     // -------------------------------------------------------------- widen x
@@ -481,7 +478,7 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
   // the CTAs in order.
   const int rows = R / p.splits;
   const int live_m = min(NTOK, p.M - m0);
-  for (int i = threadIdx.x; i < rows * live_m; i += w4t_threads(XK, NTOK)) {
+  for (int i = threadIdx.x; i < rows * live_m; i += w4t_threads(XK, NTOK, G)) {
     const int m = i / rows, r = rank * rows + i % rows;
     const uint32_t at = sbase + static_cast<uint32_t>((m * pitch + r) * 4);
     float v = 0.0f;
