@@ -218,29 +218,47 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
 
 // ---------------------------------------------------------- 4-bit weights
 // Rows of weights per CTA and CTAs sharing K (a cluster). For each cluster
-// size the rows are cut so that the CTAs fill the GPU's slots once to four
-// times (fewer in clusters of 4 and 8, which have to find their SMs in one
-// processing cluster), within `least` to `most`; the choice with the least
-// time of its busiest slot wins, counted in bytes of codes with 32 KB for
-// starting a CTA and 16 KB for a cluster's exchange.
+// size the rows are cut so that the CTAs fill the GPU once to eight times, within
+// `least` to `most`; the choice whose busiest SM has the least to do wins, in
+// bytes of codes. The CTAs of the streaming kernel, two to an SM, share its rate:
+// fewer and taller ones, one to an SM, do as well and start half as often (one row
+// through 16384 x 4096: 148 of 112 rows 12.4 us, 256 of 64 rows 14.8 us), as long
+// as an SM has twelve warps or so (128 of 64 rows, eight warps each, through
+// 8192 x 8192: 19.2 us; 148 of 112 rows 13.2 us) and x need not be loaded in parts,
+// between which a CTA waits (8 rows: 148 CTAs 16.5 us, 296 of half K 15.2 us). Clusters of 4 and 8 are placed
+// two CTAs to an SM even where SMs are free (one row through 4096 x 4096: 148 CTAs
+// of 112 rows 7.3 us, 256 of 64 rows 5.5 us). The tile kernel takes a stage in the
+// same time whatever its rows. Starting a round of CTAs counts as 32 KB, a cluster's
+// exchange as 16 KB.
 struct W4Shape {
   int rows, splits;
 };
 
-W4Shape w4_shape(int64_t N, int64_t k_stages, int64_t least, int64_t most, int64_t m_blocks,
+W4Shape w4_shape(int64_t N, int64_t k_stages, bool tile, int64_t m_blocks, int64_t segment,
                  const int* slots) {
-  constexpr int64_t step = 16;
+  constexpr int64_t step = 16, least = 64;
+  const int64_t most = tile ? W4T_MAX_ROWS : W4_MAX_ROWS;
+  const int per_sm = tile ? 1 : W4_CTAS_PER_SM;
   W4Shape best{static_cast<int>(most), 1};
   double best_t = 1e300;
   for (int i = 0; i < 4 && (1 << i) <= k_stages; ++i) {
     const int splits = 1 << i;
-    for (int64_t waves = 1; waves <= 4; ++waves) {
-      const int64_t fit = (N * splits * m_blocks + slots[i] * waves - 1) / (slots[i] * waves);
+    for (int64_t fills = 1; fills <= 8; ++fills) {
+      const int64_t room = slots[i] * fills / per_sm;
+      const int64_t fit = (N * splits * m_blocks + room - 1) / room;
       const int64_t rows = std::min(most, std::max(least, (fit + step - 1) / step * step));
       const int64_t ctas = (N + rows - 1) / rows * splits * m_blocks;
-      const double rounds = static_cast<double>((ctas + slots[i] - 1) / slots[i]);
-      const double t = rounds * (static_cast<double>((k_stages + splits - 1) / splits) * rows * 128 +
-                                 32768 + (splits > 1 ? 16384 : 0));
+      const int64_t rounds = (ctas + slots[i] - 1) / slots[i];
+      // CTAs that the busiest SM gets, and warps at a time
+      int64_t on_sm = (ctas * per_sm + slots[i] - 1) / slots[i];
+      if (splits > 2) on_sm = rounds * per_sm;
+      const int64_t warps = rows / W4_WARP_ROWS * W4_KW * std::min<int64_t>(on_sm, per_sm);
+      const int64_t slice = (k_stages + splits - 1) / splits;
+      double stage = (tile ? W4T_MAX_ROWS : rows) * 128.0;
+      if (!tile && warps < 12) stage *= 12.0 / static_cast<double>(warps);
+      if (!tile && on_sm == 1 && slice > segment) stage *= 1.25;
+      const double t = static_cast<double>(on_sm * slice) * stage +
+                       static_cast<double>(rounds) * (32768 + (splits > 1 ? 16384 : 0));
       if (t < best_t * 0.999) {
         best_t = t;
         best = {static_cast<int>(rows), splits};
@@ -325,7 +343,9 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   }
   // Up to 8 rows of x: the streaming kernel. More: the tensor-core tile kernel
   // with 16, 32 or 64 rows, in blocks of 64 (groups of 32 columns: of 32) that
-  // each pass over the weights.
+  // each pass over the weights. Through 8192 x 8192 (bf16, groups of 128) the
+  // streaming kernel takes 13.2 us for one row and 15.3 us for 8, the tile kernel
+  // 15.3 us for up to 16; through 4096 x 4096 5.5, 7.2 and 9.0 us.
   const bool tile = M > 8;
   const int nt = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : w4t_max_ntok(group);
   const int64_t m_blocks = (M + nt - 1) / nt;
@@ -355,8 +375,12 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   if (rc) return rc;
   const int threads = tile ? w4t_threads(xk, nt, group) : 32 * W4_MAX_WARPS;
   const W4Slots slots = w4_slots(dev, fn, tile ? 1 : W4_CTAS_PER_SM, threads, di.sm_count);
-  const W4Shape shape = w4_shape(N, k_stages, 64, tile ? W4T_MAX_ROWS : W4_MAX_ROWS,
-                                 m_blocks, slots.n);
+  // Stages of x that two fifths of a streaming CTA's shared memory hold.
+  const int budget = (224 << 10) / W4_CTAS_PER_SM - 1024;
+  const int live_m = static_cast<int>(std::min<int64_t>(M, W4_X_ROWS));
+  const int x_stage = live_m * W4_STAGE_K * 2 + W4_STAGE_K / group * W4_X_ROWS * 4;
+  const int x_stages = (budget * 2 / 5) / x_stage;
+  const W4Shape shape = w4_shape(N, k_stages, tile, m_blocks, x_stages, slots.n);
   const int rows = shape.rows, splits = shape.splits;
   const int64_t n_tiles = (N + rows - 1) / rows;
   if (n_tiles * splits > INT32_MAX) return refuse(SPTG_ERR_ARG, "too many columns");
@@ -369,15 +393,11 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
     while (p.stages > 2 && w4t_smem(xk, nt, rows, p.stages, p.segment) > 232448) --p.stages;
     smem = w4t_smem(xk, nt, rows, p.stages, p.segment);
   } else {
-    // Shared memory: rings of at least two stages, x of a segment in at most
-    // two fifths of the rest (a segment is a multiple of the parts of K that
-    // warps take), the rings with what is left.
-    const int budget = (224 << 10) / W4_CTAS_PER_SM - 1024;
-    const int live_m = static_cast<int>(M);
+    // Rings of at least two stages, a segment of x (a multiple of the parts
+    // of K that warps take), the rings with what is left.
     const int kw = W4_KW;
     const int slice = static_cast<int>((k_stages + splits - 1) / splits);
-    const int x_stage = live_m * W4_STAGE_K * 2 + W4_STAGE_K / group * 8 * 4;
-    p.segment = std::max(kw, (budget * 2 / 5) / x_stage / kw * kw);
+    p.segment = std::max(kw, x_stages / kw * kw);
     p.segment = std::min(p.segment, (slice + kw - 1) / kw * kw);
     while (p.segment > kw && w4_layout(group, rows, 2, p.segment, live_m).total > budget)
       p.segment -= kw;
