@@ -351,8 +351,8 @@ int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type o
  * products give. |X| stays below 2^120.)
  * group is 32, 64 or 128 and divides K. X and codes are 16-byte aligned with
  * row pitches of a multiple of 16 bytes (SPTG_ERR_ALIGN); N, M and ldy are
- * free. Up to 64 rows of X share one pass over the weights; more rows take
- * ceil(M / 64) passes. M == 0 or N == 0: nothing is done. K == 0: Y is zero.
+ * free. Up to 64 rows of X (with groups of 32: up to 32) share one pass over
+ * the weights; more rows take as many passes as needed. M == 0 or N == 0: nothing is done. K == 0: Y is zero.
  */
 int sptg_gemm_w4(int64_t M, int64_t N, int64_t K, int group, sptg_type x_type, sptg_type out_type,
                  const void* X, int64_t ldx, const float* x_scales, const uint8_t* codes,

@@ -225,11 +225,11 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
 // through 16384 x 4096: 148 of 112 rows 12.4 us, 256 of 64 rows 14.8 us), as long
 // as an SM has twelve warps or so (128 of 64 rows, eight warps each, through
 // 8192 x 8192: 19.2 us; 148 of 112 rows 13.2 us) and x need not be loaded in parts,
-// between which a CTA waits (8 rows: 148 CTAs 16.5 us, 296 of half K 15.2 us). Clusters of 4 and 8 are placed
-// two CTAs to an SM even where SMs are free (one row through 4096 x 4096: 148 CTAs
-// of 112 rows 7.3 us, 256 of 64 rows 5.5 us). The tile kernel takes a stage in the
-// same time whatever its rows. Starting a round of CTAs counts as 32 KB, a cluster's
-// exchange as 16 KB.
+// between which a CTA waits (8 rows: 148 CTAs 16.5 us, 296 of half K 15.2 us).
+// Clusters of 4 and 8 are placed two CTAs to an SM even where SMs are free (one row
+// through 4096 x 4096: 148 CTAs of 112 rows 7.3 us, 256 of 64 rows 5.5 us). The tile
+// kernel takes a stage in the same time whatever its rows. Starting a round of CTAs
+// counts as 32 KB, a cluster's exchange as 16 KB.
 struct W4Shape {
   int rows, splits;
 };
@@ -345,7 +345,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   // with 16, 32 or 64 rows, in blocks of 64 (groups of 32 columns: of 32) that
   // each pass over the weights. Through 8192 x 8192 (bf16, groups of 128) the
   // streaming kernel takes 13.2 us for one row and 15.3 us for 8, the tile kernel
-  // 15.3 us for up to 16; through 4096 x 4096 5.5, 7.2 and 9.0 us.
+  // 15.2 us for up to 16; through 4096 x 4096 5.5, 7.1 and 7.2 us.
   const bool tile = M > 8;
   const int nt = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : w4t_max_ntok(group);
   const int64_t m_blocks = (M + nt - 1) / nt;
@@ -497,7 +497,10 @@ int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, con
     return SPTG_OK;
   }
   // Tiles up to 64 rows wide (and a deeper ring of weights) where the experts
-  // have few rows on average.
+  // have few rows on average, else up to 256. Products of 2048 x 2048 bf16 weights,
+  // with 64 and 256: 8 experts of 16 rows on average 14.9 and 15.9 us, of 32 15.2
+  // and 16.6 us, of 64 20.5 and 17.7 us; 64 experts of 16 rows 79.9 and 86.5 us,
+  // of 32 87.1 and 88.3 us, of 64 95.1 and 91.5 us, of 128 139 and 102 us.
   const int tt = (!dw && T <= 32 * E) ? 64 : 256;
   const int64_t F = mode == GROUPED_DX ? K : N;
   const int64_t nf = (F + 255) / 256;

@@ -28,7 +28,9 @@
 // (stages of 256 columns: 128 bytes a row, 128-byte swizzled) and refills a stage
 // when it has read it, so that no warp ever waits for another inside a segment.
 //
-// Measured: one binary16 row through 32768 x 8192, groups of 64 with zero
+// Measured: one bf16 row through 4096 x 4096, 8192 x 8192, 16384 x 4096 and
+// 32768 x 8192 in groups of 128 5.5, 13.2, 12.6 and 34.8 us back to back, 8 rows
+// 7.1, 15.3 and 46.3 us through the first two and the last. One binary16 row through 32768 x 8192, groups of 64 with zero
 // points, 36.4 us (4.0 TB/s; the floor at 6783 GB/s is 21.7 us). The copies
 // alone take 23.4 us; what remains is bound by the issue of about 32
 // instructions for 16 x 32 codes and the scales' own. A ring shared by the CTA,
