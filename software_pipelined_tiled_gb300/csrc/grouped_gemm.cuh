@@ -41,6 +41,13 @@
 // 2-9 epilogue, warp 10 the rows left over (dW only). Two accumulators of up to 256 columns,
 // so a tile's epilogue overlaps the next tile's K-loop.
 //
+// Measured (bf16, 16 experts of 4096 x 4096, 16384 rows): Y and dX 305 us (1800
+// TFLOP/s of the 1926 that a dense product was measured at), dW 319 us: tensor-bound. 8192
+// rows through 64 experts of 2048 x 4096: Y 185 us, 6.2 TB/s of weights, rows and
+// output: memory-bound, as are 32 rows through the experts they reach (Y 31 us). A
+// few hundred rows, 1531 in 24 ragged experts of 1112 x 2056: Y and dX 30 and 27 us,
+// dW with f32 output 55 us, most of it the writing of 220 MB.
+//
 // The epilogue reads its whole share of an accumulator into registers and hands
 // it back before it converts and stores. That of Y and dX writes the transpose
 // of the accumulator: a lane holds one feature, its columns are rows of the
@@ -124,6 +131,19 @@ __device__ __forceinline__ uint64_t sdesc_mn_major_sw128(uint32_t saddr, uint32_
 // (the widths of 112 and more that the square kernel's pair tiles use).
 __host__ __device__ constexpr int grouped_mma_n(int n) {
   return n <= 96 ? (n + 31) & ~31 : (n + 15) & ~15;
+}
+
+// Pieces of 64 of a sum that one accumulator takes (a power of two). The tensor
+// core cuts off what an addition shifts out, so an error grows with the length of
+// a sum and has one sign: relative 4.7e-6 after 4000 rows of binary16. A 16-bit
+// output does not show it (2e-4); for a 32-bit output the accumulator is read after
+// 512 of the sum (256 in sums up to 1024) and the parts are added up, rounded to
+// nearest, in the epilogue's registers: 6e-7 at any length, where 32-bit additions
+// one by one leave 1.1e-6. 16384 rows of 16 experts, 4096 x 4096, f32 out: Y 340 us
+// against 330 with one accumulator, dW 444 against 380 (with 256 throughout 443 and
+// 513: while the epilogue stores a tile the next one has two accumulators to go on).
+__device__ __forceinline__ int grouped_span(int out, int chunks) {
+  return out != OUT_F32 ? 1 << 26 : chunks > 16 ? 8 : 4;
 }
 
 // One tile of work.
@@ -389,17 +409,25 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       for (int tile = worker; ok && tile < total; tile += workers) {
         const GroupedTile w = sched.at(tile);
         if (w.zeros()) continue;
-        const uint32_t b = unit & 1u;
-        if (!__all_sync(0xffffffffu, wait_bounded_lazy(tempty_bar(b), ((unit >> 1) & 1u) ^ 1u, ctl,
-                                                  WAIT_MMA_TMEM_EMPTY))) {
-          ok = false;
-          break;
-        }
-        ++unit;
-        tc_fence_after();
-        const uint32_t d = tmem_base + b * 256;
+        uint32_t b, d;
+        auto next_accumulator = [&]() {
+          b = unit & 1u;
+          d = tmem_base + b * 256;
+          ok = __all_sync(0xffffffffu, wait_bounded_lazy(tempty_bar(b), ((unit >> 1) & 1u) ^ 1u, ctl,
+                                                         WAIT_MMA_TMEM_EMPTY));
+          ++unit;
+          tc_fence_after();
+          return ok;
+        };
+        if (!next_accumulator()) break;
+        const int span = grouped_span(OUT, w.chunks);
         const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
         for (int c = 0; c < w.chunks; ++c) {
+          if (c > 0 && (c & (span - 1)) == 0) {
+            if (leader) mma_commit_g<true>(tfull_bar(b));
+            __syncwarp();
+            if (!next_accumulator()) break;
+          }
           if (!__all_sync(0xffffffffu, wait_bounded_lazy(full_bar(s), phase, ctl, WAIT_MMA_FULL))) {
             ok = false;
             break;
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             // lines of an MN-major tile (in units of 16 bytes)
             constexpr uint64_t ADV_A = A_MN ? 128 : 2, ADV_B = B_MN ? 128 : 2;
             const int steps = c == w.chunks - 1 ? w.steps : 4;
-            mma_f16_g<true>(d, ad, bd, idesc, c > 0 ? 1u : 0u);
+            mma_f16_g<true>(d, ad, bd, idesc, (c & (span - 1)) != 0 ? 1u : 0u);
 #pragma unroll
             for (int k = 1; k < 4; ++k)
               if (MODE != GROUPED_DW || steps > k)
@@ -462,6 +490,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     const int vr = lane / VPR, vc = lane % VPR;
     // this warp's blocks of 32 columns: dW takes two neighbours in turn
     constexpr int NB = TT / 64;
+    constexpr bool SUMS = OUT == OUT_F32;  // a tile's accumulators are added up here
     auto block_col = [&](int i) {
       return MODE == GROUPED_DW ? (i >> 1) * 128 + part * 64 + (i & 1) * 32 : 64 * i + 32 * part;
     };
@@ -470,29 +499,47 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
       const GroupedTile w = sched.at(tile);
       const int f = w.f0 + 128 * static_cast<int>(rank) + 32 * q;  // this warp's first feature
       uint32_t r[NB][32];
-      if (!w.zeros()) {
-        const uint32_t b = unit & 1u;
-        if (!__all_sync(0xffffffffu, wait_bounded_lazy(tfull_bar(b), (unit >> 1) & 1u, ctl,
-                                                       WAIT_EPI_TMEM_FULL)))
-          break;
-        ++unit;
-        tc_fence_after();
-        const uint32_t t_acc = tmem_base + b * 256 + (static_cast<uint32_t>(32 * q) << 16);
-        // (columns past the tile's width hold an earlier tile's sums, or
-        // anything: they are not stored)
-#pragma unroll
-        for (int i = 0; i < NB; ++i) tmem_ld_32x32b_x32(t_acc + block_col(i), r[i]);
-#pragma unroll
-        for (int i = 0; i < NB; ++i) tmem_wait_ld_regs(r[i]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(b), 0u));
-      } else {
+      if (SUMS || w.zeros()) {
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
           for (int k = 0; k < 32; ++k) r[i][k] = 0;
       }
+      bool ok = true;
+      const int span = grouped_span(OUT, w.chunks);
+      for (int c = 0; !w.zeros() && (c == 0 || c < w.chunks); c += span) {
+        const uint32_t b = unit & 1u;
+        ok = __all_sync(0xffffffffu, wait_bounded_lazy(tfull_bar(b), (unit >> 1) & 1u, ctl,
+                                                       WAIT_EPI_TMEM_FULL));
+        if (!ok) break;
+        ++unit;
+        tc_fence_after();
+        const uint32_t t_acc = tmem_base + b * 256 + (static_cast<uint32_t>(32 * q) << 16);
+        // (columns past the tile's width hold an earlier tile's sums, or
+        // anything: they are not stored)
+        if constexpr (SUMS) {
+#pragma unroll
+          for (int i = 0; i < 2 * NB; ++i) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(t_acc + block_col(i >> 1) + 16 * (i & 1), v);
+            tmem_wait_ld_regs16(v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              uint32_t& sum = r[i >> 1][16 * (i & 1) + k];
+              sum = __float_as_uint(__uint_as_float(sum) + __uint_as_float(v[k]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) tmem_ld_32x32b_x32(t_acc + block_col(i), r[i]);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) tmem_wait_ld_regs(r[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(b), 0u));
+      }
+      if (!ok) break;
       if (f >= p.F) continue;
       if constexpr (MODE == GROUPED_DW) {
         // blocks of 32 features x 128 bytes, in the tensor copy's swizzle

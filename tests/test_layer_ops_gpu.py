@@ -523,3 +523,86 @@ def test_norm_of_many_rows(rows, cols, out_dtype):
     w = 1 + rand(g, cols, dtype=dtype, std=0.2)
     check_norm(x, r, w, out_dtype or dtype)
     check_norm(x, r, w, out_dtype or dtype, h=r)  # in place
+
+
+# Long sums with a 32-bit output. All terms are positive, so every rounding toward zero adds up: a
+# part of 512 takes 32 steps of the tensor core, each rounding its running sum at most twice by a unit
+# of 2^-23; with the running sum growing evenly that is 32 units of 2^-23 of the part. The parts are
+# rounded to nearest as they are added: half a unit each, twelve parts at most.
+@pytest.mark.parametrize("length", [900, 1024, 1025, 4100, 6000])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_grouped_long_sums_in_32_bits(length, dtype):
+    g = gen(length)
+    bound = 32 * 2.0 ** -23 + 12 * 2.0 ** -24
+    n, k, sizes = 72, 200, [3, length, 20]
+    t = sum(sizes)
+    off = offsets_of(sizes)
+
+    def positive(*shape):
+        return (torch.rand(*shape, device="cuda", generator=g) + 0.5).to(dtype)
+
+    X, dY = positive(t, k), positive(t, n)
+    dw = sptg.grouped_gemm_dw(dY, X, off, out_dtype=F32)
+    ref = dY[3:3 + length].double().t() @ X[3:3 + length].double()
+    assert ((dw[1].double() - ref).abs() <= bound * ref).all()
+    long_k = length // 8 * 8
+    for rows in (20, 300):
+        off = offsets_of([rows, rows])
+        X, W = positive(2 * rows, long_k), positive(2, n, long_k)
+        y = sptg.grouped_gemm(X, W, off, out_dtype=F32)
+        ref = torch.cat([X[:rows].double() @ W[0].double().t(), X[rows:].double() @ W[1].double().t()])
+        assert ((y.double() - ref).abs() <= bound * ref).all()
+        dY, W = positive(2 * rows, long_k), positive(2, long_k, n)
+        dx = sptg.grouped_gemm_dx(dY, W, off, out_dtype=F32)
+        ref = torch.cat([dY[:rows].double() @ W[0].double(), dY[rows:].double() @ W[1].double()])
+        assert ((dx.double() - ref).abs() <= bound * ref).all()
+
+
+# Offsets past 32 bits: the last rows of tensors of more than 2^31 elements.
+def test_norm_past_two_to_the_31():
+    rows, cols = (1 << 31) // 8192 + 40, 8192
+    x = torch.zeros(rows, cols, device="cuda", dtype=BF16)
+    r = torch.zeros(rows, cols, device="cuda", dtype=BF16)
+    g = gen(31)
+    x[-30:], r[-30:], w = rand(g, 30, cols), rand(g, 30, cols), rand(g, cols)
+    h, y, scales = sptg.add_rms_norm(x, r, w, out_dtype=S8)
+    assert (scales[:-30] == 0).all()
+    # check_norm's bounds
+    t, v = norm_reference(x[-30:], r[-30:], w, 1e-6)
+    rel, a = (cols + 32) * 2.0 ** -24, v.abs().amax(1)
+    assert ((h[-30:].double() - t).abs() <= U[BF16] * t.abs() * (1 + 2.0 ** -10)).all()
+    assert ((scales[-30:].double() - a / 127.0).abs() <= rel * a / 127.0).all()
+    exact = v / (a[:, None] / 127.0)
+    assert ((y[-30:].double() - exact).abs() <= 0.5 * (1 + 2.0 ** -10) + 2 * rel * exact.abs()).all()
+
+
+@pytest.mark.parametrize("m", [1, 16])
+def test_w4_past_two_to_the_31(m):
+    g = gen(m)
+    k, group = 8192, 128
+    n = (1 << 32) // k + 200  # more than 2^31 bytes of codes
+    codes = torch.zeros(n, k // 2, device="cuda", dtype=torch.uint8)
+    scales = torch.zeros(n, k // group, device="cuda", dtype=BF16)
+    x, c, s, _, _ = w4_inputs(g, m, 150, k, group, BF16, BF16, False)
+    codes[-150:], scales[-150:] = c, s
+    y = sptg.gemm_w4(x, codes, scales)
+    ref, S = w4_reference(x, c, s, None, None)
+    assert_close(y[:, -150:], ref, S, k)
+    assert (y[:, :-150] == 0).all()
+
+
+def test_grouped_past_two_to_the_31():
+    g = gen(5)
+    e, n, k = 36, 8192, 8192
+    W = torch.zeros(e, n, k, device="cuda", dtype=BF16)
+    W[-1] = rand(g, n, k, std=0.05)
+    off = offsets_of([0] * (e - 1) + [40])
+    X, dY = rand(g, 40, k), rand(g, 40, n)
+    y, dx = sptg.grouped_gemm(X, W, off), sptg.grouped_gemm_dx(dY, W, off)
+    w = W[-1].double()
+    assert_close(y, X.double() @ w.t(), X.double().abs() @ w.abs().t(), k)
+    assert_close(dx, dY.double() @ w, dY.double().abs() @ w.abs(), n)
+    del W, w
+    dw = sptg.grouped_gemm_dw(dY, X, off)
+    assert (dw[:-1] == 0).all()
+    assert_close(dw[-1], dY.double().t() @ X.double(), dY.double().abs().t() @ X.double().abs(), 40)
