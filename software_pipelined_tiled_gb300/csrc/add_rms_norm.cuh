@@ -17,8 +17,9 @@
 // kept beside that of |h w| to tell an overflow from an infinity.
 //
 // Memory-bound: 7 bytes an element (x, r in; h, q out) and some ten flops. The
-// row stays in registers between the reduction and the outputs, so x and r are
-// read once.
+// row stays in registers (wide rows: in shared memory) between the reduction and
+// the outputs, so x and r are read once. 16384 bf16 rows of 8192 to 8 bits: 152 us,
+// 6.2 TB/s; of 4096, 72 us; 333 rows of 5000: bound by the call from the host.
 #pragma once
 
 #include <cstdint>

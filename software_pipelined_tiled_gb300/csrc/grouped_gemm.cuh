@@ -43,10 +43,10 @@
 //
 // Measured (bf16, 16 experts of 4096 x 4096, 16384 rows): Y and dX 305 us (1800
 // TFLOP/s of the 1926 that a dense product was measured at), dW 319 us: tensor-bound. 8192
-// rows through 64 experts of 2048 x 4096: Y 185 us, 6.2 TB/s of weights, rows and
-// output: memory-bound, as are 32 rows through the experts they reach (Y 31 us). A
-// few hundred rows, 1531 in 24 ragged experts of 1112 x 2056: Y and dX 30 and 27 us,
-// dW with f32 output 55 us, most of it the writing of 220 MB.
+// binary16 rows through 64 experts of 2048 x 4096: Y 185 us, 6.3 TB/s of weights,
+// rows and output: memory-bound, as are 32 rows through those of 16 experts of 4096 x
+// 2048 that they reach (Y 31 us). 1531 binary16 rows in 24 ragged experts of 1112 x
+// 2056, f32 out: Y 33 us, dW 55 us, most of it the writing of 220 MB; dX 27 us.
 //
 // The epilogue reads its whole share of an accumulator into registers and hands
 // it back before it converts and stores. That of Y and dX writes the transpose
