@@ -373,7 +373,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   const int64_t k_stages = (K + W4_STAGE_K - 1) / W4_STAGE_K;
   rc = ensure_smem(dev, fn, 232448);  // the ring's size differs from call to call
   if (rc) return rc;
-  const int threads = tile ? w4t_threads(xk, nt, group) : 32 * W4_MAX_WARPS;
+  const int threads = tile ? w4t_threads(xk, nt) : 32 * W4_MAX_WARPS;
   const W4Slots slots = w4_slots(dev, fn, tile ? 1 : W4_CTAS_PER_SM, threads, di.sm_count);
   // Stages of x that two fifths of a streaming CTA's shared memory hold.
   const int budget = (224 << 10) / W4_CTAS_PER_SM - 1024;

@@ -17,7 +17,7 @@
 //   16 warps widen, in two groups that take the stages in turn (8 in one group
 //            where registers are short): a lane turns 64 bytes of codes of its
 //            row (128 of a stage's 256 columns) into its lane of the operand
-//   4 warps  (8 with 64 rows of x) sums: a lane owns a row of weights; for each
+//   4 warps  (8 past 16 rows of x) sums: a lane owns a row of weights; for each
 //            group it reads the group's sums from tensor memory, multiplies them
 //            by its scale and adds them to its own, in 32 bits
 //   4 warps  widen a stage's x where it is 8-bit, ahead of the others (the fence
@@ -38,8 +38,11 @@
 // turn ahead of any warp that waits on it (two issuers in turn would allow that).
 //
 // Measured (bf16, groups of 128): 16, 32 and 64 rows through 32768 x 8192 46.7,
-// 57.6 and 64.4 us (the codes alone are 20 us at 6783 GB/s), 16 and 32 through
-// 8192 x 8192 15.2 and 17.6 us; 61 rows through 5001 x 4128 in groups of 32 20.3 us.
+// 52.1 and 64.4 us (the codes alone are 20 us at 6783 GB/s), through 8192 x 8192 15.2,
+// 17.3 and 20.5 us; 61 rows through 5001 x 4128 in groups of 32 19.0 us. Scales and
+// zero points read a lane's groups at a time, where alignment allows it, are worth
+// most in small groups: 16 rows through 8192 x 8192 in groups of 32 with zero points
+// 17.2 us against 25.5 us.
 // Not memory-bound (2.9 TB/s with 16 rows): a stage takes some 1200 cycles, of which
 // the widening (11 to 13 instructions for 8 codes and lane, most of them on the
 // integer pipe: 63 % of its cycles, as many of the issue slots) and the chain widen,
@@ -59,18 +62,19 @@ namespace sptg {
 
 constexpr int W4T_MAX_ROWS = 128;
 // Warps that widen the weights: 16, but 8 where other warps leave them too few
-// registers (32 rows and more, with x in 8 bits or groups of 32). 64 rows of bf16
-// through 32768 x 8192: 64.4 us with 16 and 69.5 us with 8; 61 rows through 5001 x
-// 4128 in groups of 32: 24.4 and 20.3 us.
-__host__ __device__ constexpr int w4t_widen(int xk, int ntok, int group) {
-  return ntok > 16 && (xk >= W4_S8 || group == 32) ? 8 : 16;
+// registers (32 rows and more of 8-bit x). 64 rows of bf16 through 32768 x 8192:
+// 64.4 us with 16 and 69.5 us with 8.
+__host__ __device__ constexpr int w4t_widen(int xk, int ntok) {
+  return ntok > 16 && xk >= W4_S8 ? 8 : 16;
 }
 // warps that widen x, where it is 8-bit
 __host__ __device__ constexpr int w4t_widen_x(int xk) { return xk >= W4_S8 ? 4 : 0; }
 constexpr int W4T_MAX_STAGES = 10;
-__host__ __device__ constexpr int w4t_sum_warps(int ntok) { return ntok == 64 ? 8 : 4; }
-__host__ __device__ constexpr int w4t_threads(int xk, int ntok, int group) {
-  return 32 * (w4t_widen(xk, ntok, group) + w4t_sum_warps(ntok) + w4t_widen_x(xk) + 3);
+// Warps for the sums: 8 share 32 rows of x and more (32 rows of binary16 through
+// 32768 x 8192: 52.1 us against 57.7 us with 4).
+__host__ __device__ constexpr int w4t_sum_warps(int ntok) { return ntok >= 32 ? 8 : 4; }
+__host__ __device__ constexpr int w4t_threads(int xk, int ntok) {
+  return 32 * (w4t_widen(xk, ntok) + w4t_sum_warps(ntok) + w4t_widen_x(xk) + 3);
 }
 
 // Tensor memory: 256 columns of accumulators, one for each group of a stage and
@@ -144,7 +148,7 @@ __device__ __forceinline__ void widen_word(const W4Params& p, uint32_t w, uint32
 }
 
 template <int XK, int NTOK, int G>
-__global__ void __launch_bounds__(w4t_threads(XK, NTOK, G), 1)
+__global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
     w4_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const W4Params p) {
   constexpr bool BF = XK == W4_BF16;
@@ -152,10 +156,10 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK, G), 1)
   constexpr int GROUPS = W4_STAGE_K / G;
   constexpr uint32_t IDESC = idesc_f16_f32acc(BF, 128, NTOK);
   constexpr int SUMS = w4t_sum_warps(NTOK);
-  constexpr int WIDEN = w4t_widen(XK, NTOK, G);
+  constexpr int WIDEN = w4t_widen(XK, NTOK);
   constexpr int WIDEN_X = WIDEN + SUMS, PRODUCER = WIDEN_X + w4t_widen_x(XK);  // first warps of the roles
   constexpr int X_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
-  constexpr int COLS = NTOK == 64 ? 32 : NTOK;  // rows of x a sums warp holds
+  constexpr int COLS = NTOK * 4 / SUMS;  // rows of x a sums warp holds
   constexpr int ACC_SET = GROUPS * NTOK;  // columns of a stage's accumulators
   constexpr int SETS = 2 * ACC_SET <= W4T_ACC_COLS ? 2 : 1;
   static_assert(ACC_SET <= W4T_ACC_COLS, "accumulators exceed their part of tensor memory");
@@ -248,10 +252,15 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK, G), 1)
 #pragma unroll
     for (int i = 0; i < ZS; ++i) next_z[i] = 8u;
     auto load_zeros = [&](int ks) {
-      if (zp) {
+      if (!zp) return;
+      const int at = (ks * W4_STAGE_K + 128 * c) / G;
+      if (ZS == 4 && p.wide) {
+        next_z[0] = __ldg(reinterpret_cast<const uint32_t*>(zp + at));
+      } else if (ZS == 2 && p.wide) {
+        next_z[0] = __ldg(reinterpret_cast<const uint16_t*>(zp + at));
+      } else {
 #pragma unroll
-        for (int i = 0; i < ZS; ++i)
-          next_z[i] = __ldg(zp + min((ks * W4_STAGE_K + 128 * c) / G + i, KG - 1));
+        for (int i = 0; i < ZS; ++i) next_z[i] = __ldg(zp + min(at + i, KG - 1));
       }
     };
     load_zeros(min(ks0 + group, ks1 - 1));
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK, G), 1)
 #pragma unroll
       for (int i = 0; i < ZS; ++i) {
         asm volatile("" : "+r"(next_z[i]));  // no use of the loads before this
-        z[i] = next_z[i] & 15u;
+        z[i] = (ZS > 1 && p.wide && zp ? next_z[0] >> (8 * i) : next_z[i]) & 15u;
       }
       load_zeros(min(ks0 + it + GRPS, ks1 - 1));
       if (!wait(full_bar(s), phase, WAIT_MMA_FULL)) break;
@@ -312,24 +321,41 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK, G), 1)
     const int r = 32 * q + lane;
     const int col0 = warp >= WIDEN + 4 ? COLS : 0;
     const uint16_t* sp = p.scales + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG;
-    // A stage's scales, a stage ahead. Groups past K have no sums but zeros.
+    // A stage's scales, a stage ahead; where alignment allows it in one load, two
+    // to a register. Groups past K have no sums but zeros.
     uint32_t next_s[GROUPS];
     auto load_scales = [&](int ks) {
+      if (p.wide) {
+        const uint16_t* at = sp + ks * GROUPS;
+        if constexpr (GROUPS == 8)
+          asm volatile("ld.global.nc.L2::128B.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(next_s[0]), "=r"(next_s[1]), "=r"(next_s[2]), "=r"(next_s[3])
+                       : "l"(at));
+        else if constexpr (GROUPS == 4)
+          asm volatile("ld.global.nc.L2::128B.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(next_s[0]), "=r"(next_s[1])
+                       : "l"(at));
+        else
+          asm volatile("ld.global.nc.L2::128B.b32 %0, [%1];" : "=r"(next_s[0]) : "l"(at));
+      } else {
 #pragma unroll
-      for (int i = 0; i < GROUPS; ++i)
-        asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];"
-                     : "=r"(next_s[i])
-                     : "l"(sp + min(ks * GROUPS + i, KG - 1)));
+        for (int i = 0; i < GROUPS; ++i)
+          asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];"
+                       : "=r"(next_s[i])
+                       : "l"(sp + min(ks * GROUPS + i, KG - 1)));
+      }
     };
     load_scales(ks0);
     for (int it = 0; it < stages; ++it) {
       float sc[GROUPS];
       const bool bf = BF || (XK != W4_F16 && p.out_bf16);
 #pragma unroll
+      for (int i = 0; i < GROUPS; ++i) asm volatile("" : "+r"(next_s[i]));  // no use before this
+#pragma unroll
       for (int i = 0; i < GROUPS; ++i) {
-        asm volatile("" : "+r"(next_s[i]));  // no use of the loads before this
-        sc[i] = bf ? __uint_as_float(next_s[i] << 16)
-                   : __half2float(__ushort_as_half(static_cast<unsigned short>(next_s[i])));
+        const uint32_t h = p.wide ? next_s[i >> 1] >> (16 * (i & 1)) : next_s[i];
+        sc[i] = bf ? __uint_as_float(h << 16)
+                   : __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
       }
       load_scales(min(ks0 + it + 1, ks1 - 1));
       if (!wait(done_bar(it), done_parity(it), WAIT_EPI_TMEM_FULL)) break;
@@ -495,7 +521,7 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK, G), 1)
   // the CTAs in order.
   const int rows = R / p.splits;
   const int live_m = min(NTOK, p.M - m0);
-  for (int i = threadIdx.x; i < rows * live_m; i += w4t_threads(XK, NTOK, G)) {
+  for (int i = threadIdx.x; i < rows * live_m; i += w4t_threads(XK, NTOK)) {
     const int m = i / rows, r = rank * rows + i % rows;
     const uint32_t at = sbase + static_cast<uint32_t>((m * pitch + r) * 4);
     float v = 0.0f;
