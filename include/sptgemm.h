@@ -352,7 +352,8 @@ int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type o
  * group is 32, 64 or 128 and divides K. X and codes are 16-byte aligned with
  * row pitches of a multiple of 16 bytes (SPTG_ERR_ALIGN); N, M and ldy are
  * free. Up to 64 rows of X (with groups of 32: up to 32) share one pass over
- * the weights; more rows take as many passes as needed. M == 0 or N == 0: nothing is done. K == 0: Y is zero.
+ * the weights; more rows take as many passes as needed. M == 0 or N == 0:
+ * nothing is done. K == 0: Y is zero.
  */
 int sptg_gemm_w4(int64_t M, int64_t N, int64_t K, int group, sptg_type x_type, sptg_type out_type,
                  const void* X, int64_t ldx, const float* x_scales, const uint8_t* codes,
@@ -377,7 +378,8 @@ int sptg_gemm_w4(int64_t M, int64_t N, int64_t K, int group, sptg_type x_type, s
  * X, Y, dY, dX: T rows with row pitches in elements; W and dW: E x N x K,
  * dense (N rows of K for each expert, as the weights of sptg_gemm are stored).
  * dtype: a float pair of sptg_dtype; its first type is that of X, W and dY, its
- * second that of the output. Alignment as for sptg_gemm: 16-byte aligned
+ * second that of the output. Sums are fp32; for an fp32 output they are formed
+ * in parts of up to 512 terms that are added up rounded to nearest. Alignment as for sptg_gemm: 16-byte aligned
  * bases; N and K, and each pitch, a multiple of 16 bytes in the types they
  * count. E <= 1024.
  */
