@@ -47,7 +47,7 @@
 // the widening (11 to 13 instructions for 8 codes and lane, most of them on the
 // integer pipe: 63 % of its cycles, as many of the issue slots) and the chain widen,
 // hand over, 16 MMAs (some 500 cycles to issue), commit take about the same. The
-// tensor pipe is busy 8 % (16 rows) to 22 % (64 rows) of the time. A third operand
+// tensor pipe is busy 7 % (16 rows) to 20 % (64 rows) of the time. A third operand
 // (51.5 to 50.6 us) and sleeping instead of polling (no difference) were not kept.
 //
 // Exactness: a widened weight is the integer code - zero point, |.| <= 15, in
