@@ -141,9 +141,12 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[
           "f"(c[2]), "f"(c[3]));
 }
 
+// Loads from shared memory. The memory clobber keeps them between the wait for
+// what they read and the hand-over that lets it be overwritten; `volatile` alone
+// does not.
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 
@@ -151,7 +154,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -163,7 +167,7 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
 
 __device__ __forceinline__ float2 lds64f(uint32_t addr) {
   float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 
@@ -530,9 +534,9 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
         const uint32_t addr = from + static_cast<uint32_t>(k * W4_X_ROWS * pitch * 4);
         float a;
         if (p.splits > 1)
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(addr));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(addr) : "memory");
         else
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(a) : "r"(addr));
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(a) : "r"(addr) : "memory");
         v += a;
       }
     }

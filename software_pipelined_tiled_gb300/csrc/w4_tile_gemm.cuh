@@ -31,8 +31,8 @@
 // the stage's MMAs without a branch and commits once, on a barrier that the
 // widening warps (their operand is free), the producer of x (its stage is) and
 // the sums (theirs are ready) all wait on. Two operands, and two sets of
-// accumulators where they fit, alternate from stage to stage. Codes leave their
-// ring as soon as they are in registers, so that ring is all bytes in flight; x
+// accumulators where they fit, alternate from stage to stage. A stage of codes
+// leaves its ring when the codes have been written into the operand; x
 // stays in its own until it has been multiplied. There is one issuer, in the order
 // of the stages: a barrier that is waited on by its parity may then not run a whole
 // turn ahead of any warp that waits on it (two issuers in turn would allow that).
@@ -285,13 +285,6 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         code[i] = works ? lds128(st + (code0 ^ static_cast<uint32_t>(i << 4))) : make_uint4(0, 0, 0, 0);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty_bar(s));
-      s += GRPS;
-      if (s >= S) {
-        s -= S;
-        phase ^= 1u;
-      }
       // the operand's last multiplication, two stages ago, has ended
       if (it >= 2) {
         if (!wait(done_bar(it - 2), done_parity(it - 2), WAIT_PRODUCER_EMPTY)) break;
@@ -313,7 +306,20 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ready_bar(it));
+      // The stage of codes goes back only here, when its codes have been used: an
+      // arrival right behind the loads left the loads themselves free to run after
+      // the wait above, when the next copy had overwritten the codes (17 stages in
+      // groups of 32, whose slow sums make that wait long: every call had wrong
+      // groups). Nothing is lost by it: eight to ten stages are in flight.
+      if (lane == 0) {
+        mbar_arrive(empty_bar(s));
+        mbar_arrive(ready_bar(it));
+      }
+      s += GRPS;
+      if (s >= S) {
+        s -= S;
+        phase ^= 1u;
+      }
     }
   } else if (warp < WIDEN_X) {
     // ----------------------------------------------------------------- sums
@@ -530,9 +536,10 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
       if (p.splits > 1)
         asm volatile("ld.shared::cluster.f32 %0, [%1];"
                      : "=f"(x)
-                     : "r"(map_to_cta(at, static_cast<uint32_t>(c))));
+                     : "r"(map_to_cta(at, static_cast<uint32_t>(c)))
+                     : "memory");
       else
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
       v += x;
     }
     if (p.x_scales) v *= p.x_scales[m0 + m];
