@@ -327,6 +327,15 @@ int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type o
                       const void* weight, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
                       float* scales, void* stream);
 
+/* sptg_add_rms_norm with the timeout_ms and inject_stall fields of a
+ * configuration (the others are ignored; NULL = defaults). They concern the
+ * kernel that many wide rows take, whose copies run ahead; the others wait for
+ * nothing. */
+int sptg_add_rms_norm_ex(int64_t rows, int64_t cols, sptg_type in_type, sptg_type out_type,
+                         const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                         const void* weight, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
+                         float* scales, void* stream, const sptg_config* cfg);
+
 /*
  * Product with 4-bit weights and group scales:
  *

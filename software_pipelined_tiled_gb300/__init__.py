@@ -39,7 +39,8 @@ KERNELS = {"auto": 0, "square": 1, "skinny": 2, "skinny_cluster": 3, "skinny_row
 EXPORTS = ("sptg_gemm", "sptg_gemm_ex", "sptg_gemm_strided", "sptg_gemm_host",
            "sptg_plan_square", "sptg_plan", "sptg_status_string", "sptg_last_error",
            "sptg_last_config", "sptg_device_error", "sptg_version", "sptg_gemm_skinny_noalloc",
-           "sptg_stream_scale", "sptg_stream_scale_ex", "sptg_add_rms_norm", "sptg_gemm_w4",
+           "sptg_stream_scale", "sptg_stream_scale_ex", "sptg_add_rms_norm",
+           "sptg_add_rms_norm_ex", "sptg_gemm_w4",
            "sptg_grouped_gemm", "sptg_grouped_gemm_dx", "sptg_grouped_gemm_dw")
 
 
@@ -107,6 +108,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.sptg_plan.restype = ctypes.c_int
         lib.sptg_add_rms_norm.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int, vp, i64, vp, i64,
                                           vp, ctypes.c_float, vp, i64, vp, i64, vp, vp]
+        lib.sptg_add_rms_norm_ex.argtypes = lib.sptg_add_rms_norm.argtypes + [ctypes.POINTER(Config)]
         lib.sptg_gemm_w4.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp,
                                      i64, vp, vp, i64, vp, vp, vp, i64, vp]
         lib.sptg_grouped_gemm.argtypes = [i64, i64, i64, i64, ctypes.c_int, vp, vp, i64, vp, vp,
@@ -114,7 +116,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.sptg_grouped_gemm_dx.argtypes = lib.sptg_grouped_gemm.argtypes
         lib.sptg_grouped_gemm_dw.argtypes = [i64, i64, i64, i64, ctypes.c_int, vp, vp, i64, vp,
                                              i64, vp, vp]
-        for f in (lib.sptg_add_rms_norm, lib.sptg_gemm_w4, lib.sptg_grouped_gemm,
+        for f in (lib.sptg_add_rms_norm, lib.sptg_add_rms_norm_ex, lib.sptg_gemm_w4, lib.sptg_grouped_gemm,
                   lib.sptg_grouped_gemm_dx, lib.sptg_grouped_gemm_dw):
             f.restype = ctypes.c_int
         lib.sptg_version.argtypes = []

@@ -46,6 +46,7 @@ struct NormParams {
   int stages;  // depth of the ring kernel's ring
   unsigned int* error_word;
   uint64_t timeout_ns;
+  int inject_stall;  // test hook of the ring kernel: a block's second row is never copied
 };
 
 template <bool BF16>
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const No
   };
   if (threadIdx.x == 0)
     for (int s = 0; s < S; ++s)
-      if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < p.rows)
+      if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < p.rows && !(p.inject_stall && s == 1))
         fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
   uint4 wv[PER];
 #pragma unroll
@@ -273,10 +274,13 @@ __global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const No
   }
   int s = 0;
   uint32_t phase = 0, odd = 0;
+  bool ok = true;      // this thread has seen every row so far arrive
+  int64_t landed = 0;  // rows of this block that it has
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    // (a wait that runs out leaves its rows wrong and says so; the loop and its
-    // barriers go on)
-    wait_bounded_lazy(bar0 + 8 * s, phase, ctl, WAIT_MMA_FULL);
+    // (a wait that runs out leaves this row and the block's next ones wrong and
+    // says so; the loop and its barriers go on, without waits and copies)
+    ok = ok && wait_bounded_lazy(bar0 + 8 * s, phase, ctl, WAIT_MMA_FULL);
+    landed += ok;
     const uint4* sx = reinterpret_cast<const uint4*>(ring + 2 * s * row_bytes);
     const uint4* sr = reinterpret_cast<const uint4*>(ring + (2 * s + 1) * row_bytes);
     float h[PER][8];
@@ -291,8 +295,9 @@ __global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const No
     // (its barrier also says that the stage has been read; its buffers
     // alternate, so a fast warp's next row leaves a slow one's sums alone)
     row_reduce<false>(sum, mx, s_sum[odd], s_max[odd]);
+    // (into a place whose last copy has landed, and into no other)
     const int64_t next = row + static_cast<int64_t>(S) * gridDim.x;
-    if (threadIdx.x == 0 && next < p.rows) fetch(next, s);
+    if (threadIdx.x == 0 && ok && next < p.rows) fetch(next, s);
     const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -307,6 +312,16 @@ __global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const No
     }
   }
   grid_launch_dependents();
+  if (threadIdx.x == 0 && !ok) {
+    // let the copies in flight land before the block exits: up to S rows past
+    // those that have
+    for (int64_t i = landed; i < landed + S && blockIdx.x + i * gridDim.x < p.rows; ++i) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bar0 + 8 * static_cast<uint32_t>(i % S), static_cast<uint32_t>(i / S) & 1u) &&
+             global_timer_ns() - t0 < ctl.timeout_ns) {
+      }
+    }
+  }
 }
 
 // Rows of any width, alignment and pitch: one block to a row, element by

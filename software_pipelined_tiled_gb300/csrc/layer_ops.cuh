@@ -137,12 +137,15 @@ constexpr uint64_t kOpTimeoutNs = 2000ull * 1000000ull;
 // ------------------------------------------------------- residual and norm
 int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const void* x, int64_t ldx,
                  const void* r, int64_t ldr, const void* w, float eps, void* h, int64_t ldh,
-                 void* y, int64_t ldy, float* scales, cudaStream_t stream) {
+                 void* y, int64_t ldy, float* scales, cudaStream_t stream, const sptg_config* cfg) {
   TypeInfo in, out;
   if ((in_type != SPTG_T_F16 && in_type != SPTG_T_BF16) || !type_info(in_type, in) ||
       !type_info(out_type, out) || (out.bytes == 2 && out_type != in_type))
     return refuse(SPTG_ERR_ARG, "rows are f16 or bf16, outputs s8, e4m3 or the rows' own type");
   if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return refuse(SPTG_ERR_ARG, kDimText);
+  const int timeout_ms = cfg ? cfg->timeout_ms : 0, inject_stall = cfg ? cfg->inject_stall : 0;
+  if (timeout_ms < 0 || (inject_stall != 0 && inject_stall != 1))
+    return refuse(SPTG_ERR_ARG, "timeout_ms must not be negative, inject_stall 0 or 1");
   if (!(eps > 0.0f) || !(eps < INFINITY)) return refuse(SPTG_ERR_ARG, "eps must be positive and finite");
   if (rows == 0 || cols == 0) {
     set_config("kernel=none type=%s (empty output)", in.name, {});
@@ -205,7 +208,7 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
     if (rs) return rs;
   }
   NormParams p{x, r, w, h, y, scales, ldx, ldr, ldh, ldy, rows, static_cast<int>(cols), eps,
-               stages, di.error_word, kOpTimeoutNs};
+               stages, di.error_word, timeout_ms ? timeout_ms * 1000000ull : kOpTimeoutNs, inject_stall};
   void* args[] = {&p};
   const cudaError_t e =
       launch_op(fn, dim3(static_cast<unsigned>(grid)), threads, smem, 1, stream, args);
@@ -562,9 +565,17 @@ int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type o
                       const void* x, int64_t ldx, const void* residual, int64_t ldr,
                       const void* weight, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
                       float* scales, void* stream) {
+  return sptg_add_rms_norm_ex(rows, cols, in_type, out_type, x, ldx, residual, ldr, weight, eps, h,
+                              ldh, y, ldy, scales, stream, nullptr);
+}
+
+int sptg_add_rms_norm_ex(int64_t rows, int64_t cols, sptg_type in_type, sptg_type out_type,
+                         const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                         const void* weight, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
+                         float* scales, void* stream, const sptg_config* cfg) {
   return guarded([&] {
     return add_rms_norm(rows, cols, in_type, out_type, x, ldx, residual, ldr, weight, eps, h, ldh,
-                        y, ldy, scales, static_cast<cudaStream_t>(stream));
+                        y, ldy, scales, static_cast<cudaStream_t>(stream), cfg);
   });
 }
 

@@ -10,6 +10,8 @@ needs is worked out when a check has failed.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 import software_pipelined_tiled_gb300 as _pkg
@@ -24,7 +26,7 @@ _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 _new = torch.empty
 
 _lib = _pkg.load()
-_norm, _w4 = _lib.sptg_add_rms_norm, _lib.sptg_gemm_w4
+_norm, _norm_ex, _w4 = _lib.sptg_add_rms_norm, _lib.sptg_add_rms_norm_ex, _lib.sptg_gemm_w4
 _y, _dx, _dw = _lib.sptg_grouped_gemm, _lib.sptg_grouped_gemm_dx, _lib.sptg_grouped_gemm_dw
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _pkg._current_stream)
@@ -81,7 +83,7 @@ def _call(function, device: int, stream, args):
 
 
 def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None, y=None,
-                 scales=None, stream=None):
+                 scales=None, stream=None, config=None):
     """Residual addition and root-mean-square norm: returns (h, y, scales).
 
     ``h = x + residual`` (the new residual stream, in x's type; may be x or
@@ -89,7 +91,7 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None,
     With ``out_dtype`` torch.int8 or torch.float8_e4m3fn, ``y * scales[:, None]``
     stands for v, each row scaled to the type's largest value; by default y is v
     in x's type and scales is None.  x, residual, h and y are 2-D with
-    contiguous rows.
+    contiguous rows.  config: a Config, for its timeout_ms and inject_stall.
     """
     if x.dim() != 2 or not x.is_cuda:
         _refuse("x", x, "a 2-D CUDA tensor")
@@ -123,7 +125,10 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None,
         else:
             _dense(scales, (rows,), _F32, device, "scales")
         s = scales.data_ptr()
-    _call(_norm, device, stream, (
+    function = _norm
+    if config is not None:
+        function = lambda *args: _norm_ex(*args, ctypes.byref(config))  # noqa: E731
+    _call(function, device, stream, (
         rows, cols, in_code, code, x.data_ptr(), ldx, residual.data_ptr(), ldr, weight.data_ptr(),
         eps, h.data_ptr(), ldh, y.data_ptr(), ldy, s))
     return h, y, scales

@@ -1,0 +1,52 @@
+"""The operators around the dense products where a call is unusual: their waits, their edges and their sizes."""
+import pytest
+import torch
+
+import software_pipelined_tiled_gb300 as sptg
+from test_layer_ops_gpu import BF16, E4M3, F16, F32, S8, check_norm, gen, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    torch.cuda.synchronize()
+    assert sptg.device_error() == 0
+
+
+def chosen():
+    """The numbers of the last call's choice of kernel."""
+    return {k: int(v) for k, v in (f.split("=") for f in sptg.last_config().split() if "=" in f)
+            if v.isdigit()}
+
+
+# ------------------------------------------------------------------ the norm
+RING = 4  # the kernel with a ring of rows
+
+
+@pytest.mark.parametrize("out_dtype", [S8, BF16])
+def test_norm_wait_that_runs_out_is_reported_and_the_context_survives(out_dtype):
+    # each block's second row never arrives: its wait runs out after 100 ms, nothing is copied behind
+    # it, and what was in flight lands before the block leaves
+    g = gen(50)
+    x, r, w = rand(g, 2500, 8192), rand(g, 2500, 8192), rand(g, 8192)
+    cfg = sptg.Config()
+    cfg.timeout_ms, cfg.inject_stall = 100, 1
+    sptg.add_rms_norm(x, r, w, out_dtype=out_dtype, config=cfg)
+    assert chosen()["kind"] == RING
+    assert sptg.device_error() == -5
+    assert sptg.device_error() == 0  # the word was cleared
+    check_norm(x, r, w, out_dtype)
+    assert chosen()["kind"] == RING
+
+
+def test_norm_config_refusals():
+    x = rand(gen(51), 2, 64)
+    for bad in (dict(timeout_ms=-1), dict(inject_stall=2), dict(inject_stall=-1)):
+        cfg = sptg.Config()
+        for k, v in bad.items():
+            setattr(cfg, k, v)
+        with pytest.raises(sptg.SptgError) as e:
+            sptg.add_rms_norm(x, x, x[0], config=cfg)
+        assert e.value.status == -1
