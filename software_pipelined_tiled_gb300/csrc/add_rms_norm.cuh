@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(WARP_ROW || PER == 4 ? 128 : 1024) add_rms_nor
     const bool in = live && g < groups;
     xv[i] = in ? __ldcs(px + g) : make_uint4(0, 0, 0, 0);  // read once
     rv[i] = in ? __ldcs(pr + g) : make_uint4(0, 0, 0, 0);
-    wv[i] = in ? __ldg(pw + g) : make_uint4(0, 0, 0, 0);
+    wv[i] = in ? pw[g] : make_uint4(0, 0, 0, 0);  // (coherent: the call before may have written it)
   }
   float h[PER][8];
   float sum = 0.0f;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const No
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int g = threadIdx.x + i * blockDim.x;
-    wv[i] = g < groups ? __ldg(static_cast<const uint4*>(p.w) + g) : make_uint4(0, 0, 0, 0);
+    wv[i] = g < groups ? static_cast<const uint4*>(p.w)[g] : make_uint4(0, 0, 0, 0);
   }
   int s = 0;
   uint32_t phase = 0, odd = 0;

@@ -328,23 +328,26 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
   auto load_scales = [&](int ks) {
     const uint16_t* ps = my_scales + ks * GROUPS;
     const uint8_t* pz = my_zeros + ks * GROUPS;
-    // (rows are far apart: a whole line of each is called into L2 at once)
+    // (rows are far apart: a whole line of each is called into L2 at once. Not the
+    // non-coherent path: the call before, which may have written them, can still
+    // have been running when this kernel started)
     if (p.wide) {
       if constexpr (PG == 1)
-        asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];" : "=r"(next_s[0]) : "l"(ps));
+        asm volatile("ld.global.L2::128B.u16 %0, [%1];" : "=r"(next_s[0]) : "l"(ps) : "memory");
       else if constexpr (PG == 2)
-        asm volatile("ld.global.nc.L2::128B.b32 %0, [%1];" : "=r"(next_s[0]) : "l"(ps));
+        asm volatile("ld.global.L2::128B.b32 %0, [%1];" : "=r"(next_s[0]) : "l"(ps) : "memory");
       else
-        asm volatile("ld.global.nc.L2::128B.v2.b32 {%0, %1}, [%2];"
+        asm volatile("ld.global.L2::128B.v2.b32 {%0, %1}, [%2];"
                      : "=r"(next_s[0]), "=r"(next_s[PG / 2 - 1])
-                     : "l"(ps));
+                     : "l"(ps)
+                     : "memory");
       if (p.zeros) {
         if constexpr (PG == 1)
-          asm volatile("ld.global.nc.L2::128B.u8 %0, [%1];" : "=r"(next_z[0]) : "l"(pz));
+          asm volatile("ld.global.L2::128B.u8 %0, [%1];" : "=r"(next_z[0]) : "l"(pz) : "memory");
         else if constexpr (PG == 2)
-          asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];" : "=r"(next_z[0]) : "l"(pz));
+          asm volatile("ld.global.L2::128B.u16 %0, [%1];" : "=r"(next_z[0]) : "l"(pz) : "memory");
         else
-          asm volatile("ld.global.nc.L2::128B.b32 %0, [%1];" : "=r"(next_z[0]) : "l"(pz));
+          asm volatile("ld.global.L2::128B.b32 %0, [%1];" : "=r"(next_z[0]) : "l"(pz) : "memory");
       }
     } else {
 #pragma unroll
@@ -354,8 +357,8 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
 #pragma unroll
       for (int i = 0; i < PG; ++i) {
         if (ks * GROUPS + sgroup + i < KG) {
-          next_s[i / 2] |= static_cast<uint32_t>(__ldg(ps + i)) << (16 * (i & 1));
-          if (p.zeros) next_z[i / 4] |= static_cast<uint32_t>(__ldg(pz + i)) << (8 * (i & 3));
+          next_s[i / 2] |= static_cast<uint32_t>(ps[i]) << (16 * (i & 1));
+          if (p.zeros) next_z[i / 4] |= static_cast<uint32_t>(pz[i]) << (8 * (i & 3));
         }
       }
     }

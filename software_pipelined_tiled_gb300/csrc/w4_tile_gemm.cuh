@@ -255,12 +255,12 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
       if (!zp) return;
       const int at = (ks * W4_STAGE_K + 128 * c) / G;
       if (ZS == 4 && p.wide) {
-        next_z[0] = __ldg(reinterpret_cast<const uint32_t*>(zp + at));
+        next_z[0] = *reinterpret_cast<const uint32_t*>(zp + at);
       } else if (ZS == 2 && p.wide) {
-        next_z[0] = __ldg(reinterpret_cast<const uint16_t*>(zp + at));
+        next_z[0] = *reinterpret_cast<const uint16_t*>(zp + at);
       } else {
 #pragma unroll
-        for (int i = 0; i < ZS; ++i) next_z[i] = __ldg(zp + min(at + i, KG - 1));
+        for (int i = 0; i < ZS; ++i) next_z[i] = zp[min(at + i, KG - 1)];
       }
     };
     load_zeros(min(ks0 + group, ks1 - 1));
@@ -328,27 +328,31 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
     const int col0 = warp >= WIDEN + 4 ? COLS : 0;
     const uint16_t* sp = p.scales + static_cast<int64_t>(min(n0 + r, p.N - 1)) * KG;
     // A stage's scales, a stage ahead; where alignment allows it in one load, two
-    // to a register. Groups past K have no sums but zeros.
+    // to a register. Groups past K have no sums but zeros. (No non-coherent loads
+    // here and above, as in w4_gemm.cuh.)
     uint32_t next_s[GROUPS];
     auto load_scales = [&](int ks) {
       if (p.wide) {
         const uint16_t* at = sp + ks * GROUPS;
         if constexpr (GROUPS == 8)
-          asm volatile("ld.global.nc.L2::128B.v4.b32 {%0, %1, %2, %3}, [%4];"
+          asm volatile("ld.global.L2::128B.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(next_s[0]), "=r"(next_s[1]), "=r"(next_s[2]), "=r"(next_s[3])
-                       : "l"(at));
+                       : "l"(at)
+                       : "memory");
         else if constexpr (GROUPS == 4)
-          asm volatile("ld.global.nc.L2::128B.v2.b32 {%0, %1}, [%2];"
+          asm volatile("ld.global.L2::128B.v2.b32 {%0, %1}, [%2];"
                        : "=r"(next_s[0]), "=r"(next_s[1])
-                       : "l"(at));
+                       : "l"(at)
+                       : "memory");
         else
-          asm volatile("ld.global.nc.L2::128B.b32 %0, [%1];" : "=r"(next_s[0]) : "l"(at));
+          asm volatile("ld.global.L2::128B.b32 %0, [%1];" : "=r"(next_s[0]) : "l"(at) : "memory");
       } else {
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i)
-          asm volatile("ld.global.nc.L2::128B.u16 %0, [%1];"
+          asm volatile("ld.global.L2::128B.u16 %0, [%1];"
                        : "=r"(next_s[i])
-                       : "l"(sp + min(ks * GROUPS + i, KG - 1)));
+                       : "l"(sp + min(ks * GROUPS + i, KG - 1))
+                       : "memory");
       }
     };
     load_scales(ks0);

@@ -50,3 +50,41 @@ def test_norm_config_refusals():
         with pytest.raises(sptg.SptgError) as e:
             sptg.add_rms_norm(x, x, x[0], config=cfg)
         assert e.value.status == -1
+
+
+# ----------------------------------------------------------- one after another
+@pytest.mark.parametrize("m", [1, 7, 33])
+def test_operands_written_by_the_call_before(m):
+    """Weights, scales and zero points that the previous call on the stream has just written.
+
+    A kernel starts while the one before it ends; the same calls one at a time give the same bits."""
+    n, k, group = 520, 4096, 64
+    groups = k // group
+
+    def steps(wait):
+        g = gen(52)
+        x, codes = rand(g, m, k), torch.randint(0, 256, (n, k // 2), device="cuda", generator=g,
+                                                dtype=torch.uint8)
+        weight, row = torch.empty(k, dtype=BF16, device="cuda"), rand(g, 1, k)
+        scales, zeros = torch.empty(n, groups, dtype=BF16, device="cuda"), torch.empty(n, groups, dtype=S8, device="cuda")
+        ones, none = torch.ones(k, dtype=BF16, device="cuda"), torch.zeros(n, groups, dtype=BF16, device="cuda")
+        kept = []
+        for _ in range(12):
+            a, b = rand(g, n, groups), rand(g, n, groups)
+            sptg.add_rms_norm(row, rand(g, 1, k), ones, h=row, y=weight[None])
+            wait()
+            h, y, _ = sptg.add_rms_norm(x, x, weight)
+            wait()
+            sptg.add_rms_norm(a, none, ones[:groups], y=zeros)
+            wait()
+            kept += [y, sptg.gemm_w4(x, codes, a, zeros.view(torch.uint8))]
+            wait()
+            sptg.add_rms_norm(b, none, ones[:groups], y=scales)
+            wait()
+            kept.append(sptg.gemm_w4(x, codes, scales, zeros.view(torch.uint8)))
+            wait()
+        torch.cuda.synchronize()
+        return kept
+
+    for a, b in zip(steps(torch.cuda.synchronize), steps(lambda: None)):
+        assert torch.equal(a, b)
