@@ -381,8 +381,8 @@ int sptg_gemm_w4(int64_t M, int64_t N, int64_t K, int group, sptg_type x_type, s
  * offsets[E] <= T (read by the kernel: the host never waits for them). An
  * expert may have no rows (its dW is zero). Rows of Y and dX that belong to no
  * expert are set to zero. Offsets that break these rules are clamped to
- * [0, T] and to not decreasing; results are then unspecified, but nothing
- * outside the given arrays is touched.
+ * [0, T], and each is raised to the largest before it; results are those of the
+ * offsets that this leaves.
  *
  * X, Y, dY, dX: T rows with row pitches in elements; W and dW: E x N x K,
  * dense (N rows of K for each expert, as the weights of sptg_gemm are stored).

@@ -274,26 +274,35 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
   }
   grid_dependency_wait();
   // The list of groups: experts 0 ... experts - 1, then the rows before the
-  // first and after the last. Offsets outside [0, T] or decreasing are
-  // clamped, so that no tile leaves the rows of X.
+  // first and after the last. Offsets outside [0, T] are clamped to it and
+  // smaller ones raised to the largest before them, so that no tile leaves the
+  // rows of X and each row belongs to one group.
   const int groups = MODE == GROUPED_DW ? p.experts : p.experts + 2;
   const int nf = (p.F + 255) >> 8;
   if (warp == 2) {
     const int lo = min(max(p.offsets[0], 0), p.T);
-    const int hi = min(max(p.offsets[p.experts], lo), p.T);
-    int base = 0;
+    int base = 0, before = 0;  // tiles, and the largest offset, of the groups so far
     for (int g0 = 0; g0 < groups; g0 += 32) {
       const int g = g0 + lane;
+      // where a group starts: the largest offset up to its own
+      int start = g <= p.experts ? min(max(p.offsets[g], 0), p.T) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, start, o);
+        if (lane >= o) start = max(start, up);
+      }
+      start = max(start, before);
+      before = __shfl_sync(0xffffffffu, start, 31);
       int a = 0, n = 0, tiles = 0;
       if (g < groups) {
         if (g < p.experts) {
-          a = min(max(p.offsets[g], 0), p.T);
-          n = min(max(p.offsets[g + 1], a), p.T) - a;
+          a = start;
+          n = max(min(p.offsets[g + 1], p.T), start) - start;
         } else if (g == p.experts) {
           n = lo;
         } else {
-          a = hi;
-          n = p.T - hi;
+          a = start;  // (the last expert's end)
+          n = p.T - start;
         }
         tiles = MODE == GROUPED_DW ? nf * ((p.C + 255) >> 8) : (n + TT - 1) / TT * nf;
       }

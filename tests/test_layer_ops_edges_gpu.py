@@ -88,3 +88,20 @@ def test_operands_written_by_the_call_before(m):
 
     for a, b in zip(steps(torch.cuda.synchronize), steps(lambda: None)):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ experts
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [[0, 40, 10, 64], [0, 90, 20, 30], [30, 10, 50, 40], [-7, -3, 200, 60], [70, 0, 0, 0],
+                                 [0, 300, 7, 250] * 20, [5, 0] * 40])
+def test_grouped_offsets_that_decrease_are_raised(bad, out_dtype):
+    g = gen(len(bad) + bad[1])
+    t, n, k, e = 290, 72, 136, len(bad) - 1
+    X, W, dY = rand(g, t, k), rand(g, e, n, k), rand(g, t, n)
+    raw = torch.tensor(bad, dtype=torch.int32)
+    off, good = raw.cuda(), torch.cummax(raw.clamp(0, t), 0).values.cuda()
+    for call, args in ((sptg.grouped_gemm, (X, W)), (sptg.grouped_gemm_dx, (dY, W)), (sptg.grouped_gemm_dw, (dY, X))):
+        for _ in range(3):
+            assert torch.equal(call(*args, off, out_dtype=out_dtype), call(*args, good, out_dtype=out_dtype))
+    y = sptg.grouped_gemm(X, W, off, out_dtype=out_dtype)
+    assert not y[:int(good[0])].any() and not y[int(good[-1]):].any()
