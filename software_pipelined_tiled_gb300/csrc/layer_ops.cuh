@@ -470,7 +470,7 @@ int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, con
   const int64_t cols = mode == GROUPED_Y ? N : K;
   const int64_t sum = mode == GROUPED_Y ? K : N;
   const bool dw = mode == GROUPED_DW;
-  if ((dw ? E * N * K : T * cols) == 0) {
+  if (cols == 0 || (dw ? E == 0 || N == 0 : T == 0)) {
     set_config("kernel=none dtype=%s (empty output)", d.name, {});
     return SPTG_OK;
   }
@@ -487,6 +487,16 @@ int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, con
     return refuse(SPTG_ERR_ALIGN, "TMA needs 16-byte aligned bases and row pitches");
   if (!nothing && (reinterpret_cast<uintptr_t>(offsets) & 3u))
     return refuse(SPTG_ERR_ALIGN, "offsets not aligned to their type");
+  // Tiles up to 64 rows wide (and a deeper ring of weights) where the experts
+  // have few rows on average, else up to 256. Products of 2048 x 2048 bf16 weights,
+  // with 64 and 256: 8 experts of 16 rows on average 14.9 and 15.9 us, of 32 15.2
+  // and 16.6 us, of 64 20.5 and 17.7 us; 64 experts of 16 rows 79.9 and 86.5 us,
+  // of 32 87.1 and 88.3 us, of 64 95.1 and 91.5 us, of 128 139 and 102 us.
+  const int tt = (!dw && T <= 32 * E) ? 64 : 256;
+  const int64_t F = mode == GROUPED_DX ? K : N;
+  const int64_t nf = (F + 255) / 256;
+  const int64_t tiles = dw ? E * nf * ((K + 255) / 256) : nf * (T / tt + E + 2);
+  if (tiles > INT32_MAX / 2) return refuse(SPTG_ERR_ARG, "too many tiles");
   int dev = 0;
   DeviceInfo di;
   int rc = device_info(di, dev);
@@ -499,16 +509,6 @@ int grouped(int mode, int64_t E, int64_t T, int64_t N, int64_t K, int dtype, con
     set_config("kernel=zero-fill dtype=%s", d.name, {});
     return SPTG_OK;
   }
-  // Tiles up to 64 rows wide (and a deeper ring of weights) where the experts
-  // have few rows on average, else up to 256. Products of 2048 x 2048 bf16 weights,
-  // with 64 and 256: 8 experts of 16 rows on average 14.9 and 15.9 us, of 32 15.2
-  // and 16.6 us, of 64 20.5 and 17.7 us; 64 experts of 16 rows 79.9 and 86.5 us,
-  // of 32 87.1 and 88.3 us, of 64 95.1 and 91.5 us, of 128 139 and 102 us.
-  const int tt = (!dw && T <= 32 * E) ? 64 : 256;
-  const int64_t F = mode == GROUPED_DX ? K : N;
-  const int64_t nf = (F + 255) / 256;
-  const int64_t tiles = dw ? E * nf * ((K + 255) / 256) : nf * (T / tt + E + 2);
-  if (tiles > INT32_MAX / 2) return refuse(SPTG_ERR_ARG, "too many tiles");
   KernelVariant v;
   if (mode == GROUPED_Y)
     v = d.in_bf16 ? grouped_variant_y_bf16(d.out_kind, tt) : grouped_variant_y_f16(d.out_kind, tt);
