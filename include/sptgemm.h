@@ -320,7 +320,8 @@ typedef enum {
  * itself (same pointer and pitch); nothing else may overlap. Any cols, pitch
  * and element-aligned pointers are taken; rows are read in 16-byte pieces when
  * cols and every pitch are multiples of 8 and every pointer is 16-byte aligned
- * (an 8-bit y: 8-byte). eps > 0. rows == 0 or cols == 0: nothing is done.
+ * (an 8-bit y: 8-byte). eps > 0. rows == 0 or cols == 0: nothing is done
+ * (no scales are written).
  */
 int sptg_add_rms_norm(int64_t rows, int64_t cols, sptg_type in_type, sptg_type out_type,
                       const void* x, int64_t ldx, const void* residual, int64_t ldr,

@@ -61,13 +61,16 @@ def _matrix(t, name: str):
         _refuse(name, t, "a 2-D CUDA tensor")
 
 
+def _stream(stream, device):
+    """PyTorch's stream object for a stream object or a raw handle (None: the current stream)."""
+    return torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to the stream that the call runs on."""
     if stream is None:
         return _new(shape, dtype=dtype, device=device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream(stream, device)):
         return _new(shape, dtype=dtype, device=device)
 
 
@@ -90,8 +93,8 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None,
     residual itself), ``v = h * weight / sqrt(mean(h^2) + eps)`` in 32 bits.
     With ``out_dtype`` torch.int8 or torch.float8_e4m3fn, ``y * scales[:, None]``
     stands for v, each row scaled to the type's largest value; by default y is v
-    in x's type and scales is None.  x, residual, h and y are 2-D with
-    contiguous rows.  config: a Config, for its timeout_ms and inject_stall.
+    in x's type and scales is None.  Rows without columns have scales of 0.  x,
+    residual, h and y are 2-D with contiguous rows.  config: a Config, for its timeout_ms and inject_stall.
     """
     if x.dim() != 2 or not x.is_cuda:
         _refuse("x", x, "a 2-D CUDA tensor")
@@ -125,6 +128,9 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None,
         else:
             _dense(scales, (rows,), _F32, device, "scales")
         s = scales.data_ptr()
+        if not cols:  # the library does nothing for rows without columns: their largest value is 0
+            with torch.cuda.stream(_stream(stream, on)):
+                scales.zero_()
     function = _norm
     if config is not None:
         function = lambda *args: _norm_ex(*args, ctypes.byref(config))  # noqa: E731

@@ -52,6 +52,19 @@ def test_norm_config_refusals():
         assert e.value.status == -1
 
 
+@pytest.mark.parametrize("out_dtype", [S8, E4M3])
+def test_norm_of_rows_without_columns_has_scales_of_zero(out_dtype):
+    e = torch.empty(3, 0, dtype=F16, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        s = torch.full((3,), 7.0, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        assert sptg.add_rms_norm(e, e, e[0], out_dtype=out_dtype, scales=s, stream=stream)[2] is s
+        own = sptg.add_rms_norm(e, e, e[0], out_dtype=out_dtype, stream=stream)[2]
+        side.synchronize()
+        assert (s == 0).all() and (own == 0).all()
+
+
 # ----------------------------------------------------------- one after another
 @pytest.mark.parametrize("m", [1, 7, 33])
 def test_operands_written_by_the_call_before(m):
