@@ -14,7 +14,11 @@
 // value it stands for is NaN; one whose max|h w| is zero, or so small that
 // QMAX / max|h w| overflows, or whose finite h are so large that their squares
 // overflow (y is 0 by the formula), gets q = 0 and s = 0. The maximum of |h| is
-// kept beside that of |h w| to tell an overflow from an infinity.
+// kept beside that of |h w| to tell an overflow from an infinity. Where |h w|
+// passes 32 bits although both are finite (bfloat16 only), the row is gone through
+// once more with w / 2^64, exact for every product that counts beside one of
+// 2^128, and s takes the 2^64 back. (In a loop of its own: scaling the weights
+// that the kernels hold costs registers, 16384 rows of 4096 71 -> 80 us.)
 //
 // Memory-bound: 7 bytes an element (x, r in; h, q out) and some ten flops. The
 // row stays in registers (wide rows: in shared memory) between the reduction and
@@ -90,7 +94,8 @@ struct RowScale {
 // Maxima are held as the bits of non-negative floats and compared as unsigned
 // integers, so that NaN (above every number) is kept. mx: .x max|h w|, .y max|h|.
 template <int OUTK>
-__device__ __forceinline__ RowScale row_scale(float sumsq, uint2 mx, int cols, float eps) {
+__device__ __forceinline__ RowScale row_scale(float sumsq, uint2 mx, int cols, float eps,
+                                              float unit = 1.0f) {
   RowScale s;
   s.rstd = 1.0f / sqrtf(sumsq / static_cast<float>(cols) + eps);
   constexpr float QMAX = OUTK == NORM_S8 ? 127.0f : 448.0f;
@@ -99,7 +104,7 @@ __device__ __forceinline__ RowScale row_scale(float sumsq, uint2 mx, int cols, f
   const bool overflow = !(s.rstd > 0.0f) && __uint_as_float(mx.y) < INFINITY;
   const bool bad = !(m < INFINITY) && !overflow;
   s.zero = bad || overflow || !(s.qmul < INFINITY);
-  s.scale = bad ? NAN : s.zero ? 0.0f : s.rstd * m / QMAX;
+  s.scale = bad ? NAN : s.zero ? 0.0f : s.rstd * m / QMAX * unit;  // (unit: what h w was divided by)
   return s;
 }
 
@@ -130,6 +135,50 @@ __device__ __forceinline__ void row_reduce(float& sum, uint2& mx, float* s_sum, 
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Whether the products h w of a row of finite h passed 32 bits (or w holds an
+// infinity): the same for each of the row's threads.
+template <bool BF16, int OUTK>
+__device__ __forceinline__ bool products_overflow(uint2 mx) {
+  return BF16 && OUTK != NORM_16 && mx.x == 0x7f800000u && mx.y < 0x7f800000u;
+}
+
+// What follows a row's statistics, element by element, for any width and
+// alignment. x + r is formed once more. h may be x or r itself: each element is
+// read by the thread that then writes it. THREADS: of the row, 0 for the block's.
+template <bool BF16, int OUTK, int THREADS>
+__device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, float sum, uint2 mx,
+                                           float* s_sum, uint2* s_max) {
+  constexpr bool WARP_ROW = THREADS == 32;
+  const int lanes = THREADS ? THREADS : static_cast<int>(blockDim.x);
+  const int lane = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ldx;
+  const uint16_t* r = static_cast<const uint16_t*>(p.r) + row * p.ldr;
+  float part = 1.0f, unit = 1.0f;  // the weights' part that counts, 1 / part
+  if (products_overflow<BF16, OUTK>(mx)) {
+    unit = 18446744073709551616.0f;  // 2^64
+    part = 1.0f / unit;
+    mx.x = 0;
+    for (int i = lane; i < p.cols; i += lanes)
+      mx.x = max(mx.x, abs_bits((load16<BF16>(x, i) + load16<BF16>(r, i)) * (load16<BF16>(p.w, i) * part)));
+    if constexpr (!WARP_ROW) __syncthreads();  // the first sums have been read
+    float none = 0.0f;
+    row_reduce<WARP_ROW>(none, mx, s_sum, s_max);
+  }
+  const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps, unit);
+  constexpr int H_OUT = BF16 ? OUT_BF16 : OUT_F16;
+  for (int i = lane; i < p.cols; i += lanes) {
+    const float h = load16<BF16>(x, i) + load16<BF16>(r, i);
+    const float w = load16<BF16>(p.w, i);
+    store_out<H_OUT>(p.h, row * p.ldh + i, h);
+    if constexpr (OUTK == NORM_16)
+      store_out<H_OUT>(p.q, row * p.ldq + i, h * sc.rstd * w);
+    else
+      static_cast<uint8_t*>(p.q)[row * p.ldq + i] =
+          sc.zero ? 0 : static_cast<uint8_t>(quant2<OUTK>(h * (w * part) * sc.qmul, 0.0f));
+  }
+  if (OUTK != NORM_16 && lane == 0) p.scales[row] = sc.scale;
+}
 
 // 8 elements of x and r to h, with their part of the row's sum and maxima.
 template <bool BF16, int OUTK>
@@ -215,6 +264,10 @@ __global__ void __launch_bounds__(WARP_ROW || PER == 4 ? 128 : 1024) add_rms_nor
   row_reduce<WARP_ROW>(sum, mx, s_sum, s_max);
   grid_launch_dependents();
   if (!live) return;
+  if (products_overflow<BF16, OUTK>(mx)) {
+    finish_row<BF16, OUTK, WARP_ROW ? 32 : 0>(p, row, sum, mx, s_sum, s_max);
+    return;
+  }
   const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -298,13 +351,17 @@ __global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const No
     // (into a place whose last copy has landed, and into no other)
     const int64_t next = row + static_cast<int64_t>(S) * gridDim.x;
     if (threadIdx.x == 0 && ok && next < p.rows) fetch(next, s);
-    const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
+    if (products_overflow<BF16, OUTK>(mx)) {
+      finish_row<BF16, OUTK, 0>(p, row, sum, mx, s_sum[odd], s_max[odd]);
+    } else {
+      const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int g = threadIdx.x + i * blockDim.x;
-      if (g < groups) store_group<BF16, OUTK>(p, row, g, h[i], wv[i], sc);
+      for (int i = 0; i < PER; ++i) {
+        const int g = threadIdx.x + i * blockDim.x;
+        if (g < groups) store_group<BF16, OUTK>(p, row, g, h[i], wv[i], sc);
+      }
+      if (OUTK != NORM_16 && threadIdx.x == 0) p.scales[row] = sc.scale;
     }
-    if (OUTK != NORM_16 && threadIdx.x == 0) p.scales[row] = sc.scale;
     odd ^= 1u;
     if (++s == S) {
       s = 0;
@@ -326,8 +383,7 @@ __global__ void __launch_bounds__(MAX_THREADS) add_rms_norm_ring_kernel(const No
 
 // Rows of any width, alignment and pitch: one block to a row, element by
 // element, x + r formed a second time for the outputs (the second read comes
-// from L2). h may be r itself: each element is read by the thread that later
-// writes it, in both passes.
+// from L2).
 template <bool BF16, int OUTK>
 __global__ void __launch_bounds__(512) add_rms_norm_any_kernel(const NormParams p) {
   __shared__ float s_sum[32];
@@ -348,19 +404,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_any_kernel(const NormParams 
   }
   row_reduce<false>(sum, mx, s_sum, s_max);
   grid_launch_dependents();
-  const RowScale sc = row_scale<OUTK>(sum, mx, p.cols, p.eps);
-  constexpr int H_OUT = BF16 ? OUT_BF16 : OUT_F16;
-  for (int i = threadIdx.x; i < p.cols; i += 512) {
-    const float h = load16<BF16>(x, i) + load16<BF16>(r, i);
-    const float w = load16<BF16>(p.w, i);
-    store_out<H_OUT>(p.h, row * p.ldh + i, h);
-    if constexpr (OUTK == NORM_16)
-      store_out<H_OUT>(p.q, row * p.ldq + i, h * sc.rstd * w);
-    else
-      static_cast<uint8_t*>(p.q)[row * p.ldq + i] =
-          sc.zero ? 0 : static_cast<uint8_t>(quant2<OUTK>(h * w * sc.qmul, 0.0f));
-  }
-  if (OUTK != NORM_16 && threadIdx.x == 0) p.scales[row] = sc.scale;
+  finish_row<BF16, OUTK, 512>(p, row, sum, mx, s_sum, s_max);
 }
 
 }  // namespace sptg

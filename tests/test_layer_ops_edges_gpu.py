@@ -52,6 +52,23 @@ def test_norm_config_refusals():
         assert e.value.status == -1
 
 
+@pytest.mark.parametrize("out_dtype", [S8, E4M3, BF16])
+@pytest.mark.parametrize("rows,cols", [(5, 64), (5, 1024), (3, 3000), (640, 4096), (4, 65), (2, 16392),
+                                       (2000, 8192)])
+def test_norm_of_rows_whose_products_with_the_weight_pass_32_bits(rows, cols, out_dtype):
+    g = gen(rows + cols)
+    x, r, w = rand(g, rows, cols), rand(g, rows, cols, std=3.0), rand(g, cols, std=3e30)
+    x[1::2] *= 1e10  # about 1e41 with the weight, 1e31 when normalised
+    check_norm(x, r, w, out_dtype)
+    if out_dtype != BF16:
+        x[1, cols // 2], x[0, 0] = float("inf"), float("nan")
+        s = sptg.add_rms_norm(x, r, w, out_dtype=out_dtype)[2]
+        assert torch.isnan(s[:2]).all() and torch.isfinite(s[2:]).all()
+        x[0, 0], x[1, cols // 2] = 1.0, 1.0
+        w[5] = float("inf")
+        assert torch.isnan(sptg.add_rms_norm(x, r, w, out_dtype=out_dtype)[2]).all()
+
+
 @pytest.mark.parametrize("out_dtype", [S8, E4M3])
 def test_norm_of_rows_without_columns_has_scales_of_zero(out_dtype):
     e = torch.empty(3, 0, dtype=F16, device="cuda")
