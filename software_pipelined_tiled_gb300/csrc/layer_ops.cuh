@@ -134,6 +134,31 @@ constexpr const char* kDimText = "dimensions must be in [0, 2^31 - 4096]";
 
 constexpr uint64_t kOpTimeoutNs = 2000ull * 1000000ull;
 
+// Blocks of a kernel that an SM holds at once, and its registers a thread, by
+// device, kernel, threads and shared memory.
+struct Residency {
+  int blocks, regs;
+};
+std::map<std::tuple<int, const void*, int, int>, Residency> g_residency;
+
+int residency(Residency& out, int dev, const void* fn, int threads, int smem) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  const auto key = std::make_tuple(dev, fn, threads, smem);
+  const auto it = g_residency.find(key);
+  if (it != g_residency.end()) {
+    out = it->second;
+    return SPTG_OK;
+  }
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&out.blocks, fn, threads, smem);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, fn);
+  if (e != cudaSuccess) return cuda_fail(e, "occupancy of a kernel");
+  out.blocks = std::max(1, out.blocks);
+  out.regs = attr.numRegs;
+  g_residency[key] = out;
+  return SPTG_OK;
+}
+
 // ------------------------------------------------------- residual and norm
 int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const void* x, int64_t ldx,
                  const void* r, int64_t ldr, const void* w, float eps, void* h, int64_t ldh,
@@ -174,7 +199,7 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
   // times through the GPU, rows through the ring kernel's blocks. Rows past
   // 16384 elements take the kernel for any width.
   const auto round32 = [](int64_t n) { return static_cast<int>((n + 31) / 32 * 32); };
-  int kind = NORM_ANY, threads = 512, smem = 0, stages = 0;
+  int kind = NORM_ANY, threads = 512, smem = 0, stages = 0, regs = 0;
   int64_t grid = rows;
   if (vectors && cols <= 1024) {
     kind = cols <= 512 ? NORM_WARP_2 : NORM_WARP_4;
@@ -187,26 +212,30 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
     const bool four = cols > 2048 && cols <= 4096 && rows >= 4 * di.sm_count;
     kind = four ? NORM_BLOCK_4 : NORM_BLOCK_2;
     threads = four ? round32((cols / 8 + 3) / 4) : round32((cols / 8 + 1) / 2);
-    // blocks of the ring kernel: three rows ahead, as many to an SM as its
-    // shared memory and 96 registers a thread allow
-    const int ring_threads = round32((cols / 8 + 3) / 4);
-    const int ring_stages = 3;
-    const int ring_smem = norm_ring_smem(static_cast<int>(cols), ring_stages);
-    const int per_sm = std::max(1, std::min(224 * 1024 / (ring_smem + 2048), 65536 / (96 * ring_threads)));
-    const int64_t blocks = static_cast<int64_t>(per_sm) * di.sm_count;
-    if (cols > 4096 && rows >= 3 * blocks) {
-      kind = NORM_RING_4;
-      threads = ring_threads;
-      stages = ring_stages;
-      smem = ring_smem;
-      grid = blocks;
+    // The ring kernel: three rows ahead, as many blocks as the GPU holds at once
+    // (rows are dealt out to all blocks from the start; 16384 binary16 rows of 6144
+    // to int8, two blocks to an SM by their registers: 117 us, with three 134 us).
+    if (cols > 4096 && rows >= 3 * di.sm_count) {
+      const int ring_threads = round32((cols / 8 + 3) / 4);
+      const int ring_stages = 3;
+      const int ring_smem = norm_ring_smem(static_cast<int>(cols), ring_stages);
+      const void* ring = norm_variant(in_type == SPTG_T_BF16, out_kind, NORM_RING_4);
+      Residency res;
+      int rs = ensure_smem(dev, ring, norm_ring_smem(16384, 3));
+      if (!rs) rs = residency(res, dev, ring, ring_threads, ring_smem);
+      if (rs) return rs;
+      const int64_t blocks = static_cast<int64_t>(res.blocks) * di.sm_count;
+      if (rows >= 3 * blocks) {
+        kind = NORM_RING_4;
+        threads = ring_threads;
+        stages = ring_stages;
+        smem = ring_smem;
+        grid = blocks;
+        regs = res.regs;
+      }
     }
   }
   const void* fn = norm_variant(in_type == SPTG_T_BF16, out_kind, kind);
-  if (smem) {
-    const int rs = ensure_smem(dev, fn, norm_ring_smem(16384, 3));
-    if (rs) return rs;
-  }
   NormParams p{x, r, w, h, y, scales, ldx, ldr, ldh, ldy, rows, static_cast<int>(cols), eps,
                stages, di.error_word, timeout_ms ? timeout_ms * 1000000ull : kOpTimeoutNs, inject_stall};
   void* args[] = {&p};
@@ -214,8 +243,8 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
       launch_op(fn, dim3(static_cast<unsigned>(grid)), threads, smem, 1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "add_rms_norm launch");
   set_config("kernel=add_rms_norm type=%s out_bytes=%lld kind=%lld threads=%lld grid=%lld stages=%lld "
-             "smem=%lld",
-             in.name, {out.bytes, kind, threads, grid, stages, smem});
+             "smem=%lld regs=%lld",
+             in.name, {out.bytes, kind, threads, grid, stages, smem, regs});
   return SPTG_OK;
 }
 

@@ -22,7 +22,43 @@ def chosen():
 
 
 # ------------------------------------------------------------------ the norm
-RING = 4  # the kernel with a ring of rows
+WARP_2, WARP_4, BLOCK_2, BLOCK_4, RING, ANY = range(6)  # its kernels, by last_config's kind
+
+
+@pytest.mark.parametrize("out_dtype", [S8, E4M3, None])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("cols", [4104, 4352, 5128, 6144, 8192, 16384])
+def test_norm_ring_has_as_many_blocks_as_the_gpu_holds(cols, dtype, out_dtype):
+    """Rows are dealt out to all blocks from the start: one that waits for an SM makes the call longer."""
+    x = torch.ones(3000, cols, dtype=dtype, device="cuda")
+    sptg.add_rms_norm(x, x, x[0], out_dtype=out_dtype)
+    c, sms = chosen(), torch.cuda.get_device_properties(0).multi_processor_count
+    assert c["kind"] == RING and c["grid"] % sms == 0
+    per_sm, registers = c["grid"] // sms, -(-c["regs"] // 8) * 8  # handed out in eights
+
+    # an SM's registers lie in four parts of 16384, and a warp in one of them; of its 228 KB of shared
+    # memory, 1 KB a block are the system's
+    warps = 4 * (16384 // (32 * registers))
+
+    def fits(n):
+        return n * c["threads"] // 32 <= warps and n * (c["smem"] + 1024 + 1024) <= 228 * 1024
+    assert fits(per_sm) and not fits(per_sm + 1)
+
+
+@pytest.mark.parametrize("out_dtype", [S8, E4M3, None])
+@pytest.mark.parametrize("rows,cols,kind", [(40, 512, WARP_2), (33, 520, WARP_4), (300, 2048, BLOCK_2),
+                                            (20, 4096, BLOCK_2), (700, 4096, BLOCK_4), (650, 3000, BLOCK_4),
+                                            (300, 6144, BLOCK_2), (1900, 4104, RING), (1500, 5000, RING),
+                                            (1500, 6144, RING), (930, 8192, RING), (470, 12000, RING),
+                                            (460, 16384, RING), (5, 16392, ANY), (700, 4095, ANY)])
+def test_norm_by_each_of_its_kernels(rows, cols, kind, out_dtype):
+    g = gen(rows + cols)
+    dtype = BF16 if rows % 20 else F16
+    x, r = rand(g, rows, cols, dtype=dtype), rand(g, rows, cols, dtype=dtype, std=3.0)
+    w = 1 + rand(g, cols, dtype=dtype, std=0.2)
+    check_norm(x, r, w, out_dtype or dtype)
+    assert chosen()["kind"] == kind
+    check_norm(x, r, w, out_dtype or dtype, h=r)  # in place
 
 
 @pytest.mark.parametrize("out_dtype", [S8, BF16])
