@@ -381,7 +381,6 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   const bool tile = M > 8;
   const int nt = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : w4t_max_ntok(group);
   const int64_t m_blocks = (M + nt - 1) / nt;
-  if (m_blocks > 65535) return refuse(SPTG_ERR_ARG, "at most 64 * 65535 rows of x");
   int xk;
   const void* fn;
   switch (x_type) {
@@ -473,10 +472,14 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   p.timeout_ns = kOpTimeoutNs;
   void* tile_args[] = {&mw, &mx, &p};
   void* stream_args[] = {&mw, &p};
-  const cudaError_t e =
-      launch_op(fn, dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_blocks)),
-                launch_threads, smem, splits, stream, tile ? tile_args : stream_args);
-  if (e != cudaSuccess) return cuda_fail(e, "gemm_w4 launch");
+  // a grid is at most 65535 high: more rows take several launches
+  for (int64_t first = 0; first < m_blocks; first += 65535) {
+    p.m_first = static_cast<int>(first * nt);
+    const unsigned high = static_cast<unsigned>(std::min<int64_t>(65535, m_blocks - first));
+    const cudaError_t e = launch_op(fn, dim3(static_cast<unsigned>(n_tiles * splits), high),
+                                    launch_threads, smem, splits, stream, tile ? tile_args : stream_args);
+    if (e != cudaSuccess) return cuda_fail(e, "gemm_w4 launch");
+  }
   set_config("kernel=w4 type=%s x_rows=%lld group=%lld rows=%lld splits=%lld stages=%lld grid=%lld "
              "m_blocks=%lld threads=%lld segment=%lld smem=%lld",
              xt.name, {nt, group, rows, splits, p.stages, n_tiles * splits, m_blocks, launch_threads,

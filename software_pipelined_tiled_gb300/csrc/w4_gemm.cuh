@@ -77,6 +77,7 @@ constexpr int W4_MAX_ROWS = W4_WARP_ROWS * W4_MAX_WARPS / W4_KW;
 
 struct W4Params {
   int M, N, K;
+  int m_first;             // tile kernel: first row of x of this launch
   const void* x;           // M rows of K, ldx elements apart
   int64_t ldx;
   int rows;                // rows of weights per CTA, a multiple of 16

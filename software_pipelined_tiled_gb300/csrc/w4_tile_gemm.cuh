@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x) % p.splits;
   const int n0 = static_cast<int>(blockIdx.x) / p.splits * R;
-  const int m0 = static_cast<int>(blockIdx.y) * NTOK;
+  const int m0 = p.m_first + static_cast<int>(blockIdx.y) * NTOK;
   const int KS = (p.K + W4_STAGE_K - 1) / W4_STAGE_K;
   const int ks0 = static_cast<int>(static_cast<int64_t>(KS) * rank / p.splits);
   const int ks1 = static_cast<int>(static_cast<int64_t>(KS) * (rank + 1) / p.splits);

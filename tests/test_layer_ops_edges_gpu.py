@@ -3,7 +3,8 @@ import pytest
 import torch
 
 import software_pipelined_tiled_gb300 as sptg
-from test_layer_ops_gpu import BF16, E4M3, F16, F32, S8, check_norm, gen, rand
+from test_layer_ops_gpu import (BF16, E4M3, F16, F32, S8, assert_close, check_norm, gen, rand, w4_inputs,
+                                w4_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -116,6 +117,20 @@ def test_norm_of_rows_without_columns_has_scales_of_zero(out_dtype):
         own = sptg.add_rms_norm(e, e, e[0], out_dtype=out_dtype, stream=stream)[2]
         side.synchronize()
         assert (s == 0).all() and (own == 0).all()
+
+
+# ------------------------------------------------------------ 4-bit weights
+@pytest.mark.parametrize("group,block", [(32, 32), (128, 64)])
+def test_w4_of_more_rows_than_a_grid_is_high(group, block):
+    m, n = block * 65535 + 33, 16
+    g = gen(group)
+    x, codes, scales, z, _ = w4_inputs(g, m, n, group, group, BF16, BF16, True)
+    y = sptg.gemm_w4(x, codes, scales, z)
+    assert chosen()["launches"] == 2
+    for a in (slice(0, 100), slice(m // 2, m // 2 + 100), slice(m - 200, m)):
+        ref, S = w4_reference(x[a], codes, scales, z, None)
+        assert_close(y[a], ref, S, group)
+    assert torch.equal(y[-65:], sptg.gemm_w4(x[-65:], codes, scales, z))
 
 
 # ----------------------------------------------------------- one after another
