@@ -354,11 +354,10 @@ int sptg_add_rms_norm_ex(int64_t rows, int64_t cols, sptg_type in_type, sptg_typ
  *             NULL: 8 everywhere
  *   Y         M x N of out_type (SPTG_T_F16 or SPTG_T_BF16), row pitch ldy
  *
- * Products and sums are exact to fp32 accumulation; Y is rounded once. (For up
- * to 8 rows the zero points come out of the groups' sums, so a weight equal to
- * its zero point contributes 0 only to fp32 accuracy, and a row of X that holds
- * an infinity or a NaN gives NaN; for more rows such a row gives what the
- * products give. |X| stays below 2^120.)
+ * Products are exact, a group's sum of them and the sum of the scaled groups are
+ * fp32, and Y is rounded once: a weight equal to its zero point adds nothing, an
+ * infinity or a NaN in X what its products are, to its own row. (A group's sum of
+ * products has to stay in the fp32 range before its scale.)
  * group is 32, 64 or 128 and divides K. X and codes are 16-byte aligned with
  * row pitches of a multiple of 16 bytes (SPTG_ERR_ALIGN); N, M and ldy are
  * free. Up to 64 rows of X (with groups of 32: up to 32) share one pass over

@@ -409,7 +409,7 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   // Stages of x that two fifths of a streaming CTA's shared memory hold.
   const int budget = (224 << 10) / W4_CTAS_PER_SM - 1024;
   const int live_m = static_cast<int>(std::min<int64_t>(M, W4_X_ROWS));
-  const int x_stage = live_m * W4_STAGE_K * 2 + W4_STAGE_K / group * W4_X_ROWS * 4;
+  const int x_stage = live_m * W4_STAGE_K * 2;
   const int x_stages = (budget * 2 / 5) / x_stage;
   const W4Shape shape = w4_shape(N, k_stages, tile, m_blocks, x_stages, slots.n);
   const int rows = shape.rows, splits = shape.splits;

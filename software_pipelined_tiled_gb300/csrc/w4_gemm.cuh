@@ -7,16 +7,16 @@
 // 128 columns; z: a zero point 0 ... 15 for each group, or 8 everywhere; x: 16
 // bits, or 8 bits (int8, e4m3) with a 32-bit scale xs for each row.
 //
-// The zero points come out of the sums: sum x (w - z) = sum x w - z sum x. The
-// codes then need no arithmetic at all before the tensor core, only masks:
-// in binary16 a code in the low bits of a half is the number code * 2^-24 (a
-// subnormal, exact), one in bits 4-7 is 16 times that; in bfloat16 a code under
-// the exponent of 128 is 128 + code. 8-bit x is exact in binary16. The products
-// are exact, the sums are kept in 32 bits for each group, the group's zero
-// point (bfloat16: 128 + z) times the group's sum of x is taken off in 32 bits,
-// and the scaled result is added to the running sum in 32 bits. The only
-// rounding to 16 bits is that of Y. (Subtracting the zero point from every code
-// first costs 8 instructions more for 16 x 32 codes, beside about 24.)
+// Exactness: a code less its zero point is an integer of at most 15, exact in the
+// 16-bit type of the product (8-bit x is exact in binary16). The products are
+// exact, the sums are kept in 32 bits for each group, and the group's scale
+// multiplies the group's sum as it is added to the running sum in 32 bits. The
+// only rounding to 16 bits is that of Y. (Taking the zero points out of the
+// groups' sums instead, sum x (w - z) = sum x w - z sum x, with codes that are
+// masked only, forms sums 10 to 30 times as large, whose rounding does not cancel,
+// and turns an infinity in x into NaN. It saved 8 instructions for 16 x 32 codes
+// and needed the sums of x: one binary16 row through 32768 x 8192 36.2 us against
+// 38.0, one bf16 row 34.6 against 34.7, 8 bf16 rows 45.9 against 42.5.)
 //
 // Memory-bound: N * K / 2 bytes of codes, each read once. A CTA takes a block of
 // rows of weights and a range of K (the whole, or a share of it in a cluster of
@@ -29,13 +29,13 @@
 // when it has read it, so that no warp ever waits for another inside a segment.
 //
 // Measured: one bf16 row through 4096 x 4096, 8192 x 8192, 16384 x 4096 and
-// 32768 x 8192 in groups of 128 5.5, 13.2, 12.6 and 34.8 us back to back, 8 rows
-// 7.1, 15.3 and 46.3 us through the first two and the last. One binary16 row through 32768 x 8192, groups of 64 with zero
-// points, 36.4 us (4.0 TB/s; the floor at 6783 GB/s is 21.7 us). The copies
-// alone take 23.4 us; what remains is bound by the issue of about 32
-// instructions for 16 x 32 codes and the scales' own. A ring shared by the CTA,
-// x travelling in its stages, needed two CTA-wide barriers a stage and took
-// 46 us, whatever was taken out of the arithmetic.
+// 32768 x 8192 in groups of 128 5.8, 13.6, 12.7 and 34.7 us back to back, 8 rows
+// 7.0, 14.9, 13.4 and 42.5 us; int8 rows through 8192 x 8192 13.9 and 16 us. One
+// binary16 row through 32768 x 8192, groups of 64 with zero points, 38.0 us
+// (3.9 TB/s; the floor at 6788 GB/s is 21.7 us). The copies alone take 23.4 us;
+// what remains is bound by the issue of the instructions that make operands of the
+// codes. A ring shared by the CTA, x travelling in its stages, needed two CTA-wide
+// barriers a stage and took 46 us, whatever was taken out of the arithmetic.
 //
 // The multiply is the warp-wide 16 x 8 x 16 instruction, whose operands live
 // in registers: codes are spread in registers and never stored, and with up to
@@ -100,10 +100,10 @@ struct W4Params {
 
 __host__ __device__ constexpr int w4_x_bytes(int xk) { return xk >= W4_S8 ? 1 : 2; }
 
-// Shared memory of a CTA, in this order: the rings, x (16 bits), the sums of x
-// over groups, the scales, the barriers. The partial sums reuse the front.
+// Shared memory of a CTA, in this order: the rings, x (16 bits), the scales, the
+// barriers. The partial sums reuse the front.
 struct W4Layout {
-  int warps, ring, x, xsum, table, bars, total;
+  int warps, ring, x, table, bars, total;
 };
 __host__ __device__ constexpr int w4_red_pitch(int rows) { return rows + 4; }
 __host__ __device__ constexpr W4Layout w4_layout(int group, int rows, int stages, int segment,
@@ -112,8 +112,7 @@ __host__ __device__ constexpr W4Layout w4_layout(int group, int rows, int stages
   l.warps = rows / W4_WARP_ROWS * W4_KW;
   l.ring = 0;
   l.x = l.warps * stages * W4_WARP_ROWS * (W4_STAGE_K / 2);
-  l.xsum = l.x + segment * live_m * W4_STAGE_K * 2;
-  l.table = l.xsum + segment * (W4_STAGE_K / group) * W4_X_ROWS * 4;
+  l.table = l.x + segment * live_m * W4_STAGE_K * 2;
   l.bars = l.table + l.warps * W4_WARP_ROWS * (W4_STAGE_K / group) * 8;
   // (the partial sums of all warps take the place of everything before)
   const int red = W4_KW * W4_X_ROWS * w4_red_pitch(rows) * 4;
@@ -187,22 +186,49 @@ __device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask, uint32_t mag
   return r;
 }
 
-// The eight codes of a word as column pairs: (0,4), (2,6) in `a`, (1,5), (3,7)
-// in `b`. Binary16: a as code * 2^-24, b as code * 2^-20. bfloat16 has room for
-// a code in the low four bits only: 128 + code everywhere, three shifts.
+// The zero point of a group as spread_codes takes it, in both halves: 128 + z in
+// bfloat16, 1024 + z in binary16.
 template <bool BF>
-__device__ __forceinline__ void spread_codes(const W4Params& p, uint32_t w, uint32_t (&a)[2],
-                                             uint32_t (&b)[2]) {
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
+  return ((BF ? 0x4300u : 0x6400u) | z) * 0x00010001u;
+}
+// binary16: -(64 + z) beside it, for the codes in bits 4-7
+__device__ __forceinline__ uint32_t zero_pair_high(uint32_t z2) {
+  return pick(z2 << 4, 0x00f000f0u, 0xd400d400u);
+}
+
+// The eight codes of a word, less the zero point, as column pairs: (0,4), (2,6)
+// in `a`, (1,5), (3,7) in `b`. A mask and an exponent's bits make numbers of the
+// codes of a word two at a time, and one subtraction (exact) takes the zero point
+// and the exponent's own value off both. Binary16 takes the codes of bits 4-7
+// where they are, as 1024 + 16 code, and a multiply-add brings them down;
+// bfloat16 has room for a code in the low four bits only: three shifts.
+template <bool BF>
+__device__ __forceinline__ void spread_codes(const W4Params& p, uint32_t w, uint32_t z2,
+                                             uint32_t z2h, uint32_t (&a)[2], uint32_t (&b)[2]) {
   if constexpr (BF) {
-    a[0] = pick(w, p.mask_lo, p.magic);
-    b[0] = pick(w >> 4, p.mask_lo, p.magic);
-    a[1] = pick(w >> 8, p.mask_lo, p.magic);
-    b[1] = pick(w >> 12, p.mask_lo, p.magic);
+    auto sub = [&](uint32_t v) {
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&z2));
+      return *reinterpret_cast<const uint32_t*>(&d);
+    };
+    a[0] = sub(pick(w, p.mask_lo, p.magic));
+    b[0] = sub(pick(w >> 4, p.mask_lo, p.magic));
+    a[1] = sub(pick(w >> 8, p.mask_lo, p.magic));
+    b[1] = sub(pick(w >> 12, p.mask_lo, p.magic));
   } else {
-    a[0] = w & p.mask_lo;
-    b[0] = w & p.mask_hi;
-    a[1] = (w >> 8) & p.mask_lo;
-    b[1] = (w >> 8) & p.mask_hi;
+    constexpr uint32_t SIXTEENTH = 0x2c002c00u;
+    const __half2 z = *reinterpret_cast<const __half2*>(&z2);
+    const __half2 zh = *reinterpret_cast<const __half2*>(&z2h);
+    const __half2 f = *reinterpret_cast<const __half2*>(&SIXTEENTH);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = pick(w >> (8 * i), p.mask_lo, p.magic), hi = pick(w >> (8 * i), p.mask_hi, p.magic);
+      const __half2 dl = __hsub2(*reinterpret_cast<const __half2*>(&lo), z);
+      const __half2 dh = __hfma2(*reinterpret_cast<const __half2*>(&hi), f, zh);
+      a[i] = *reinterpret_cast<const uint32_t*>(&dl);
+      b[i] = *reinterpret_cast<const uint32_t*>(&dh);
+    }
   }
 }
 
@@ -375,11 +401,7 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
       const float sc = bf ? __uint_as_float(h << 16)
                           : __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
       const uint32_t z = p.zeros ? next_z[i / 4] >> (8 * (i % 4)) & 15u : 8u;
-      // 2^23 + z, as a float; bfloat16: -(128 + z), binary16: -z * 2^-24 (both
-      // exact)
-      const float zf = __uint_as_float(z | 0x4b000000u);
-      table[i * WR] = BF ? make_float2(sc, 8388480.0f - zf)
-                         : make_float2(sc * 16777216.0f, fmaf(zf, -1.0f / 16777216.0f, 0.5f));
+      table[i * WR] = make_float2(sc, __uint_as_float(zero_pair<BF>(z)));
     }
   };
 
@@ -397,12 +419,11 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
     const int first = ks0 + seg * p.segment;
     const int units = (min(ks1, first + p.segment) - first) * W4_UNITS;
     if (seg > 0) __syncthreads();  // every warp is done with the one before
-    // 8 columns of a row of x a thread; G / 8 neighbouring threads a group
+    // 8 columns of a row of x a thread
     for (int i = threadIdx.x; i < units * 4 * p.M; i += blockDim.x) {
       const int m = i / (units * 4), c = i - m * (units * 4);
       const int k = first * W4_STAGE_K + c * 8;
       uint4 b = make_uint4(0, 0, 0, 0);
-      float sum = 0.0f;
       if (k < p.K) {
         const uint8_t* src = static_cast<const uint8_t*>(p.x) +
                              (static_cast<int64_t>(m) * p.ldx + k) * XB;
@@ -415,25 +436,7 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
         }
         b = pair_x<XK>(v);
       }
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if constexpr (BF) {
-          sum += __uint_as_float(w[q] << 16) + __uint_as_float(w[q] & 0xffff0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
-          sum += f.x + f.y;
-        }
-      }
       *reinterpret_cast<uint4*>(smem + lay.x + ((c >> 2) * p.M + m) * 64 + (c & 3) * 16) = b;
-      // the lanes of a group are in the loop together: their number divides
-      // a row's, and the block's
-      const uint32_t mask = (G == 128 ? 0xffffu << (lane & 16) : G == 64 ? 0xffu << (lane & 24)
-                                                                         : 0xfu << (lane & 28));
-#pragma unroll
-      for (int o = G / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-      if ((c & (G / 8 - 1)) == 0)
-        reinterpret_cast<float*>(smem + lay.xsum)[(c / (G / 8)) * W4_X_ROWS + m] = sum;
     }
     __syncthreads();
     // -------------------------------------------------------------- stages
@@ -452,11 +455,9 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
       const uint32_t xu = static_cast<uint32_t>((ks - first) * W4_UNITS * p.M * 64);
       const uint32_t x_step = static_cast<uint32_t>(p.M * 64);
       const uint32_t tab = sbase + lay.table + (warp * (WR * GROUPS) + g) * 8;
-      const uint32_t xsums = sbase + lay.xsum + (ks - first) * (GROUPS * W4_X_ROWS * 4) + t * 8;
-      // sums of products over a group; binary16: the pairs of spread_codes'
-      // a and b apart, b's 16 times too large
-      constexpr int PARTS = BF ? 1 : 2;
-      float part[PARTS][4];
+      float part[4];                // a group's sums of products,
+      float2 f[2];                  // its factors and zero points in rows g and g + 8
+      uint32_t zh[2] = {0u, 0u};
       // (four units at a time: unrolled further, the loads all move to the
       // front and spill)
       constexpr int UB = 4;
@@ -465,31 +466,27 @@ __global__ void __launch_bounds__(32 * W4_MAX_WARPS, W4_CTAS_PER_SM)
 #pragma unroll
         for (int ui = 0; ui < UB; ++ui) {
           const int u = u0 + ui;
+          const bool start = ui % UPG == 0;  // of the group
+          if (start) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              f[h] = lds64f(tab + (u / UPG * WR + 8 * h) * 8);
+              if constexpr (!BF) zh[h] = zero_pair_high(__float_as_uint(f[h].y));
+            }
+          }
           // rows 8 apart share their low three bits: the same swizzle
           const uint32_t off = codes + (swz ^ static_cast<uint32_t>(u << 4));
           uint32_t al[2], bl[2], ah[2], bh[2];
-          spread_codes<BF>(p, lds32(off), al, bl);
-          spread_codes<BF>(p, lds32(off + 1024), ah, bh);
+          spread_codes<BF>(p, lds32(off), __float_as_uint(f[0].y), zh[0], al, bl);
+          spread_codes<BF>(p, lds32(off + 1024), __float_as_uint(f[1].y), zh[1], ah, bh);
           const uint32_t a[4] = {al[0], ah[0], al[1], ah[1]};
           const uint32_t b[4] = {bl[0], bh[0], bl[1], bh[1]};
           const uint4 x = lds128(x_row + xu + static_cast<uint32_t>(u) * x_step);
-          const bool start = ui % UPG == 0;  // of the group
-          mma_m16n8k16<BF>(part[0], a, x.x, x.y, start);
-          mma_m16n8k16<BF>(part[PARTS - 1], b, x.z, x.w, start && PARTS == 2);
+          mma_m16n8k16<BF>(part, a, x.x, x.y, start);
+          mma_m16n8k16<BF>(part, b, x.z, x.w, false);
           if (ui % UPG == UPG - 1) {
-            const int gi = u / UPG;
-            const float2 sx = lds64f(xsums + gi * (W4_X_ROWS * 4));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 f = lds64f(tab + (gi * WR + 8 * h) * 8);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float v = part[0][2 * h + i];
-                if constexpr (!BF) v = fmaf(part[1][2 * h + i], 0.0625f, v);
-                v = fmaf(f.y, i ? sx.y : sx.x, v);
-                acc[2 * h + i] = fmaf(f.x, v, acc[2 * h + i]);
-              }
-            }
+            for (int i = 0; i < 4; ++i) acc[i] = fmaf(f[i >> 1].x, part[i], acc[i]);
           }
         }
       }

@@ -133,6 +133,60 @@ def test_w4_of_more_rows_than_a_grid_is_high(group, block):
     assert torch.equal(y[-65:], sptg.gemm_w4(x[-65:], codes, scales, z))
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("xdtype", [BF16, F16, S8, E4M3])
+@pytest.mark.parametrize("m,n,k,group", [(1, 300, 4096, 128), (3, 4100, 8192, 64), (5, 70, 2080, 32),
+                                         (8, 1000, 8192, 128), (16, 300, 4096, 64), (40, 200, 2048, 32)])
+def test_w4_weights_at_their_zero_points_add_nothing(m, n, k, group, xdtype, zeros):
+    """All codes equal their zero points: 0.  One code a row that does not: its product alone, rounded once."""
+    g = gen(m + n)
+    dtype = xdtype if xdtype in (BF16, F16) else BF16
+    x, _, scales, z, xs = w4_inputs(g, m, n, k, group, dtype, xdtype, zeros)
+    if xdtype in (BF16, F16):
+        x = x.abs() * 100  # of one sign, so that nothing cancels that should not be there
+    code = (torch.full((n, k), 8, dtype=torch.uint8, device="cuda") if z is None
+            else z.repeat_interleave(group, 1))
+    codes = code[:, 0::2] | code[:, 1::2] << 4
+    assert not sptg.gemm_w4(x, codes, scales, z, x_scales=xs).any()
+    at = torch.randint(0, k, (n,), device="cuda", generator=g)
+    rows = torch.arange(n, device="cuda")
+    old = code[rows, at].int()
+    code[rows, at] = torch.where(old < 15, old + 1, old - 1).to(torch.uint8)
+    codes = code[:, 0::2] | code[:, 1::2] << 4
+    one = torch.where(old < 15, 1.0, -1.0) * scales[rows, at // group].float()
+    want = x[:, at].float() * one  # exact in 32 bits
+    if xs is not None:
+        want = want * xs[:, None]
+    assert torch.equal(sptg.gemm_w4(x, codes, scales, z, x_scales=xs), want.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [(1, 70, 256, 64), (4, 300, 8192, 128), (8, 130, 2080, 32),
+                                         (12, 140, 512, 128)])
+def test_w4_rows_with_infinities_give_what_the_formula_gives(m, n, k, group, zeros, dtype):
+    g = gen(m + n)
+    x, codes, scales, z, _ = w4_inputs(g, m, n, k, group, dtype, dtype, zeros)
+    clean = sptg.gemm_w4(x, codes, scales, z)
+    inf = float("inf")
+    x[0, 100] = inf
+    if m > 1:
+        x[1, 5], x[1, k - 1] = -inf, -inf
+        x[2, 7], x[2, 200] = inf, -inf
+        x[3, k // 2] = float("nan")
+    y = sptg.gemm_w4(x, codes, scales, z)
+    w = torch.stack([codes & 15, codes >> 4], 2).reshape(n, k).double()
+    w = w - (8.0 if z is None else z.double().repeat_interleave(group, 1))
+    w = w * scales.double().repeat_interleave(group, 1)
+    for i in range(min(m, 4)):
+        bad = ~torch.isfinite(x[i])
+        ref = (x[i, bad].double()[None] * w[:, bad]).sum(1)  # what is finite beside them changes nothing
+        assert torch.equal(torch.isnan(y[i]), torch.isnan(ref))
+        fine = ~torch.isnan(ref)
+        assert torch.equal(y[i].double()[fine], ref[fine])
+    assert torch.equal(y[4:], clean[4:])
+
+
 # ----------------------------------------------------------- one after another
 @pytest.mark.parametrize("m", [1, 7, 33])
 def test_operands_written_by_the_call_before(m):

@@ -56,3 +56,27 @@ def test_w4_tiles_of_many_stages(n, k, group, zeros, m, xdtype):
     close_in_the_mean(y, ref)
     for _ in range(5):
         assert torch.equal(y, sptg.gemm_w4(x, codes, scales, z, x_scales=xs))
+
+
+# K in two segments and more, after each of which x is loaded anew, and more stages than a warp's ring
+# holds; segments that end in the middle of the last one
+@pytest.mark.parametrize("m", [1, 5, 8])
+@pytest.mark.parametrize("xdtype", [BF16, F16, S8, E4M3])
+@pytest.mark.parametrize("n,k,group,zeros", [(18001, 24608, 32, True), (18000, 20480, 32, False),
+                                             (8200, 24640, 64, False), (18001, 16640, 64, True),
+                                             (18000, 16512, 128, True), (32768, 8192, 128, False)])
+def test_w4_streams_of_many_segments(n, k, group, zeros, m, xdtype):
+    g = gen(n + m)
+    dtype = xdtype if xdtype in (BF16, F16) else (BF16 if m == 5 else F16)
+    x, codes, scales, z, xs = w4_inputs(g, m, n, k, group, dtype, xdtype, zeros)
+    y = sptg.gemm_w4(x, codes, scales, z, x_scales=xs)
+    c = chosen()
+    stages = -(-(-(-k // 256)) // c["splits"])
+    assert c["x_rows"] == 8 and stages > 2 * c["stages"]
+    if m > 1:
+        assert stages > c["segment"]
+    ref, S = w4_reference(x, codes, scales, z, xs)
+    assert_close(y, ref, S, k)
+    close_in_the_mean(y, ref)
+    for _ in range(5):
+        assert torch.equal(y, sptg.gemm_w4(x, codes, scales, z, x_scales=xs))
