@@ -4,6 +4,12 @@ Argument checks and marshalling only, as in the package's ``gemm``: every step
 runs in the library's CUDA kernels.  Outputs that the caller does not pass are
 allocated on the stream that the call runs on.
 
+``stream`` (a torch.cuda.Stream or a raw handle; by default PyTorch's current
+stream) is where a call runs.  It does not wait for any other: what was written
+on another stream has to be waited for first (``stream.wait_stream``), as has the
+call itself before its results are used elsewhere.  The tensors passed may be
+dropped as soon as the call returns: the allocator learns that the stream uses them.
+
 A decoding step makes these calls for every layer and token, so the checks are
 written for little time: each looks at attributes only, and what a message
 needs is worked out when a check has failed.
@@ -74,8 +80,15 @@ def _empty(shape, dtype, device, stream):
         return _new(shape, dtype=dtype, device=device)
 
 
-def _call(function, device: int, stream, args):
-    handle = _raw_stream(device) if stream is None else _pkg._stream_handle(stream)
+def _call(function, device: int, stream, args, tensors):
+    if stream is None:
+        handle = _raw_stream(device)
+    else:
+        handle = _pkg._stream_handle(stream)
+        user = _stream(stream, device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(user)
     if device == _current_device():
         rc = function(*args, handle)
     else:
@@ -136,7 +149,7 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, out_dtype=None, h=None,
         function = lambda *args: _norm_ex(*args, ctypes.byref(config))  # noqa: E731
     _call(function, device, stream, (
         rows, cols, in_code, code, x.data_ptr(), ldx, residual.data_ptr(), ldr, weight.data_ptr(),
-        eps, h.data_ptr(), ldh, y.data_ptr(), ldy, s))
+        eps, h.data_ptr(), ldh, y.data_ptr(), ldy, s), (x, residual, weight, h, y, scales))
     return h, y, scales
 
 
@@ -176,7 +189,8 @@ def gemm_w4(x, codes, scales, zeros=None, x_scales=None, out=None, stream=None):
     _call(_w4, device, stream, (
         m, n, k, group, code, out_code, x.data_ptr(), ldx,
         None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), ldw,
-        scales.data_ptr(), None if zeros is None else zeros.data_ptr(), out.data_ptr(), ldo))
+        scales.data_ptr(), None if zeros is None else zeros.data_ptr(), out.data_ptr(), ldo),
+        (x, codes, scales, zeros, x_scales, out))
     return out
 
 
@@ -208,7 +222,7 @@ def _by_rows(function, rows, W, offsets, by_k, out, out_dtype, stream, name):
     else:
         ldo = _pitch(out, t, cols, out_dtype, device, "out")
     _call(function, device, stream, (e, t, n, k, pair, offsets.data_ptr(), rows.data_ptr(), ld,
-                                     W.data_ptr(), out.data_ptr(), ldo))
+                                     W.data_ptr(), out.data_ptr(), ldo), (rows, W, offsets, out))
     return out
 
 
@@ -249,5 +263,5 @@ def grouped_gemm_dw(dY, X, offsets, out=None, out_dtype=None, stream=None):
     else:
         _dense(out, (e, n, k), out_dtype, device, "out")
     _call(_dw, device, stream, (e, t, n, k, pair, offsets.data_ptr(), dY.data_ptr(), ldy,
-                                X.data_ptr(), ldx, out.data_ptr()))
+                                X.data_ptr(), ldx, out.data_ptr()), (dY, X, offsets, out))
     return out

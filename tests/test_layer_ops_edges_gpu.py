@@ -3,8 +3,8 @@ import pytest
 import torch
 
 import software_pipelined_tiled_gb300 as sptg
-from test_layer_ops_gpu import (BF16, E4M3, F16, F32, S8, assert_close, check_norm, gen, rand, w4_inputs,
-                                w4_reference)
+from test_layer_ops_gpu import (BF16, E4M3, F16, F32, S8, assert_close, check_norm, gen, offsets_of, rand,
+                                w4_inputs, w4_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -240,3 +240,39 @@ def test_grouped_offsets_that_decrease_are_raised(bad, out_dtype):
             assert torch.equal(call(*args, off, out_dtype=out_dtype), call(*args, good, out_dtype=out_dtype))
     y = sptg.grouped_gemm(X, W, off, out_dtype=out_dtype)
     assert not y[:int(good[0])].any() and not y[int(good[-1]):].any()
+
+
+# ------------------------------------------------------------------- streams
+def _operators(g):
+    """name: (operator, its tensors, other arguments)."""
+    t, n, k, e = 4096, 1024, 2048, 4
+    off = offsets_of([1000, 0, 3000, 96])
+    X, W, dY = rand(g, t, k), rand(g, e, n, k), rand(g, t, n)
+    w4x, codes, scales, z, xs = w4_inputs(g, 256, 4096, 4096, 64, BF16, S8, True)
+    return {"norm": (sptg.add_rms_norm, [rand(g, t, k), rand(g, t, k), rand(g, k)], dict(out_dtype=S8)),
+            "w4": (lambda x, c, s, z, xs, **kw: sptg.gemm_w4(x, c, s, z, x_scales=xs, **kw),
+                   [w4x, codes, scales, z, xs], {}),
+            "y": (sptg.grouped_gemm, [X, W, off], {}), "dx": (sptg.grouped_gemm_dx, [dY, W, off], {}),
+            "dw": (sptg.grouped_gemm_dw, [dY, X, off], {})}
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", ["norm", "w4", "y", "dx", "dw"])
+def test_tensors_dropped_after_a_call_on_another_stream_stay_as_they_are(name, raw):
+    """The stream is still busy with something else when the inputs are dropped and their memory is asked for."""
+    f, args, kw = _operators(gen(60))[name]
+    want = f(*args, **kw)
+    side = torch.cuda.Stream()
+    copies = [a.clone() for a in args]
+    sizes = [a.numel() * a.element_size() for a in args]
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)  # some 20 ms
+    got = f(*copies, stream=side.cuda_stream if raw else side, **kw)
+    del copies
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes]
+    side.synchronize()
+    for a, b in zip(*((want, got) if isinstance(got, tuple) else ((want,), (got,)))):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    del junk
