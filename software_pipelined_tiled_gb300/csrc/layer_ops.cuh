@@ -69,10 +69,8 @@ int make_map_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint
   n.dt = static_cast<int>(dt);
   n.swizzle = static_cast<int>(swizzle);
   const cuuint64_t dims[3] = {inner, rows, planes}, strides[2] = {pitch, plane};
-  const cuuint32_t box[3] = {box_inner, box_rows, box_planes}, estr[3] = {1, 1, 1};
-  const CUresult r = enc(&n.map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t box[3] = {box_inner, box_rows, box_planes};
+  const CUresult r = encode_tiled(enc, &n.map, dt, 3, base, dims, strides, box, swizzle);
   if (r != CUDA_SUCCESS) {
     char b[160];
     snprintf(b, sizeof(b), "cuTensorMapEncodeTiled failed (%d) for %llux%llux%llu", (int)r,

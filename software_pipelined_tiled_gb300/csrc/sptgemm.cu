@@ -303,6 +303,27 @@ int make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const void*
   return rc;
 }
 
+// Encodes a tensor map (element strides of one). This is a call of the driver,
+// which wants a current context: a host thread that has made no call of the
+// runtime's yet (one of a pool, or PyTorch's for gradients) has none until its
+// device is set.
+CUresult encode_tiled(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map,
+                      CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
+                      const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = CUDA_SUCCESS;
+  for (int i = 0; i < 2; ++i) {
+    r = enc(map, dt, rank, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    int dev = 0;
+    if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess ||
+        cudaSetDevice(dev) != cudaSuccess)
+      break;
+  }
+  return r;
+}
+
 int encode_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const void* base,
                   uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t box_inner,
                   uint32_t box_outer, CUtensorMapSwizzle swizzle) {
@@ -314,10 +335,7 @@ int encode_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const voi
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {pitch * static_cast<uint64_t>(esize)};
   cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = encode_tiled(enc, map, dt, 2, base, dims, strides, box, swizzle);
   if (r != CUDA_SUCCESS) {
     char b[160];
     snprintf(b, sizeof(b), "cuTensorMapEncodeTiled failed (%d) for %llux%llu box %ux%u", (int)r,
@@ -362,10 +380,8 @@ int make_map_kchunks(CUtensorMap* map, CUtensorMapDataType dt, const void* base,
   cuuint64_t dims[3] = {64, rows, K / 64};
   cuuint64_t strides[2] = {pitch * 2, 128};
   cuuint32_t box[3] = {64, box_rows, ksub};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r =
+      encode_tiled(enc, map, dt, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   if (r != CUDA_SUCCESS) return SPTG_ERR_ARG;
   ChunkMapEntry& e = t_chunk_maps[t_chunk_next];
   t_chunk_next = (t_chunk_next + 1) % kChunkMapCache;

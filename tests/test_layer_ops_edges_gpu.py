@@ -1,4 +1,6 @@
 """The operators around the dense products where a call is unusual: their waits, their edges and their sizes."""
+import threading
+
 import pytest
 import torch
 
@@ -276,3 +278,35 @@ def test_tensors_dropped_after_a_call_on_another_stream_stay_as_they_are(name, r
     for a, b in zip(*((want, got) if isinstance(got, tuple) else ((want,), (got,)))):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     del junk
+
+
+@pytest.mark.parametrize("name", ["norm", "w4", "w4 row", "y", "dx", "dw", "gemm", "gemm skinny", "gemm int8"])
+def test_first_call_of_a_host_thread(name):
+    """A thread that has made no CUDA call of its own: one of a pool, or automatic differentiation's."""
+    g = gen(61)
+    if name.startswith("gemm"):
+        dtype, m = (S8, 256) if name == "gemm int8" else (BF16, 64 if "skinny" in name else 256)
+        A, B = (torch.randint(-9, 9, (r, 512), device="cuda", generator=g).to(dtype) for r in (m, 384))
+        f, args, kw = sptg.gemm, [A, B], {}
+    else:
+        f, args, kw = _operators(g)[name.split()[0]]
+        if name == "w4 row":
+            args = [a[:1] if a is args[0] or a is args[4] else a for a in args]
+    want, got = f(*args, **kw), []
+    # new addresses, so that no tensor map of theirs is at hand
+    copies = [a.clone() for a in args]
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            got.append(f(*copies, **kw))
+        except Exception as e:  # reported below, on the main thread
+            got.append(e)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not isinstance(got[0], Exception), got[0]
+    for a, b in zip(*((want, got[0]) if isinstance(want, tuple) else ((want,), (got[0],)))):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
