@@ -10,6 +10,9 @@ on another stream has to be waited for first (``stream.wait_stream``), as has th
 call itself before its results are used elsewhere.  The tensors passed may be
 dropped as soon as the call returns: the allocator learns that the stream uses them.
 
+``grouped_gemm`` takes part in PyTorch's automatic differentiation; the other
+calls, like ``gemm``, return tensors without a history.
+
 A decoding step makes these calls for every layer and token, so the checks are
 written for little time: each looks at attributes only, and what a message
 needs is worked out when a check has failed.
@@ -226,6 +229,24 @@ def _by_rows(function, rows, W, offsets, by_k, out, out_dtype, stream, name):
     return out
 
 
+class _GroupedGemm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, offsets, out_dtype):
+        ctx.save_for_backward(X, W, offsets)
+        return _by_rows(_y, X, W, offsets, True, None, out_dtype, None, "X")
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        X, W, offsets = ctx.saved_tensors
+        dY = dY.to(X.dtype)
+        if not dY.is_contiguous() or dY.data_ptr() % 16:
+            dY = dY.clone(memory_format=torch.contiguous_format)
+        dX = grouped_gemm_dx(dY, W, offsets) if ctx.needs_input_grad[0] else None
+        dW = grouped_gemm_dw(dY, X, offsets) if ctx.needs_input_grad[1] else None
+        return dX, dW, None, None
+
+
 def grouped_gemm(X, W, offsets, out=None, out_dtype=None, stream=None):
     """Products grouped by expert: ``Y[t] = X[t] @ W[e].T`` for the rows t of expert e.
 
@@ -233,7 +254,21 @@ def grouped_gemm(X, W, offsets, out=None, out_dtype=None, stream=None):
     GPU, rows ``offsets[e]`` to ``offsets[e + 1] - 1`` belonging to expert e
     (read there: the call does not wait for them).  Rows of no expert get
     zeros.  out_dtype: the operands' type (default) or float32.  Returns Y, T x N.
+
+    Where X or W requires a gradient, backward runs grouped_gemm_dx and
+    grouped_gemm_dw on Y's gradient in the operands' type, and gives gradients of
+    that type; ``out`` is then refused.
     """
+    if (X.requires_grad or W.requires_grad) and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out cannot be given where X or W requires a gradient")
+        if stream is None:
+            return _GroupedGemm.apply(X, W, offsets, out_dtype)
+        stream = _stream(stream, W.device)
+        for t in (X, W, offsets):
+            t.record_stream(stream)
+        with torch.cuda.stream(stream):  # (backward runs there as well)
+            return _GroupedGemm.apply(X, W, offsets, out_dtype)
     return _by_rows(_y, X, W, offsets, True, out, out_dtype, stream, "X")
 
 

@@ -244,6 +244,62 @@ def test_grouped_offsets_that_decrease_are_raised(bad, out_dtype):
     assert not y[:int(good[0])].any() and not y[int(good[-1]):].any()
 
 
+@pytest.mark.parametrize("out_dtype", [None, F32])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_grouped_gemm_in_automatic_differentiation(dtype, out_dtype):
+    """Against the formula in 64 bits, by the bounds of a product (the gradient of Y is exact in 16 bits)."""
+    g = gen(31)
+    sizes, n, k = [19, 0, 40, 70], 48, 56
+    off, o = offsets_of(sizes), [0, 19, 19, 59, 129]
+    X, W, G = rand(g, 135, k, dtype=dtype), rand(g, 4, n, k, dtype=dtype), rand(g, 135, n, dtype=dtype)
+    for t in (X, W):
+        t.requires_grad_()
+    y = sptg.grouped_gemm(X, W, off, out_dtype=out_dtype)
+    assert torch.equal(y, sptg.grouped_gemm(X.detach(), W.detach(), off, out_dtype=out_dtype))
+    y.backward(G.to(y.dtype))
+    assert X.grad.dtype == dtype and W.grad.dtype == dtype
+    x, w, d = X.detach().double(), W.detach().double(), G.double()
+    for e in range(4):
+        r = slice(o[e], o[e + 1])
+        assert_close(X.grad[r], d[r] @ w[e], d[r].abs() @ w[e].abs(), n)
+        assert_close(W.grad[e], d[r].t() @ x[r], d[r].abs().t() @ x[r].abs(), o[e + 1] - o[e])
+    assert not X.grad[129:].any()  # rows of no expert
+    assert torch.equal(X.grad, sptg.grouped_gemm_dx(G, W.detach(), off))
+    assert torch.equal(W.grad, sptg.grouped_gemm_dw(G, X.detach(), off))
+
+
+def test_grouped_gemm_gradients_in_unusual_graphs():
+    g = gen(33)
+    off = offsets_of([30, 2, 0, 68])
+    X, W = rand(g, 100, 64).requires_grad_(), rand(g, 4, 32, 64).requires_grad_()
+    ones = torch.ones(100, 32, dtype=BF16, device="cuda")
+    want = sptg.grouped_gemm_dx(ones, W.detach(), off), sptg.grouped_gemm_dw(ones, X.detach(), off)
+    sptg.grouped_gemm(X, W, off).sum().backward()  # an expanded gradient, strides of zero
+    assert torch.equal(X.grad, want[0]) and torch.equal(W.grad, want[1])
+    wide = torch.ones(100 * 32 + 1, dtype=BF16, device="cuda")[1:].view(100, 32)  # not 16-byte aligned
+    gx, = torch.autograd.grad(sptg.grouped_gemm(X, W.detach(), off), X, wide)
+    assert torch.equal(gx, want[0])
+    gw, = torch.autograd.grad(sptg.grouped_gemm(X.detach(), W, off), W, ones)
+    assert torch.equal(gw, want[1])
+    with torch.no_grad():
+        assert not sptg.grouped_gemm(X, W, off).requires_grad
+        sptg.grouped_gemm(X, W, off, out=torch.empty_like(ones))
+    with pytest.raises(ValueError):
+        sptg.grouped_gemm(X, W, off, out=torch.empty_like(ones))
+    with pytest.raises(ValueError):
+        sptg.grouped_gemm(X, W, off[:3])
+    gx, = torch.autograd.grad(sptg.grouped_gemm(X, W, off), X, ones, create_graph=True)
+    with pytest.raises(RuntimeError):  # the gradient has no derivative of its own
+        gx.sum().backward()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        y = sptg.grouped_gemm(X, W, off, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        gx, gw = torch.autograd.grad(y, (X, W), ones)
+        assert torch.equal(gx, want[0]) and torch.equal(gw, want[1])
+
+
 # ------------------------------------------------------------------- streams
 def _operators(g):
     """name: (operator, its tensors, other arguments)."""
