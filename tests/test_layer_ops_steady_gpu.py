@@ -1,7 +1,8 @@
-"""The 4-bit kernels past their first stages: rings that wrap, barriers that turn, segments that follow each other.
+"""The layer operators past their first stages: rings that wrap, barriers that turn, segments that follow each other.
 
-Small products are cut along K until a CTA has a stage or three; these are wide enough to leave a CTA
-more stages than its ring holds, in every type of x, group size and number of rows.
+Small products with 4-bit weights are cut along K until a CTA has a stage or three; these are wide enough
+to leave a CTA more stages than its ring holds, in every type of x, group size and number of rows.  Every
+operator gives the same bits when it is called again.
 
 Bounds, derived before the first run: each value as in test_layer_ops_gpu.  In the mean, rounding an exact
 value to nearest is off by the unit in the last place over sqrt(12), that is at most 2 u / sqrt(12) =
@@ -13,7 +14,8 @@ import pytest
 import torch
 
 import software_pipelined_tiled_gb300 as sptg
-from test_layer_ops_gpu import BF16, E4M3, F16, S8, U, assert_close, gen, w4_inputs, w4_reference
+from test_layer_ops_gpu import (BF16, E4M3, F16, F32, S8, U, assert_close, gen, offsets_of, rand, w4_inputs,
+                                w4_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +82,53 @@ def test_w4_streams_of_many_segments(n, k, group, zeros, m, xdtype):
     close_in_the_mean(y, ref)
     for _ in range(5):
         assert torch.equal(y, sptg.gemm_w4(x, codes, scales, z, x_scales=xs))
+
+
+# the same bits on every call, for the operators whose kernels hand work from warp to warp
+def _again(f, *args, **kw):
+    first = f(*args, **kw)
+    for _ in range(5):
+        for a, b in zip(*((t if isinstance(t, tuple) else (t,)) for t in (first, f(*args, **kw)))):
+            if a is not None:
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("out_dtype", [E4M3, S8, None])
+@pytest.mark.parametrize("rows,cols", [(1, 4096), (700, 4096), (333, 5000), (1900, 8192), (16384, 8192), (3, 5001)])
+def test_norm_gives_the_same_bits_on_every_call(rows, cols, out_dtype):
+    g = gen(rows)
+    _again(sptg.add_rms_norm, rand(g, rows, cols), rand(g, rows, cols), rand(g, cols), out_dtype=out_dtype)
+
+
+# the sizes of a decoding step, of a prompt's ragged experts, and of rows that fill whole tiles and do not
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("sizes,n,k", [([3, 0, 9, 1, 0, 0, 12, 0, 7], 4096, 2048), ([300, 0, 1025, 17, 700], 1048, 1160),
+                                       ([256, 512, 1000, 1024], 2048, 2048)])
+def test_grouped_gives_the_same_bits_on_every_call(sizes, n, k, out_dtype):
+    g = gen(n)
+    t, off = sum(sizes), offsets_of(sizes)
+    X, W, dY = rand(g, t, k), rand(g, len(sizes), n, k), rand(g, t, n)
+    _again(sptg.grouped_gemm, X, W, off, out_dtype=out_dtype)
+    _again(sptg.grouped_gemm_dx, dY, W, off, out_dtype=out_dtype)
+    _again(sptg.grouped_gemm_dw, dY, X, off, out_dtype=out_dtype)
+
+
+# K cut over a cluster's CTAs
+@pytest.mark.parametrize("m", [1, 8, 16, 33, 64])
+@pytest.mark.parametrize("xdtype", [BF16, S8])
+def test_w4_in_clusters_gives_the_same_bits_on_every_call(m, xdtype):
+    x, codes, scales, z, xs = w4_inputs(gen(m), m, 4096, 8192, 128, BF16, xdtype, True)
+    _again(sptg.gemm_w4, x, codes, scales, z, x_scales=xs)
+    assert chosen()["splits"] > 1
+
+
+# widths of dW's last tile of columns, in steps of 8, past one and past two tiles
+@pytest.mark.parametrize("cols", [104, 112, 120, 136, 144, 232, 360, 368, 2056])
+def test_grouped_dw_of_every_width(cols):
+    g = gen(cols)
+    off, o = offsets_of([70, 33, 0, 128]), [0, 70, 103, 103, 231]
+    X, dY = rand(g, 231, cols), rand(g, 231, 136)
+    dw = sptg.grouped_gemm_dw(dY, X, off, out_dtype=F32)
+    for e in range(4):
+        d, x = dY[o[e]:o[e + 1]].double(), X[o[e]:o[e + 1]].double()
+        assert_close(dw[e], d.t() @ x, d.abs().t() @ x.abs(), o[e + 1] - o[e])
