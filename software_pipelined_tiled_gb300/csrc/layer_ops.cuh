@@ -416,10 +416,10 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   W4Params p;
   int smem, launch_threads = threads;
   if (tile) {
-    // as many stages of codes as fit beside two to four of x
-    p.segment = nt == 64 ? 3 : W4T_MAX_X_STAGES;
+    // as many stages of codes as fit beside three or four of x
+    p.segment = w4t_x_stages(nt);
     p.stages = W4T_MAX_STAGES;
-    while (p.stages > 2 && w4t_smem(xk, nt, rows, p.stages, p.segment) > 232448) --p.stages;
+    while (p.stages > W4T_MIN_STAGES && w4t_smem(xk, nt, rows, p.stages, p.segment) > 232448) --p.stages;
     smem = w4t_smem(xk, nt, rows, p.stages, p.segment);
   } else {
     // Rings of at least two stages, a segment of x (a multiple of the parts

@@ -69,6 +69,12 @@ __host__ __device__ constexpr int w4t_widen(int xk, int ntok) {
 }
 // warps that widen x, where it is 8-bit
 __host__ __device__ constexpr int w4t_widen_x(int xk) { return xk >= W4_S8 ? 4 : 0; }
+// Stages of the ring of codes. Four at least: with an odd number a place in the
+// ring goes from one group of widening warps to the other, and a group may wait
+// for its next turn there only when the copy of the turn between has landed, or
+// that turn's parity would be taken for its own. A group that comes to a stage
+// knows that the one four before it has been multiplied.
+constexpr int W4T_MIN_STAGES = 4;
 constexpr int W4T_MAX_STAGES = 10;
 // Warps for the sums: 8 share 32 rows of x and more (32 rows of binary16 through
 // 32768 x 8192: 52.1 us against 57.7 us with 4).
@@ -99,6 +105,15 @@ __host__ __device__ constexpr int w4t_bars_at(int xk, int ntok, int rows, int st
 __host__ __device__ constexpr int w4t_smem(int xk, int ntok, int rows, int stages, int x_stages) {
   return w4t_bars_at(xk, ntok, rows, stages, x_stages) + W4T_BARS * 8 + 16 + 1024;
 }
+
+// stages of x in their ring
+__host__ __device__ constexpr int w4t_x_stages(int ntok) { return ntok == 64 ? 3 : W4T_MAX_X_STAGES; }
+constexpr bool w4t_fits(int xk, int ntok) {
+  return w4t_smem(xk, ntok, W4T_MAX_ROWS, W4T_MIN_STAGES, w4t_x_stages(ntok)) <= 232448;
+}
+static_assert(w4t_fits(W4_BF16, 64) && w4t_fits(W4_S8, 64) && w4t_fits(W4_BF16, 32) &&
+                  w4t_fits(W4_S8, 32) && w4t_fits(W4_BF16, 16) && w4t_fits(W4_S8, 16),
+              "the shortest ring of codes does not fit");
 
 // The eight codes of a word, less the zero point (exact), as four columns of the
 // operand: a mask and an exponent's bits make numbers of the codes of a word two
@@ -269,7 +284,7 @@ __global__ void __launch_bounds__(w4t_threads(XK, NTOK), 1)
     // the operand
     const uint32_t code0 = static_cast<uint32_t>(r * 128 + (((4 * c) ^ (r & 7)) << 4));
     const uint32_t dst0 = tmem_base + W4T_ACC_COLS + 64 * c + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    int s = group;  // (at least two stages)
+    int s = group;
     uint32_t phase = 0;
     for (int it = group; it < stages; it += GRPS) {
       uint32_t z[ZS];
