@@ -366,3 +366,43 @@ def test_first_call_of_a_host_thread(name):
     assert not isinstance(got[0], Exception), got[0]
     for a, b in zip(*((want, got[0]) if isinstance(want, tuple) else ((want,), (got[0],)))):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_host_threads_on_streams_of_their_own():
+    """Every operator at the same time as the others, and as the dense product, gives the bits that it gives alone."""
+    g = gen(62)
+    calls = [(f, args, kw) for f, args, kw in _operators(g).values()]
+    x, codes, scales, z, xs = w4_inputs(g, 5, 4096, 4096, 64, F16, F16, True)
+    calls.append((sptg.gemm_w4, [x, codes, scales, z], {}))
+    x, codes, scales, z, xs = w4_inputs(g, 16, 1000, 4096, 128, BF16, BF16, False)  # two blocks to an SM would fit
+    calls.append((sptg.gemm_w4, [x, codes, scales, z], {}))
+    calls.append((sptg.gemm, [rand(g, 512, 2048), rand(g, 768, 2048)], {}))
+    alone = [f(*args, **kw) for f, args, kw in calls]
+    torch.cuda.synchronize()
+    results = {}
+
+    def work(t):
+        try:
+            stream, out = torch.cuda.Stream(), []
+            with torch.cuda.stream(stream):
+                for rep in range(8):
+                    for j in range(len(calls)):
+                        i = (j + t + rep) % len(calls)  # threads interleave different kernels
+                        f, args, kw = calls[i]
+                        out.append((i, f(*args, **kw)))
+            stream.synchronize()
+            results[t] = out
+        except Exception as e:  # reported below, on the main thread
+            results[t] = e
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for thread in threads:
+        thread.start()
+    for thread in threads:
+        thread.join()
+    torch.cuda.synchronize()
+    for t in range(4):
+        assert not isinstance(results[t], Exception), results[t]
+        for i, got in results[t]:
+            for a, b in zip(*((v if isinstance(v, tuple) else (v,)) for v in (alone[i], got))):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
