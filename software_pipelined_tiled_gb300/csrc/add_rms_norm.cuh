@@ -22,8 +22,9 @@
 //
 // Memory-bound: 7 bytes an element (x, r in; h, q out) and some ten flops. The
 // row stays in registers (wide rows: in shared memory) between the reduction and
-// the outputs, so x and r are read once. 16384 bf16 rows of 8192 to 8 bits: 152 us,
-// 6.2 TB/s; of 4096, 72 us; 333 rows of 5000: bound by the call from the host.
+// the outputs, so x and r are read once. 16384 bf16 rows of 8192 to e4m3 155 us,
+// 6.1 TB/s, to int8 159 us, to bf16 169 us; of 4096 72 us to e4m3, 76 us to int8;
+// 333 rows of 5000: bound by the call from the host.
 #pragma once
 
 #include <cstdint>

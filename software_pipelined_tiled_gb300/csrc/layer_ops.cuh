@@ -252,12 +252,12 @@ int add_rms_norm(int64_t rows, int64_t cols, int in_type, int out_type, const vo
 // `least` to `most`; the choice whose busiest SM has the least to do wins, in
 // bytes of codes. The CTAs of the streaming kernel, two to an SM, share its rate:
 // fewer and taller ones, one to an SM, do as well and start half as often (one row
-// through 16384 x 4096: 148 of 112 rows 12.4 us, 256 of 64 rows 14.8 us), as long
+// through 16384 x 4096: 148 of 112 rows 12.8 us, 256 of 64 rows 14.5 us), as long
 // as an SM has twelve warps or so (128 of 64 rows, eight warps each, through
-// 8192 x 8192: 19.2 us; 148 of 112 rows 13.2 us) and x need not be loaded in parts,
-// between which a CTA waits (8 rows: 148 CTAs 16.5 us, 296 of half K 15.2 us).
+// 8192 x 8192: 19.1 us; 148 of 112 rows 13.6 us) and x need not be loaded in parts,
+// between which a CTA waits (8 rows: 148 CTAs 15.7 us, 296 of half K 15.0 us).
 // Clusters of 4 and 8 are placed two CTAs to an SM even where SMs are free (one row
-// through 4096 x 4096: 148 CTAs of 112 rows 7.3 us, 256 of 64 rows 5.5 us). The tile
+// through 4096 x 4096: 148 CTAs of 112 rows 8.1 us, 256 of 64 rows 5.8 us). The tile
 // kernel takes a stage in the same time whatever its rows. Starting a round of CTAs
 // counts as 32 KB, a cluster's exchange as 16 KB.
 struct W4Shape {
@@ -374,8 +374,9 @@ int gemm_w4(int64_t M, int64_t N, int64_t K, int group, int x_type, int out_type
   // Up to 8 rows of x: the streaming kernel. More: the tensor-core tile kernel
   // with 16, 32 or 64 rows, in blocks of 64 (groups of 32 columns: of 32) that
   // each pass over the weights. Through 8192 x 8192 (bf16, groups of 128) the
-  // streaming kernel takes 13.2 us for one row and 15.3 us for 8, the tile kernel
-  // 15.2 us for up to 16; through 4096 x 4096 5.5, 7.1 and 7.2 us.
+  // streaming kernel takes 13.6 us for one row and 15.0 us for 8, the tile kernel
+  // 15.8 us for 8 and 9 and 16.4 us for 16; through 4096 x 4096 5.8 and 7.0 us, the
+  // tile kernel 7.7 us for 8 and 8.0 us for 16.
   const bool tile = M > 8;
   const int nt = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : w4t_max_ntok(group);
   const int64_t m_blocks = (M + nt - 1) / nt;

@@ -30,12 +30,13 @@
 //
 // Measured: one bf16 row through 4096 x 4096, 8192 x 8192, 16384 x 4096 and
 // 32768 x 8192 in groups of 128 5.8, 13.6, 12.7 and 34.7 us back to back, 8 rows
-// 7.0, 14.9, 13.4 and 42.5 us; int8 rows through 8192 x 8192 13.9 and 16 us. One
+// 7.0, 15.0, 13.4 and 42.5 us; one int8 row through 8192 x 8192 13.9 us, 8 16.5. One
 // binary16 row through 32768 x 8192, groups of 64 with zero points, 38.0 us
 // (3.9 TB/s; the floor at 6788 GB/s is 21.7 us). The copies alone take 23.4 us;
 // what remains is bound by the issue of the instructions that make operands of the
-// codes. A ring shared by the CTA, x travelling in its stages, needed two CTA-wide
-// barriers a stage and took 46 us, whatever was taken out of the arithmetic.
+// codes (61 % of the slots, 44 % of the integer pipe). A ring shared by the CTA, x
+// travelling in its stages, needed two CTA-wide barriers a stage and took 46 us,
+// whatever was taken out of the arithmetic.
 //
 // The multiply is the warp-wide 16 x 8 x 16 instruction, whose operands live
 // in registers: codes are spread in registers and never stored, and with up to
@@ -199,7 +200,8 @@ __device__ __forceinline__ uint32_t zero_pair_high(uint32_t z2) {
 
 // The eight codes of a word, less the zero point, as column pairs: (0,4), (2,6)
 // in `a`, (1,5), (3,7) in `b`. A mask and an exponent's bits make numbers of the
-// codes of a word two at a time, and one subtraction (exact) takes the zero point
+// codes of a word two at a time (a published method for 4-bit weights; the
+// constants follow from the two formats), and one subtraction (exact) takes the zero point
 // and the exponent's own value off both. Binary16 takes the codes of bits 4-7
 // where they are, as 1024 + 16 code, and a multiply-add brings them down;
 // bfloat16 has room for a code in the low four bits only: three shifts.

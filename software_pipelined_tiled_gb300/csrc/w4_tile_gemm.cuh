@@ -37,17 +37,19 @@
 // of the stages: a barrier that is waited on by its parity may then not run a whole
 // turn ahead of any warp that waits on it (two issuers in turn would allow that).
 //
-// Measured (bf16, groups of 128): 16, 32 and 64 rows through 32768 x 8192 46.7,
-// 52.1 and 64.4 us (the codes alone are 20 us at 6783 GB/s), through 8192 x 8192 15.2,
-// 17.3 and 20.5 us; 61 rows through 5001 x 4128 in groups of 32 19.0 us. Scales and
-// zero points read a lane's groups at a time, where alignment allows it, are worth
-// most in small groups: 16 rows through 8192 x 8192 in groups of 32 with zero points
-// 17.2 us against 25.5 us.
+// Measured (bf16, groups of 128): 16, 32 and 64 rows through 32768 x 8192 48.5,
+// 54.3 and 63.9 us (the codes alone are 20 us at 6788 GB/s), through 8192 x 8192 16.4,
+// 18.1 and 20.7 us; 16 int8 rows 15.8 us; 61 rows through 5001 x 4128 in groups of 32
+// 19.5 us. More rows take a pass for each 64: 256, 1024 and 4096 rows through 8192 x
+// 8192 62, 217 and 837 us (657 TFLOP/s). Scales and zero points read a lane's groups
+// at a time, where alignment allows it, are worth most in small groups: 16 rows
+// through 8192 x 8192 in groups of 32 with zero points went from 25.5 to 17.2 us
+// (18.0 now).
 // Not memory-bound (2.9 TB/s with 16 rows): a stage takes some 1200 cycles, of which
 // the widening (11 to 13 instructions for 8 codes and lane, most of them on the
-// integer pipe: 63 % of its cycles, as many of the issue slots) and the chain widen,
+// integer pipe: 62 % of its cycles, 59 % of the issue slots) and the chain widen,
 // hand over, 16 MMAs (some 500 cycles to issue), commit take about the same. The
-// tensor pipe is busy 7 % (16 rows) to 20 % (64 rows) of the time. A third operand
+// tensor pipe is busy 9 % (16 rows) to 25 % (64 rows) of the time. A third operand
 // (51.5 to 50.6 us) and sleeping instead of polling (no difference) were not kept.
 //
 // Exactness: a widened weight is the integer code - zero point, |.| <= 15, in
