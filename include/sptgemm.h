@@ -292,6 +292,7 @@ typedef enum {
   SPTG_T_BF16 = 1,  /* bfloat16 */
   SPTG_T_S8 = 2,    /* int8; quantised values are -127 ... 127 */
   SPTG_T_E4M3 = 3,  /* 8-bit float, 4 exponent and 3 fraction bits, largest 448 */
+  SPTG_T_F32 = 4,   /* binary32 (a router's logits, sums of gradients) */
   SPTG_T_RANGE_MIN_ = -2147483647 - 1, /* as for sptg_dtype: any int is rejected cleanly */
   SPTG_T_RANGE_MAX_ = 2147483647
 } sptg_type;
@@ -401,6 +402,128 @@ int sptg_grouped_gemm_dx(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype 
 int sptg_grouped_gemm_dw(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype dtype,
                          const int32_t* offsets, const void* dY, int64_t lddy, const void* X,
                          int64_t ldx, void* dW, void* stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * The operators around an expert layer: which experts a row goes to, the rows
+ * sorted by expert for the grouped products, their outputs added up by row, and
+ * the end of a block. As the operators above: asynchronous, no allocation, no
+ * copies to the host, graph capture, the same bits on every call. Rows of
+ * SPTG_T_F16 or SPTG_T_BF16 take any width, pitch and element-aligned pointer; they
+ * are read in 16-byte pieces when the width and every pitch are multiples of 8
+ * and every pointer is 16-byte aligned. Outputs overlap nothing unless said.
+ */
+
+/*
+ * Routing. Of each row of E logits:
+ *
+ *   s_e = 1 / (1 + exp(-l_e))  (sigmoid = 1)  or  exp(l_e) / sum exp(l)  (0)
+ *   key_e = s_e + bias[e]                              (bias may be NULL)
+ *   of `groups` groups of E / groups neighbouring experts the top_groups with the
+ *   largest sums of their group_best (1 or 2) largest keys are kept, and of their
+ *   experts the `top` with the largest keys, largest first
+ *   w = scale * s_e                                    (renormalize = 0)
+ *   w = scale * s_e / (sum of the chosen s)            (renormalize = 1)
+ *
+ * Keys are compared as exact arithmetic would (the kernel goes to 64 bits where
+ * 32 do not settle a choice); equal ones in the order of their experts, as are
+ * groups. Without a bias (or with one of zeros), where groups are 1 or group_best
+ * is 1, logits stand for the keys. An expert whose logit or bias is -infinity is never chosen:
+ * a row with fewer than `top` experts left has -1 with weight 0 in its last
+ * places. A row that holds a NaN (or, with a softmax, +infinity) gets experts 0 ... top
+ * - 1 with weights NaN.
+ *
+ * logits: rows x E of SPTG_T_F16, SPTG_T_BF16 or SPTG_T_F32, row pitch ld;
+ * bias: E; weights, experts: rows x top, dense. E <= 1024, top <= 16, groups <= 32.
+ *
+ * The gradient: dlogits (of the logits' type, row pitch ldd, written whole) from
+ * dweights (rows x top), the logits and the experts that were chosen. Experts
+ * outside [0, E) add nothing; the choice and the bias have no gradient.
+ */
+int sptg_route_experts(int64_t rows, int64_t E, int top, sptg_type type, const void* logits, int64_t ld,
+                       const float* bias, int sigmoid, int groups, int top_groups, int group_best,
+                       int renormalize, float scale, float* weights, int32_t* experts, void* stream);
+int sptg_route_experts_dlogits(int64_t rows, int64_t E, int top, sptg_type type, const void* logits,
+                               int64_t ld, const int32_t* experts, const float* dweights, int sigmoid,
+                               int renormalize, float scale, void* dlogits, int64_t ldd, void* stream);
+
+/*
+ * Dispatch: the rows * top entries (t, j), sorted by experts[t, j], entries of one
+ * expert in their own order; those whose expert lies outside [0, E) come last.
+ *
+ *   places[t, j]            where the entry went, rows x top
+ *   sorted[places[t, j]]    = x[t], rows * top rows of cols
+ *   offsets[e]              the first place of expert e, E + 1 values: what
+ *                           sptg_grouped_gemm takes
+ *
+ * rows * top <= 2^31 - 4096, E <= 1024. The gradient by x is sptg_combine_rows of
+ * the sorted rows' gradient without weights.
+ *
+ * Combination:  out[t] = base[t] + sum_j weights[t, j] * y[places[t, j]]
+ *
+ * in 32 bits, rounded once. y: y_rows x cols; weights: rows x top (NULL: 1); base:
+ * rows x cols, or NULL; out may be base. A place outside [0, y_rows) adds nothing.
+ *
+ * Its gradients:  dy[places[t, j]] = weights[t, j] * dout[t],
+ *                 dweights[t, j] = <y[places[t, j]], dout[t]>
+ *
+ * (base's is dout). places has to name each row of y once, as sptg_dispatch_rows
+ * writes it: a row of dy that none names is left as it was, one that several name
+ * gets the value of one of them. A place outside [0, y_rows) has dweights 0.
+ * dweights may be NULL (then y is not read).
+ */
+int sptg_dispatch_rows(int64_t rows, int64_t cols, int top, int64_t E, sptg_type type, const void* x,
+                       int64_t ldx, const int32_t* experts, void* sorted, int64_t lds, int32_t* places,
+                       int32_t* offsets, void* stream);
+int sptg_combine_rows(int64_t rows, int64_t cols, int top, int64_t y_rows, sptg_type type, const void* y,
+                      int64_t ldy, const int32_t* places, const float* weights, const void* base,
+                      int64_t ldb, void* out, int64_t ldo, void* stream);
+int sptg_combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, sptg_type type,
+                           const void* dout, int64_t ldd, const void* y, int64_t ldy, const int32_t* places,
+                           const float* weights, void* dy, int64_t lddy, float* dweights, void* stream);
+
+/* What a gate multiplies: nothing, a column (cols values), a row (rows values,
+ * ldg apart), or an element (rows x cols, row pitch ldg). */
+typedef enum {
+  SPTG_GATE_NONE = 0,
+  SPTG_GATE_COLS = 1,
+  SPTG_GATE_ROWS = 2,
+  SPTG_GATE_FULL = 3,
+  SPTG_GATE_RANGE_MIN_ = -2147483647 - 1, /* as for sptg_dtype: any int is rejected cleanly */
+  SPTG_GATE_RANGE_MAX_ = 2147483647
+} sptg_gate;
+
+/*
+ * The end of a block: norm of its output y, gate, scaled residual, and the norm
+ * before the next block.
+ *
+ *   u = y * block_weight / sqrt(mean(y^2) + eps)     (block_weight NULL: u = y)
+ *   t = alpha * residual + gate * u                  (fp32)
+ *   h = t rounded                                    (the new residual stream)
+ *   v = t * weight / sqrt(mean(t^2) + eps)           rounded to the rows' type
+ *
+ * h may be y or residual (same pointer and pitch). A row whose sum of squares
+ * passes the fp32 range is normalised to 0.
+ *
+ * The gradients of y, residual, gate, weight and block_weight from dh and dv
+ * (either may be NULL: 0). dy, dresidual and an element-wise dgate are of the rows'
+ * type; dweight, dblock_weight (cols values) and dgate by column (cols) or row (rows, dense)
+ * of out_type: SPTG_T_F32 or the rows' type. They are summed up in fp32 in a fixed order
+ * of the rows, by way of a workspace of sptg_gate_add_rms_norm_grad_workspace
+ * bytes (16-byte aligned; not shared by calls that run at the same time).
+ */
+int sptg_gate_add_rms_norm(int64_t rows, int64_t cols, sptg_type type, const void* y, int64_t ldy,
+                           const void* residual, int64_t ldr, const void* block_weight, const void* gate,
+                           sptg_gate gate_kind, int64_t ldg, float alpha, const void* weight, float eps,
+                           void* h, int64_t ldh, void* v, int64_t ldv, void* stream);
+int64_t sptg_gate_add_rms_norm_grad_workspace(int64_t rows, int64_t cols);
+int sptg_gate_add_rms_norm_grad(int64_t rows, int64_t cols, sptg_type type, const void* dh, int64_t lddh,
+                                const void* dv, int64_t lddv, const void* y, int64_t ldy,
+                                const void* residual, int64_t ldr, const void* block_weight,
+                                const void* gate, sptg_gate gate_kind, int64_t ldg, float alpha,
+                                const void* weight, float eps, void* dy, int64_t lddy, void* dresidual,
+                                int64_t lddr, void* dgate, int64_t lddg, void* dweight, void* dblock_weight,
+                                sptg_type out_type, void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

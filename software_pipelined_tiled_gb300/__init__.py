@@ -24,6 +24,8 @@ __all__ = ["DTYPES", "SptgError", "Config", "load", "gemm", "gemm_host", "gemm_r
            "gemm_skinny_noalloc_raw",
            "stream_scale",
            "add_rms_norm", "gemm_w4", "grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw",
+           "route_experts", "route_experts_dlogits", "dispatch_rows", "dispatch_rows_dx", "combine_rows",
+           "combine_rows_grad", "gate_add_rms_norm", "gate_add_rms_norm_grad",
            "last_config",
            "last_error", "device_error", "status_string", "LIB_PATH", "build"]
 
@@ -41,7 +43,10 @@ EXPORTS = ("sptg_gemm", "sptg_gemm_ex", "sptg_gemm_strided", "sptg_gemm_host",
            "sptg_last_config", "sptg_device_error", "sptg_version", "sptg_gemm_skinny_noalloc",
            "sptg_stream_scale", "sptg_stream_scale_ex", "sptg_add_rms_norm",
            "sptg_add_rms_norm_ex", "sptg_gemm_w4",
-           "sptg_grouped_gemm", "sptg_grouped_gemm_dx", "sptg_grouped_gemm_dw")
+           "sptg_grouped_gemm", "sptg_grouped_gemm_dx", "sptg_grouped_gemm_dw",
+           "sptg_route_experts", "sptg_route_experts_dlogits", "sptg_dispatch_rows",
+           "sptg_combine_rows", "sptg_combine_rows_grad", "sptg_gate_add_rms_norm",
+           "sptg_gate_add_rms_norm_grad_workspace", "sptg_gate_add_rms_norm_grad")
 
 
 class SptgError(RuntimeError):
@@ -118,6 +123,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                              i64, vp, vp]
         for f in (lib.sptg_add_rms_norm, lib.sptg_add_rms_norm_ex, lib.sptg_gemm_w4, lib.sptg_grouped_gemm,
                   lib.sptg_grouped_gemm_dx, lib.sptg_grouped_gemm_dw):
+            f.restype = ctypes.c_int
+        i, fl = ctypes.c_int, ctypes.c_float
+        lib.sptg_route_experts.argtypes = [i64, i64, i, i, vp, i64, vp, i, i, i, i, i, fl, vp, vp, vp]
+        lib.sptg_route_experts_dlogits.argtypes = [i64, i64, i, i, vp, i64, vp, vp, i, i, fl, vp, i64, vp]
+        lib.sptg_dispatch_rows.argtypes = [i64, i64, i, i64, i, vp, i64, vp, vp, i64, vp, vp, vp]
+        lib.sptg_combine_rows.argtypes = [i64, i64, i, i64, i, vp, i64, vp, vp, vp, i64, vp, i64, vp]
+        lib.sptg_combine_rows_grad.argtypes = [i64, i64, i, i64, i, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]
+        lib.sptg_gate_add_rms_norm.argtypes = [i64, i64, i, vp, i64, vp, i64, vp, vp, i, i64, fl, vp, fl,
+                                               vp, i64, vp, i64, vp]
+        lib.sptg_gate_add_rms_norm_grad.argtypes = [i64, i64, i, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
+                                                    i, i64, fl, vp, fl, vp, i64, vp, i64, vp, i64, vp, vp,
+                                                    i, vp, i64, vp]
+        lib.sptg_gate_add_rms_norm_grad_workspace.argtypes = [i64, i64]
+        lib.sptg_gate_add_rms_norm_grad_workspace.restype = i64
+        for f in (lib.sptg_route_experts, lib.sptg_route_experts_dlogits, lib.sptg_dispatch_rows,
+                  lib.sptg_combine_rows, lib.sptg_combine_rows_grad, lib.sptg_gate_add_rms_norm,
+                  lib.sptg_gate_add_rms_norm_grad):
             f.restype = ctypes.c_int
         lib.sptg_version.argtypes = []
         lib.sptg_version.restype = ctypes.c_int
@@ -337,15 +359,22 @@ def device_error(stream=None) -> int:
     return int(load().sptg_device_error(_stream_handle(stream)))
 
 
-# The operators around the products live in layers.py, which imports PyTorch;
-# they are looked up on first use, so that importing the package stays light.
+# The operators around the products live in layers.py and expert_layers.py, which import
+# PyTorch; they are looked up on first use, so that importing the package stays light.
 _LAYERS = ("add_rms_norm", "gemm_w4", "grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw")
+_EXPERT_LAYERS = ("route_experts", "route_experts_dlogits", "dispatch_rows", "dispatch_rows_dx",
+                  "combine_rows", "combine_rows_grad", "gate_add_rms_norm", "gate_add_rms_norm_grad")
 
 
 def __getattr__(name: str):
-    if name not in _LAYERS:
+    if name in _LAYERS:
+        from . import layers as module
+        names = _LAYERS
+    elif name in _EXPERT_LAYERS:
+        from . import expert_layers as module
+        names = _EXPERT_LAYERS
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import layers
-    for n in _LAYERS:
-        globals()[n] = getattr(layers, n)
+    for n in names:
+        globals()[n] = getattr(module, n)
     return globals()[name]

@@ -1,0 +1,31 @@
+// route_experts.cu -- instantiations of the router's kernels.
+#include "route_experts.cuh"
+#include "variants.h"
+
+namespace sptg {
+
+template <int TYPE>
+const void* route_variant_of(int kind) {
+  switch (kind) {
+    case ROUTE_8_8: return reinterpret_cast<const void*>(&route_experts_kernel<TYPE, 8, 8>);
+    case ROUTE_16_8: return reinterpret_cast<const void*>(&route_experts_kernel<TYPE, 16, 8>);
+    case ROUTE_32_8: return reinterpret_cast<const void*>(&route_experts_kernel<TYPE, 32, 8>);
+    case ROUTE_32_16: return reinterpret_cast<const void*>(&route_experts_kernel<TYPE, 32, 16>);
+    case ROUTE_32_32: return reinterpret_cast<const void*>(&route_experts_kernel<TYPE, 32, 32>);
+    default: return reinterpret_cast<const void*>(&route_experts_kernel<TYPE, 32, 64>);
+  }
+}
+
+const void* route_variant(int type, int kind) {
+  return type == ROUTE_F32    ? route_variant_of<ROUTE_F32>(kind)
+         : type == ROUTE_BF16 ? route_variant_of<ROUTE_BF16>(kind)
+                              : route_variant_of<ROUTE_F16>(kind);
+}
+
+const void* route_dlogits_variant(int type) {
+  return type == ROUTE_F32    ? reinterpret_cast<const void*>(&route_experts_dlogits_kernel<ROUTE_F32>)
+         : type == ROUTE_BF16 ? reinterpret_cast<const void*>(&route_experts_dlogits_kernel<ROUTE_BF16>)
+                              : reinterpret_cast<const void*>(&route_experts_dlogits_kernel<ROUTE_F16>);
+}
+
+}  // namespace sptg

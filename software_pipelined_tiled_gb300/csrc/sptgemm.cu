@@ -23,7 +23,10 @@
 #include "sptgemm.h"
 
 #include "add_rms_norm.cuh"  // NormParams
+#include "expert_rows.cuh"  // SortParams, RowsParams
+#include "gate_norm.cuh"  // GateNormParams
 #include "grouped_gemm.cuh"  // GroupedParams
+#include "route_experts.cuh"  // RouteParams
 #include "skinny_cluster_gemm.cuh"  // SkinnyClusterParams
 #include "skinny_gemm.cuh"  // SkinnyParams
 #include "skinny_pair_gemm.cuh"  // SkinnyPairParams
@@ -1813,3 +1816,4 @@ int sptg_gemm_skinny_noalloc(int64_t M, int64_t N, int64_t K, sptg_dtype dtype, 
 
 // The operators around the dense products (their own entry points).
 #include "layer_ops.cuh"
+#include "expert_ops.cuh"

@@ -79,4 +79,25 @@ KernelVariant grouped_variant_dx_f16(int out_kind, int tt);
 KernelVariant grouped_variant_dw_bf16(int out_kind, int tt);
 KernelVariant grouped_variant_dw_f16(int out_kind, int tt);
 
+// The router's kernels (type: RouteType), with the lanes of a warp and the
+// experts of a lane that a row takes; the gradient of its logits.
+enum RouteKind : int { ROUTE_8_8, ROUTE_16_8, ROUTE_32_8, ROUTE_32_16, ROUTE_32_32, ROUTE_32_64 };
+const void* route_variant(int type, int kind);
+const void* route_dlogits_variant(int type);
+
+// Rows to their experts and back, in pieces of 16 bytes or element by element.
+const void* dispatch_sort_variant();
+const void* dispatch_copy_variant(bool vectors);
+const void* combine_rows_variant(bool bf16, bool vectors);
+const void* combine_rows_grad_variant(bool bf16, bool vectors);
+
+// Gate, scaled residual and norms: one or two pieces of 8 elements a thread, or
+// rows of any width and alignment; backwards with blocks of up to 512 threads,
+// up to 1024, those with two pieces each, or any; the sums over the blocks.
+enum GateNormKind : int { GATE_NORM_1, GATE_NORM_2, GATE_NORM_ANY };
+enum GateGradKind : int { GATE_GRAD_512, GATE_GRAD_1024, GATE_GRAD_2048, GATE_GRAD_ANY };
+const void* gate_norm_variant(bool bf16, int kind);
+const void* gate_norm_grad_variant(bool bf16, int kind);
+const void* gate_norm_columns_variant();
+
 }  // namespace sptg
