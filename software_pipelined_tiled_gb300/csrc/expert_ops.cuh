@@ -8,6 +8,10 @@ namespace {
 
 bool off_by(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
+// Rows of these operators stop where a block's next piece is a 32-bit number still.
+constexpr int64_t kMaxCols = static_cast<int64_t>(1) << 30;
+constexpr const char* kRowText = "rows must be in [0, 2^31 - 4096], their elements in [0, 2^30]";
+
 // 16-bit row types and their names.
 bool row_type(int type, bool& bf16, const char*& name) {
   TypeInfo t;
@@ -75,9 +79,11 @@ int route_experts(int64_t rows, int64_t E, int top, int type, const void* logits
   p.size = static_cast<int>(E) / groups;
   int group_slots = 1;
   while (group_slots < groups) group_slots *= 2;
-  constexpr int lanes_of[] = {8, 16, 32, 32, 32, 32}, per_of[] = {8, 8, 8, 16, 32, 64};
+  // (32768 rows of 128 bf16 logits: 12.7 us with 16 experts a lane, 15.1 us with 8; of 256: 22.8
+  // us either way, one row 3.7 us with 8, 4.3 us with 16.)
+  constexpr int lanes_of[] = {8, 8, 16, 32, 32, 32, 32}, per_of[] = {8, 16, 8, 8, 16, 32, 64};
   int v = 0;
-  for (; v < 5; ++v)
+  for (; v < 6; ++v)
     if (top <= lanes_of[v] && group_slots <= lanes_of[v] &&
         ceil_div(p.size, lanes_of[v] / group_slots) <= per_of[v])
       break;
@@ -103,13 +109,20 @@ int route_experts(int64_t rows, int64_t E, int top, int type, const void* logits
   p.groups = groups;
   p.top_groups = top_groups;
   p.group_best = group_best;
-  const int64_t grid = ceil_div(rows, ROUTE_WARPS * (32 / lanes_of[v]));
+  // Several turns a warp fill its lanes with picks (32768 rows of 256 experts in
+  // warps of one row each took 1.5 times as many instructions), where there
+  // are rows for eight warps an SM all the same.
+  p.slots_log2 = top <= 8 ? 3 : 4;
+  const int at_once = 32 / lanes_of[v];
+  const int64_t busy = rows / (static_cast<int64_t>(at_once) * 8 * di.sm_count);
+  p.turns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(lanes_of[v] >> p.slots_log2, busy)));
+  const int64_t grid = ceil_div(rows, ROUTE_WARPS * at_once * p.turns);
   void* args[] = {&p};
   const cudaError_t e = launch_op(route_variant(kind, v), dim3(static_cast<unsigned>(grid)),
                                   32 * ROUTE_WARPS, 0, 1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "route_experts launch");
-  set_config("kernel=route type=%s lanes=%lld per=%lld chunk=%lld wide=%lld grid=%lld", name,
-             {lanes_of[v], per_of[v], p.chunk, p.wide, grid});
+  set_config("kernel=route type=%s lanes=%lld per=%lld chunk=%lld wide=%lld turns=%lld grid=%lld", name,
+             {lanes_of[v], per_of[v], p.chunk, p.wide, p.turns, grid});
   return SPTG_OK;
 }
 
@@ -138,9 +151,10 @@ int route_dlogits(int64_t rows, int64_t E, int top, int type, const void* logits
   const int piece = 16 / bytes;
   RouteGradParams p{logits, ld, rows, experts, dweights, dlogits, ldd, static_cast<int>(E), top, sigmoid, renorm, scale, 0};
   p.wide = E % piece == 0 && ld % piece == 0 && ldd % piece == 0 && !off_by(logits, 16) && !off_by(dlogits, 16);
-  const int64_t grid = ceil_div(rows, ROUTE_WARPS);
+  const int slots = top <= 8 ? 8 : 16;
+  const int64_t grid = ceil_div(rows, ROUTE_WARPS * 32 / slots);
   void* args[] = {&p};
-  const cudaError_t e = launch_op(route_dlogits_variant(kind), dim3(static_cast<unsigned>(grid)),
+  const cudaError_t e = launch_op(route_dlogits_variant(kind, slots), dim3(static_cast<unsigned>(grid)),
                                   32 * ROUTE_WARPS, 0, 1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "route_experts_dlogits launch");
   set_config("kernel=route_dlogits type=%s wide=%lld grid=%lld", name, {p.wide, grid});
@@ -149,7 +163,7 @@ int route_dlogits(int64_t rows, int64_t E, int top, int type, const void* logits
 
 // ------------------------------------------------- rows to experts and back
 int rows_sizes(int64_t rows, int64_t cols, int top) {
-  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return refuse(SPTG_ERR_ARG, kDimText);
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxCols) return refuse(SPTG_ERR_ARG, kRowText);
   if (top < 1 || rows * top > kMaxDim) return refuse(SPTG_ERR_ARG, "top must be at least 1 and rows * top below 2^31");
   return SPTG_OK;
 }
@@ -158,6 +172,42 @@ int rows_sizes(int64_t rows, int64_t cols, int top) {
 unsigned column_parts(int64_t rows, int64_t pieces, int sm_count) {
   const int64_t most = ceil_div(pieces, ROWS_THREADS), want = ceil_div(2 * sm_count, rows);
   return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({most, want, 65535})));
+}
+
+// CTAs of a long sort: a cluster of 16 where the GPU places one, else the 8 that it always does.
+std::map<int, int> g_sort_cluster;
+
+int sort_cluster(int dev, int& ctas) {
+  const void* fn = dispatch_sort_variant();
+  const int smem = sort_smem(DISPATCH_MAX_EXPERTS);
+  int rc = ensure_smem(dev, fn, smem);
+  if (rc) return rc;
+  std::lock_guard<std::mutex> lk(g_mu);
+  const auto it = g_sort_cluster.find(dev);
+  if (it != g_sort_cluster.end()) {
+    ctas = it->second;
+    return SPTG_OK;
+  }
+  ctas = 8;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+    cudaLaunchConfig_t lc;
+    memset(&lc, 0, sizeof(lc));
+    lc.gridDim = dim3(16, 1, 1);
+    lc.blockDim = dim3(32 * SORT_WARPS, 1, 1);
+    lc.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &lc) == cudaSuccess && n > 0) ctas = 16;
+  }
+  cudaGetLastError();
+  g_sort_cluster[dev] = ctas;
+  return SPTG_OK;
 }
 
 int dispatch_rows(int64_t rows, int64_t cols, int top, int64_t E, int type, const void* x, int64_t ldx,
@@ -193,15 +243,21 @@ int dispatch_rows(int64_t rows, int64_t cols, int top, int64_t E, int type, cons
   s.offsets = offsets;
   s.entries = rows * top;
   s.E = static_cast<int>(E);
-  const int ctas = s.entries > 4096 ? SORT_CLUSTER : 1;
+  s.bits = 0;
+  while (E >> s.bits) ++s.bits;
+  int ctas = 1;
+  if (s.entries > 4096) {
+    rc = sort_cluster(dev, ctas);
+    if (rc) return rc;
+  }
   s.per_warp = ceil_div(ceil_div(s.entries, ctas * SORT_WARPS), 32) * 32;
-  rc = ensure_smem(dev, dispatch_sort_variant(), sort_smem(SORT_WARPS, DISPATCH_MAX_EXPERTS));
+  rc = ensure_smem(dev, dispatch_sort_variant(), sort_smem(DISPATCH_MAX_EXPERTS));
   if (rc) return rc;
   void* sort_args[] = {&s};
   cudaError_t e = launch_op(dispatch_sort_variant(), dim3(static_cast<unsigned>(ctas)), 32 * SORT_WARPS,
-                            sort_smem(SORT_WARPS, s.E), ctas, stream, sort_args);
+                            sort_smem(s.E), ctas, stream, sort_args);
   if (e != cudaSuccess) return cuda_fail(e, "dispatch_rows sort launch");
-  const bool vectors = cols % 8 == 0 && in_pieces(x, ldx) && in_pieces(sorted, lds);
+  const bool aligned = cols % 8 == 0 && in_pieces(x, ldx) && in_pieces(sorted, lds);
   if (copies) {
     RowsParams p{};
     p.x = x;
@@ -212,14 +268,14 @@ int dispatch_rows(int64_t rows, int64_t cols, int top, int64_t E, int type, cons
     p.out_rows = s.entries;
     p.cols = static_cast<int>(cols);
     p.top = top;
-    const unsigned parts = column_parts(rows, cols / (vectors ? 8 : 1), di.sm_count);
+    const unsigned parts = column_parts(rows, ceil_div(cols + (aligned ? 0 : 7), 8), di.sm_count);
     void* args[] = {&p};
-    e = launch_op(dispatch_copy_variant(vectors), dim3(static_cast<unsigned>(rows), parts), ROWS_THREADS, 0,
+    e = launch_op(dispatch_copy_variant(aligned), dim3(static_cast<unsigned>(rows), parts), ROWS_THREADS, 0,
                   1, stream, args);
     if (e != cudaSuccess) return cuda_fail(e, "dispatch_rows copy launch");
   }
-  set_config("kernel=dispatch type=%s sort_ctas=%lld per_warp=%lld vectors=%lld", name,
-             {ctas, s.per_warp, vectors});
+  set_config("kernel=dispatch type=%s sort_ctas=%lld per_warp=%lld aligned=%lld", name,
+             {ctas, s.per_warp, aligned});
   return SPTG_OK;
 }
 
@@ -245,7 +301,7 @@ int combine_rows(int64_t rows, int64_t cols, int top, int64_t y_rows, int type, 
   DeviceInfo di;
   rc = device_info(di, dev);
   if (rc) return rc;
-  const bool vectors = cols % 8 == 0 && in_pieces(y, ldy) && in_pieces(out, ldo) && in_pieces(base, ldb);
+  const bool aligned = cols % 8 == 0 && in_pieces(y, ldy) && in_pieces(out, ldo) && in_pieces(base, ldb);
   RowsParams p{};
   p.x = y;
   p.ldx = ldy;
@@ -258,12 +314,12 @@ int combine_rows(int64_t rows, int64_t cols, int top, int64_t y_rows, int type, 
   p.ldo = ldo;
   p.cols = static_cast<int>(cols);
   p.top = top;
-  const unsigned parts = column_parts(rows, cols / (vectors ? 8 : 1), di.sm_count);
+  const unsigned parts = column_parts(rows, ceil_div(cols + (aligned ? 0 : 7), 8), di.sm_count);
   void* args[] = {&p};
-  const cudaError_t e = launch_op(combine_rows_variant(bf16, vectors), dim3(static_cast<unsigned>(rows), parts),
+  const cudaError_t e = launch_op(combine_rows_variant(bf16, aligned), dim3(static_cast<unsigned>(rows), parts),
                                   ROWS_THREADS, 0, 1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "combine_rows launch");
-  set_config("kernel=combine type=%s vectors=%lld parts=%lld", name, {vectors, parts});
+  set_config("kernel=combine type=%s aligned=%lld parts=%lld", name, {aligned, parts});
   return SPTG_OK;
 }
 
@@ -292,7 +348,7 @@ int combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, int t
   DeviceInfo di;
   rc = device_info(di, dev);
   if (rc) return rc;
-  const bool vectors = cols % 8 == 0 && in_pieces(dout, ldd) && in_pieces(dy, lddy) &&
+  const bool aligned = cols % 8 == 0 && in_pieces(dout, ldd) && in_pieces(dy, lddy) &&
                        (!dweights || in_pieces(y, ldy));
   RowsParams p{};
   p.x = y;
@@ -308,20 +364,24 @@ int combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, int t
   p.cols = static_cast<int>(cols);
   p.top = top;
   void* args[] = {&p};
-  const cudaError_t e = launch_op(combine_rows_grad_variant(bf16, vectors), dim3(static_cast<unsigned>(rows)),
+  const cudaError_t e = launch_op(combine_rows_grad_variant(bf16, aligned), dim3(static_cast<unsigned>(rows)),
                                   ROWS_THREADS, 0, 1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "combine_rows_grad launch");
-  set_config("kernel=combine_grad type=%s vectors=%lld", name, {vectors});
+  set_config("kernel=combine_grad type=%s aligned=%lld", name, {aligned});
   return SPTG_OK;
 }
 
 // -------------------------------------------- gate, scaled residual and norms
-constexpr int64_t kGateGradBlocks = 456;  // blocks that add up gradients over rows, at most
+constexpr int kGateRingSmem = 225 * 1024;  // what a ring may take: two rows of five operands of 8192 elements
+
+// Blocks that add up gradients over rows, at most: those of narrow rows are small,
+// and an SM holds more of them.
+int64_t gate_grad_blocks(int64_t cols) { return 456 * std::max<int64_t>(1, std::min<int64_t>(8, 4096 / std::max<int64_t>(cols, 1))); }
 
 int gate_norm_checks(int64_t rows, int64_t cols, int type, int gate_kind, float alpha, float eps, bool& bf16,
                      const char*& name) {
   if (!row_type(type, bf16, name)) return refuse(SPTG_ERR_ARG, "rows are f16 or bf16");
-  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return refuse(SPTG_ERR_ARG, kDimText);
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxCols) return refuse(SPTG_ERR_ARG, kRowText);
   if (gate_kind < SPTG_GATE_NONE || gate_kind > SPTG_GATE_FULL) return refuse(SPTG_ERR_ARG, "unknown kind of gate");
   if (!(eps > 0.0f) || !(eps < INFINITY)) return refuse(SPTG_ERR_ARG, "eps must be positive and finite");
   if (!(alpha > -INFINITY && alpha < INFINITY)) return refuse(SPTG_ERR_ARG, "alpha must be finite");
@@ -330,6 +390,23 @@ int gate_norm_checks(int64_t rows, int64_t cols, int type, int gate_kind, float 
 
 // Threads of a block that holds a row of `pieces` pieces, `per` to a thread.
 int row_threads(int64_t pieces, int per) { return static_cast<int>(ceil_div(ceil_div(pieces, per), 32) * 32); }
+
+// The operands of a ring, in the kernels' order, without those that are null.
+GateRing gate_ring(const void* y, int64_t ldy, const void* x, int64_t ldx, const void* dh, int64_t lddh,
+                   const void* dv, int64_t lddv, const void* gate, int64_t ldg) {
+  GateRing r{};
+  const auto add = [&](const void* p, int64_t ld) {
+    if (p == nullptr) return;
+    r.src[r.ops] = p;
+    r.ld[r.ops++] = ld;
+  };
+  add(y, ldy);
+  add(x, ldx);
+  add(dh, lddh);
+  add(dv, lddv);
+  add(gate, ldg);
+  return r;
+}
 
 int gate_norm(int64_t rows, int64_t cols, int type, const void* y, int64_t ldy, const void* x, int64_t ldx,
               const void* w1, const void* gate, int gate_kind, int64_t ldg, float alpha, const void* w2,
@@ -363,20 +440,50 @@ int gate_norm(int64_t rows, int64_t cols, int type, const void* y, int64_t ldy, 
   if (vectors && pieces <= 2048) {
     kind = pieces <= 512 ? GATE_NORM_1 : GATE_NORM_2;
     threads = row_threads(pieces, kind == GATE_NORM_1 ? 1 : 2);
+  } else if (cols <= 16384 - 8) {  // (a piece more where a row's first is cut by a boundary)
+    kind = GATE_NORM_SHIFTED;
+    threads = row_threads(ceil_div(cols + 7, 8), 2);
+  }
+  int64_t grid = rows;
+  int smem = 0, stages = 0;
+  // Rows for several turns of the blocks that the GPU holds: rings of two rows, four
+  // pieces a thread (16384 rows of 8192: 171 us, a row to a block 211 us, rings with two
+  // pieces a thread 244 us; of 4096: 90, 144 and 108 us; three rows ahead are no faster).
+  // Rows of 512 elements: a row to a block, 36 us for 32768 either way.
+  if (vectors && pieces > 64 && pieces <= 2048 && rows >= 3 * di.sm_count) {
+    const void* fn = gate_norm_variant(bf16, GATE_NORM_RING);
+    const int ring_threads = row_threads(pieces, 4);
+    const int ring_smem = gate_ring_smem(static_cast<int>(cols), gate_kind == SPTG_GATE_FULL ? 3 : 2, 2);
+    Residency res;
+    rc = ensure_smem(dev, fn, kGateRingSmem);
+    if (!rc) rc = residency(res, dev, fn, ring_threads, ring_smem);
+    if (rc) return rc;
+    const int64_t blocks = static_cast<int64_t>(res.blocks) * di.sm_count;
+    if (rows >= 3 * blocks) {
+      kind = GATE_NORM_RING;
+      threads = ring_threads;
+      stages = 2;
+      smem = ring_smem;
+      grid = blocks;
+    }
   }
   GateNormParams p{y, x, w1, w2, gate_kind == SPTG_GATE_NONE ? nullptr : gate, ldy, ldx, ldg, h, v, ldh, ldv,
-                   rows, static_cast<int>(cols), gate_kind, alpha, eps};
+                   rows, static_cast<int>(cols), gate_kind, alpha, eps, {}};
+  p.ring = gate_ring(y, ldy, x, ldx, nullptr, 0, nullptr, 0, gate_kind == SPTG_GATE_FULL ? gate : nullptr, ldg);
+  p.ring.stages = stages;
+  p.ring.error_word = di.error_word;
+  p.ring.timeout_ns = kOpTimeoutNs;
   void* args[] = {&p};
-  const cudaError_t e = launch_op(gate_norm_variant(bf16, kind), dim3(static_cast<unsigned>(rows)), threads, 0,
+  const cudaError_t e = launch_op(gate_norm_variant(bf16, kind), dim3(static_cast<unsigned>(grid)), threads, smem,
                                   1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "gate_add_rms_norm launch");
-  set_config("kernel=gate_norm type=%s kind=%lld threads=%lld", name, {kind, threads});
+  set_config("kernel=gate_norm type=%s kind=%lld threads=%lld grid=%lld stages=%lld", name, {kind, threads, grid, stages});
   return SPTG_OK;
 }
 
 int64_t gate_grad_workspace(int64_t rows, int64_t cols) {
-  if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxDim) return 0;
-  return 3 * std::min(rows, kGateGradBlocks) * cols * 4;
+  if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxCols) return 0;
+  return 2 * std::min(rows, gate_grad_blocks(cols)) * cols * 4;
 }
 
 int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t lddh, const void* dv,
@@ -430,19 +537,35 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
                        in_pieces(w2, 0) && in_pieces(dh, lddh) && in_pieces(dv, lddv) && in_pieces(dy, lddy) &&
                        in_pieces(dx, lddx) && (!by_col || in_pieces(gate, 0)) &&
                        (!full || (in_pieces(gate, ldg) && in_pieces(dgate, lddg)));
-  const int64_t pieces = cols / 8;
+  enum { GATE_GRAD_RING, GATE_GRAD_SHIFTED, GATE_GRAD_ANY };
   int kind = GATE_GRAD_ANY, threads = GATE_ANY_THREADS;
   int64_t blocks = 2 * di.sm_count;
-  if (vectors && pieces <= 2048) {
-    kind = pieces <= 512 ? GATE_GRAD_512 : pieces <= 1024 ? GATE_GRAD_1024 : GATE_GRAD_2048;
-    threads = row_threads(pieces, kind == GATE_GRAD_2048 ? 2 : 1);
-    if (threads > 512) blocks = di.sm_count;
+  int smem = 0, stages = 0;
+  const void* fn = gate_norm_grad_any_variant(bf16);
+  if (cols <= 8192) {
+    kind = vectors ? GATE_GRAD_RING : GATE_GRAD_SHIFTED;
+    fn = bf16 ? gate_norm_grad_bf16(gate_kind, w1 != nullptr, vectors)
+              : gate_norm_grad_f16(gate_kind, w1 != nullptr, vectors);
+    threads = row_threads(ceil_div(cols, 8), 2);
+    if (vectors) {
+      stages = 2;
+      smem = gate_ring_smem(static_cast<int>(cols), 2 + (dh != nullptr) + (dv != nullptr) + full, stages);
+    }
+    Residency res;
+    rc = ensure_smem(dev, fn, kGateRingSmem);
+    if (!rc) rc = residency(res, dev, fn, threads, smem);
+    if (rc) return rc;
+    blocks = static_cast<int64_t>(res.blocks) * di.sm_count;
   }
-  blocks = std::min({rows, blocks, kGateGradBlocks});
+  blocks = std::min({rows, blocks, gate_grad_blocks(cols)});
   const int out_kind = out_type == SPTG_T_F32 ? OUT_F32 : bf16 ? OUT_BF16 : OUT_F16;
   GateNormGradParams p;
   p.f = GateNormParams{y, x, w1, w2, gate_kind == SPTG_GATE_NONE ? nullptr : gate, ldy, ldx, ldg, nullptr,
-                       nullptr, 0, 0, rows, static_cast<int>(cols), gate_kind, alpha, eps};
+                       nullptr, 0, 0, rows, static_cast<int>(cols), gate_kind, alpha, eps, {}};
+  p.f.ring = gate_ring(y, ldy, x, ldx, dh, lddh, dv, lddv, full ? gate : nullptr, ldg);
+  p.f.ring.stages = stages;
+  p.f.ring.error_word = di.error_word;
+  p.f.ring.timeout_ns = kOpTimeoutNs;
   p.dh = dh;
   p.dv = dv;
   p.lddh = lddh;
@@ -456,7 +579,7 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
   p.out_kind = out_kind;
   p.part = static_cast<float*>(workspace);
   void* args[] = {&p};
-  cudaError_t e = launch_op(gate_norm_grad_variant(bf16, kind), dim3(static_cast<unsigned>(blocks)), threads, 0,
+  cudaError_t e = launch_op(fn, dim3(static_cast<unsigned>(blocks)), threads, smem,
                             1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "gate_add_rms_norm_grad launch");
   ColumnSumParams c;
@@ -464,14 +587,16 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
   c.blocks = static_cast<int>(blocks);
   c.cols = static_cast<int>(cols);
   c.out_kind = out_kind;
-  c.out[0] = dw2;
-  c.out[1] = w1 ? dw1 : nullptr;
-  c.out[2] = by_col ? dgate : nullptr;
+  c.dw2 = dw2;
+  c.dw1 = w1 ? dw1 : nullptr;
+  c.dgate = by_col ? dgate : nullptr;
+  c.w1 = w1;
+  c.gate = by_col ? gate : nullptr;
   void* column_args[] = {&c};
-  e = launch_op(gate_norm_columns_variant(), dim3(static_cast<unsigned>(ceil_div(cols, 32)), by_col ? 3 : w1 ? 2 : 1),
+  e = launch_op(gate_norm_columns_variant(bf16), dim3(static_cast<unsigned>(ceil_div(cols, 32)), by_col || w1 ? 2 : 1),
                 1024, 0, 1, stream, column_args);
   if (e != cudaSuccess) return cuda_fail(e, "gate_add_rms_norm_grad columns launch");
-  set_config("kernel=gate_norm_grad type=%s kind=%lld threads=%lld grid=%lld", name, {kind, threads, blocks});
+  set_config("kernel=gate_norm_grad type=%s kind=%lld threads=%lld grid=%lld stages=%lld", name, {kind, threads, blocks, stages});
   return SPTG_OK;
 }
 

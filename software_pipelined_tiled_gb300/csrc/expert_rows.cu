@@ -7,25 +7,25 @@ namespace sptg {
 
 const void* dispatch_sort_variant() { return reinterpret_cast<const void*>(&dispatch_sort_kernel<SORT_WARPS>); }
 
-const void* dispatch_copy_variant(bool vectors) {
-  return vectors ? reinterpret_cast<const void*>(&dispatch_copy_kernel<8>)
-                 : reinterpret_cast<const void*>(&dispatch_copy_kernel<1>);
+const void* dispatch_copy_variant(bool aligned) {
+  return aligned ? reinterpret_cast<const void*>(&dispatch_copy_kernel<true>)
+                 : reinterpret_cast<const void*>(&dispatch_copy_kernel<false>);
 }
 
-const void* combine_rows_variant(bool bf16, bool vectors) {
+const void* combine_rows_variant(bool bf16, bool aligned) {
   if (bf16)
-    return vectors ? reinterpret_cast<const void*>(&combine_rows_kernel<true, 8>)
-                   : reinterpret_cast<const void*>(&combine_rows_kernel<true, 1>);
-  return vectors ? reinterpret_cast<const void*>(&combine_rows_kernel<false, 8>)
-                 : reinterpret_cast<const void*>(&combine_rows_kernel<false, 1>);
+    return aligned ? reinterpret_cast<const void*>(&combine_rows_kernel<true, true>)
+                   : reinterpret_cast<const void*>(&combine_rows_kernel<true, false>);
+  return aligned ? reinterpret_cast<const void*>(&combine_rows_kernel<false, true>)
+                 : reinterpret_cast<const void*>(&combine_rows_kernel<false, false>);
 }
 
-const void* combine_rows_grad_variant(bool bf16, bool vectors) {
+const void* combine_rows_grad_variant(bool bf16, bool aligned) {
   if (bf16)
-    return vectors ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<true, 8>)
-                   : reinterpret_cast<const void*>(&combine_rows_grad_kernel<true, 1>);
-  return vectors ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<false, 8>)
-                 : reinterpret_cast<const void*>(&combine_rows_grad_kernel<false, 1>);
+    return aligned ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<true, true>)
+                   : reinterpret_cast<const void*>(&combine_rows_grad_kernel<true, false>);
+  return aligned ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<false, true>)
+                 : reinterpret_cast<const void*>(&combine_rows_grad_kernel<false, false>);
 }
 
 }  // namespace sptg

@@ -10,19 +10,21 @@
 //
 // All but the sort are bound by memory: each row is read once and written once,
 // and `place` is a permutation, so that each row has one writer and nothing needs
-// an atomic. Rows go through registers in pieces of 8 elements (16 bytes), or
-// element by element where width, pitch or alignment forbid it.
+// an atomic. Rows go through registers in pieces of 8 elements (16 bytes), shifted
+// together where width, pitch or address put them off 16-byte boundaries.
 #pragma once
 
 #include <cstdint>
 
 #include "common.cuh"
+#include "shifted.cuh"
 
 namespace sptg {
 
 constexpr int DISPATCH_MAX_EXPERTS = 1024;
 constexpr int SORT_WARPS = 32;
-constexpr int SORT_CLUSTER = 8;  // CTAs that share a long sort
+constexpr int SORT_MAX_CLUSTER = 16;
+constexpr int SORT_STEPS = 4;  // of 32 entries, whose loads are in flight together
 
 struct SortParams {
   const int32_t* experts;  // entries
@@ -31,12 +33,11 @@ struct SortParams {
   int64_t entries;
   int64_t per_warp;        // entries of a warp, a multiple of 32
   int E;
+  int bits;                // of E
 };
 
-// Counts by warp and expert, then one array for the totals of the CTA.
-__host__ __device__ constexpr int sort_smem(int warps, int E) {
-  return (warps + 1) * (E + 1) * 4;
-}
+// Counts by warp and expert, then the totals of the CTA.
+__host__ __device__ constexpr int sort_smem(int E) { return (SORT_WARPS + 1) * (E + 1) * 4; }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
   uint32_t v;
@@ -44,41 +45,63 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
   return v;
 }
 
-// Stable sort of the entries by expert, by counting: one cluster of CTAs. Every
-// warp has a run of neighbouring entries of its own, counts them by expert, learns
-// from the other warps and CTAs how many entries go before its own of each expert,
-// and goes through its run once more to hand out the places. No atomics: a warp
-// takes 32 entries at a time, and the lanes of equal experts find each other.
-template <int SORT_WARPS>
-__global__ void __launch_bounds__(32 * SORT_WARPS) dispatch_sort_kernel(const SortParams p) {
-  extern __shared__ uint32_t counts[];  // [SORT_WARPS][bins], then the CTA's totals
-  __shared__ uint32_t s_warp[SORT_WARPS];
+// Stable sort of the entries by expert, by counting: one cluster of CTAs, no
+// atomics. Every warp has a run of neighbouring entries of its own. It takes 32 at
+// a time, the lanes of equal experts find each other by the bits of their numbers,
+// and it notes for each entry how many of its expert came before it in the run
+// (in places). When all have been counted, a warp's entries of an expert start
+// behind those of the warps and CTAs before it.
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
+    dispatch_sort_kernel(const __grid_constant__ SortParams p) {
+  extern __shared__ uint32_t counts[];  // [WARPS][bins], then the CTA's totals
+  __shared__ uint32_t s_warp[WARPS];
+  constexpr int THREADS = 32 * WARPS;
+  constexpr uint32_t ALL = 0xffffffffu;
   const int bins = p.E + 1;  // (the last: entries of no expert)
-  uint32_t* totals = counts + SORT_WARPS * bins;
-  constexpr int SORT_THREADS = 32 * SORT_WARPS;
+  uint32_t* totals = counts + WARPS * bins;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t before_me = (1u << lane) - 1u;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(gridDim.x);
-  for (int i = threadIdx.x; i < SORT_WARPS * bins; i += SORT_THREADS) counts[i] = 0;
+  for (int i = threadIdx.x; i < WARPS * bins; i += THREADS) counts[i] = 0;
   __syncthreads();
   grid_dependency_wait();
   uint32_t* mine = counts + warp * bins;
-  const int64_t begin = (static_cast<int64_t>(rank) * SORT_WARPS + warp) * p.per_warp;
+  const int64_t begin = (static_cast<int64_t>(rank) * WARPS + warp) * p.per_warp;
   const int64_t end = min(p.entries, begin + p.per_warp);
-  const auto bin_of = [&](int64_t i) {
-    const int e = p.experts[i];
-    return e < 0 || e >= p.E ? p.E : e;
-  };
-  for (int64_t i = begin + lane; i - lane < end; i += 32) {
-    const int b = i < end ? bin_of(i) : bins;
-    const uint32_t same = __match_any_sync(0xffffffffu, b);
-    if (i < end && lane == __ffs(same) - 1) mine[b] += __popc(same);
-    __syncwarp();
+  const auto bin_of = [&](int e) { return e < 0 || e >= p.E ? p.E : e; };
+  for (int64_t i0 = begin; i0 < end; i0 += 32 * SORT_STEPS) {
+    int b[SORT_STEPS];
+#pragma unroll
+    for (int k = 0; k < SORT_STEPS; ++k) {
+      const int64_t i = i0 + 32 * k + lane;
+      b[k] = i < end ? bin_of(p.experts[i]) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < SORT_STEPS; ++k) {
+      const int64_t i = i0 + 32 * k + lane;
+      if (i - lane >= end) break;
+      uint32_t same = __ballot_sync(ALL, i < end);
+      for (int bit = 0; bit < p.bits; ++bit) {
+        const bool one = (b[k] >> bit) & 1;
+        const uint32_t ones = __ballot_sync(ALL, one);
+        same &= one ? ones : ~ones;
+      }
+      if (i < end) {
+        const uint32_t n = mine[b[k]];
+        p.places[i] = static_cast<int32_t>(n + __popc(same & before_me));
+        __syncwarp(__activemask());
+        if ((same & before_me) == 0) mine[b[k]] = n + __popc(same);
+      }
+      __syncwarp();
+    }
   }
   __syncthreads();
   // entries of each expert in the warps before, and in the CTA
-  for (int b = threadIdx.x; b < bins; b += SORT_THREADS) {
+  for (int b = threadIdx.x; b < bins; b += THREADS) {
     uint32_t sum = 0;
-    for (int w = 0; w < SORT_WARPS; ++w) {
+#pragma unroll 8
+    for (int w = 0; w < WARPS; ++w) {
       const uint32_t n = counts[w * bins + b];
       counts[w * bins + b] = sum;
       sum += n;
@@ -89,27 +112,33 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) dispatch_sort_kernel(const So
   // this thread's expert: entries of it in the CTAs before this one, and in all
   const int e = threadIdx.x;
   uint32_t before = 0, all = 0;
-  if (e < p.E) {
-    const uint32_t at = smem_addr(totals + e);
-    for (int c = 0; c < ctas; ++c) {
-      const uint32_t n = ld_cluster_u32(map_to_cta(at, c));
-      if (c < rank) before += n;
-      all += n;
+  {
+    const uint32_t at = smem_addr(totals + min(e, p.E));
+    uint32_t n[SORT_MAX_CLUSTER];
+#pragma unroll
+    for (int c = 0; c < SORT_MAX_CLUSTER; ++c)
+      n[c] = e < p.E && c < ctas ? ld_cluster_u32(map_to_cta(at, c)) : 0;
+#pragma unroll
+    for (int c = 0; c < SORT_MAX_CLUSTER; ++c) {
+      if (c < rank) before += n[c];
+      all += n[c];
     }
   }
-  uint32_t none_before = 0;  // (of entries of no expert)
-  for (int c = 0; c < rank; ++c) none_before += ld_cluster_u32(map_to_cta(smem_addr(totals + p.E), c));
+  // entries of no expert in the CTAs before this one, the same for each warp
+  uint32_t none_before = lane < rank ? ld_cluster_u32(map_to_cta(smem_addr(totals + p.E), lane)) : 0;
+  none_before = __reduce_add_sync(ALL, none_before);
   // where each expert starts
   uint32_t sum = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+    const uint32_t up = __shfl_up_sync(ALL, sum, o);
     if (lane >= o) sum += up;
   }
   if (lane == 31) s_warp[warp] = sum;
   __syncthreads();
   uint32_t base = 0, live = 0;
-  for (int w = 0; w < SORT_WARPS; ++w) {
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
     const uint32_t n = s_warp[w];
     if (w < warp) base += n;
     live += n;
@@ -119,23 +148,16 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) dispatch_sort_kernel(const So
     if (e < p.E) p.offsets[e] = static_cast<int32_t>(start);
     if (e == 0) p.offsets[p.E] = static_cast<int32_t>(live);
   }
-  if (e < p.E)
-    for (int w = 0; w < SORT_WARPS; ++w) counts[w * bins + e] += start + before;
-  if (e < SORT_WARPS) counts[e * bins + p.E] += live + none_before;
-  cluster_sync();  // (the totals have been read, and this CTA's counts are places now)
-  grid_launch_dependents();
-  for (int64_t i = begin + lane; i - lane < end; i += 32) {
-    const int b = i < end ? bin_of(i) : bins;
-    const uint32_t same = __match_any_sync(0xffffffffu, b);
-    uint32_t place = 0;
-    if (i < end) place = mine[b] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (i < end) {
-      p.places[i] = static_cast<int32_t>(place);
-      if (lane == __ffs(same) - 1) mine[b] += __popc(same);
-    }
-    __syncwarp();
+  if (e < p.E) {
+#pragma unroll 8
+    for (int w = 0; w < WARPS; ++w) counts[w * bins + e] += start + before;
   }
+  if (e < WARPS) counts[e * bins + p.E] += live + none_before;
+  cluster_sync();  // (the totals have been read, and this CTA's counts are first places now)
+  grid_launch_dependents();
+#pragma unroll 4
+  for (int64_t i = begin + lane; i < end; i += 32)
+    p.places[i] += static_cast<int32_t>(mine[bin_of(p.experts[i])]);
 }
 
 struct RowsParams {
@@ -158,83 +180,75 @@ struct RowsParams {
 constexpr int ROWS_THREADS = 128;
 constexpr int ROWS_AT_ONCE = 8;  // entries of a row whose loads are in flight together
 
-template <int VEC>
-struct RowPiece {
-  uint4 v;
-};
-template <>
-struct RowPiece<1> {
-  uint16_t v;
-};
-
-template <int VEC>
-__device__ __forceinline__ RowPiece<VEC> load_piece(const void* base, int64_t row, int64_t ld, int i) {
-  RowPiece<VEC> r;
-  const uint16_t* p = static_cast<const uint16_t*>(base) + row * ld;
-  if constexpr (VEC == 8)
-    r.v = reinterpret_cast<const uint4*>(p)[i];
-  else
-    r.v = p[i];
-  return r;
+__device__ __forceinline__ const uint16_t* row_of(const void* base, int64_t row, int64_t ld) {
+  return static_cast<const uint16_t*>(base) + row * ld;
+}
+__device__ __forceinline__ uint16_t* row_of(void* base, int64_t row, int64_t ld) {
+  return static_cast<uint16_t*>(base) + row * ld;
 }
 
-template <int VEC>
-__device__ __forceinline__ void store_piece(void* base, int64_t row, int64_t ld, int i,
-                                            const RowPiece<VEC>& r) {
-  uint16_t* p = static_cast<uint16_t*>(base) + row * ld;
-  if constexpr (VEC == 8)
-    reinterpret_cast<uint4*>(p)[i] = r.v;
-  else
-    p[i] = r.v;
-}
-
-template <bool BF16, int VEC>
-__device__ __forceinline__ void unpack_piece(const RowPiece<VEC>& r, float (&f)[VEC]) {
-  if constexpr (VEC == 8) {
-    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+template <bool BF16>
+__device__ __forceinline__ void unpack_piece(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (BF16) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = h.x;
-        f[2 * i + 1] = h.y;
-      }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
     }
-  } else if constexpr (BF16) {
-    f[0] = __uint_as_float(static_cast<uint32_t>(r.v) << 16);
-  } else {
-    f[0] = __half2float(__ushort_as_half(r.v));
   }
 }
 
-template <bool BF16, int VEC>
-__device__ __forceinline__ RowPiece<VEC> pack_piece(const float (&f)[VEC]) {
+template <bool BF16>
+__device__ __forceinline__ uint4 pack_piece(const float (&f)[8]) {
   constexpr int OUT = BF16 ? OUT_BF16 : OUT_F16;
-  RowPiece<VEC> r;
-  if constexpr (VEC == 8)
-    r.v = make_uint4(pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]), pack2<OUT>(f[4], f[5]),
-                     pack2<OUT>(f[6], f[7]));
+  return make_uint4(pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]), pack2<OUT>(f[4], f[5]),
+                    pack2<OUT>(f[6], f[7]));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float to_float(uint16_t v) {
+  if constexpr (BF16)
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
   else
-    r.v = static_cast<uint16_t>(pack2<OUT>(f[0], 0.0f));
-  return r;
+    return __half2float(__ushort_as_half(v));
+}
+template <bool BF16>
+__device__ __forceinline__ uint16_t from_float(float v) {
+  return static_cast<uint16_t>(pack2<BF16 ? OUT_BF16 : OUT_F16>(v, 0.0f));
 }
 
 // Rows of x to their places: a block to a row and a part of its columns
 // (blockIdx.y). A place outside of the sorted rows is passed over.
-template <int VEC>
-__global__ void __launch_bounds__(ROWS_THREADS) dispatch_copy_kernel(const RowsParams p) {
+template <bool ALIGNED>
+__global__ void __launch_bounds__(ROWS_THREADS) dispatch_copy_kernel(const __grid_constant__ RowsParams p) {
   const int64_t row = blockIdx.x;
   grid_dependency_wait();
-  const int pieces = p.cols / VEC;
+  const uint16_t* x = row_of(p.x, row, p.ldx);
   const int32_t* places = p.places + row * p.top;
-  for (int i = blockIdx.y * ROWS_THREADS + threadIdx.x; i < pieces; i += gridDim.y * ROWS_THREADS) {
-    const RowPiece<VEC> v = load_piece<VEC>(p.x, row, p.ldx, i);
+  const int thread = blockIdx.y * ROWS_THREADS + threadIdx.x, threads = gridDim.y * ROWS_THREADS;
+  if constexpr (ALIGNED) {
+    for (int c = 8 * thread; c < p.cols; c += 8 * threads) {
+      const uint4 v = *reinterpret_cast<const uint4*>(x + c);
+      for (int j = 0; j < p.top; ++j) {
+        const int64_t to = places[j];
+        if (to >= 0 && to < p.out_rows) *reinterpret_cast<uint4*>(row_of(p.out, to, p.ldo) + c) = v;
+      }
+    }
+  } else {  // cut by each row written; x from L1 for all but the first
     for (int j = 0; j < p.top; ++j) {
       const int64_t to = places[j];
-      if (to >= 0 && to < p.out_rows) store_piece<VEC>(p.out, to, p.ldo, i, v);
+      if (to < 0 || to >= p.out_rows) continue;
+      uint16_t* out = row_of(p.out, to, p.ldo);
+      const CutRow cut(out, p.cols);
+#pragma unroll 2
+      for (int c = cut.body + 8 * thread; c < cut.tail; c += 8 * threads)
+        *reinterpret_cast<uint4*>(out + c) = shifted(load_words(x + c));
+      for (int i = thread; i < cut.ends; i += threads) out[cut.end(i)] = x[cut.end(i)];
     }
   }
   grid_launch_dependents();
@@ -242,54 +256,81 @@ __global__ void __launch_bounds__(ROWS_THREADS) dispatch_copy_kernel(const RowsP
 
 // Sums of the rows that a row's places name, in 32 bits and in the order of the
 // places, rounded once. A place outside of y counts as a row of zeros.
-template <bool BF16, int VEC>
-__global__ void __launch_bounds__(ROWS_THREADS) combine_rows_kernel(const RowsParams p) {
+template <bool BF16, bool ALIGNED>
+__global__ void __launch_bounds__(ROWS_THREADS) combine_rows_kernel(const __grid_constant__ RowsParams p) {
   const int64_t row = blockIdx.x;
   grid_dependency_wait();
-  const int pieces = p.cols / VEC;
   const int32_t* places = p.places + row * p.top;
   const float* weights = p.weights ? p.weights + row * p.top : nullptr;
-  for (int i = blockIdx.y * ROWS_THREADS + threadIdx.x; i < pieces; i += gridDim.y * ROWS_THREADS) {
-    float sum[VEC];
-    if (p.base) {
-      unpack_piece<BF16, VEC>(load_piece<VEC>(p.base, row, p.ldb, i), sum);
-    } else {
+  const uint16_t* base = p.base ? row_of(p.base, row, p.ldb) : nullptr;
+  uint16_t* out = row_of(p.out, row, p.ldo);
+  const int thread = blockIdx.y * ROWS_THREADS + threadIdx.x, threads = gridDim.y * ROWS_THREADS;
+  // All rows' loads of a piece (Raw) are in flight before the first is used.
+  const auto add_rows = [&](auto raw, auto load, auto add) {
+    using Raw = decltype(raw);
+    constexpr int AT_ONCE = ALIGNED ? ROWS_AT_ONCE : ROWS_AT_ONCE / 2;
+    for (int j0 = 0; j0 < p.top; j0 += AT_ONCE) {
+      Raw v[AT_ONCE];
+      float w[AT_ONCE];
+      bool in[AT_ONCE];
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) sum[c] = 0.0f;
-    }
-    for (int j0 = 0; j0 < p.top; j0 += ROWS_AT_ONCE) {
-      RowPiece<VEC> v[ROWS_AT_ONCE];
-      float w[ROWS_AT_ONCE];
-      bool in[ROWS_AT_ONCE];
-#pragma unroll
-      for (int j = 0; j < ROWS_AT_ONCE; ++j) {
+      for (int j = 0; j < AT_ONCE; ++j) {
         const int64_t from = j0 + j < p.top ? places[j0 + j] : -1;
         in[j] = from >= 0 && from < p.x_rows;
         w[j] = in[j] && weights ? weights[j0 + j] : 1.0f;
-        if (in[j]) v[j] = load_piece<VEC>(p.x, from, p.ldx, i);
+        if (in[j]) v[j] = load(row_of(p.x, from, p.ldx));
       }
 #pragma unroll
-      for (int j = 0; j < ROWS_AT_ONCE; ++j) {
-        if (!in[j]) continue;
-        float f[VEC];
-        unpack_piece<BF16, VEC>(v[j], f);
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) sum[c] += w[j] * f[c];
-      }
+      for (int j = 0; j < AT_ONCE; ++j)
+        if (in[j]) add(v[j], w[j]);
     }
-    store_piece<VEC>(p.out, row, p.ldo, i, pack_piece<BF16, VEC>(sum));
+  };
+  float sum[8];
+  const auto add_piece = [&](const uint4& v, float w) {
+    float f[8];
+    unpack_piece<BF16>(v, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] += w * f[k];
+  };
+  const auto start_piece = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+    if (base)
+      unpack_piece<BF16>(ALIGNED ? *reinterpret_cast<const uint4*>(base + c) : shifted(load_words(base + c)), sum);
+  };
+  if constexpr (ALIGNED) {
+    for (int c = 8 * thread; c < p.cols; c += 8 * threads) {
+      start_piece(c);
+      add_rows(uint4(), [&](const uint16_t* y) { return *reinterpret_cast<const uint4*>(y + c); }, add_piece);
+      *reinterpret_cast<uint4*>(out + c) = pack_piece<BF16>(sum);
+    }
+  } else {
+    const CutRow cut(out, p.cols);
+    for (int c = cut.body + 8 * thread; c < cut.tail; c += 8 * threads) {
+      start_piece(c);
+      add_rows(ShiftedPiece(), [&](const uint16_t* y) { return load_words(y + c); },
+               [&](const ShiftedPiece& v, float w) { add_piece(shifted(v), w); });
+      *reinterpret_cast<uint4*>(out + c) = pack_piece<BF16>(sum);
+    }
+    for (int i = thread; i < cut.ends; i += threads) {
+      const int c = cut.end(i);
+      float s = base ? to_float<BF16>(base[c]) : 0.0f;
+      add_rows(uint16_t(), [&](const uint16_t* y) { return y[c]; },
+               [&](uint16_t v, float w) { s += w * to_float<BF16>(v); });
+      out[c] = from_float<BF16>(s);
+    }
   }
   grid_launch_dependents();
 }
 
 // Gradients of the sum by y and by the weights, a block to a row: a piece of
 // dout is multiplied by each weight for dy, and by each row of y for dw.
-template <bool BF16, int VEC>
-__global__ void __launch_bounds__(ROWS_THREADS) combine_rows_grad_kernel(const RowsParams p) {
+template <bool BF16, bool ALIGNED>
+__global__ void __launch_bounds__(ROWS_THREADS) combine_rows_grad_kernel(const __grid_constant__ RowsParams p) {
   __shared__ float s_sum[ROWS_THREADS / 32][ROWS_AT_ONCE];
   const int64_t row = blockIdx.x;
   grid_dependency_wait();
-  const int pieces = p.cols / VEC;
+  const uint16_t* dout = row_of(p.dout, row, p.ldd);
   const int32_t* places = p.places + row * p.top;
   const float* weights = p.weights ? p.weights + row * p.top : nullptr;
   for (int j0 = 0; j0 < p.top; j0 += ROWS_AT_ONCE) {
@@ -302,26 +343,52 @@ __global__ void __launch_bounds__(ROWS_THREADS) combine_rows_grad_kernel(const R
       w[j] = at[j] >= 0 && weights ? weights[j0 + j] : 1.0f;
       dot[j] = 0.0f;
     }
-    for (int i = threadIdx.x; i < pieces; i += ROWS_THREADS) {
-      float d[VEC];
-      unpack_piece<BF16, VEC>(load_piece<VEC>(p.dout, row, p.ldd, i), d);
-      RowPiece<VEC> v[ROWS_AT_ONCE];
+    // one piece of dy and its part of dw
+    const auto piece = [&](int j, uint16_t* dy, const float (&d)[8], const uint4& y) {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = d[k] * w[j];
+      *reinterpret_cast<uint4*>(dy) = pack_piece<BF16>(f);
       if (p.dweights) {
+        unpack_piece<BF16>(y, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dot[j] += d[k] * f[k];
+      }
+    };
+    if constexpr (ALIGNED) {
+      for (int c = 8 * threadIdx.x; c < p.cols; c += 8 * ROWS_THREADS) {
+        float d[8];
+        unpack_piece<BF16>(*reinterpret_cast<const uint4*>(dout + c), d);
+        uint4 v[ROWS_AT_ONCE];
+        if (p.dweights) {
+#pragma unroll
+          for (int j = 0; j < ROWS_AT_ONCE; ++j)
+            if (at[j] >= 0) v[j] = *reinterpret_cast<const uint4*>(row_of(p.x, at[j], p.ldx) + c);
+        }
 #pragma unroll
         for (int j = 0; j < ROWS_AT_ONCE; ++j)
-          if (at[j] >= 0) v[j] = load_piece<VEC>(p.x, at[j], p.ldx, i);
+          if (at[j] >= 0) piece(j, row_of(p.out, at[j], p.ldo) + c, d, v[j]);
       }
+    } else {  // cut by each row of dy; dout from L1 for all but the first
 #pragma unroll
       for (int j = 0; j < ROWS_AT_ONCE; ++j) {
         if (at[j] < 0) continue;
-        float f[VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) f[c] = d[c] * w[j];
-        store_piece<VEC>(p.out, at[j], p.ldo, i, pack_piece<BF16, VEC>(f));
-        if (p.dweights) {
-          unpack_piece<BF16, VEC>(v[j], f);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) dot[j] += d[c] * f[c];
+        uint16_t* dy = row_of(p.out, at[j], p.ldo);
+        // (without dw y is not read, and may not be there)
+        const uint16_t* y = p.dweights ? row_of(p.x, at[j], p.ldx) : dout;
+        const CutRow cut(dy, p.cols);
+#pragma unroll 2
+        for (int c = cut.body + 8 * threadIdx.x; c < cut.tail; c += 8 * ROWS_THREADS) {
+          const ShiftedPiece a = load_words(dout + c), b = load_words(y + c);
+          float d[8];
+          unpack_piece<BF16>(shifted(a), d);
+          piece(j, dy + c, d, shifted(b));
+        }
+        for (int i = threadIdx.x; i < cut.ends; i += ROWS_THREADS) {
+          const int c = cut.end(i);
+          const float d = to_float<BF16>(dout[c]);
+          dot[j] += d * to_float<BF16>(y[c]);
+          dy[c] = from_float<BF16>(d * w[j]);
         }
       }
     }

@@ -16,19 +16,40 @@
 // forward call, rows' statistics are cheaper formed anew than written and read.
 //
 // Memory-bound: 8 bytes an element forward, 12 backward (16-bit rows, dh and dv
-// both given). A row stays in registers between its reductions. Backwards a block
-// goes through rows of its own choice and keeps the sums over rows (dw1, dw2, dg of
-// columns) in registers; its sums go to a workspace and a second kernel adds
-// those of all blocks up, in a fixed order.
+// both given). A row stays on the SM between its reductions. Backwards a block
+// goes through rows of its own choice and keeps two sums over rows for each column
+// in registers: of dv hn, which is dw2, and of e = dh' yn, from which both dw1 = g e and a
+// column's dg = w1 e follow (g inside the sum where it differs from row to row). They go
+// to a workspace, and a second kernel adds those of all blocks up, in a fixed order.
 #pragma once
 
 #include <cstdint>
 
 #include "common.cuh"
+#include "shifted.cuh"
 
 namespace sptg {
 
 enum GateKind : int { GATE_NONE = 0, GATE_COLS = 1, GATE_ROWS = 2, GATE_FULL = 3 };
+
+// A ring of rows in shared memory, filled by bulk copies that run ahead of the
+// block: the rows of up to five operands and a barrier to a stage. Row i of a block
+// is row blockIdx.x + i * gridDim.x of the call.
+constexpr int GATE_MAX_STAGES = 4;
+constexpr int GATE_MAX_OPS = 5;
+__host__ __device__ constexpr int gate_row_bytes(int cols) { return (2 * cols + 127) & ~127; }
+__host__ __device__ constexpr int gate_ring_smem(int cols, int ops, int stages) {
+  return stages * ops * gate_row_bytes(cols) + 128;
+}
+
+struct GateRing {
+  const void* src[GATE_MAX_OPS];  // y, x, dh if given, dv if given, the gate if full
+  int64_t ld[GATE_MAX_OPS];
+  int ops, stages;
+  unsigned int* error_word;  // where a wait that runs out reports
+  uint64_t timeout_ns;
+  int inject_stall;          // test hook: a block's second row is never copied
+};
 
 struct GateNormParams {
   const void* y;
@@ -43,6 +64,7 @@ struct GateNormParams {
   int64_t rows;
   int cols, gate_kind;
   float alpha, eps;
+  GateRing ring;
 };
 
 struct GateNormGradParams {
@@ -56,13 +78,17 @@ struct GateNormGradParams {
   void* dgate;       // ROWS, FULL
   int64_t lddg;
   int out_kind;      // of ROWS' dgate: OUT_F32 or the rows' type
-  float* part;       // [3][blocks][cols]: w2, w1, gate
+  float* part;       // [2][blocks][cols]: sums of dv hn, and of e
 };
 
 struct ColumnSumParams {
   const float* part;
   int blocks, cols, out_kind;
-  void* out[3];      // null: not wanted
+  void* dw2;
+  void* dw1;         // null: not wanted
+  void* dgate;       // of columns, or null
+  const void* w1;    // what the second sum is multiplied by for dgate (null: 1)
+  const void* gate;  // and for dw1 (null: 1)
 };
 
 // Sums over a block, the same for each thread: lanes by halves, then warps in
@@ -127,28 +153,58 @@ __device__ __forceinline__ float reciprocal_rms(float sumsq, int cols, float eps
   return 1.0f / sqrtf(sumsq / static_cast<float>(cols) + eps);
 }
 
-// One row to a block, PER pieces of 8 elements a thread.
-template <bool BF16, int PER>
-__global__ void __launch_bounds__(1024) gate_norm_kernel(const GateNormParams p) {
+// One row to a block, PER pieces of 8 elements a thread (not ALIGNED: pieces by h's
+// 16-byte boundaries, so that h may be y or x). h may be y or x: each thread has read
+// what it writes.
+template <bool BF16, int PER, bool ALIGNED>
+__global__ void __launch_bounds__(1024) gate_norm_kernel(const __grid_constant__ GateNormParams p) {
   __shared__ float s_sum[2][32];
   const int64_t row = blockIdx.x;
-  const int pieces = p.cols >> 3;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  grid_dependency_wait();
-  uint4 yv[PER], xv[PER], w1[PER], w2[PER], gv[PER];
-  const uint4* py = row_pieces(p.y, row, p.ldy);
-  const uint4* px = row_pieces(p.x, row, p.ldx);
+  const uint16_t* y = static_cast<const uint16_t*>(p.y) + row * p.ldy;
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ldx;
+  uint16_t* h_row = static_cast<uint16_t*>(p.h) + row * p.ldh;
+  uint16_t* v_row = static_cast<uint16_t*>(p.v) + row * p.ldv;
+  const uint16_t* w1 = static_cast<const uint16_t*>(p.w1);
+  const uint16_t* w2 = static_cast<const uint16_t*>(p.w2);
   const bool by_column = p.gate_kind == GATE_COLS || p.gate_kind == GATE_FULL;
-  const uint4* pg = row_pieces(p.gate, p.gate_kind == GATE_FULL ? row : 0, p.ldg);
+  const uint16_t* gate = static_cast<const uint16_t*>(p.gate) + (p.gate_kind == GATE_FULL ? row * p.ldg : 0);
+  const int start = ALIGNED ? 0 : -shift_of(h_row);
+  const auto first = [&](int i) { return start + 8 * static_cast<int>(threadIdx.x + i * blockDim.x); };
+  const auto load = [&](const uint16_t* from, int i) {
+    return first(i) < p.cols ? load_piece<ALIGNED>(from, first(i), p.cols) : none;
+  };
+  grid_dependency_wait();
+  uint4 yv[PER], xv[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int at = threadIdx.x + i * blockDim.x;
-    const bool in = at < pieces;
-    yv[i] = in ? __ldcs(py + at) : none;
-    xv[i] = in ? __ldcs(px + at) : none;
-    gv[i] = in && by_column ? pg[at] : none;
-    w1[i] = in && p.w1 ? static_cast<const uint4*>(p.w1)[at] : none;
-    w2[i] = in ? static_cast<const uint4*>(p.w2)[at] : none;
+    if constexpr (ALIGNED) {  // read once
+      yv[i] = first(i) < p.cols ? __ldcs(reinterpret_cast<const uint4*>(y + first(i))) : none;
+      xv[i] = first(i) < p.cols ? __ldcs(reinterpret_cast<const uint4*>(x + first(i))) : none;
+    }
+  }
+  uint4 w1v[PER], w2v[PER], gv[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (!ALIGNED) {
+      if (inside_row(first(i), p.cols)) {
+        const ShiftedPiece a = load_words(y + first(i)), b = load_words(x + first(i));
+        yv[i] = shifted(a);
+        xv[i] = shifted(b);
+      } else {
+        // (the row's ends: all loads in one branch, so that they are in flight together)
+        const bool in = first(i) < p.cols;
+        yv[i] = in ? load_elements(y, first(i), p.cols) : none;
+        xv[i] = in ? load_elements(x, first(i), p.cols) : none;
+        gv[i] = in && by_column ? load_elements(gate, first(i), p.cols) : none;
+        w1v[i] = in && p.w1 ? load_elements(w1, first(i), p.cols) : none;
+        w2v[i] = in ? load_elements(w2, first(i), p.cols) : none;
+        continue;
+      }
+    }
+    gv[i] = by_column ? load(gate, i) : none;
+    w1v[i] = p.w1 ? load(w1, i) : none;
+    w2v[i] = load(w2, i);
   }
   const float gr = p.gate_kind == GATE_ROWS ? gate_load<BF16>(p.gate, row * p.ldg) : 1.0f;
   float r1 = 1.0f;
@@ -156,10 +212,10 @@ __global__ void __launch_bounds__(1024) gate_norm_kernel(const GateNormParams p)
     float sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      float y[8];
-      gate_unpack<BF16>(yv[i], y);
+      float f[8];
+      gate_unpack<BF16>(yv[i], f);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum[0] += y[c] * y[c];
+      for (int c = 0; c < 8; ++c) sum[0] += f[c] * f[c];
     }
     block_sums<1>(sum, s_sum[0]);
     r1 = reciprocal_rms(sum[0], p.cols, p.eps);
@@ -168,43 +224,40 @@ __global__ void __launch_bounds__(1024) gate_norm_kernel(const GateNormParams p)
   float sum[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    float y[8], x[8], w[8], g[8];
-    gate_unpack<BF16>(yv[i], y);
-    gate_unpack<BF16>(xv[i], x);
-    gate_unpack<BF16>(w1[i], w);
+    float yf[8], xf[8], w[8], g[8];
+    gate_unpack<BF16>(yv[i], yf);
+    gate_unpack<BF16>(xv[i], xf);
+    gate_unpack<BF16>(w1v[i], w);
     gate_unpack<BF16>(gv[i], g);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float u = p.w1 ? y[c] * r1 * w[c] : y[c];
-      h[i][c] = p.alpha * x[c] + (by_column ? g[c] : gr) * u;
+      const float u = p.w1 ? yf[c] * r1 * w[c] : yf[c];
+      h[i][c] = p.alpha * xf[c] + (by_column ? g[c] : gr) * u;
       sum[0] += h[i][c] * h[i][c];
     }
   }
   block_sums<1>(sum, s_sum[1]);
   grid_launch_dependents();
   const float r2 = reciprocal_rms(sum[0], p.cols, p.eps);
-  uint4* ph = row_pieces(p.h, row, p.ldh);
-  uint4* pv = row_pieces(p.v, row, p.ldv);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int at = threadIdx.x + i * blockDim.x;
-    if (at >= pieces) continue;
+    if (first(i) >= p.cols) continue;
     float w[8];
-    gate_unpack<BF16>(w2[i], w);
-    ph[at] = gate_pack<BF16>(h[i]);
+    gate_unpack<BF16>(w2v[i], w);
+    store_piece<ALIGNED>(h_row, first(i), p.cols, gate_pack<BF16>(h[i]));
 #pragma unroll
     for (int c = 0; c < 8; ++c) w[c] *= h[i][c] * r2;
-    pv[at] = gate_pack<BF16>(w);
+    store_piece<ALIGNED>(v_row, first(i), p.cols, gate_pack<BF16>(w));
   }
 }
 
-// Rows of any width and alignment: one to a block, element by element, read anew
-// for each step (from L1 and L2). h may be y or x: each element is read for the
+// Rows of any width: one to a block, element by element, read anew for each step
+// (from L1 and L2). h may be y or x: each element is read for the
 // last time by the thread that then writes it.
 constexpr int GATE_ANY_THREADS = 512;
 
 template <bool BF16>
-__global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_any_kernel(const GateNormParams p) {
+__global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_any_kernel(const __grid_constant__ GateNormParams p) {
   __shared__ float s_sum[2][32];
   constexpr int H_OUT = BF16 ? OUT_BF16 : OUT_F16;
   const int64_t row = blockIdx.x;
@@ -253,151 +306,380 @@ __device__ __forceinline__ void store_kind(void* p, int64_t i, float v, int kind
     store_out<OUT_F16>(p, i, v);
 }
 
-// Backwards: every gridDim.x-th row to a block, PER pieces of 8 elements a thread.
-template <bool BF16, int PER, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS) gate_norm_grad_kernel(const GateNormGradParams p) {
-  // (alternating, so that a fast warp's next row leaves a slow one's sums alone)
-  __shared__ float s_sum[2][3][64];
-  const GateNormParams& f = p.f;
-  const int pieces = f.cols >> 3;
+// Starts the copies of the block's row i into its stage (one thread).
+__device__ __forceinline__ void ring_fetch(const GateNormParams& p, int64_t i, int s, uint32_t bar0,
+                                           uint32_t data0, uint64_t policy) {
+  const int64_t row = blockIdx.x + i * gridDim.x;
+  if (row >= p.rows || (p.ring.inject_stall && i == 1)) return;
+  const uint32_t row_bytes = gate_row_bytes(p.cols), bytes = 2u * p.cols;
+  uint32_t dst = data0 + s * p.ring.ops * row_bytes;
+  mbar_arrive_expect_tx(bar0 + 8 * s, p.ring.ops * bytes);
+#pragma unroll
+  for (int o = 0; o < GATE_MAX_OPS; ++o)
+    if (o < p.ring.ops) {
+      bulk_load_1d(dst, static_cast<const uint16_t*>(p.ring.src[o]) + row * p.ring.ld[o], bytes, bar0 + 8 * s,
+                   policy);
+      dst += row_bytes;
+    }
+}
+
+// Lets the copies in flight land before the block leaves: those up to a ring past
+// the rows that have.
+__device__ __forceinline__ void ring_drain(const GateNormParams& p, int64_t landed, uint32_t bar0) {
+  for (int64_t i = landed; i < landed + p.ring.stages && blockIdx.x + i * gridDim.x < p.rows; ++i) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar0 + 8 * static_cast<uint32_t>(i % p.ring.stages),
+                          static_cast<uint32_t>(i / p.ring.stages) & 1u) &&
+           global_timer_ns() - t0 < p.ring.timeout_ns) {
+    }
+  }
+}
+
+// Forwards, many rows: a fixed number of blocks with a ring each. PER pieces of 8
+// elements a thread.
+template <bool BF16, int PER>
+__global__ void __launch_bounds__(512) gate_norm_ring_kernel(const __grid_constant__ GateNormParams p) {
+  extern __shared__ __align__(128) uint8_t ring_data[];
+  __shared__ float s_sum[2][2][32];
+  __shared__ __align__(8) uint64_t bars[GATE_MAX_STAGES];
+  __shared__ int abort_word;
+  const int pieces = p.cols >> 3;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  const bool by_column = f.gate_kind == GATE_COLS || f.gate_kind == GATE_FULL;
-  const float inv_cols = 1.0f / static_cast<float>(f.cols);
+  const bool by_column = p.gate_kind == GATE_COLS || p.gate_kind == GATE_FULL;
+  const bool full = p.gate_kind == GATE_FULL;
+  const uint32_t bar0 = smem_addr(bars), data0 = smem_addr(ring_data);
+  const int row_bytes = gate_row_bytes(p.cols), stage_bytes = p.ring.ops * row_bytes;
+  const uint64_t policy = policy_evict_first();  // read once
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   grid_dependency_wait();
+  if (threadIdx.x == 0)
+    for (int i = 0; i < p.ring.stages; ++i) ring_fetch(p, i, i, bar0, data0, policy);
+  const WaitCtl ctl{p.ring.timeout_ns, p.ring.error_word, &abort_word};
   uint4 w1[PER], w2[PER], gv[PER];
-  float sum_w2[PER][8], sum_w1[PER][8], sum_g[PER][8];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int at = threadIdx.x + i * blockDim.x;
     const bool in = at < pieces;
-    w1[i] = in && f.w1 ? static_cast<const uint4*>(f.w1)[at] : none;
-    w2[i] = in ? static_cast<const uint4*>(f.w2)[at] : none;
-    gv[i] = in && f.gate_kind == GATE_COLS ? static_cast<const uint4*>(f.gate)[at] : none;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) sum_w2[i][c] = sum_w1[i][c] = sum_g[i][c] = 0.0f;
+    w1[i] = in && p.w1 ? static_cast<const uint4*>(p.w1)[at] : none;
+    w2[i] = in ? static_cast<const uint4*>(p.w2)[at] : none;
+    gv[i] = in && p.gate_kind == GATE_COLS ? static_cast<const uint4*>(p.gate)[at] : none;
   }
-  int odd = 0;
-  for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x, odd ^= 1) {
-    uint4 yv[PER], xv[PER], dhv[PER], dvv[PER];
+  int odd = 0, s = 0;
+  uint32_t phase = 0;
+  bool ok = true;  // this thread has seen every row so far arrive
+  int64_t landed = 0;
+  int64_t n = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++n, odd ^= 1) {
+    const float gr = p.gate_kind == GATE_ROWS ? gate_load<BF16>(p.gate, row * p.ldg) : 1.0f;
+    // (a wait that runs out leaves this row and the block's next ones wrong and
+    // says so; the loop and its barriers go on, without waits and copies)
+    ok = ok && wait_bounded_lazy(bar0 + 8 * s, phase, ctl, WAIT_MMA_FULL);
+    landed += ok;
+    const uint4* sy = reinterpret_cast<const uint4*>(ring_data + s * stage_bytes);
+    const uint4* sx = reinterpret_cast<const uint4*>(ring_data + s * stage_bytes + row_bytes);
+    const uint4* sg = reinterpret_cast<const uint4*>(ring_data + s * stage_bytes + 2 * row_bytes);
+    float h[PER][8];  // y, then h
+    float sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = threadIdx.x + i * blockDim.x;
-      const bool in = at < pieces;
-      yv[i] = in ? __ldcs(row_pieces(f.y, row, f.ldy) + at) : none;
-      xv[i] = in ? __ldcs(row_pieces(f.x, row, f.ldx) + at) : none;
-      dhv[i] = in && p.dh ? __ldcs(row_pieces(p.dh, row, p.lddh) + at) : none;
-      dvv[i] = in && p.dv ? __ldcs(row_pieces(p.dv, row, p.lddv) + at) : none;
-      if (f.gate_kind == GATE_FULL) gv[i] = in ? __ldcs(row_pieces(f.gate, row, f.ldg) + at) : none;
+      gate_unpack<BF16>(at < pieces ? sy[at] : none, h[i]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[0] += h[i][c] * h[i][c];
     }
-    const float gr = f.gate_kind == GATE_ROWS ? gate_load<BF16>(f.gate, row * f.ldg) : 1.0f;
     float r1 = 1.0f;
-    if (f.w1) {
-      float s[1] = {0.0f};
+    if (p.w1) {
+      block_sums<1>(sum, s_sum[odd][0]);
+      r1 = reciprocal_rms(sum[0], p.cols, p.eps);
+    }
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = threadIdx.x + i * blockDim.x;
+      float x[8], w[8], g[8];
+      gate_unpack<BF16>(at < pieces ? sx[at] : none, x);
+      if (full) gv[i] = at < pieces ? sg[at] : none;
+      gate_unpack<BF16>(w1[i], w);
+      gate_unpack<BF16>(gv[i], g);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float u = p.w1 ? h[i][c] * r1 * w[c] : h[i][c];
+        h[i][c] = p.alpha * x[c] + (by_column ? g[c] : gr) * u;
+        sum[0] += h[i][c] * h[i][c];
+      }
+    }
+    block_sums<1>(sum, s_sum[odd][1]);
+    // (the stage has been read; into a place whose last copy has landed, no other)
+    if (threadIdx.x == 0 && ok) ring_fetch(p, n + p.ring.stages, s, bar0, data0, policy);
+    const float r2 = reciprocal_rms(sum[0], p.cols, p.eps);
+    uint4* ph = row_pieces(p.h, row, p.ldh);
+    uint4* pv = row_pieces(p.v, row, p.ldv);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = threadIdx.x + i * blockDim.x;
+      if (at >= pieces) continue;
+      float w[8];
+      gate_unpack<BF16>(w2[i], w);
+      ph[at] = gate_pack<BF16>(h[i]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] *= h[i][c] * r2;
+      pv[at] = gate_pack<BF16>(w);
+    }
+    if (++s == p.ring.stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  grid_launch_dependents();
+  if (threadIdx.x == 0 && !ok) ring_drain(p, landed, bar0);
+}
+
+// Backwards: a fixed number of blocks, PER pieces of 8 elements a thread, whose sums
+// over rows stay in registers. RING: rows on 16-byte boundaries, through a ring; else
+// a row's pieces are loaded together, shifted, into registers.
+template <bool BF16, int PER, int GATE, bool BLOCK, bool RING>
+__global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_constant__ GateNormGradParams p) {
+  extern __shared__ __align__(128) uint8_t ring_data[];
+  // (alternating, so that a fast warp's next row leaves a slow one's sums alone)
+  __shared__ float s_sum[2][3][64];
+  __shared__ __align__(8) uint64_t bars[GATE_MAX_STAGES];
+  __shared__ int abort_word;
+  const GateNormParams& f = p.f;
+  const int pieces = (f.cols + 7) >> 3;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const float inv_cols = 1.0f / static_cast<float>(f.cols);
+  const int op_dv = p.dh ? 3 : 2, op_gate = f.ring.ops - 1;
+  const uint32_t bar0 = smem_addr(bars), data0 = smem_addr(ring_data);
+  const int row_bytes = gate_row_bytes(f.cols), stage_bytes = f.ring.ops * row_bytes;
+  const uint64_t policy = policy_evict_first();  // read once
+  if (RING && threadIdx.x == 0) {
+    for (int s = 0; s < f.ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  if (RING && threadIdx.x == 0)
+    for (int i = 0; i < f.ring.stages; ++i) ring_fetch(f, i, i, bar0, data0, policy);
+  const WaitCtl ctl{f.ring.timeout_ns, f.ring.error_word, &abort_word};
+  // a column's factors: of u in h (w1, and the gate of columns), and w2
+  float gw[PER][8];
+  uint4 w2[PER];
+  float sum_w2[PER][8], sum_e[PER][8];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int at = threadIdx.x + i * blockDim.x;
+    const bool in = at < pieces;
+    w2[i] = in ? load_piece<RING>(static_cast<const uint16_t*>(f.w2), 8 * at, f.cols) : none;
+    if (BLOCK) gate_unpack<BF16>(in ? load_piece<RING>(static_cast<const uint16_t*>(f.w1), 8 * at, f.cols) : none, gw[i]);
+    float g[8];
+    if (GATE == GATE_COLS) gate_unpack<BF16>(in ? load_piece<RING>(static_cast<const uint16_t*>(f.gate), 8 * at, f.cols) : none, g);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (!BLOCK) gw[i][c] = 1.0f;
+      if (GATE == GATE_COLS) gw[i][c] *= g[c];
+      sum_w2[i][c] = sum_e[i][c] = 0.0f;
+    }
+  }
+  int odd = 0, s = 0;
+  uint32_t phase = 0;
+  bool ok = true;  // this thread has seen every row so far arrive
+  int64_t landed = 0, n = 0;
+  for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x, ++n, odd ^= 1) {
+    const float gr = GATE == GATE_ROWS ? gate_load<BF16>(f.gate, row * f.ldg) : 1.0f;
+    // (a wait that runs out leaves this row and the block's next ones wrong and
+    // says so; the loop and its barriers go on, without waits and copies)
+    if (RING) ok = ok && wait_bounded_lazy(bar0 + 8 * s, phase, ctl, WAIT_MMA_FULL);
+    landed += ok;
+    const uint8_t* stage = ring_data + s * stage_bytes;
+    uint4 early[PER][GATE_MAX_OPS];  // (not RING)
+    if constexpr (!RING) {
+      const int ops[GATE_MAX_OPS] = {0, 1, p.dh ? 2 : -1, p.dv ? op_dv : -1, GATE == GATE_FULL ? op_gate : -1};
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
+        const int first = 8 * static_cast<int>(threadIdx.x + i * blockDim.x);
+        if (inside_row(first, f.cols)) {
+          ShiftedPiece words[GATE_MAX_OPS];
+#pragma unroll
+          for (int o = 0; o < GATE_MAX_OPS; ++o)
+            if (ops[o] >= 0)
+              words[o] = load_words(static_cast<const uint16_t*>(f.ring.src[ops[o]]) + row * f.ring.ld[ops[o]] + first);
+#pragma unroll
+          for (int o = 0; o < GATE_MAX_OPS; ++o)
+            if (ops[o] >= 0) early[i][o] = shifted(words[o]);
+        } else if (first < f.cols) {
+#pragma unroll
+          for (int o = 0; o < GATE_MAX_OPS; ++o)
+            if (ops[o] >= 0)
+              early[i][o] = load_elements(static_cast<const uint16_t*>(f.ring.src[ops[o]]) + row * f.ring.ld[ops[o]],
+                                          first, f.cols);
+        }
+      }
+    }
+    // piece i of y, x, dh, dv or the gate
+    const auto operand = [&](int op, int i) {
+      if constexpr (!RING) return early[i][op];
+      const int slot = op <= 2 ? op : op == 3 ? op_dv : op_gate;
+      return reinterpret_cast<const uint4*>(stage + slot * row_bytes)[threadIdx.x + i * blockDim.x];
+    };
+    const auto store = [&](void* to, int64_t ld, int at, const float (&v)[8]) {
+      store_piece<RING>(static_cast<uint16_t*>(to) + row * ld, 8 * at, f.cols, gate_pack<BF16>(v));
+    };
+    uint4 yv[PER], gv[PER];
+    float r1 = 1.0f;
+    float s1[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = threadIdx.x + i * blockDim.x;
+      if (at >= pieces) continue;
+      yv[i] = operand(0, i);
+      if (GATE == GATE_FULL) gv[i] = operand(4, i);
+      if (BLOCK) {
         float y[8];
         gate_unpack<BF16>(yv[i], y);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) s[0] += y[c] * y[c];
+        for (int c = 0; c < 8; ++c) s1[0] += y[c] * y[c];
       }
-      block_sums<1>(s, s_sum[odd][0]);
-      r1 = reciprocal_rms(s[0], f.cols, f.eps);
     }
-    float h[PER][8];  // then dh' g
+    if (BLOCK) {
+      block_sums<1>(s1, s_sum[odd][0]);
+      r1 = reciprocal_rms(s1[0], f.cols, f.eps);
+    }
+    const float gr1 = gr * r1;
+    float h[PER][8];  // then dh'
     float s2[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      float y[8], x[8], w[8], g[8], dv[8], ww[8];
+      const int at = threadIdx.x + i * blockDim.x;
+      if (at >= pieces) continue;
+      float y[8], x[8], g[8], dv[8], w[8];
       gate_unpack<BF16>(yv[i], y);
-      gate_unpack<BF16>(xv[i], x);
-      gate_unpack<BF16>(w1[i], w);
-      gate_unpack<BF16>(gv[i], g);
-      gate_unpack<BF16>(dvv[i], dv);
-      gate_unpack<BF16>(w2[i], ww);
+      gate_unpack<BF16>(operand(1, i), x);
+      if (GATE == GATE_FULL) gate_unpack<BF16>(gv[i], g);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float u = f.w1 ? y[c] * r1 * w[c] : y[c];
-        h[i][c] = f.alpha * x[c] + (by_column ? g[c] : gr) * u;
-        s2[0] += h[i][c] * h[i][c];
-        s2[1] += dv[c] * ww[c] * h[i][c];
+        float u = y[c] * gr1 * gw[i][c];
+        if (GATE == GATE_FULL) u *= g[c];
+        h[i][c] = fmaf(f.alpha, x[c], u);
+        s2[0] = fmaf(h[i][c], h[i][c], s2[0]);
+      }
+      if (p.dv) {
+        gate_unpack<BF16>(operand(3, i), dv);
+        gate_unpack<BF16>(w2[i], w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s2[1] = fmaf(dv[c] * w[c], h[i][c], s2[1]);
       }
     }
     block_sums<2>(s2, s_sum[odd][1]);
     const float r2 = reciprocal_rms(s2[0], f.cols, f.eps);
     const float m2 = s2[1] * r2 * inv_cols;
+    const float back = -(r2 * m2);
     float s3[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = threadIdx.x + i * blockDim.x;
-      float y[8], w[8], g[8], dv[8], ww[8], dh[8], dx[8], dg[8];
+      if (at >= pieces) continue;
+      float y[8], g[8], dh[8], dg[8];
       gate_unpack<BF16>(yv[i], y);
-      gate_unpack<BF16>(w1[i], w);
-      gate_unpack<BF16>(gv[i], g);
-      gate_unpack<BF16>(dvv[i], dv);
-      gate_unpack<BF16>(dhv[i], dh);
-      gate_unpack<BF16>(w2[i], ww);
+      if (GATE == GATE_FULL) gate_unpack<BF16>(gv[i], g);
+      if (p.dh) {
+        gate_unpack<BF16>(operand(2, i), dh);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dh[c] = 0.0f;
+      }
+      if (p.dv) {
+        float dv[8], w[8];
+        gate_unpack<BF16>(operand(3, i), dv);
+        gate_unpack<BF16>(w2[i], w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float hn = h[i][c] * r2;
+          sum_w2[i][c] = fmaf(dv[c], hn, sum_w2[i][c]);
+          h[i][c] = fmaf(hn, back, fmaf(dv[c] * w[c], r2, dh[c]));
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) h[i][c] = dh[c];
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float hn = h[i][c] * r2;
-        const float d = dh[c] + r2 * (dv[c] * ww[c] - hn * m2);
-        sum_w2[i][c] += dv[c] * hn;
-        dx[c] = f.alpha * d;
-        const float yn = y[c] * r1;
-        const float u = f.w1 ? yn * w[c] : y[c];
-        dg[c] = d * u;
-        s3[1] += dg[c];
-        const float du = d * (by_column ? g[c] : gr);
-        h[i][c] = du;
-        sum_w1[i][c] += du * yn;
-        s3[0] += du * w[c] * yn;
-        if (f.gate_kind == GATE_COLS) sum_g[i][c] += dg[c];
+        float e = h[i][c] * (y[c] * r1);
+        if (GATE == GATE_FULL) {
+          dg[c] = e * gw[i][c];
+          e *= g[c];
+        } else if (GATE == GATE_ROWS) {
+          e *= gr;
+        }
+        sum_e[i][c] += e;
+        s3[0] = fmaf(e, gw[i][c], s3[0]);
+        dh[c] = f.alpha * h[i][c];
       }
-      if (at < pieces) {
-        row_pieces(p.dx, row, p.lddx)[at] = gate_pack<BF16>(dx);
-        if (f.gate_kind == GATE_FULL) row_pieces(p.dgate, row, p.lddg)[at] = gate_pack<BF16>(dg);
+      store(p.dx, p.lddx, at, dh);
+      if (GATE == GATE_FULL) store(p.dgate, p.lddg, at, dg);
+      if (GATE == GATE_ROWS) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s3[1] = fmaf(h[i][c] * gw[i][c], y[c] * r1, s3[1]);
       }
     }
-    if (f.w1 || f.gate_kind == GATE_ROWS) block_sums<2>(s3, s_sum[odd][2]);
-    if (f.gate_kind == GATE_ROWS && threadIdx.x == 0) store_kind(p.dgate, row, s3[1], p.out_kind);
-    const float m1 = s3[0] * inv_cols;
+    block_sums<2>(s3, s_sum[odd][2]);
+    // (the stage has been read; into a place whose last copy has landed, no other)
+    if (RING && threadIdx.x == 0 && ok) ring_fetch(f, n + f.ring.stages, s, bar0, data0, policy);
+    if (GATE == GATE_ROWS && threadIdx.x == 0) store_kind(p.dgate, row, s3[1], p.out_kind);
+    const float back1 = BLOCK ? -(s3[0] * inv_cols * r1 * r1) : 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = threadIdx.x + i * blockDim.x;
       if (at >= pieces) continue;
-      float y[8], w[8], dy[8];
+      float y[8], g[8];
       gate_unpack<BF16>(yv[i], y);
-      gate_unpack<BF16>(w1[i], w);
+      if (GATE == GATE_FULL) gate_unpack<BF16>(gv[i], g);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) dy[c] = f.w1 ? r1 * (h[i][c] * w[c] - y[c] * r1 * m1) : h[i][c];
-      row_pieces(p.dy, row, p.lddy)[at] = gate_pack<BF16>(dy);
+      for (int c = 0; c < 8; ++c) {
+        float d = h[i][c] * gr1 * gw[i][c];
+        if (GATE == GATE_FULL) d *= g[c];
+        h[i][c] = BLOCK ? fmaf(y[c], back1, d) : d;
+      }
+      store(p.dy, p.lddy, at, h[i]);
+    }
+    if (RING && ++s == f.ring.stages) {
+      s = 0;
+      phase ^= 1u;
     }
   }
   grid_launch_dependents();
+  if (RING && threadIdx.x == 0 && !ok) ring_drain(f, landed, bar0);
   const int64_t plane = static_cast<int64_t>(gridDim.x) * f.cols;
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * f.cols;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int at = threadIdx.x + i * blockDim.x;
     if (at >= pieces) continue;
+    const auto sums_out = [&](float* to, const float (&v)[8]) {
+      if constexpr (RING) {
 #pragma unroll
-    for (int c = 0; c < 8; c += 4) {
-      const int64_t to = at * 8 + c;
-      *reinterpret_cast<float4*>(part + to) =
-          make_float4(sum_w2[i][c], sum_w2[i][c + 1], sum_w2[i][c + 2], sum_w2[i][c + 3]);
-      if (f.w1)
-        *reinterpret_cast<float4*>(part + plane + to) =
-            make_float4(sum_w1[i][c], sum_w1[i][c + 1], sum_w1[i][c + 2], sum_w1[i][c + 3]);
-      if (f.gate_kind == GATE_COLS)
-        *reinterpret_cast<float4*>(part + 2 * plane + to) =
-            make_float4(sum_g[i][c], sum_g[i][c + 1], sum_g[i][c + 2], sum_g[i][c + 3]);
-    }
+        for (int c = 0; c < 8; c += 4)
+          *reinterpret_cast<float4*>(to + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (8 * at + c < f.cols) to[c] = v[c];
+      }
+    };
+    sums_out(part + 8 * at, sum_w2[i]);
+    if (BLOCK || GATE == GATE_COLS) sums_out(part + plane + 8 * at, sum_e[i]);
   }
 }
 
 // The same for rows of any width and alignment, element by element. The block's
 // sums over rows lie in the workspace, each written by one thread only.
 template <bool BF16>
-__global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_grad_any_kernel(const GateNormGradParams p) {
+__global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_grad_any_kernel(const __grid_constant__ GateNormGradParams p) {
   __shared__ float s_sum[2][3][64];
   constexpr int OUT = BF16 ? OUT_BF16 : OUT_F16;
   const GateNormParams& f = p.f;
@@ -447,14 +729,13 @@ __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_grad_any_kernel(co
     for (int c = threadIdx.x; c < f.cols; c += GATE_ANY_THREADS) {
       const float hn = h_at(c) * r2, dv = dv_at(c), d = d_at(c, dv, hn);
       part[c] = (first ? 0.0f : part[c]) + dv * hn;
-      const float u = u_at(c), yn = gate_load<BF16>(y, c) * r1, dg = d * u, du = d * gate_at(c);
+      const float dg = d * u_at(c);
+      float e = d * gate_load<BF16>(y, c) * r1;
+      s3[0] += dg * gate_at(c);
       s3[1] += dg;
       if (f.gate_kind == GATE_FULL) store_out<OUT>(p.dgate, row * p.lddg + c, dg);
-      if (f.gate_kind == GATE_COLS) part[2 * plane + c] = (first ? 0.0f : part[2 * plane + c]) + dg;
-      if (f.w1) {
-        part[plane + c] = (first ? 0.0f : part[plane + c]) + du * yn;
-        s3[0] += du * gate_load<BF16>(f.w1, c) * yn;
-      }
+      if (f.gate_kind != GATE_COLS) e *= gate_at(c);
+      if (f.w1 || f.gate_kind == GATE_COLS) part[plane + c] = (first ? 0.0f : part[plane + c]) + e;
     }
     if (f.w1 || f.gate_kind == GATE_ROWS) block_sums<2>(s3, s_sum[odd][2]);
     if (f.gate_kind == GATE_ROWS && threadIdx.x == 0) store_kind(p.dgate, row, s3[1], p.out_kind);
@@ -471,14 +752,12 @@ __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_grad_any_kernel(co
 
 // The blocks' sums of 32 columns added up by a block: every 32nd block's to a
 // warp, then the warps' in turn.
-template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) gate_norm_columns_kernel(const ColumnSumParams p) {
+template <bool BF16, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) gate_norm_columns_kernel(const __grid_constant__ ColumnSumParams p) {
   __shared__ float s[WARPS][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
-  void* out = p.out[blockIdx.y];
   grid_dependency_wait();
-  if (out == nullptr) return;
   const float* part = p.part + static_cast<int64_t>(blockIdx.y) * p.blocks * p.cols;
   float sum = 0.0f;
   if (c < p.cols) {
@@ -492,7 +771,12 @@ __global__ void __launch_bounds__(32 * WARPS) gate_norm_columns_kernel(const Col
     sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) sum += s[w][lane];
-    store_kind(out, c, sum, p.out_kind);
+    if (blockIdx.y == 0) {
+      store_kind(p.dw2, c, sum, p.out_kind);
+    } else {
+      if (p.dw1) store_kind(p.dw1, c, p.gate ? sum * gate_load<BF16>(p.gate, c) : sum, p.out_kind);
+      if (p.dgate) store_kind(p.dgate, c, p.w1 ? sum * gate_load<BF16>(p.w1, c) : sum, p.out_kind);
+    }
   }
 }
 

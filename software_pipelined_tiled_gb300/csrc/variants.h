@@ -80,24 +80,27 @@ KernelVariant grouped_variant_dw_bf16(int out_kind, int tt);
 KernelVariant grouped_variant_dw_f16(int out_kind, int tt);
 
 // The router's kernels (type: RouteType), with the lanes of a warp and the
-// experts of a lane that a row takes; the gradient of its logits.
-enum RouteKind : int { ROUTE_8_8, ROUTE_16_8, ROUTE_32_8, ROUTE_32_16, ROUTE_32_32, ROUTE_32_64 };
+// experts of a lane that a row takes; the gradient of its logits, with 8 or 16
+// lanes a row.
+enum RouteKind : int { ROUTE_8_8, ROUTE_8_16, ROUTE_16_8, ROUTE_32_8, ROUTE_32_16, ROUTE_32_32, ROUTE_32_64 };
 const void* route_variant(int type, int kind);
-const void* route_dlogits_variant(int type);
+const void* route_dlogits_variant(int type, int slots);
 
-// Rows to their experts and back, in pieces of 16 bytes or element by element.
+// Rows to their experts and back; aligned: all rows on 16-byte boundaries.
 const void* dispatch_sort_variant();
-const void* dispatch_copy_variant(bool vectors);
-const void* combine_rows_variant(bool bf16, bool vectors);
-const void* combine_rows_grad_variant(bool bf16, bool vectors);
+const void* dispatch_copy_variant(bool aligned);
+const void* combine_rows_variant(bool bf16, bool aligned);
+const void* combine_rows_grad_variant(bool bf16, bool aligned);
 
-// Gate, scaled residual and norms: one or two pieces of 8 elements a thread, or
-// rows of any width and alignment; backwards with blocks of up to 512 threads,
-// up to 1024, those with two pieces each, or any; the sums over the blocks.
-enum GateNormKind : int { GATE_NORM_1, GATE_NORM_2, GATE_NORM_ANY };
-enum GateGradKind : int { GATE_GRAD_512, GATE_GRAD_1024, GATE_GRAD_2048, GATE_GRAD_ANY };
+// Gate, scaled residual and norms: a row to a block with one or two pieces of 8
+// elements a thread; rows through rings of blocks; rows off 16-byte boundaries; rows of
+// any width. Backwards by the kind of gate, whether the block's output is normalised,
+// and whether rows go through a ring; or rows of any width; the sums over the blocks.
+enum GateNormKind : int { GATE_NORM_1, GATE_NORM_2, GATE_NORM_RING, GATE_NORM_SHIFTED, GATE_NORM_ANY };
 const void* gate_norm_variant(bool bf16, int kind);
-const void* gate_norm_grad_variant(bool bf16, int kind);
-const void* gate_norm_columns_variant();
+const void* gate_norm_grad_bf16(int gate_kind, bool block, bool ring);
+const void* gate_norm_grad_f16(int gate_kind, bool block, bool ring);
+const void* gate_norm_grad_any_variant(bool bf16);
+const void* gate_norm_columns_variant(bool bf16);
 
 }  // namespace sptg
