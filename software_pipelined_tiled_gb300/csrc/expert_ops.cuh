@@ -243,6 +243,26 @@ int dispatch_rows(int64_t rows, int64_t cols, int top, int64_t E, int type, cons
   s.offsets = offsets;
   s.entries = rows * top;
   s.E = static_cast<int>(E);
+  const bool aligned = cols % 8 == 0 && in_pieces(x, ldx) && in_pieces(sorted, lds);
+  RowsParams p{};
+  p.x = x;
+  p.ldx = ldx;
+  p.places = places;
+  p.out = sorted;
+  p.ldo = lds;
+  p.out_rows = s.entries;
+  p.cols = static_cast<int>(cols);
+  p.top = top;
+  const unsigned parts = column_parts(rows, ceil_div(cols + (aligned ? 0 : 7), 8), di.sm_count);
+  void* args[] = {&p, &s};
+  cudaError_t e;
+  if (s.entries <= SMALL_ENTRIES) {
+    e = launch_op(dispatch_small_variant(aligned), dim3(static_cast<unsigned>(rows + 1), parts), ROWS_THREADS, 0,
+                  1, stream, args);
+    if (e != cudaSuccess) return cuda_fail(e, "dispatch_rows launch");
+    set_config("kernel=dispatch_small type=%s aligned=%lld parts=%lld", name, {aligned, parts});
+    return SPTG_OK;
+  }
   s.bits = 0;
   while (E >> s.bits) ++s.bits;
   int ctas = 1;
@@ -254,24 +274,12 @@ int dispatch_rows(int64_t rows, int64_t cols, int top, int64_t E, int type, cons
   rc = ensure_smem(dev, dispatch_sort_variant(), sort_smem(DISPATCH_MAX_EXPERTS));
   if (rc) return rc;
   void* sort_args[] = {&s};
-  cudaError_t e = launch_op(dispatch_sort_variant(), dim3(static_cast<unsigned>(ctas)), 32 * SORT_WARPS,
-                            sort_smem(s.E), ctas, stream, sort_args);
+  e = launch_op(dispatch_sort_variant(), dim3(static_cast<unsigned>(ctas)), 32 * SORT_WARPS, sort_smem(s.E), ctas,
+                stream, sort_args);
   if (e != cudaSuccess) return cuda_fail(e, "dispatch_rows sort launch");
-  const bool aligned = cols % 8 == 0 && in_pieces(x, ldx) && in_pieces(sorted, lds);
   if (copies) {
-    RowsParams p{};
-    p.x = x;
-    p.ldx = ldx;
-    p.places = places;
-    p.out = sorted;
-    p.ldo = lds;
-    p.out_rows = s.entries;
-    p.cols = static_cast<int>(cols);
-    p.top = top;
-    const unsigned parts = column_parts(rows, ceil_div(cols + (aligned ? 0 : 7), 8), di.sm_count);
-    void* args[] = {&p};
-    e = launch_op(dispatch_copy_variant(aligned), dim3(static_cast<unsigned>(rows), parts), ROWS_THREADS, 0,
-                  1, stream, args);
+    e = launch_op(dispatch_copy_variant(aligned), dim3(static_cast<unsigned>(rows), parts), ROWS_THREADS, 0, 1,
+                  stream, args);
     if (e != cudaSuccess) return cuda_fail(e, "dispatch_rows copy launch");
   }
   set_config("kernel=dispatch type=%s sort_ctas=%lld per_warp=%lld aligned=%lld", name,
@@ -372,7 +380,9 @@ int combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, int t
 }
 
 // -------------------------------------------- gate, scaled residual and norms
-constexpr int kGateRingSmem = 225 * 1024;  // what a ring may take: two rows of five operands of 8192 elements
+// What a ring may take beside a kernel's own few KB: two rows of three operands of 16384
+// elements, or of five of 8192.
+constexpr int kGateRingSmem = 223 * 1024;
 
 // Blocks that add up gradients over rows, at most: those of narrow rows are small,
 // and an SM holds more of them.
@@ -446,14 +456,16 @@ int gate_norm(int64_t rows, int64_t cols, int type, const void* y, int64_t ldy, 
   }
   int64_t grid = rows;
   int smem = 0, stages = 0;
-  // Rows for several turns of the blocks that the GPU holds: rings of two rows, four
-  // pieces a thread (16384 rows of 8192: 171 us, a row to a block 211 us, rings with two
-  // pieces a thread 244 us; of 4096: 90, 144 and 108 us; three rows ahead are no faster).
-  // Rows of 512 elements: a row to a block, 36 us for 32768 either way.
+  // Rows for several turns of the blocks that the GPU holds: rings, four pieces a thread
+  // (16384 rows of 8192: 171 us, a row to a block 211 us; of 4096: 87 and 144 us; 32768 of 512
+  // take 36 us either way, and are left to the simpler kernel). Rings of two rows, of three
+  // where wide ones leave an SM two blocks (8192 rows of 8192: 87.6 us, with two 90.7 us; 16384
+  // of 4096: 89.2 and 87.3 us; with a gate's row as well, 8192 of 5000: 74.0 and 66.6 us).
   if (vectors && pieces > 64 && pieces <= 2048 && rows >= 3 * di.sm_count) {
+    const bool full = gate_kind == SPTG_GATE_FULL;
     const void* fn = gate_norm_variant(bf16, GATE_NORM_RING);
-    const int ring_threads = row_threads(pieces, 4);
-    const int ring_smem = gate_ring_smem(static_cast<int>(cols), gate_kind == SPTG_GATE_FULL ? 3 : 2, 2);
+    const int ring_threads = row_threads(pieces, 4), ring_stages = cols > 4096 && cols <= 8192 && !full ? 3 : 2;
+    const int ring_smem = gate_ring_smem(static_cast<int>(cols), full ? 3 : 2, ring_stages);
     Residency res;
     rc = ensure_smem(dev, fn, kGateRingSmem);
     if (!rc) rc = residency(res, dev, fn, ring_threads, ring_smem);
@@ -462,7 +474,7 @@ int gate_norm(int64_t rows, int64_t cols, int type, const void* y, int64_t ldy, 
     if (rows >= 3 * blocks) {
       kind = GATE_NORM_RING;
       threads = ring_threads;
-      stages = 2;
+      stages = ring_stages;
       smem = ring_smem;
       grid = blocks;
     }
@@ -548,7 +560,7 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
               : gate_norm_grad_f16(gate_kind, w1 != nullptr, vectors);
     threads = row_threads(ceil_div(cols, 8), 2);
     if (vectors) {
-      stages = 2;
+      stages = 2;  // (a third row: no faster, and one block an SM less of narrow rows)
       smem = gate_ring_smem(static_cast<int>(cols), 2 + (dh != nullptr) + (dv != nullptr) + full, stages);
     }
     Residency res;

@@ -12,6 +12,11 @@ const void* dispatch_copy_variant(bool aligned) {
                  : reinterpret_cast<const void*>(&dispatch_copy_kernel<false>);
 }
 
+const void* dispatch_small_variant(bool aligned) {
+  return aligned ? reinterpret_cast<const void*>(&dispatch_small_kernel<true>)
+                 : reinterpret_cast<const void*>(&dispatch_small_kernel<false>);
+}
+
 const void* combine_rows_variant(bool bf16, bool aligned) {
   if (bf16)
     return aligned ? reinterpret_cast<const void*>(&combine_rows_kernel<true, true>)

@@ -222,26 +222,22 @@ __device__ __forceinline__ uint16_t from_float(float v) {
   return static_cast<uint16_t>(pack2<BF16 ? OUT_BF16 : OUT_F16>(v, 0.0f));
 }
 
-// Rows of x to their places: a block to a row and a part of its columns
-// (blockIdx.y). A place outside of the sorted rows is passed over.
-template <bool ALIGNED>
-__global__ void __launch_bounds__(ROWS_THREADS) dispatch_copy_kernel(const __grid_constant__ RowsParams p) {
-  const int64_t row = blockIdx.x;
-  grid_dependency_wait();
+// One thread's part of a row of x to the rows of out that `place(j)` names.
+template <bool ALIGNED, typename Place>
+__device__ __forceinline__ void copy_row(const RowsParams& p, int64_t row, Place place) {
   const uint16_t* x = row_of(p.x, row, p.ldx);
-  const int32_t* places = p.places + row * p.top;
   const int thread = blockIdx.y * ROWS_THREADS + threadIdx.x, threads = gridDim.y * ROWS_THREADS;
   if constexpr (ALIGNED) {
     for (int c = 8 * thread; c < p.cols; c += 8 * threads) {
       const uint4 v = *reinterpret_cast<const uint4*>(x + c);
       for (int j = 0; j < p.top; ++j) {
-        const int64_t to = places[j];
+        const int64_t to = place(j);
         if (to >= 0 && to < p.out_rows) *reinterpret_cast<uint4*>(row_of(p.out, to, p.ldo) + c) = v;
       }
     }
   } else {  // cut by each row written; x from L1 for all but the first
     for (int j = 0; j < p.top; ++j) {
-      const int64_t to = places[j];
+      const int64_t to = place(j);
       if (to < 0 || to >= p.out_rows) continue;
       uint16_t* out = row_of(p.out, to, p.ldo);
       const CutRow cut(out, p.cols);
@@ -251,6 +247,86 @@ __global__ void __launch_bounds__(ROWS_THREADS) dispatch_copy_kernel(const __gri
       for (int i = thread; i < cut.ends; i += threads) out[cut.end(i)] = x[cut.end(i)];
     }
   }
+}
+
+// Rows of x to their places: a block to a row and a part of its columns
+// (blockIdx.y). A place outside of the sorted rows is passed over.
+template <bool ALIGNED>
+__global__ void __launch_bounds__(ROWS_THREADS) dispatch_copy_kernel(const __grid_constant__ RowsParams p) {
+  const int64_t row = blockIdx.x;
+  grid_dependency_wait();
+  const int32_t* places = p.places + row * p.top;
+  copy_row<ALIGNED>(p, row, [&](int j) { return places[j]; });
+  grid_launch_dependents();
+}
+
+// Few entries, in one launch: every block finds the places of its own row by
+// counting the entries that go before each of them, and copies the row; one more
+// block (the last) counts the experts' entries for the offsets.
+constexpr int SMALL_ENTRIES = 2048;
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(ROWS_THREADS)
+    dispatch_small_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ SortParams s) {
+  __shared__ int s_count[DISPATCH_MAX_EXPERTS + 1];
+  __shared__ int s_place[SMALL_ENTRIES];
+  constexpr uint32_t ALL = 0xffffffffu;
+  const int n = static_cast<int>(s.entries), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const auto bin_at = [&](int i) {
+    const int e = s.experts[i];
+    return e < 0 || e >= s.E ? s.E : e;
+  };
+  grid_dependency_wait();
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y != 0) return;
+    for (int e = threadIdx.x; e <= s.E; e += ROWS_THREADS) s_count[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += ROWS_THREADS) atomicAdd(&s_count[bin_at(i)], 1);
+    __syncthreads();
+    if (warp == 0) {
+      int base = 0;
+      for (int e0 = 0; e0 <= s.E; e0 += 32) {
+        const int mine = e0 + lane < s.E ? s_count[e0 + lane] : 0;
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(ALL, sum, o);
+          if (lane >= o) sum += up;
+        }
+        if (e0 + lane <= s.E) s.offsets[e0 + lane] = base + sum - mine;
+        base += __shfl_sync(ALL, sum, 31);
+      }
+    }
+    return;
+  }
+  const int64_t row = blockIdx.x;
+  const int first = static_cast<int>(row) * p.top;
+  for (int j = threadIdx.x; j < p.top; j += ROWS_THREADS) s_place[j] = 0;
+  __syncthreads();
+  // every fourth run of 32 entries to a warp, against eight of the row's at a time
+  for (int j0 = 0; j0 < p.top; j0 += ROWS_AT_ONCE) {
+    int mine[ROWS_AT_ONCE], before[ROWS_AT_ONCE];
+#pragma unroll
+    for (int j = 0; j < ROWS_AT_ONCE; ++j) {
+      mine[j] = j0 + j < p.top ? bin_at(first + j0 + j) : -1;
+      before[j] = 0;
+    }
+    for (int i = threadIdx.x; i < n; i += ROWS_THREADS) {
+      const int b = bin_at(i);
+#pragma unroll
+      for (int j = 0; j < ROWS_AT_ONCE; ++j)
+        before[j] += b < mine[j] || (b == mine[j] && i < first + j0 + j);
+    }
+#pragma unroll
+    for (int j = 0; j < ROWS_AT_ONCE; ++j) {
+      const int sum = __reduce_add_sync(ALL, before[j]);
+      if (lane == 0 && j0 + j < p.top) atomicAdd(&s_place[j0 + j], sum);
+    }
+  }
+  __syncthreads();
+  if (blockIdx.y == 0)
+    for (int j = threadIdx.x; j < p.top; j += ROWS_THREADS) s.places[first + j] = s_place[j];
+  copy_row<ALIGNED>(p, row, [&](int j) { return s_place[j]; });
   grid_launch_dependents();
 }
 

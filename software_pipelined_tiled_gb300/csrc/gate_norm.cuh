@@ -92,23 +92,28 @@ struct ColumnSumParams {
 };
 
 // Sums over a block, the same for each thread: lanes by halves, then warps in
-// turn. s: 32 * N floats.
+// turn. s: a place for each warp's sums.
 template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float* s) {
+__device__ __forceinline__ void block_sums(float (&v)[N], float4* s) {
+  static_assert(N <= 4, "a warp's sums are one 16-byte word");
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   const int warps = static_cast<int>(blockDim.x) >> 5;
   if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i * 32 + (threadIdx.x >> 5)] = v[i];
+    s[threadIdx.x >> 5] = make_float4(v[0], N > 1 ? v[N > 1 ? 1 : 0] : 0.0f, N > 2 ? v[N > 2 ? 2 : 0] : 0.0f,
+                                      N > 3 ? v[N > 3 ? 3 : 0] : 0.0f);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.0f;
-  for (int w = 0; w < warps; ++w)
+#pragma unroll 4
+  for (int w = 0; w < warps; ++w) {
+    const float4 a = s[w];
+    const float part[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += s[i * 32 + w];
+    for (int i = 0; i < N; ++i) v[i] += part[i];
+  }
 }
 
 template <bool BF16>
@@ -142,6 +147,59 @@ __device__ __forceinline__ float gate_load(const void* p, int64_t i) {
     return __half2float(static_cast<const __half*>(p)[i]);
 }
 
+// Two floats in one register pair and the instructions that take two at a time:
+// the ring kernels are short of issue slots and registers, not of arithmetic.
+typedef unsigned long long float_pair;
+__device__ __forceinline__ float_pair pair_of(float a, float b) {
+  float_pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float_pair pair_of(float a) { return pair_of(a, a); }
+__device__ __forceinline__ float2 floats_of(float_pair p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ float_pair fma2(float_pair a, float_pair b, float_pair c) {
+  float_pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float_pair mul2(float_pair a, float_pair b) {
+  float_pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float_pair add2(float_pair a, float_pair b) {
+  float_pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum_of(float_pair p) {
+  const float2 f = floats_of(p);
+  return f.x + f.y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void pair_unpack(const uint4& v, float_pair (&f)[4]) {
+  float a[8];
+  gate_unpack<BF16>(v, a);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair_of(a[2 * i], a[2 * i + 1]);
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 pair_pack(const float_pair (&f)[4]) {
+  constexpr int OUT = BF16 ? OUT_BF16 : OUT_F16;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = floats_of(f[i]);
+    w[i] = pack2<OUT>(a.x, a.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ const uint4* row_pieces(const void* p, int64_t row, int64_t ld) {
   return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + row * ld);
 }
@@ -149,8 +207,11 @@ __device__ __forceinline__ uint4* row_pieces(void* p, int64_t row, int64_t ld) {
   return reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + row * ld);
 }
 
-__device__ __forceinline__ float reciprocal_rms(float sumsq, int cols, float eps) {
-  return 1.0f / sqrtf(sumsq / static_cast<float>(cols) + eps);
+// 1 / sqrt(sumsq * inv_cols + eps): the approximation and a step of Newton's. (An
+// infinite sum: 0; the step would make it NaN. NaN stays.)
+__device__ __forceinline__ float reciprocal_rms(float sumsq, float inv_cols, float eps) {
+  const float m = fmaf(sumsq, inv_cols, eps), r = rsqrtf(m);
+  return m == INFINITY ? 0.0f : r * fmaf(-0.5f * m * r, r, 1.5f);
 }
 
 // One row to a block, PER pieces of 8 elements a thread (not ALIGNED: pieces by h's
@@ -158,9 +219,10 @@ __device__ __forceinline__ float reciprocal_rms(float sumsq, int cols, float eps
 // what it writes.
 template <bool BF16, int PER, bool ALIGNED>
 __global__ void __launch_bounds__(1024) gate_norm_kernel(const __grid_constant__ GateNormParams p) {
-  __shared__ float s_sum[2][32];
+  __shared__ float4 s_sum[2][32];
   const int64_t row = blockIdx.x;
   const uint4 none = make_uint4(0, 0, 0, 0);
+  const float inv_cols = 1.0f / static_cast<float>(p.cols);
   const uint16_t* y = static_cast<const uint16_t*>(p.y) + row * p.ldy;
   const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ldx;
   uint16_t* h_row = static_cast<uint16_t*>(p.h) + row * p.ldh;
@@ -218,7 +280,7 @@ __global__ void __launch_bounds__(1024) gate_norm_kernel(const __grid_constant__
       for (int c = 0; c < 8; ++c) sum[0] += f[c] * f[c];
     }
     block_sums<1>(sum, s_sum[0]);
-    r1 = reciprocal_rms(sum[0], p.cols, p.eps);
+    r1 = reciprocal_rms(sum[0], inv_cols, p.eps);
   }
   float h[PER][8];
   float sum[1] = {0.0f};
@@ -238,7 +300,7 @@ __global__ void __launch_bounds__(1024) gate_norm_kernel(const __grid_constant__
   }
   block_sums<1>(sum, s_sum[1]);
   grid_launch_dependents();
-  const float r2 = reciprocal_rms(sum[0], p.cols, p.eps);
+  const float r2 = reciprocal_rms(sum[0], inv_cols, p.eps);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (first(i) >= p.cols) continue;
@@ -258,9 +320,10 @@ constexpr int GATE_ANY_THREADS = 512;
 
 template <bool BF16>
 __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_any_kernel(const __grid_constant__ GateNormParams p) {
-  __shared__ float s_sum[2][32];
+  __shared__ float4 s_sum[2][32];
   constexpr int H_OUT = BF16 ? OUT_BF16 : OUT_F16;
   const int64_t row = blockIdx.x;
+  const float inv_cols = 1.0f / static_cast<float>(p.cols);
   grid_dependency_wait();
   const uint16_t* y = static_cast<const uint16_t*>(p.y) + row * p.ldy;
   const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ldx;
@@ -275,7 +338,7 @@ __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_any_kernel(const _
       sum[0] += a * a;
     }
     block_sums<1>(sum, s_sum[0]);
-    r1 = reciprocal_rms(sum[0], p.cols, p.eps);
+    r1 = reciprocal_rms(sum[0], inv_cols, p.eps);
   }
   const auto h_at = [&](int c) {
     const float a = gate_load<BF16>(y, c);
@@ -289,7 +352,7 @@ __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_any_kernel(const _
   }
   block_sums<1>(sum, s_sum[1]);
   grid_launch_dependents();
-  const float r2 = reciprocal_rms(sum[0], p.cols, p.eps);
+  const float r2 = reciprocal_rms(sum[0], inv_cols, p.eps);
   for (int c = threadIdx.x; c < p.cols; c += GATE_ANY_THREADS) {
     const float h = h_at(c);
     store_out<H_OUT>(p.h, row * p.ldh + c, h);
@@ -340,13 +403,15 @@ __device__ __forceinline__ void ring_drain(const GateNormParams& p, int64_t land
 template <bool BF16, int PER>
 __global__ void __launch_bounds__(512) gate_norm_ring_kernel(const __grid_constant__ GateNormParams p) {
   extern __shared__ __align__(128) uint8_t ring_data[];
-  __shared__ float s_sum[2][2][32];
+  // (alternating, so that a fast warp's next row leaves a slow one's sums alone)
+  __shared__ float4 s_sum[2][2][32];
   __shared__ __align__(8) uint64_t bars[GATE_MAX_STAGES];
   __shared__ int abort_word;
   const int pieces = p.cols >> 3;
   const uint4 none = make_uint4(0, 0, 0, 0);
   const bool by_column = p.gate_kind == GATE_COLS || p.gate_kind == GATE_FULL;
   const bool full = p.gate_kind == GATE_FULL;
+  const float inv_cols = 1.0f / static_cast<float>(p.cols);
   const uint32_t bar0 = smem_addr(bars), data0 = smem_addr(ring_data);
   const int row_bytes = gate_row_bytes(p.cols), stage_bytes = p.ring.ops * row_bytes;
   const uint64_t policy = policy_evict_first();  // read once
@@ -369,71 +434,89 @@ __global__ void __launch_bounds__(512) gate_norm_ring_kernel(const __grid_consta
     w2[i] = in ? static_cast<const uint4*>(p.w2)[at] : none;
     gv[i] = in && p.gate_kind == GATE_COLS ? static_cast<const uint4*>(p.gate)[at] : none;
   }
+  const float_pair alpha = pair_of(p.alpha);
+  // The sum of squares of y is formed a row ahead, so that it goes through the
+  // threads together with the row's own: one barrier a row.
+  const auto square_sum = [&](int stage) {
+    const uint4* sy = reinterpret_cast<const uint4*>(ring_data + stage * stage_bytes);
+    float_pair sq = pair_of(0.0f);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = threadIdx.x + i * blockDim.x;
+      if (at >= pieces) continue;
+      float_pair y[4];
+      pair_unpack<BF16>(sy[at], y);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sq = fma2(y[c], y[c], sq);
+    }
+    return sum_of(sq);
+  };
   int odd = 0, s = 0;
   uint32_t phase = 0;
-  bool ok = true;  // this thread has seen every row so far arrive
-  int64_t landed = 0;
+  // This thread has seen every row so far arrive. (A wait that runs out leaves its
+  // row and the block's next ones wrong and says so; the loop and its barriers go
+  // on, without waits and copies.)
+  bool ok = wait_bounded_lazy(bar0, 0, ctl, WAIT_MMA_FULL);
+  int64_t landed = ok;
+  float next[1] = {p.w1 ? square_sum(0) : 0.0f};
+  block_sums<1>(next, s_sum[1][1]);
   int64_t n = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++n, odd ^= 1) {
     const float gr = p.gate_kind == GATE_ROWS ? gate_load<BF16>(p.gate, row * p.ldg) : 1.0f;
-    // (a wait that runs out leaves this row and the block's next ones wrong and
-    // says so; the loop and its barriers go on, without waits and copies)
-    ok = ok && wait_bounded_lazy(bar0 + 8 * s, phase, ctl, WAIT_MMA_FULL);
-    landed += ok;
     const uint4* sy = reinterpret_cast<const uint4*>(ring_data + s * stage_bytes);
     const uint4* sx = reinterpret_cast<const uint4*>(ring_data + s * stage_bytes + row_bytes);
     const uint4* sg = reinterpret_cast<const uint4*>(ring_data + s * stage_bytes + 2 * row_bytes);
-    float h[PER][8];  // y, then h
-    float sum[1] = {0.0f};
+    const float r1 = p.w1 ? reciprocal_rms(next[0], inv_cols, p.eps) : 1.0f;
+    float_pair h[PER][4];
+    float_pair sq = pair_of(0.0f);
+    const float_pair factor = pair_of(by_column ? r1 : r1 * gr);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = threadIdx.x + i * blockDim.x;
-      gate_unpack<BF16>(at < pieces ? sy[at] : none, h[i]);
+      if (at >= pieces) continue;
+      float_pair x[4], w[4], g[4];
+      pair_unpack<BF16>(sy[at], h[i]);
+      pair_unpack<BF16>(sx[at], x);
+      if (full) gv[i] = sg[at];
+      pair_unpack<BF16>(w1[i], w);
+      pair_unpack<BF16>(gv[i], g);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum[0] += h[i][c] * h[i][c];
-    }
-    float r1 = 1.0f;
-    if (p.w1) {
-      block_sums<1>(sum, s_sum[odd][0]);
-      r1 = reciprocal_rms(sum[0], p.cols, p.eps);
-    }
-    sum[0] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int at = threadIdx.x + i * blockDim.x;
-      float x[8], w[8], g[8];
-      gate_unpack<BF16>(at < pieces ? sx[at] : none, x);
-      if (full) gv[i] = at < pieces ? sg[at] : none;
-      gate_unpack<BF16>(w1[i], w);
-      gate_unpack<BF16>(gv[i], g);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float u = p.w1 ? h[i][c] * r1 * w[c] : h[i][c];
-        h[i][c] = p.alpha * x[c] + (by_column ? g[c] : gr) * u;
-        sum[0] += h[i][c] * h[i][c];
+      for (int c = 0; c < 4; ++c) {
+        float_pair u = mul2(h[i][c], factor);
+        if (p.w1) u = mul2(u, w[c]);
+        if (by_column) u = mul2(u, g[c]);
+        h[i][c] = fma2(alpha, x[c], u);
+        sq = fma2(h[i][c], h[i][c], sq);
       }
     }
-    block_sums<1>(sum, s_sum[odd][1]);
+    const int later = s + 1 == p.ring.stages ? 0 : s + 1;
+    const uint32_t later_phase = later == 0 ? phase ^ 1u : phase;
+    float sums[2] = {sum_of(sq), 0.0f};
+    if (row + gridDim.x < p.rows) {
+      ok = ok && wait_bounded_lazy(bar0 + 8 * later, later_phase, ctl, WAIT_MMA_FULL);
+      landed += ok;
+      if (p.w1) sums[1] = square_sum(later);
+    }
+    block_sums<2>(sums, s_sum[odd][0]);
+    next[0] = sums[1];
     // (the stage has been read; into a place whose last copy has landed, no other)
     if (threadIdx.x == 0 && ok) ring_fetch(p, n + p.ring.stages, s, bar0, data0, policy);
-    const float r2 = reciprocal_rms(sum[0], p.cols, p.eps);
+    const float_pair r2 = pair_of(reciprocal_rms(sums[0], inv_cols, p.eps));
     uint4* ph = row_pieces(p.h, row, p.ldh);
     uint4* pv = row_pieces(p.v, row, p.ldv);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = threadIdx.x + i * blockDim.x;
       if (at >= pieces) continue;
-      float w[8];
-      gate_unpack<BF16>(w2[i], w);
-      ph[at] = gate_pack<BF16>(h[i]);
+      float_pair w[4];
+      pair_unpack<BF16>(w2[i], w);
+      ph[at] = pair_pack<BF16>(h[i]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] *= h[i][c] * r2;
-      pv[at] = gate_pack<BF16>(w);
+      for (int c = 0; c < 4; ++c) w[c] = mul2(mul2(h[i][c], r2), w[c]);
+      pv[at] = pair_pack<BF16>(w);
     }
-    if (++s == p.ring.stages) {
-      s = 0;
-      phase ^= 1u;
-    }
+    s = later;
+    phase = later_phase;
   }
   grid_launch_dependents();
   if (threadIdx.x == 0 && !ok) ring_drain(p, landed, bar0);
@@ -446,7 +529,7 @@ template <bool BF16, int PER, int GATE, bool BLOCK, bool RING>
 __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_constant__ GateNormGradParams p) {
   extern __shared__ __align__(128) uint8_t ring_data[];
   // (alternating, so that a fast warp's next row leaves a slow one's sums alone)
-  __shared__ float s_sum[2][3][64];
+  __shared__ float4 s_sum[2][3][32];
   __shared__ __align__(8) uint64_t bars[GATE_MAX_STAGES];
   __shared__ int abort_word;
   const GateNormParams& f = p.f;
@@ -468,35 +551,68 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     for (int i = 0; i < f.ring.stages; ++i) ring_fetch(f, i, i, bar0, data0, policy);
   const WaitCtl ctl{f.ring.timeout_ns, f.ring.error_word, &abort_word};
   // a column's factors: of u in h (w1, and the gate of columns), and w2
-  float gw[PER][8];
+  float_pair gw[PER][4];
   uint4 w2[PER];
-  float sum_w2[PER][8], sum_e[PER][8];
+  float_pair sum_w2[PER][4], sum_e[PER][4];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int at = threadIdx.x + i * blockDim.x;
     const bool in = at < pieces;
-    w2[i] = in ? load_piece<RING>(static_cast<const uint16_t*>(f.w2), 8 * at, f.cols) : none;
-    if (BLOCK) gate_unpack<BF16>(in ? load_piece<RING>(static_cast<const uint16_t*>(f.w1), 8 * at, f.cols) : none, gw[i]);
-    float g[8];
-    if (GATE == GATE_COLS) gate_unpack<BF16>(in ? load_piece<RING>(static_cast<const uint16_t*>(f.gate), 8 * at, f.cols) : none, g);
+    const auto column = [&](const void* w) {
+      return in ? load_piece<RING>(static_cast<const uint16_t*>(w), 8 * at, f.cols) : none;
+    };
+    w2[i] = column(f.w2);
+    if (BLOCK) pair_unpack<BF16>(column(f.w1), gw[i]);
+    float_pair g[4];
+    if (GATE == GATE_COLS) pair_unpack<BF16>(column(f.gate), g);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (!BLOCK) gw[i][c] = 1.0f;
-      if (GATE == GATE_COLS) gw[i][c] *= g[c];
-      sum_w2[i][c] = sum_e[i][c] = 0.0f;
+    for (int c = 0; c < 4; ++c) {
+      if (!BLOCK) gw[i][c] = pair_of(1.0f);
+      if (GATE == GATE_COLS) gw[i][c] = mul2(gw[i][c], g[c]);
+      sum_w2[i][c] = sum_e[i][c] = pair_of(0.0f);
     }
   }
+  const float_pair alpha = pair_of(f.alpha);
+  // y's sum of squares. Through a ring it is formed a row ahead, so that it goes
+  // through the threads together with other sums: two barriers a row, not three.
+  const auto square_sum = [&](const auto& piece) {
+    float_pair sq = pair_of(0.0f);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (threadIdx.x + i * blockDim.x >= pieces) continue;
+      float_pair y[4];
+      pair_unpack<BF16>(piece(i), y);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sq = fma2(y[c], y[c], sq);
+    }
+    return sum_of(sq);
+  };
+  const auto staged_sum = [&](int stage) {
+    const uint4* y = reinterpret_cast<const uint4*>(ring_data + stage * stage_bytes);
+    return square_sum([&](int i) { return y[threadIdx.x + i * blockDim.x]; });
+  };
   int odd = 0, s = 0;
   uint32_t phase = 0;
-  bool ok = true;  // this thread has seen every row so far arrive
+  // This thread has seen every row so far arrive. (A wait that runs out leaves its
+  // row and the block's next ones wrong and says so; the loop and its barriers go
+  // on, without waits and copies.)
+  bool ok = true;
   int64_t landed = 0, n = 0;
+  float s1[1] = {0.0f};
+  if (RING) {
+    ok = wait_bounded_lazy(bar0, 0, ctl, WAIT_MMA_FULL);
+    landed = ok;
+    if (BLOCK) {
+      s1[0] = staged_sum(0);
+      block_sums<1>(s1, s_sum[1][0]);
+    }
+  }
   for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x, ++n, odd ^= 1) {
     const float gr = GATE == GATE_ROWS ? gate_load<BF16>(f.gate, row * f.ldg) : 1.0f;
-    // (a wait that runs out leaves this row and the block's next ones wrong and
-    // says so; the loop and its barriers go on, without waits and copies)
-    if (RING) ok = ok && wait_bounded_lazy(bar0 + 8 * s, phase, ctl, WAIT_MMA_FULL);
-    landed += ok;
     const uint8_t* stage = ring_data + s * stage_bytes;
+    const auto store = [&](void* to, int64_t ld, int at, const float_pair (&v)[4]) {
+      store_piece<RING>(static_cast<uint16_t*>(to) + row * ld, 8 * at, f.cols, pair_pack<BF16>(v));
+    };
     uint4 early[PER][GATE_MAX_OPS];  // (not RING)
     if constexpr (!RING) {
       const int ops[GATE_MAX_OPS] = {0, 1, p.dh ? 2 : -1, p.dv ? op_dv : -1, GATE == GATE_FULL ? op_gate : -1};
@@ -527,130 +643,126 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
       const int slot = op <= 2 ? op : op == 3 ? op_dv : op_gate;
       return reinterpret_cast<const uint4*>(stage + slot * row_bytes)[threadIdx.x + i * blockDim.x];
     };
-    const auto store = [&](void* to, int64_t ld, int at, const float (&v)[8]) {
-      store_piece<RING>(static_cast<uint16_t*>(to) + row * ld, 8 * at, f.cols, gate_pack<BF16>(v));
-    };
     uint4 yv[PER], gv[PER];
-    float r1 = 1.0f;
-    float s1[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int at = threadIdx.x + i * blockDim.x;
-      if (at >= pieces) continue;
+      if (threadIdx.x + i * blockDim.x >= pieces) continue;
       yv[i] = operand(0, i);
       if (GATE == GATE_FULL) gv[i] = operand(4, i);
-      if (BLOCK) {
-        float y[8];
-        gate_unpack<BF16>(yv[i], y);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) s1[0] += y[c] * y[c];
-      }
     }
-    if (BLOCK) {
+    if (BLOCK && !RING) {
+      s1[0] = square_sum([&](int i) { return yv[i]; });
       block_sums<1>(s1, s_sum[odd][0]);
-      r1 = reciprocal_rms(s1[0], f.cols, f.eps);
     }
-    const float gr1 = gr * r1;
-    float h[PER][8];  // then dh'
-    float s2[2] = {0.0f, 0.0f};
+    const float r1 = BLOCK ? reciprocal_rms(s1[0], inv_cols, f.eps) : 1.0f;
+    const float_pair gr1 = pair_of(gr * r1), r1p = pair_of(r1);
+    float_pair h[PER][4];  // then dh'
+    float_pair dot = pair_of(0.0f), sq = pair_of(0.0f);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int at = threadIdx.x + i * blockDim.x;
-      if (at >= pieces) continue;
-      float y[8], x[8], g[8], dv[8], w[8];
-      gate_unpack<BF16>(yv[i], y);
-      gate_unpack<BF16>(operand(1, i), x);
-      if (GATE == GATE_FULL) gate_unpack<BF16>(gv[i], g);
+      if (threadIdx.x + i * blockDim.x >= pieces) continue;
+      float_pair y[4], x[4], g[4], dv[4], w[4];
+      pair_unpack<BF16>(yv[i], y);
+      pair_unpack<BF16>(operand(1, i), x);
+      if (GATE == GATE_FULL) pair_unpack<BF16>(gv[i], g);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float u = y[c] * gr1 * gw[i][c];
-        if (GATE == GATE_FULL) u *= g[c];
-        h[i][c] = fmaf(f.alpha, x[c], u);
-        s2[0] = fmaf(h[i][c], h[i][c], s2[0]);
+      for (int c = 0; c < 4; ++c) {
+        float_pair u = mul2(y[c], gr1);
+        if (BLOCK || GATE == GATE_COLS) u = mul2(u, gw[i][c]);
+        if (GATE == GATE_FULL) u = mul2(u, g[c]);
+        h[i][c] = fma2(alpha, x[c], u);
+        sq = fma2(h[i][c], h[i][c], sq);
       }
       if (p.dv) {
-        gate_unpack<BF16>(operand(3, i), dv);
-        gate_unpack<BF16>(w2[i], w);
+        pair_unpack<BF16>(operand(3, i), dv);
+        pair_unpack<BF16>(w2[i], w);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) s2[1] = fmaf(dv[c] * w[c], h[i][c], s2[1]);
+        for (int c = 0; c < 4; ++c) dot = fma2(mul2(dv[c], w[c]), h[i][c], dot);
       }
     }
+    float s2[2] = {sum_of(sq), sum_of(dot)};
     block_sums<2>(s2, s_sum[odd][1]);
-    const float r2 = reciprocal_rms(s2[0], f.cols, f.eps);
+    const float r2 = reciprocal_rms(s2[0], inv_cols, f.eps);
     const float m2 = s2[1] * r2 * inv_cols;
-    const float back = -(r2 * m2);
-    float s3[2] = {0.0f, 0.0f};
+    const float_pair r2p = pair_of(r2), back = pair_of(-(r2 * m2)), grp = pair_of(gr);
+    dot = pair_of(0.0f);  // of e and gw
+    float_pair row_dg = pair_of(0.0f);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = threadIdx.x + i * blockDim.x;
       if (at >= pieces) continue;
-      float y[8], g[8], dh[8], dg[8];
-      gate_unpack<BF16>(yv[i], y);
-      if (GATE == GATE_FULL) gate_unpack<BF16>(gv[i], g);
+      float_pair y[4], g[4], dh[4], dg[4];
+      pair_unpack<BF16>(yv[i], y);
+      if (GATE == GATE_FULL) pair_unpack<BF16>(gv[i], g);
       if (p.dh) {
-        gate_unpack<BF16>(operand(2, i), dh);
+        pair_unpack<BF16>(operand(2, i), dh);
       } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) dh[c] = 0.0f;
+        for (int c = 0; c < 4; ++c) dh[c] = pair_of(0.0f);
       }
       if (p.dv) {
-        float dv[8], w[8];
-        gate_unpack<BF16>(operand(3, i), dv);
-        gate_unpack<BF16>(w2[i], w);
+        float_pair dv[4], w[4];
+        pair_unpack<BF16>(operand(3, i), dv);
+        pair_unpack<BF16>(w2[i], w);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float hn = h[i][c] * r2;
-          sum_w2[i][c] = fmaf(dv[c], hn, sum_w2[i][c]);
-          h[i][c] = fmaf(hn, back, fmaf(dv[c] * w[c], r2, dh[c]));
+        for (int c = 0; c < 4; ++c) {
+          const float_pair hn = mul2(h[i][c], r2p);
+          sum_w2[i][c] = fma2(dv[c], hn, sum_w2[i][c]);
+          h[i][c] = fma2(hn, back, fma2(mul2(dv[c], w[c]), r2p, dh[c]));
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) h[i][c] = dh[c];
+        for (int c = 0; c < 4; ++c) h[i][c] = dh[c];
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float e = h[i][c] * (y[c] * r1);
+      for (int c = 0; c < 4; ++c) {
+        float_pair e = mul2(h[i][c], mul2(y[c], r1p));
         if (GATE == GATE_FULL) {
-          dg[c] = e * gw[i][c];
-          e *= g[c];
+          dg[c] = mul2(e, gw[i][c]);
+          e = mul2(e, g[c]);
         } else if (GATE == GATE_ROWS) {
-          e *= gr;
+          row_dg = fma2(e, gw[i][c], row_dg);
+          e = mul2(e, grp);
         }
-        sum_e[i][c] += e;
-        s3[0] = fmaf(e, gw[i][c], s3[0]);
-        dh[c] = f.alpha * h[i][c];
+        sum_e[i][c] = add2(sum_e[i][c], e);
+        dot = fma2(e, gw[i][c], dot);
+        dh[c] = mul2(alpha, h[i][c]);
       }
       store(p.dx, p.lddx, at, dh);
       if (GATE == GATE_FULL) store(p.dgate, p.lddg, at, dg);
-      if (GATE == GATE_ROWS) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) s3[1] = fmaf(h[i][c] * gw[i][c], y[c] * r1, s3[1]);
-      }
     }
-    block_sums<2>(s3, s_sum[odd][2]);
+    const int later = s + 1 == f.ring.stages ? 0 : s + 1;
+    const uint32_t later_phase = later == 0 ? phase ^ 1u : phase;
+    float s3[3] = {sum_of(dot), sum_of(row_dg), 0.0f};
+    if (RING && row + gridDim.x < f.rows) {
+      ok = ok && wait_bounded_lazy(bar0 + 8 * later, later_phase, ctl, WAIT_MMA_FULL);
+      landed += ok;
+      if (BLOCK) s3[2] = staged_sum(later);
+    }
+    block_sums<3>(s3, s_sum[odd][2]);
+    s1[0] = s3[2];
     // (the stage has been read; into a place whose last copy has landed, no other)
     if (RING && threadIdx.x == 0 && ok) ring_fetch(f, n + f.ring.stages, s, bar0, data0, policy);
     if (GATE == GATE_ROWS && threadIdx.x == 0) store_kind(p.dgate, row, s3[1], p.out_kind);
-    const float back1 = BLOCK ? -(s3[0] * inv_cols * r1 * r1) : 0.0f;
+    const float_pair back1 = pair_of(-(s3[0] * inv_cols * r1 * r1));
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = threadIdx.x + i * blockDim.x;
       if (at >= pieces) continue;
-      float y[8], g[8];
-      gate_unpack<BF16>(yv[i], y);
-      if (GATE == GATE_FULL) gate_unpack<BF16>(gv[i], g);
+      float_pair y[4], g[4];
+      pair_unpack<BF16>(yv[i], y);
+      if (GATE == GATE_FULL) pair_unpack<BF16>(gv[i], g);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float d = h[i][c] * gr1 * gw[i][c];
-        if (GATE == GATE_FULL) d *= g[c];
-        h[i][c] = BLOCK ? fmaf(y[c], back1, d) : d;
+      for (int c = 0; c < 4; ++c) {
+        float_pair d = mul2(h[i][c], gr1);
+        if (BLOCK || GATE == GATE_COLS) d = mul2(d, gw[i][c]);
+        if (GATE == GATE_FULL) d = mul2(d, g[c]);
+        h[i][c] = BLOCK ? fma2(y[c], back1, d) : d;
       }
       store(p.dy, p.lddy, at, h[i]);
     }
-    if (RING && ++s == f.ring.stages) {
-      s = 0;
-      phase ^= 1u;
-    }
+    s = later;
+    phase = later_phase;
   }
   grid_launch_dependents();
   if (RING && threadIdx.x == 0 && !ok) ring_drain(f, landed, bar0);
@@ -660,7 +772,14 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
   for (int i = 0; i < PER; ++i) {
     const int at = threadIdx.x + i * blockDim.x;
     if (at >= pieces) continue;
-    const auto sums_out = [&](float* to, const float (&v)[8]) {
+    const auto sums_out = [&](float* to, const float_pair (&pairs)[4]) {
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 a = floats_of(pairs[c]);
+        v[2 * c] = a.x;
+        v[2 * c + 1] = a.y;
+      }
       if constexpr (RING) {
 #pragma unroll
         for (int c = 0; c < 8; c += 4)
@@ -680,7 +799,7 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
 // sums over rows lie in the workspace, each written by one thread only.
 template <bool BF16>
 __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_grad_any_kernel(const __grid_constant__ GateNormGradParams p) {
-  __shared__ float s_sum[2][3][64];
+  __shared__ float4 s_sum[2][3][32];
   constexpr int OUT = BF16 ? OUT_BF16 : OUT_F16;
   const GateNormParams& f = p.f;
   const bool by_column = f.gate_kind == GATE_COLS || f.gate_kind == GATE_FULL;
@@ -703,7 +822,7 @@ __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_grad_any_kernel(co
         s[0] += a * a;
       }
       block_sums<1>(s, s_sum[odd][0]);
-      r1 = reciprocal_rms(s[0], f.cols, f.eps);
+      r1 = reciprocal_rms(s[0], inv_cols, f.eps);
     }
     const auto gate_at = [&](int c) { return by_column ? gate_load<BF16>(f.gate, g0 + c) : gr; };
     const auto u_at = [&](int c) {
@@ -719,7 +838,7 @@ __global__ void __launch_bounds__(GATE_ANY_THREADS) gate_norm_grad_any_kernel(co
       s2[1] += dv_at(c) * gate_load<BF16>(f.w2, c) * h;
     }
     block_sums<2>(s2, s_sum[odd][1]);
-    const float r2 = reciprocal_rms(s2[0], f.cols, f.eps);
+    const float r2 = reciprocal_rms(s2[0], inv_cols, f.eps);
     const float m2 = s2[1] * r2 * inv_cols;
     const auto d_at = [&](int c, float dv, float hn) {
       return (p.dh ? gate_load<BF16>(p.dh, row * p.lddh + c) : 0.0f) +

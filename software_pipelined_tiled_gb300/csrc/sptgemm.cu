@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>

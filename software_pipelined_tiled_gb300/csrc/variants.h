@@ -89,6 +89,7 @@ const void* route_dlogits_variant(int type, int slots);
 // Rows to their experts and back; aligned: all rows on 16-byte boundaries.
 const void* dispatch_sort_variant();
 const void* dispatch_copy_variant(bool aligned);
+const void* dispatch_small_variant(bool aligned);
 const void* combine_rows_variant(bool bf16, bool aligned);
 const void* combine_rows_grad_variant(bool bf16, bool aligned);
 
