@@ -411,7 +411,9 @@ int sptg_grouped_gemm_dw(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype 
  * copies to the host, graph capture, the same bits on every call. Rows of
  * SPTG_T_F16 or SPTG_T_BF16 take any width, pitch and element-aligned pointer; they
  * are read in 16-byte pieces when the width and every pitch are multiples of 8
- * and every pointer is 16-byte aligned. Outputs overlap nothing unless said.
+ * and every pointer is 16-byte aligned, else in pairs of words shifted together (up to
+ * 16376 columns; the gradients of the norms up to 8192). cols <= 2^30. Outputs overlap
+ * nothing unless said.
  */
 
 /*
@@ -511,11 +513,15 @@ typedef enum {
  * of out_type: SPTG_T_F32 or the rows' type. They are summed up in fp32 in a fixed order
  * of the rows, by way of a workspace of sptg_gate_add_rms_norm_grad_workspace
  * bytes (16-byte aligned; not shared by calls that run at the same time).
+ *
+ * cfg: its fields timeout_ms and inject_stall, as for sptg_add_rms_norm_ex (the
+ * others are ignored; NULL = defaults).
  */
 int sptg_gate_add_rms_norm(int64_t rows, int64_t cols, sptg_type type, const void* y, int64_t ldy,
                            const void* residual, int64_t ldr, const void* block_weight, const void* gate,
                            sptg_gate gate_kind, int64_t ldg, float alpha, const void* weight, float eps,
-                           void* h, int64_t ldh, void* v, int64_t ldv, void* stream);
+                           void* h, int64_t ldh, void* v, int64_t ldv, void* stream,
+                           const sptg_config* cfg);
 int64_t sptg_gate_add_rms_norm_grad_workspace(int64_t rows, int64_t cols);
 int sptg_gate_add_rms_norm_grad(int64_t rows, int64_t cols, sptg_type type, const void* dh, int64_t lddh,
                                 const void* dv, int64_t lddv, const void* y, int64_t ldy,
@@ -523,7 +529,8 @@ int sptg_gate_add_rms_norm_grad(int64_t rows, int64_t cols, sptg_type type, cons
                                 const void* gate, sptg_gate gate_kind, int64_t ldg, float alpha,
                                 const void* weight, float eps, void* dy, int64_t lddy, void* dresidual,
                                 int64_t lddr, void* dgate, int64_t lddg, void* dweight, void* dblock_weight,
-                                sptg_type out_type, void* workspace, int64_t workspace_bytes, void* stream);
+                                sptg_type out_type, void* workspace, int64_t workspace_bytes, void* stream,
+                                const sptg_config* cfg);
 
 #ifdef __cplusplus
 }

@@ -131,10 +131,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.sptg_combine_rows.argtypes = [i64, i64, i, i64, i, vp, i64, vp, vp, vp, i64, vp, i64, vp]
         lib.sptg_combine_rows_grad.argtypes = [i64, i64, i, i64, i, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]
         lib.sptg_gate_add_rms_norm.argtypes = [i64, i64, i, vp, i64, vp, i64, vp, vp, i, i64, fl, vp, fl,
-                                               vp, i64, vp, i64, vp]
+                                               vp, i64, vp, i64, vp, ctypes.POINTER(Config)]
         lib.sptg_gate_add_rms_norm_grad.argtypes = [i64, i64, i, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
                                                     i, i64, fl, vp, fl, vp, i64, vp, i64, vp, i64, vp, vp,
-                                                    i, vp, i64, vp]
+                                                    i, vp, i64, vp, ctypes.POINTER(Config)]
         lib.sptg_gate_add_rms_norm_grad_workspace.argtypes = [i64, i64]
         lib.sptg_gate_add_rms_norm_grad_workspace.restype = i64
         for f in (lib.sptg_route_experts, lib.sptg_route_experts_dlogits, lib.sptg_dispatch_rows,

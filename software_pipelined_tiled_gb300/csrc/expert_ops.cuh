@@ -388,13 +388,15 @@ constexpr int kGateRingSmem = 223 * 1024;
 // and an SM holds more of them.
 int64_t gate_grad_blocks(int64_t cols) { return 456 * std::max<int64_t>(1, std::min<int64_t>(8, 4096 / std::max<int64_t>(cols, 1))); }
 
-int gate_norm_checks(int64_t rows, int64_t cols, int type, int gate_kind, float alpha, float eps, bool& bf16,
-                     const char*& name) {
+int gate_norm_checks(int64_t rows, int64_t cols, int type, int gate_kind, float alpha, float eps,
+                     const sptg_config* cfg, bool& bf16, const char*& name) {
   if (!row_type(type, bf16, name)) return refuse(SPTG_ERR_ARG, "rows are f16 or bf16");
   if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxCols) return refuse(SPTG_ERR_ARG, kRowText);
   if (gate_kind < SPTG_GATE_NONE || gate_kind > SPTG_GATE_FULL) return refuse(SPTG_ERR_ARG, "unknown kind of gate");
   if (!(eps > 0.0f) || !(eps < INFINITY)) return refuse(SPTG_ERR_ARG, "eps must be positive and finite");
   if (!(alpha > -INFINITY && alpha < INFINITY)) return refuse(SPTG_ERR_ARG, "alpha must be finite");
+  if (cfg && (cfg->timeout_ms < 0 || (cfg->inject_stall != 0 && cfg->inject_stall != 1)))
+    return refuse(SPTG_ERR_ARG, "timeout_ms must not be negative, inject_stall 0 or 1");
   return SPTG_OK;
 }
 
@@ -418,12 +420,19 @@ GateRing gate_ring(const void* y, int64_t ldy, const void* x, int64_t ldx, const
   return r;
 }
 
+void set_ring(GateRing& r, int stages, const DeviceInfo& di, const sptg_config* cfg) {
+  r.stages = stages;
+  r.error_word = di.error_word;
+  r.timeout_ns = cfg && cfg->timeout_ms ? cfg->timeout_ms * 1000000ull : kOpTimeoutNs;
+  r.inject_stall = cfg ? cfg->inject_stall : 0;
+}
+
 int gate_norm(int64_t rows, int64_t cols, int type, const void* y, int64_t ldy, const void* x, int64_t ldx,
               const void* w1, const void* gate, int gate_kind, int64_t ldg, float alpha, const void* w2,
-              float eps, void* h, int64_t ldh, void* v, int64_t ldv, cudaStream_t stream) {
+              float eps, void* h, int64_t ldh, void* v, int64_t ldv, cudaStream_t stream, const sptg_config* cfg) {
   bool bf16;
   const char* name;
-  int rc = gate_norm_checks(rows, cols, type, gate_kind, alpha, eps, bf16, name);
+  int rc = gate_norm_checks(rows, cols, type, gate_kind, alpha, eps, cfg, bf16, name);
   if (rc) return rc;
   if (rows == 0 || cols == 0) {
     set_config("kernel=none type=%s (empty output)", name, {});
@@ -482,9 +491,7 @@ int gate_norm(int64_t rows, int64_t cols, int type, const void* y, int64_t ldy, 
   GateNormParams p{y, x, w1, w2, gate_kind == SPTG_GATE_NONE ? nullptr : gate, ldy, ldx, ldg, h, v, ldh, ldv,
                    rows, static_cast<int>(cols), gate_kind, alpha, eps, {}};
   p.ring = gate_ring(y, ldy, x, ldx, nullptr, 0, nullptr, 0, gate_kind == SPTG_GATE_FULL ? gate : nullptr, ldg);
-  p.ring.stages = stages;
-  p.ring.error_word = di.error_word;
-  p.ring.timeout_ns = kOpTimeoutNs;
+  set_ring(p.ring, stages, di, cfg);
   void* args[] = {&p};
   const cudaError_t e = launch_op(gate_norm_variant(bf16, kind), dim3(static_cast<unsigned>(grid)), threads, smem,
                                   1, stream, args);
@@ -502,10 +509,11 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
                    int64_t lddv, const void* y, int64_t ldy, const void* x, int64_t ldx, const void* w1,
                    const void* gate, int gate_kind, int64_t ldg, float alpha, const void* w2, float eps,
                    void* dy, int64_t lddy, void* dx, int64_t lddx, void* dgate, int64_t lddg, void* dw2,
-                   void* dw1, int out_type, void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+                   void* dw1, int out_type, void* workspace, int64_t workspace_bytes, cudaStream_t stream,
+                   const sptg_config* cfg) {
   bool bf16;
   const char* name;
-  int rc = gate_norm_checks(rows, cols, type, gate_kind, alpha, eps, bf16, name);
+  int rc = gate_norm_checks(rows, cols, type, gate_kind, alpha, eps, cfg, bf16, name);
   if (rc) return rc;
   if (out_type != SPTG_T_F32 && out_type != type)
     return refuse(SPTG_ERR_ARG, "the weights' gradients are f32 or of the rows' type");
@@ -575,9 +583,7 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
   p.f = GateNormParams{y, x, w1, w2, gate_kind == SPTG_GATE_NONE ? nullptr : gate, ldy, ldx, ldg, nullptr,
                        nullptr, 0, 0, rows, static_cast<int>(cols), gate_kind, alpha, eps, {}};
   p.f.ring = gate_ring(y, ldy, x, ldx, dh, lddh, dv, lddv, full ? gate : nullptr, ldg);
-  p.f.ring.stages = stages;
-  p.f.ring.error_word = di.error_word;
-  p.f.ring.timeout_ns = kOpTimeoutNs;
+  set_ring(p.f.ring, stages, di, cfg);
   p.dh = dh;
   p.dv = dv;
   p.lddh = lddh;
@@ -664,10 +670,10 @@ int sptg_combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, 
 int sptg_gate_add_rms_norm(int64_t rows, int64_t cols, sptg_type type, const void* y, int64_t ldy,
                            const void* residual, int64_t ldr, const void* block_weight, const void* gate,
                            sptg_gate gate_kind, int64_t ldg, float alpha, const void* weight, float eps,
-                           void* h, int64_t ldh, void* v, int64_t ldv, void* stream) {
+                           void* h, int64_t ldh, void* v, int64_t ldv, void* stream, const sptg_config* cfg) {
   return guarded([&] {
     return gate_norm(rows, cols, type, y, ldy, residual, ldr, block_weight, gate, gate_kind, ldg, alpha,
-                     weight, eps, h, ldh, v, ldv, static_cast<cudaStream_t>(stream));
+                     weight, eps, h, ldh, v, ldv, static_cast<cudaStream_t>(stream), cfg);
   });
 }
 
@@ -681,12 +687,13 @@ int sptg_gate_add_rms_norm_grad(int64_t rows, int64_t cols, sptg_type type, cons
                                 const void* gate, sptg_gate gate_kind, int64_t ldg, float alpha,
                                 const void* weight, float eps, void* dy, int64_t lddy, void* dresidual,
                                 int64_t lddr, void* dgate, int64_t lddg, void* dweight, void* dblock_weight,
-                                sptg_type out_type, void* workspace, int64_t workspace_bytes, void* stream) {
+                                sptg_type out_type, void* workspace, int64_t workspace_bytes, void* stream,
+                                const sptg_config* cfg) {
   return guarded([&] {
     return gate_norm_grad(rows, cols, type, dh, lddh, dv, lddv, y, ldy, residual, ldr, block_weight, gate,
                           gate_kind, ldg, alpha, weight, eps, dy, lddy, dresidual, lddr, dgate, lddg,
                           dweight, dblock_weight, out_type, workspace, workspace_bytes,
-                          static_cast<cudaStream_t>(stream));
+                          static_cast<cudaStream_t>(stream), cfg);
   });
 }
 

@@ -258,8 +258,8 @@ __device__ __forceinline__ Pair pair_exp(Pair x) {
 }
 
 // A key for the comparison of two experts whose scores lie close: the logit itself
-// where logits stand for the keys; else the score, with a bias if there is one. z: the
-// softmax's sum, of exponentials from the largest logit m on. Scores without a
+// where logits stand for the keys; else the score, with a bias if there is one. z: with
+// a bias the softmax's sum, of exponentials from the largest logit m on. Scores without a
 // bias are only compared with one another, and are all multiplied by exp(-m) if m
 // < 0, so that none is too small.
 enum RouteKey : int { KEY_LOGIT, KEY_SCORE, KEY_BIASED };
@@ -499,7 +499,9 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       k[j] = l[j] > -INFINITY && b[j] != -INFINITY ? (k[j] & ~PLACE) | (PLACE - j) : 0u;
     if constexpr (SORTED) sort_down<0, PER>(k);
     bool unsettled = false;
-    Pair z2 = {0.0f, 0.0f};  // the softmax's sum as a Pair, once it has been needed
+    // what scores are divided by, as a Pair: a softmax's sum beside a bias, once it has been needed
+    Pair z2 = {1.0f, 0.0f};
+    bool summed = p.sigmoid || !biased;
     if (p.groups > 1) {
       uint32_t t1 = 0, t2 = 0;
       if constexpr (SORTED) {
@@ -536,7 +538,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
           if constexpr (SORTED) {
             // the groups' sums anew, from each lane's two best keys
             const int kind = direct ? KEY_LOGIT : biased ? KEY_BIASED : KEY_SCORE;
-            if (!p.sigmoid && biased && !(z2.hi > 0.0f)) z2 = route_pair_z<TYPE, LANES>(p, row, first, count, m, mask);
+            if (!summed) z2 = route_pair_z<TYPE, LANES>(p, row, first, count, m, mask);
+            summed = true;
             float most_l = m;  // (a sigmoid's m is the lane's so far)
             for (int o = LANES / 2; o > 0; o >>= 1) most_l = fmaxf(most_l, __shfl_xor_sync(mask, most_l, o));
             Pair d[2];
@@ -653,8 +656,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
         if (SORTED && __ballot_sync(mask, near || differs) != 0) {
           // The picks and the extra ones, ranked by Pairs.
           const int kind = biased ? KEY_BIASED : KEY_LOGIT;  // (without a bias logits order the scores)
-          if (!p.sigmoid && biased && !(z2.hi > 0.0f))
-            z2 = route_pair_z<TYPE, LANES>(p, row, first, count, m, mask);
+          if (!summed) z2 = route_pair_z<TYPE, LANES>(p, row, first, count, m, mask);
           const Pair none = {-INFINITY, 0.0f};
           Pair a = pair_key(ol, ob, m, z2, kind, p.sigmoid), c = none;
           if (own < 0) a = none;

@@ -7,9 +7,14 @@ checks holds here too.
 ``route_experts``, ``dispatch_rows``, ``combine_rows`` and ``gate_add_rms_norm``
 take part in PyTorch's automatic differentiation: where an input requires a
 gradient (and none of the outputs is given), backward runs the functions that
-compute the gradients, which can also be called by themselves.
+compute the gradients, which can also be called by themselves.  All of them can
+be captured in a CUDA graph; a backward pass only while no other graph of the
+same leaves is alive (PyTorch's rule: a leaf's node keeps to the stream that it was
+made on, which may not join the capture).
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -352,7 +357,13 @@ def _gate_of(gate, rows, cols, dtype, device):
     return _GATE_FULL, _pitch(gate, rows, cols, dtype, device, "gate")
 
 
-def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream):
+def _with_config(function, config):
+    """A library call whose last argument, after the stream, is a configuration."""
+    cfg = None if config is None else ctypes.byref(config)
+    return lambda *args: function(*args, cfg)
+
+
+def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream, config=None):
     code = _row_type(y, "y")
     rows, cols = shape = y.shape
     dtype, device, on = y.dtype, y.get_device(), y.device
@@ -370,7 +381,7 @@ def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, st
         v, ldv = _empty(shape, dtype, on, stream), cols
     else:
         ldv = _pitch(v, rows, cols, dtype, device, "v")
-    _call(_gate_norm, device, stream, (
+    _call(_with_config(_gate_norm, config), device, stream, (
         rows, cols, code, y.data_ptr(), ldy, residual.data_ptr(), ldr,
         None if block_weight is None else block_weight.data_ptr(), None if gate is None else gate.data_ptr(),
         kind, ldg, alpha, weight.data_ptr(), eps, h.data_ptr(), ldh, v.data_ptr(), ldv),
@@ -398,7 +409,7 @@ class _GateAddRmsNorm(torch.autograd.Function):
 
 
 def gate_add_rms_norm(y, residual, weight, block_weight=None, gate=None, alpha: float = 1.0,
-                      eps: float = 1e-6, h=None, v=None, stream=None):
+                      eps: float = 1e-6, h=None, v=None, stream=None, config=None):
     """The end of a block: norm of its output, gate, scaled residual, norm before the next: returns (h, v).
 
     ``u = y * block_weight / sqrt(mean(y^2) + eps)`` (u = y without block_weight),
@@ -406,17 +417,18 @@ def gate_add_rms_norm(y, residual, weight, block_weight=None, gate=None, alpha: 
     residual itself), ``v = h * weight / sqrt(mean(h^2) + eps)``, in 32 bits, h
     and v rounded once each.  y, residual: T x C, float16 or bfloat16; weights: C
     values; gate: None, C values (or 1 x C), T x 1 or T x C, all of y's type.
+    config: a Config, for its timeout_ms and inject_stall.
 
     Differentiable by all tensors (gate_add_rms_norm_grad).
     """
     if _any_grad(y, residual, weight, block_weight, gate):
         return _differentiated(_GateAddRmsNorm, stream, y.device,
                                (y, residual, weight, block_weight, gate, alpha, eps), (h, v))
-    return _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream)
+    return _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream, config)
 
 
 def gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight=None, gate=None, alpha: float = 1.0,
-                           eps: float = 1e-6, out_dtype=None, stream=None):
+                           eps: float = 1e-6, out_dtype=None, stream=None, config=None):
     """Gradients of gate_add_rms_norm: returns those of (y, residual, weight, block_weight, gate).
 
     dh, dv: gradients of h and v (T x C of y's type; either may be None).
@@ -447,7 +459,7 @@ def gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight=None, gate=
         dgate = _empty(gate.shape, dtype if kind == _GATE_FULL else out_dtype, on, stream)
     space = _workspace(rows, cols)
     workspace = _empty((space,), torch.uint8, on, stream)
-    _call(_gate_norm_grad, device, stream, (
+    _call(_with_config(_gate_norm_grad, config), device, stream, (
         rows, cols, code, None if dh is None else dh.data_ptr(), lddh, None if dv is None else dv.data_ptr(),
         lddv, y.data_ptr(), ldy, residual.data_ptr(), ldr,
         None if block_weight is None else block_weight.data_ptr(), None if gate is None else gate.data_ptr(),

@@ -82,8 +82,8 @@ def test_combine_grad_refusals(lib):
 
 def test_gate_norm_refusals(lib):
     def call(T=2, C=16, t=BF16, y=OK, ldy=16, r=OK, ldr=16, w1=OK, g=OK, k=3, ldg=16, a=1.0, w2=OK, eps=1e-6, h=OK,
-             ldh=16, v=OK, ldv=16):
-        return lib.sptg_gate_add_rms_norm(T, C, t, y, ldy, r, ldr, w1, g, k, ldg, a, w2, eps, h, ldh, v, ldv, None)
+             ldh=16, v=OK, ldv=16, cfg=None):
+        return lib.sptg_gate_add_rms_norm(T, C, t, y, ldy, r, ldr, w1, g, k, ldg, a, w2, eps, h, ldh, v, ldv, None, cfg)
 
     for bad in (dict(t=S8), dict(t=F32), dict(T=-1), dict(C=1 << 31), dict(k=-1), dict(k=4), dict(eps=0.0), dict(eps=NAN),
                 dict(eps=INF), dict(a=INF), dict(a=NAN), dict(y=None), dict(r=None), dict(g=None), dict(w2=None),
@@ -94,6 +94,16 @@ def test_gate_norm_refusals(lib):
                 dict(v=OK + 1)):
         assert call(**bad) == ALIGN, bad
     assert call(T=0, y=None) == 0 and call(C=0, y=None) == 0
+    for bad in bad_configs():
+        assert call(cfg=bad) == ARG
+
+
+def bad_configs():
+    out = []
+    for name, value in (("timeout_ms", -1), ("inject_stall", 2), ("inject_stall", -1)):
+        out.append(sptg.Config())
+        setattr(out[-1], name, value)
+    return out
 
 
 def test_gate_norm_grad_refusals(lib):
@@ -104,9 +114,9 @@ def test_gate_norm_grad_refusals(lib):
 
     def call(T=2, C=16, t=BF16, dh=OK, lddh=16, dv=OK, lddv=16, y=OK, ldy=16, r=OK, ldr=16, w1=OK, g=OK, k=3, ldg=16,
              a=1.0, w2=OK, eps=1e-6, dy=OK, lddy=16, dr=OK, lddr=16, dg=OK, lddg=16, dw2=OK, dw1=OK, ot=F32, ws=OK,
-             n=size):
+             n=size, cfg=None):
         return lib.sptg_gate_add_rms_norm_grad(T, C, t, dh, lddh, dv, lddv, y, ldy, r, ldr, w1, g, k, ldg, a, w2, eps, dy,
-                                               lddy, dr, lddr, dg, lddg, dw2, dw1, ot, ws, n, None)
+                                               lddy, dr, lddr, dg, lddg, dw2, dw1, ot, ws, n, None, cfg)
 
     for bad in (dict(t=S8), dict(T=-1), dict(C=1 << 31), dict(k=4), dict(eps=-1.0), dict(a=NAN), dict(ot=F16), dict(ot=S8),
                 dict(y=None), dict(r=None), dict(g=None), dict(w2=None), dict(dy=None), dict(dr=None), dict(dg=None),
@@ -118,6 +128,8 @@ def test_gate_norm_grad_refusals(lib):
                 dict(w2=OK + 1), dict(dy=OK + 1), dict(dr=OK + 1), dict(dg=OK + 1), dict(dw2=OK + 2),
                 dict(dw1=OK + 2), dict(k=1, dg=OK + 2), dict(ws=OK + 8)):
         assert call(**bad) == ALIGN, bad
+    for bad in bad_configs():
+        assert call(cfg=bad) == ARG
 
 
 def test_python_refuses_bad_tensors():
