@@ -7,11 +7,15 @@ One step, as a serving process makes it for the tokens in flight:
 1. residual addition and norm into int8 with a scale for each row (``add_rms_norm``);
 2. a dense projection with 4-bit weights on those rows (``gemm_w4``);
 3. residual addition and norm into 16 bits;
-4. a router's logits (``gemm``), the best experts of each row, rows sorted by expert;
-5. two products grouped by expert around an activation (``grouped_gemm``).
+4. a router's logits (``gemm``), the best experts of each row (``route_experts``), rows
+   sorted by expert (``dispatch_rows``);
+5. two products grouped by expert around an activation (``grouped_gemm``), added up by
+   row (``combine_rows``);
+6. the block's end: norm, gate, residual and the next block's norm (``gate_add_rms_norm``).
 
-A training step then takes the gradients of the experts' weights and inputs
-(``grouped_gemm_dw``, ``grouped_gemm_dx``).  Weights and inputs are random.  The
+A training step then takes the gradients of the experts' weights and inputs and of
+the router's logits (``combine_rows_grad``, ``grouped_gemm_dw``, ``grouped_gemm_dx``,
+``dispatch_rows_dx``, ``route_experts_dlogits``).  Weights and inputs are random.  The
 script prints the time of a step and how far it is from a plain float32 version
 on the same data.
 """
@@ -46,22 +50,12 @@ def make_layer(hidden: int, inner: int, experts: int, dtype=torch.bfloat16, seed
                    + 0.001).to(dtype),
         "zeros": torch.randint(6, 10, (hidden, hidden // GROUP), device="cuda", generator=g,
                                dtype=torch.uint8),
+        "norm_out": normal(hidden, std=0.3), "norm3": 1 + normal(hidden, std=0.1),
+        "gate": normal(hidden, std=0.5),
         "router": normal(experts, hidden, std=hidden ** -0.5),
         "up": normal(experts, inner, hidden, std=hidden ** -0.5),
         "down": normal(experts, hidden, inner, std=inner ** -0.5),
     }
-
-
-def route(logits, top: int):
-    """Rows sorted by expert: (row of each sorted row, its weight, offsets of the experts)."""
-    weights, chosen = torch.topk(torch.softmax(logits.float(), dim=1), top, dim=1)
-    weights = weights / weights.sum(1, keepdim=True)
-    expert, order = torch.sort(chosen.reshape(-1), stable=True)
-    counts = torch.zeros(logits.shape[1], dtype=torch.int64, device=logits.device)
-    counts.index_add_(0, expert, torch.ones_like(expert))
-    offsets = torch.zeros(logits.shape[1] + 1, dtype=torch.int32, device=logits.device)
-    torch.cumsum(counts, 0, out=offsets[1:])
-    return order // top, weights.reshape(-1)[order], offsets
 
 
 def forward(layer: dict, x, residual, top: int) -> dict:
@@ -69,27 +63,38 @@ def forward(layer: dict, x, residual, top: int) -> dict:
     h, q, s = sptg.add_rms_norm(x, residual, layer["norm1"], eps=EPS, out_dtype=torch.int8)
     a = sptg.gemm_w4(q, layer["codes"], layer["scales"], layer["zeros"], x_scales=s)
     h, y, _ = sptg.add_rms_norm(a, h, layer["norm2"], eps=EPS)
-    rows, weight, offsets = route(sptg.gemm(y, layer["router"]), top)
-    sorted_rows = y[rows]
+    logits = sptg.gemm(y, layer["router"])
+    weights, experts = sptg.route_experts(logits, top)
+    sorted_rows, places, offsets = sptg.dispatch_rows(y, experts, logits.shape[1])
     u = sptg.grouped_gemm(sorted_rows, layer["up"], offsets)
     act = torch.nn.functional.silu(u)
     d = sptg.grouped_gemm(act, layer["down"], offsets)
-    out = torch.zeros(y.shape, dtype=torch.float32, device=y.device)
-    out.index_add_(0, rows, d.float() * weight[:, None])
-    return {"out": out.to(y.dtype), "residual": h, "y": y, "rows": rows, "weight": weight,
-            "offsets": offsets, "sorted_rows": sorted_rows, "u": u, "act": act}
+    out = sptg.combine_rows(d, places, weights)
+    next_residual, next_y = sptg.gate_add_rms_norm(out, h, layer["norm3"], block_weight=layer["norm_out"],
+                                                   gate=layer["gate"], eps=EPS)
+    return {"out": out, "residual": next_residual, "next": next_y, "y": y, "logits": logits, "experts": experts,
+            "weights": weights, "places": places, "offsets": offsets, "sorted_rows": sorted_rows, "u": u, "act": act,
+            "d": d}
+
+
+def by_place(kept: dict) -> dict:
+    """The row of each sorted row, and its weight."""
+    order = torch.argsort(kept["places"].reshape(-1))
+    return {"rows": order // kept["places"].shape[1], "weight": kept["weights"].reshape(-1)[order]}
 
 
 def expert_gradients(layer: dict, kept: dict, dout) -> dict:
-    """Gradients of the experts' weights (float32) and of the rows that went into them."""
-    offsets = kept["offsets"]
-    dd = (dout[kept["rows"]].float() * kept["weight"][:, None]).to(dout.dtype)
+    """Gradients of the experts' weights (float32), of the rows that went into them, and of the router's logits."""
+    offsets, places = kept["offsets"], kept["places"]
+    dd, dweights = sptg.combine_rows_grad(dout, kept["d"], places, kept["weights"])
     dact = sptg.grouped_gemm_dx(dd, layer["down"], offsets)
     sig = torch.sigmoid(kept["u"].float())
     du = (dact.float() * sig * (1 + kept["u"].float() * (1 - sig))).to(dout.dtype)
+    rows = sptg.grouped_gemm_dx(du, layer["up"], offsets)
     return {"down": sptg.grouped_gemm_dw(dd, kept["act"], offsets, out_dtype=torch.float32),
             "up": sptg.grouped_gemm_dw(du, kept["sorted_rows"], offsets, out_dtype=torch.float32),
-            "rows": sptg.grouped_gemm_dx(du, layer["up"], offsets)}
+            "rows": rows, "y": sptg.dispatch_rows_dx(rows, places),
+            "logits": sptg.route_experts_dlogits(dweights, kept["logits"], kept["experts"])}
 
 
 def plain_forward(layer: dict, x, residual, kept: dict):
@@ -128,6 +133,7 @@ def main(argv=None) -> dict:
     residual = torch.randn(a.rows, a.hidden, device="cuda", generator=g).bfloat16()
     kept = forward(layer, x, residual, a.top)
     grads = expert_gradients(layer, kept, kept["out"])
+    kept.update(by_place(kept))
     ref = plain_forward(layer, x, residual, kept)
     off = float((kept["out"].float() - ref).norm() / ref.norm())
 
