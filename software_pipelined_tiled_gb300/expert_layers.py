@@ -36,14 +36,6 @@ _GATE_NONE, _GATE_COLS, _GATE_ROWS, _GATE_FULL = range(4)
 _grad_enabled = torch.is_grad_enabled
 
 
-def _any_grad(*tensors) -> bool:
-    """Whether a call on these tensors (or None) has to keep a history."""
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            return _grad_enabled()
-    return False
-
-
 def _differentiated(function, stream, device, args, outputs):
     """A torch.autograd.Function's apply on the call's stream (backward runs there as well)."""
     for o in outputs:
@@ -297,7 +289,8 @@ def combine_rows(y, places, weights=None, base=None, out=None, stream=None):
     Differentiable by y, weights and base (combine_rows_grad); places then has to
     name every row of y once.
     """
-    if _any_grad(y, weights, base):
+    if ((y.requires_grad or (weights is not None and weights.requires_grad)
+         or (base is not None and base.requires_grad)) and _grad_enabled()):
         return _differentiated(_CombineRows, stream, y.device, (y, places, weights, base), (out,))
     return _run_combine(y, places, weights, base, out, stream)
 
@@ -357,10 +350,9 @@ def _gate_of(gate, rows, cols, dtype, device):
     return _GATE_FULL, _pitch(gate, rows, cols, dtype, device, "gate")
 
 
-def _with_config(function, config):
-    """A library call whose last argument, after the stream, is a configuration."""
-    cfg = None if config is None else ctypes.byref(config)
-    return lambda *args: function(*args, cfg)
+def _tail(config):
+    """The argument that follows the stream."""
+    return (None if config is None else ctypes.byref(config),)
 
 
 def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream, config=None):
@@ -381,11 +373,11 @@ def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, st
         v, ldv = _empty(shape, dtype, on, stream), cols
     else:
         ldv = _pitch(v, rows, cols, dtype, device, "v")
-    _call(_with_config(_gate_norm, config), device, stream, (
+    _call(_gate_norm, device, stream, (
         rows, cols, code, y.data_ptr(), ldy, residual.data_ptr(), ldr,
         None if block_weight is None else block_weight.data_ptr(), None if gate is None else gate.data_ptr(),
         kind, ldg, alpha, weight.data_ptr(), eps, h.data_ptr(), ldh, v.data_ptr(), ldv),
-        (y, residual, weight, block_weight, gate, h, v))
+        (y, residual, weight, block_weight, gate, h, v), _tail(config))
     return h, v
 
 
@@ -421,7 +413,9 @@ def gate_add_rms_norm(y, residual, weight, block_weight=None, gate=None, alpha: 
 
     Differentiable by all tensors (gate_add_rms_norm_grad).
     """
-    if _any_grad(y, residual, weight, block_weight, gate):
+    if ((y.requires_grad or residual.requires_grad or weight.requires_grad
+         or (block_weight is not None and block_weight.requires_grad)
+         or (gate is not None and gate.requires_grad)) and _grad_enabled()):
         return _differentiated(_GateAddRmsNorm, stream, y.device,
                                (y, residual, weight, block_weight, gate, alpha, eps), (h, v))
     return _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream, config)
@@ -459,12 +453,13 @@ def gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight=None, gate=
         dgate = _empty(gate.shape, dtype if kind == _GATE_FULL else out_dtype, on, stream)
     space = _workspace(rows, cols)
     workspace = _empty((space,), torch.uint8, on, stream)
-    _call(_with_config(_gate_norm_grad, config), device, stream, (
+    _call(_gate_norm_grad, device, stream, (
         rows, cols, code, None if dh is None else dh.data_ptr(), lddh, None if dv is None else dv.data_ptr(),
         lddv, y.data_ptr(), ldy, residual.data_ptr(), ldr,
         None if block_weight is None else block_weight.data_ptr(), None if gate is None else gate.data_ptr(),
         kind, ldg, alpha, weight.data_ptr(), eps, dy.data_ptr(), cols, dresidual.data_ptr(), cols,
         None if dgate is None else dgate.data_ptr(), cols, dweight.data_ptr(),
         None if dblock is None else dblock.data_ptr(), _TYPES[out_dtype], workspace.data_ptr(), space),
-        (dh, dv, y, residual, weight, block_weight, gate, dy, dresidual, dweight, dblock, dgate, workspace))
+        (dh, dv, y, residual, weight, block_weight, gate, dy, dresidual, dweight, dblock, dgate, workspace),
+        _tail(config))
     return dy, dresidual, dweight, dblock, dgate

@@ -83,7 +83,7 @@ def _empty(shape, dtype, device, stream):
         return _new(shape, dtype=dtype, device=device)
 
 
-def _call(function, device: int, stream, args, tensors):
+def _call(function, device: int, stream, args, tensors, tail=()):
     if stream is None:
         handle = _raw_stream(device)
     else:
@@ -93,10 +93,10 @@ def _call(function, device: int, stream, args, tensors):
             if t is not None:
                 t.record_stream(user)
     if device == _current_device():
-        rc = function(*args, handle)
+        rc = function(*args, handle, *tail)
     else:
         with torch.cuda.device(device):
-            rc = function(*args, handle)
+            rc = function(*args, handle, *tail)
     if rc:
         raise _pkg.SptgError(rc, _pkg.last_error() or _pkg.status_string(rc))
 
