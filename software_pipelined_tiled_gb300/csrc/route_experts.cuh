@@ -552,10 +552,18 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
               const Pair v = pair_key(el, eb, most_l, z2, kind, p.sigmoid);
               (i ? d[1] : d[0]) = c ? v : Pair{-INFINITY, 0.0f};
             }
-            // (a lane's third key near its second: it might be its second)
+            // A lane's third key near its second might be its second, unless it is a tie with it.
             const float second = from_order_bits(k[1] & ~PLACE);
-            unsettled = k[2] != 0 && !(second - from_order_bits(k[2] & ~PLACE) >
-                                       route_apart<PER>(second, b_most, p.sigmoid));
+            const float apart = route_apart<PER>(second, b_most, p.sigmoid);
+            const int e1 = first + static_cast<int>(PLACE - (k[1] & PLACE));
+#pragma unroll
+            for (int j = 2; j < PER; ++j)
+              if (k[j] != 0 && !(second - from_order_bits(k[j] & ~PLACE) > apart)) {
+                const int e = first + static_cast<int>(PLACE - (k[j] & PLACE));
+                if (route_load<TYPE>(p.logits, row * p.ld + e) != route_load<TYPE>(p.logits, row * p.ld + e1) ||
+                    (p.bias && p.bias[e] != p.bias[e1]))
+                  unsettled = true;
+              }
             if (d[1] > d[0]) {
               const Pair v = d[0];
               d[0] = d[1];
@@ -571,9 +579,14 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
             rank = 0;
 #pragma unroll 1
             for (int o = 0; o < p.groups; ++o) {
-              const Pair other = pair_lane(sum, mask, (lane - sub) + (o << p.lanes_log2));
+              const int at = (lane - sub) + (o << p.lanes_log2);
+              const Pair other = pair_lane(sum, mask, at);
               rank += other > sum || (other == sum && o < g);
-              if (kind != KEY_LOGIT && o != g && g < p.groups && sum.hi > -INFINITY && !pairs_apart(sum, other, 4.0f * b_most))
+              // (of the same two keys: a tie, as between groups of a row of zeros)
+              const Pair other1 = pair_lane(d[0], mask, at), other2 = pair_lane(d[1], mask, at);
+              const bool tie = other1 == d[0] && other2 == d[1];
+              if (kind != KEY_LOGIT && o != g && g < p.groups && sum.hi > -INFINITY && !tie &&
+                  !pairs_apart(sum, other, 4.0f * b_most))
                 unsettled = true;
             }
             kept = rank < p.top_groups;
@@ -647,13 +660,20 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
         const float nl = __shfl_down_sync(mask, ol, 1, LANES), nb = __shfl_down_sync(mask, ob, 1, LANES);
         const float ll = __shfl_sync(mask, ol, base + p.top - 1), lb = __shfl_sync(mask, ob, base + p.top - 1);
         if (near && ol == nl && ob == nb) near = false;
-        bool differs = extra && (el != ll || eb != lb);
-        if constexpr (SORTED) {
-          unsettled = unsettled || near_last(k[1]);  // (several in one lane)
-        } else {
-          unsettled = unsettled || near || differs;
-        }
-        if (SORTED && __ballot_sync(mask, near || differs) != 0) {
+        // (and all others of the lane that lie as near)
+        bool differs = extra && (el != ll || eb != lb), others = false, others_differ = false;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (k[j] != best && near_last(k[j])) {
+            const int e = first + static_cast<int>(PLACE - (k[j] & PLACE));
+            others = true;
+            others_differ = others_differ || route_load<TYPE>(p.logits, row * p.ld + e) != ll ||
+                            (p.bias && p.bias[e] != lb);
+          }
+        const bool rank = __ballot_sync(mask, near || differs || others_differ) != 0;
+        // (ranked is one expert a lane beside the picks, and none of unsorted keys)
+        unsettled = unsettled || (rank && (others || !SORTED));
+        if (SORTED && rank) {
           // The picks and the extra ones, ranked by Pairs.
           const int kind = biased ? KEY_BIASED : KEY_LOGIT;  // (without a bias logits order the scores)
           if (!summed) z2 = route_pair_z<TYPE, LANES>(p, row, first, count, m, mask);
@@ -713,10 +733,11 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
     }
   }
 
-  const int64_t row = row0 + my_row;
+  const bool live = my_slot < p.top && my_row < AT_ONCE * p.turns && row0 + my_row < p.rows;
+  const int64_t row = min(row0 + my_row, p.rows - 1);
   float my_l = pick >= 0 ? route_load<TYPE>(p.logits, row * p.ld + pick) : -INFINITY;
   if (!exact) {
-    const uint32_t doubts = __ballot_sync(ALL, doubt && row < p.rows);
+    const uint32_t doubts = __ballot_sync(ALL, doubt && live);
     for (int r = 0; doubts != 0 && r < 32 >> p.slots_log2; ++r) {
       if (((doubts >> (r << p.slots_log2)) & ((1u << slots) - 1u)) == 0) continue;
       // (with fewer lanes a row than a warp has, all of the warp's parts do the same)
@@ -750,7 +771,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
     pick = my_slot;
     w = NAN;
   }
-  if (my_slot < p.top && my_row < AT_ONCE * p.turns && row < p.rows) {
+  if (live) {
     p.weights[row * p.top + my_slot] = w;
     p.experts[row * p.top + my_slot] = pick;
   }

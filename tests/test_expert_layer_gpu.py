@@ -130,7 +130,7 @@ def test_route(rows, e, top, groups, top_groups, group_best, scores, biased, ren
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups,top_groups,group_best", [(1, 1, 2), (8, 4, 2), (8, 3, 1)])
-@pytest.mark.parametrize("kind", ["zero bias", "steps", "equal rows", "neighbours"])
+@pytest.mark.parametrize("kind", ["zero bias", "steps", "equal rows", "neighbours", "zeros"])
 def test_route_decides_ties_and_close_calls_as_exact_arithmetic_does(kind, groups, top_groups, group_best,
                                                                      scores, dtype):
     g = gen(5)
@@ -142,6 +142,9 @@ def test_route_decides_ties_and_close_calls_as_exact_arithmetic_does(kind, group
     elif kind == "equal rows":
         logits = logits[:, :1].expand(2000, 128).contiguous()
         bias = torch.randint(0, 2, (128,), device="cuda", generator=g).float() * 0.01
+    elif kind == "zeros":  # rows of padding
+        logits[::3] = 0
+        bias = torch.randint(-1, 2, (128,), device="cuda", generator=g).float() * 0.001
     else:  # logits that lie closer than the roundings of their scores
         logits = (1.0 + torch.randint(0, 40, (2000, 128), device="cuda", generator=g) * 2.0 ** -22).to(dtype)
         bias = torch.randint(0, 3, (128,), device="cuda", generator=g).float() * 2.0 ** -24
