@@ -33,7 +33,7 @@ _workspace = _lib.sptg_gate_add_rms_norm_grad_workspace
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 4}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GATE_NONE, _GATE_COLS, _GATE_ROWS, _GATE_FULL = range(4)
-_grad_enabled = torch.is_grad_enabled
+_grad_enabled, _new_like = torch.is_grad_enabled, torch.empty_like
 
 
 def _differentiated(function, stream, device, args, outputs):
@@ -57,6 +57,13 @@ def _as_rows(t, dtype):
     if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= t.shape[1]:
         return t
     return t.clone(memory_format=torch.contiguous_format)
+
+
+def _like(t, stream):
+    """A new tensor of another's shape and type, dense, that belongs to the call's stream."""
+    if stream is None and t.is_contiguous():
+        return _new_like(t)
+    return _empty(t.shape, t.dtype, t.device, stream)
 
 
 def _row_type(t, name: str) -> int:
@@ -164,7 +171,7 @@ def route_experts_dlogits(dweights, logits, experts, scores: str = "softmax", re
     _dense(experts, (rows, top), _I32, device, "experts")
     _dense(dweights, (rows, top), _F32, device, "dweights")
     if out is None:
-        out, ldo = _empty((rows, e), dtype, logits.device, stream), e
+        out, ldo = _like(logits, stream), e
     else:
         ldo = _pitch(out, rows, e, dtype, device, "out")
     _call(_route_grad, device, stream, (
@@ -315,7 +322,7 @@ def combine_rows_grad(dout, y, places, weights=None, dy=None, dweights=None, nee
     if weights is not None:
         _dense(weights, (rows, top), _F32, device, "weights")
     if dy is None:
-        dy, lddy = _empty((y_rows, cols), dtype, on, stream), cols
+        dy, lddy = _like(y, stream), cols
     else:
         lddy = _pitch(dy, y_rows, cols, dtype, device, "dy")
     if weights is None or not need_weights:
@@ -357,8 +364,8 @@ def _tail(config):
 
 def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream, config=None):
     code = _row_type(y, "y")
-    rows, cols = shape = y.shape
-    dtype, device, on = y.dtype, y.get_device(), y.device
+    rows, cols = y.shape
+    dtype, device = y.dtype, y.get_device()
     ldy = cols if y.is_contiguous() else _pitch(y, rows, cols, dtype, device, "y")
     ldr = _pitch(residual, rows, cols, dtype, device, "residual")
     _dense(weight, (cols,), dtype, device, "weight")
@@ -366,11 +373,11 @@ def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, st
         _dense(block_weight, (cols,), dtype, device, "block_weight")
     kind, ldg = _gate_of(gate, rows, cols, dtype, device)
     if h is None:
-        h, ldh = _empty(shape, dtype, on, stream), cols
+        h, ldh = _like(y, stream), cols
     else:
         ldh = _pitch(h, rows, cols, dtype, device, "h")
     if v is None:
-        v, ldv = _empty(shape, dtype, on, stream), cols
+        v, ldv = _like(y, stream), cols
     else:
         ldv = _pitch(v, rows, cols, dtype, device, "v")
     _call(_gate_norm, device, stream, (
@@ -431,7 +438,7 @@ def gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight=None, gate=
     Those of inputs that are None are None.
     """
     code = _row_type(y, "y")
-    rows, cols = shape = y.shape
+    rows, cols = y.shape
     dtype, device, on = y.dtype, y.get_device(), y.device
     if out_dtype is None:
         out_dtype = dtype
@@ -445,7 +452,7 @@ def gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight=None, gate=
     kind, ldg = _gate_of(gate, rows, cols, dtype, device)
     lddh = cols if dh is None else _pitch(dh, rows, cols, dtype, device, "dh")
     lddv = cols if dv is None else _pitch(dv, rows, cols, dtype, device, "dv")
-    dy, dresidual = _empty(shape, dtype, on, stream), _empty(shape, dtype, on, stream)
+    dy, dresidual = _like(y, stream), _like(y, stream)
     dweight = _empty((cols,), out_dtype, on, stream)
     dblock = None if block_weight is None else _empty((cols,), out_dtype, on, stream)
     dgate = None
