@@ -381,8 +381,13 @@ int combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, int t
 
 // -------------------------------------------- gate, scaled residual and norms
 // What a ring may take beside a kernel's own few KB: two rows of three operands of 16384
-// elements, or of five of 8192.
-constexpr int kGateRingSmem = 223 * 1024;
+// elements, or of five of 8192. With cut rows a block keeps 4 KB about their ends, and has a
+// thread for each of them: 16 to an operand.
+int gate_ring_most(bool cut) { return (cut ? 219 : 223) * 1024; }
+int ring_threads_of(int64_t pieces, int per, int ops, bool cut) {
+  const int threads = static_cast<int>(ceil_div(ceil_div(pieces, per), 32) * 32);
+  return cut ? std::max(threads, static_cast<int>(ceil_div(16 * ops, 32) * 32)) : threads;
+}
 
 // Blocks that add up gradients over rows, at most: those of narrow rows are small,
 // and an SM holds more of them.
@@ -474,9 +479,9 @@ int gate_norm(int64_t rows, int64_t cols, int type, const void* y, int64_t ldy, 
     const bool full = gate_kind == SPTG_GATE_FULL;
     const void* fn = gate_norm_variant(bf16, GATE_NORM_RING);
     const int ring_threads = row_threads(pieces, 4), ring_stages = cols > 4096 && cols <= 8192 && !full ? 3 : 2;
-    const int ring_smem = gate_ring_smem(static_cast<int>(cols), full ? 3 : 2, ring_stages);
+    const int ring_smem = gate_ring_smem(static_cast<int>(cols), full ? 3 : 2, ring_stages, false);
     Residency res;
-    rc = ensure_smem(dev, fn, kGateRingSmem);
+    rc = ensure_smem(dev, fn, gate_ring_most(false));
     if (!rc) rc = residency(res, dev, fn, ring_threads, ring_smem);
     if (rc) return rc;
     const int64_t blocks = static_cast<int64_t>(res.blocks) * di.sm_count;
@@ -557,27 +562,28 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
                        in_pieces(w2, 0) && in_pieces(dh, lddh) && in_pieces(dv, lddv) && in_pieces(dy, lddy) &&
                        in_pieces(dx, lddx) && (!by_col || in_pieces(gate, 0)) &&
                        (!full || (in_pieces(gate, ldg) && in_pieces(dgate, lddg)));
-  enum { GATE_GRAD_RING, GATE_GRAD_SHIFTED, GATE_GRAD_ANY };
+  enum { GATE_GRAD_RING, GATE_GRAD_CUT, GATE_GRAD_ANY };
   int kind = GATE_GRAD_ANY, threads = GATE_ANY_THREADS;
   int64_t blocks = 2 * di.sm_count;
   int smem = 0, stages = 0;
   const void* fn = gate_norm_grad_any_variant(bf16);
+  const int64_t row_pieces = vectors ? cols / 8 : ceil_div(cols + 7, 8);
   if (cols <= 8192) {
-    kind = vectors ? GATE_GRAD_RING : GATE_GRAD_SHIFTED;
-    fn = bf16 ? gate_norm_grad_bf16(gate_kind, w1 != nullptr, vectors)
-              : gate_norm_grad_f16(gate_kind, w1 != nullptr, vectors);
-    threads = row_threads(ceil_div(cols, 8), 2);
-    if (vectors) {
-      stages = 2;  // (a third row: no faster, and one block an SM less of narrow rows)
-      smem = gate_ring_smem(static_cast<int>(cols), 2 + (dh != nullptr) + (dv != nullptr) + full, stages);
-    }
+    kind = vectors ? GATE_GRAD_RING : GATE_GRAD_CUT;
+    fn = bf16 ? gate_norm_grad_bf16(gate_kind, w1 != nullptr, !vectors)
+              : gate_norm_grad_f16(gate_kind, w1 != nullptr, !vectors);
+    const int ops = 2 + (dh != nullptr) + (dv != nullptr) + full;
+    threads = ring_threads_of(std::min<int64_t>(row_pieces, 1024), 2, ops, !vectors);
+    stages = 2;  // (a third row: no faster, and one block an SM less of narrow rows)
+    smem = gate_ring_smem(static_cast<int>(cols), ops, stages, !vectors);
     Residency res;
-    rc = ensure_smem(dev, fn, kGateRingSmem);
+    rc = ensure_smem(dev, fn, gate_ring_most(!vectors));
     if (!rc) rc = residency(res, dev, fn, threads, smem);
     if (rc) return rc;
     blocks = static_cast<int64_t>(res.blocks) * di.sm_count;
   }
   blocks = std::min({rows, blocks, gate_grad_blocks(cols)});
+  if (kind == GATE_GRAD_CUT && blocks < rows) blocks = std::max<int64_t>(8, blocks / 8 * 8);  // (see RowCut)
   const int out_kind = out_type == SPTG_T_F32 ? OUT_F32 : bf16 ? OUT_BF16 : OUT_F16;
   GateNormGradParams p;
   p.f = GateNormParams{y, x, w1, w2, gate_kind == SPTG_GATE_NONE ? nullptr : gate, ldy, ldx, ldg, nullptr,

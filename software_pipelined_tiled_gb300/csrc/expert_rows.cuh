@@ -87,10 +87,10 @@ __global__ void __launch_bounds__(32 * WARPS)
         const uint32_t ones = __ballot_sync(ALL, one);
         same &= one ? ones : ~ones;
       }
+      const uint32_t n = i < end ? mine[b[k]] : 0u;
+      __syncwarp();
       if (i < end) {
-        const uint32_t n = mine[b[k]];
         p.places[i] = static_cast<int32_t>(n + __popc(same & before_me));
-        __syncwarp(__activemask());
         if ((same & before_me) == 0) mine[b[k]] = n + __popc(same);
       }
       __syncwarp();

@@ -24,6 +24,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "shifted.cuh"
@@ -37,9 +38,10 @@ enum GateKind : int { GATE_NONE = 0, GATE_COLS = 1, GATE_ROWS = 2, GATE_FULL = 3
 // is row blockIdx.x + i * gridDim.x of the call.
 constexpr int GATE_MAX_STAGES = 4;
 constexpr int GATE_MAX_OPS = 5;
-__host__ __device__ constexpr int gate_row_bytes(int cols) { return (2 * cols + 127) & ~127; }
-__host__ __device__ constexpr int gate_ring_smem(int cols, int ops, int stages) {
-  return stages * ops * gate_row_bytes(cols) + 128;
+// (A cut row, below, takes up to 62 bytes more.)
+__host__ __device__ constexpr int gate_row_bytes(int cols, bool cut) { return (2 * cols + (cut ? 64 : 0) + 127) & ~127; }
+__host__ __device__ constexpr int gate_ring_smem(int cols, int ops, int stages, bool cut) {
+  return stages * ops * gate_row_bytes(cols, cut) + 128;
 }
 
 struct GateRing {
@@ -369,21 +371,182 @@ __device__ __forceinline__ void store_kind(void* p, int64_t i, float v, int kind
     store_out<OUT_F16>(p, i, v);
 }
 
+__device__ __forceinline__ const uint16_t* ring_src(const GateRing& r, int o, int64_t row) {
+  return static_cast<const uint16_t*>(r.src[o]) + row * r.ld[o];
+}
+
 // Starts the copies of the block's row i into its stage (one thread).
 __device__ __forceinline__ void ring_fetch(const GateNormParams& p, int64_t i, int s, uint32_t bar0,
                                            uint32_t data0, uint64_t policy) {
   const int64_t row = blockIdx.x + i * gridDim.x;
   if (row >= p.rows || (p.ring.inject_stall && i == 1)) return;
-  const uint32_t row_bytes = gate_row_bytes(p.cols), bytes = 2u * p.cols;
+  const uint32_t row_bytes = gate_row_bytes(p.cols, false), bytes = 2u * p.cols;
   uint32_t dst = data0 + s * p.ring.ops * row_bytes;
   mbar_arrive_expect_tx(bar0 + 8 * s, p.ring.ops * bytes);
 #pragma unroll
   for (int o = 0; o < GATE_MAX_OPS; ++o)
     if (o < p.ring.ops) {
-      bulk_load_1d(dst, static_cast<const uint16_t*>(p.ring.src[o]) + row * p.ring.ld[o], bytes, bar0 + 8 * s,
-                   policy);
+      bulk_load_1d(dst, ring_src(p.ring, o, row), bytes, bar0 + 8 * s, policy);
       dst += row_bytes;
     }
+}
+
+// Rows cut by 16-byte boundaries, backwards. Bulk copies take whole 16-byte words, so they
+// fetch the words that lie inside of a row, and 16 threads its first and last few
+// elements, which lie in words that are other rows' too. In shared memory a row keeps its
+// place between boundaries: element e of an operand whose rows start `shift` elements
+// behind one is element 8 + shift + e of its buffer. What is before and behind the row
+// there is zero, and stays so: blocks take rows a multiple of 8 apart, so
+// that an operand's shift is the same for all rows of a block. Pieces are laid out by the
+// rows that are written; an operand with another shift is read in two words. The pieces
+// at a row's ends go through shared memory, from where 16 threads write an element each.
+// (4096 rows of 5001 with a full gate: 165 us; with each row loaded into registers and its
+// ends written element by element by the threads that hold them 262 us.)
+struct RowCut {
+  int head, words, tail;  // elements before the first whole word, words, elements behind
+  __device__ __forceinline__ RowCut(int shift, int cols) {
+    head = shift ? min(cols, 8 - shift) : 0;
+    words = (cols - head) >> 3;
+    tail = cols - head - 8 * words;
+  }
+  // The element that the i-th of 16 threads has, or -1: 8 before the words, 8 behind.
+  __device__ __forceinline__ int end(int i, int cols) const {
+    if (i < 8) return i < head ? i : -1;
+    return i - 8 < tail ? cols - tail + i - 8 : -1;
+  }
+};
+
+// One operand of a ring, or one element at the end of a row: where it is in the block's first
+// row, how far apart the block's rows are, and where it goes.
+struct RingPart {
+  const uint16_t* at;  // null: none
+  int64_t step;
+  uint32_t bytes, offset;
+};
+
+constexpr int GATE_MAX_OUTS = 3;
+
+// What the threads that move rows know. (In shared memory: registers are what the
+// kernel is short of.)
+struct RingCutShared {
+  RingPart copies[GATE_MAX_OPS];
+  RingPart in[16 * GATE_MAX_OPS];
+  RingPart out[16 * GATE_MAX_OUTS];
+  uint4 ends[2][GATE_MAX_OUTS][2];  // by the row's parity and output: first and last piece
+  uint32_t bytes;                   // of a row, all operands
+};
+struct RingWholeShared {};
+
+// Fills sh and the ring's zeros; the caller synchronises.
+__device__ __forceinline__ void ring_setup(const GateNormParams& p, RingCutShared& sh, uint8_t* ring) {
+  const int t = threadIdx.x, row_bytes = gate_row_bytes(p.cols, true);
+  if (t < 32) {
+    uint32_t bytes = 0;
+    if (t < p.ring.ops) {
+      const uint16_t* src = ring_src(p.ring, t, blockIdx.x);
+      const RowCut cut(shift_of(src), p.cols);
+      bytes = 16u * cut.words;
+      sh.copies[t] = {src + cut.head, static_cast<int64_t>(gridDim.x) * p.ring.ld[t], bytes,
+                      static_cast<uint32_t>(t * row_bytes + (cut.head ? 32 : 16))};
+    }
+    bytes = __reduce_add_sync(0xffffffffu, bytes);
+    if (t == 0) sh.bytes = bytes;
+  }
+  if (t < 16 * p.ring.ops) {
+    const int o = t >> 4;
+    const uint16_t* src = ring_src(p.ring, o, blockIdx.x);
+    const int shift = shift_of(src), e = RowCut(shift, p.cols).end(t & 15, p.cols);
+    sh.in[t] = {e < 0 ? nullptr : src + e, static_cast<int64_t>(gridDim.x) * p.ring.ld[o], 2,
+                static_cast<uint32_t>(o * row_bytes + 2 * (8 + shift + e))};
+  }
+  // zeros around the rows, in the words that no copy writes
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  for (int i = t; i < p.ring.stages * p.ring.ops; i += blockDim.x) {
+    const int shift = shift_of(ring_src(p.ring, i % p.ring.ops, blockIdx.x));
+    uint4* w = reinterpret_cast<uint4*>(ring + i * row_bytes);
+    const int last = 1 + ((shift + p.cols) >> 3);
+    w[0] = none;
+    if (shift) w[1] = none;
+    w[last] = none;
+    w[last + 1] = none;
+  }
+}
+
+// An output's row ends: the threads' elements, where the pieces (that start `start`
+// elements behind the row's first) are laid out by this output's boundaries. Returns
+// whether they are.
+__device__ __forceinline__ bool ring_output(const GateNormParams& p, RingCutShared& sh, int o, const void* out,
+                                            int64_t ld, int start) {
+  const uint16_t* row = static_cast<const uint16_t*>(out) + blockIdx.x * ld;
+  const int shift = shift_of(row), i = static_cast<int>(threadIdx.x) - 16 * o;
+  if (i >= 0 && i < 16) {
+    const int e = shift + start == 0 ? RowCut(shift, p.cols).end(i, p.cols) : -1;
+    sh.out[threadIdx.x] = {e < 0 ? nullptr : row + e, static_cast<int64_t>(gridDim.x) * ld, 2,
+                           static_cast<uint32_t>(32 * o + (i < 8 ? 2 * (shift + i) : 16 + 2 * (i - 8)))};
+  }
+  return shift + start == 0;
+}
+
+// Starts the copies of the block's row i, of a cut row, into its stage (the first warp; a
+// lane an operand).
+__device__ __forceinline__ void ring_fetch_cut(const GateNormParams& p, const RingCutShared& sh, int64_t i, int s,
+                                               uint32_t bar0, uint32_t data0, uint64_t policy) {
+  if (blockIdx.x + i * gridDim.x >= p.rows || (p.ring.inject_stall && i == 1)) return;
+  if (threadIdx.x == 0) mbar_arrive_expect_tx(bar0 + 8 * s, sh.bytes);
+  __syncwarp();
+  if (threadIdx.x < p.ring.ops) {
+    const RingPart c = sh.copies[threadIdx.x];
+    if (c.bytes > 0)
+      bulk_load_1d(data0 + s * p.ring.ops * gate_row_bytes(p.cols, true) + c.offset, c.at + i * c.step, c.bytes,
+                   bar0 + 8 * s, policy);
+  }
+}
+
+// The first and last elements of row i, one a thread and operand: loaded when the row's
+// copies are started, and stored a barrier later, so that nobody waits for them.
+__device__ __forceinline__ void ends_load(const GateNormParams& p, const RingCutShared& sh, int64_t i, uint16_t& v) {
+  if (threadIdx.x >= 16 * p.ring.ops || blockIdx.x + i * gridDim.x >= p.rows) return;
+  const RingPart e = sh.in[threadIdx.x];
+  if (e.at) v = e.at[i * e.step];
+}
+__device__ __forceinline__ void ends_store(const GateNormParams& p, const RingCutShared& sh, int64_t i, uint8_t* stage,
+                                           uint16_t v) {
+  if (threadIdx.x >= 16 * p.ring.ops || blockIdx.x + i * gridDim.x >= p.rows) return;
+  const RingPart e = sh.in[threadIdx.x];
+  if (e.at) *reinterpret_cast<uint16_t*>(stage + e.offset) = v;
+}
+// Those of the outputs, written behind the barrier that follows them.
+__device__ __forceinline__ void ends_write(const RingCutShared& sh, int outs, int64_t i, int odd) {
+  if (threadIdx.x >= 16 * outs) return;
+  const RingPart e = sh.out[threadIdx.x];
+  if (e.at)
+    const_cast<uint16_t*>(e.at)[i * e.step] =
+        *reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(sh.ends[odd]) + e.offset);
+}
+
+static __device__ __noinline__ void store_apart(uint16_t* row, int first, int cols, uint4 v) {
+  store_shifted(row, first, cols, v);
+}
+
+// A piece of an output's cut row. alike: whether pieces are laid out by this output's boundaries.
+__device__ __forceinline__ void ring_store(RingCutShared& sh, int o, int odd, bool alike, uint16_t* row, int first,
+                                           int cols, const uint4& v) {
+  if (alike && first >= 0 && first + 8 <= cols)
+    *reinterpret_cast<uint4*>(row + first) = v;
+  else if (alike)
+    sh.ends[odd][o][first < 0 ? 0 : 1] = v;
+  else
+    store_apart(row, first, cols, v);
+}
+
+// Piece `at` of an operand in a ring, `apart` elements behind the pieces' own shift.
+template <bool CUT>
+__device__ __forceinline__ uint4 ring_piece(const uint8_t* row, int at, int apart) {
+  const uint4* w = reinterpret_cast<const uint4*>(row) + at;
+  if (!CUT) return w[0];
+  w += 1 + (apart >> 3);
+  if ((apart & 7) == 0) return w[0];
+  return shifted(ShiftedPiece{w[0], w[1], apart & 7});
 }
 
 // Lets the copies in flight land before the block leaves: those up to a ring past
@@ -413,7 +576,7 @@ __global__ void __launch_bounds__(512) gate_norm_ring_kernel(const __grid_consta
   const bool full = p.gate_kind == GATE_FULL;
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
   const uint32_t bar0 = smem_addr(bars), data0 = smem_addr(ring_data);
-  const int row_bytes = gate_row_bytes(p.cols), stage_bytes = p.ring.ops * row_bytes;
+  const int row_bytes = gate_row_bytes(p.cols, false), stage_bytes = p.ring.ops * row_bytes;
   const uint64_t policy = policy_evict_first();  // read once
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -523,32 +686,61 @@ __global__ void __launch_bounds__(512) gate_norm_ring_kernel(const __grid_consta
 }
 
 // Backwards: a fixed number of blocks, PER pieces of 8 elements a thread, whose sums
-// over rows stay in registers. RING: rows on 16-byte boundaries, through a ring; else
-// a row's pieces are loaded together, shifted, into registers.
-template <bool BF16, int PER, int GATE, bool BLOCK, bool RING>
+// over rows stay in registers. CUT: rows off 16-byte boundaries.
+template <bool BF16, int PER, int GATE, bool BLOCK, bool CUT>
 __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_constant__ GateNormGradParams p) {
   extern __shared__ __align__(128) uint8_t ring_data[];
   // (alternating, so that a fast warp's next row leaves a slow one's sums alone)
   __shared__ float4 s_sum[2][3][32];
   __shared__ __align__(8) uint64_t bars[GATE_MAX_STAGES];
   __shared__ int abort_word;
+  __shared__ typename std::conditional<CUT, RingCutShared, RingWholeShared>::type sh;
   const GateNormParams& f = p.f;
-  const int pieces = (f.cols + 7) >> 3;
+  int start = CUT ? -shift_of(static_cast<const uint16_t*>(p.dx) + blockIdx.x * p.lddx) : 0;
+  // (rows that fill the block to the last piece leave no room for one more: stores in parts)
+  if (CUT && (f.cols - start + 7) >> 3 > PER * static_cast<int>(blockDim.x)) start = 0;
+  const int pieces = (f.cols - start + 7) >> 3;
   const uint4 none = make_uint4(0, 0, 0, 0);
   const float inv_cols = 1.0f / static_cast<float>(f.cols);
   const int op_dv = p.dh ? 3 : 2, op_gate = f.ring.ops - 1;
   const uint32_t bar0 = smem_addr(bars), data0 = smem_addr(ring_data);
-  const int row_bytes = gate_row_bytes(f.cols), stage_bytes = f.ring.ops * row_bytes;
+  const int row_bytes = gate_row_bytes(f.cols, CUT), stage_bytes = f.ring.ops * row_bytes;
   const uint64_t policy = policy_evict_first();  // read once
-  if (RING && threadIdx.x == 0) {
+  if (threadIdx.x == 0) {
     for (int s = 0; s < f.ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
     abort_word = 0;
     fence_mbar_init();
   }
+  const auto slot_of = [&](int op) { return op <= 2 ? op : op == 3 ? op_dv : op_gate; };
+  int apart[GATE_MAX_OPS] = {0, 0, 0, 0, 0};
+  bool dx_alike = true, dg_alike = true, dy_alike = true;
+  if constexpr (CUT) {
+    ring_setup(f, sh, ring_data);
+#pragma unroll
+    for (int o = 0; o < GATE_MAX_OPS; ++o) {
+      const bool given = o < 2 || (o == 2 && p.dh) || (o == 3 && p.dv) || (o == 4 && GATE == GATE_FULL);
+      if (given) apart[o] = shift_of(ring_src(f.ring, slot_of(o), blockIdx.x)) + start;
+    }
+    dx_alike = ring_output(f, sh, 0, p.dx, p.lddx, start);
+    dy_alike = ring_output(f, sh, 1, p.dy, p.lddy, start);
+    if (GATE == GATE_FULL) dg_alike = ring_output(f, sh, 2, p.dgate, p.lddg, start);
+  }
+  constexpr int OUTS = GATE == GATE_FULL ? 3 : 2;
   __syncthreads();
   grid_dependency_wait();
-  if (RING && threadIdx.x == 0)
-    for (int i = 0; i < f.ring.stages; ++i) ring_fetch(f, i, i, bar0, data0, policy);
+  uint16_t end = 0;
+  if constexpr (!CUT) {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < f.ring.stages; ++i) ring_fetch(f, i, i, bar0, data0, policy);
+  } else {
+    if (threadIdx.x < 32)
+      for (int i = 0; i < f.ring.stages; ++i) ring_fetch_cut(f, sh, i, i, bar0, data0, policy);
+    for (int i = 0; i < f.ring.stages; ++i) {
+      ends_load(f, sh, i, end);
+      ends_store(f, sh, i, ring_data + i * stage_bytes, end);
+    }
+    __syncthreads();
+  }
   const WaitCtl ctl{f.ring.timeout_ns, f.ring.error_word, &abort_word};
   // a column's factors: of u in h (w1, and the gate of columns), and w2
   float_pair gw[PER][4];
@@ -559,7 +751,7 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     const int at = threadIdx.x + i * blockDim.x;
     const bool in = at < pieces;
     const auto column = [&](const void* w) {
-      return in ? load_piece<RING>(static_cast<const uint16_t*>(w), 8 * at, f.cols) : none;
+      return in ? load_piece<!CUT>(static_cast<const uint16_t*>(w), start + 8 * at, f.cols) : none;
     };
     w2[i] = column(f.w2);
     if (BLOCK) pair_unpack<BF16>(column(f.w1), gw[i]);
@@ -573,75 +765,45 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     }
   }
   const float_pair alpha = pair_of(f.alpha);
-  // y's sum of squares. Through a ring it is formed a row ahead, so that it goes
-  // through the threads together with other sums: two barriers a row, not three.
-  const auto square_sum = [&](const auto& piece) {
+  // y's sum of squares is formed a row ahead, so that it goes through the threads
+  // together with other sums: two barriers a row, not three.
+  const auto square_sum = [&](int stage) {
     float_pair sq = pair_of(0.0f);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (threadIdx.x + i * blockDim.x >= pieces) continue;
+      const int at = threadIdx.x + i * blockDim.x;
+      if (at >= pieces) continue;
       float_pair y[4];
-      pair_unpack<BF16>(piece(i), y);
+      pair_unpack<BF16>(ring_piece<CUT>(ring_data + stage * stage_bytes, at, apart[0]), y);
 #pragma unroll
       for (int c = 0; c < 4; ++c) sq = fma2(y[c], y[c], sq);
     }
     return sum_of(sq);
-  };
-  const auto staged_sum = [&](int stage) {
-    const uint4* y = reinterpret_cast<const uint4*>(ring_data + stage * stage_bytes);
-    return square_sum([&](int i) { return y[threadIdx.x + i * blockDim.x]; });
   };
   int odd = 0, s = 0;
   uint32_t phase = 0;
   // This thread has seen every row so far arrive. (A wait that runs out leaves its
   // row and the block's next ones wrong and says so; the loop and its barriers go
   // on, without waits and copies.)
-  bool ok = true;
-  int64_t landed = 0, n = 0;
+  bool ok = wait_bounded_lazy(bar0, 0, ctl, WAIT_MMA_FULL);
+  int64_t landed = ok, n = 0;
   float s1[1] = {0.0f};
-  if (RING) {
-    ok = wait_bounded_lazy(bar0, 0, ctl, WAIT_MMA_FULL);
-    landed = ok;
-    if (BLOCK) {
-      s1[0] = staged_sum(0);
-      block_sums<1>(s1, s_sum[1][0]);
-    }
+  if (BLOCK) {
+    s1[0] = square_sum(0);
+    block_sums<1>(s1, s_sum[1][0]);
   }
   for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x, ++n, odd ^= 1) {
     const float gr = GATE == GATE_ROWS ? gate_load<BF16>(f.gate, row * f.ldg) : 1.0f;
     const uint8_t* stage = ring_data + s * stage_bytes;
-    const auto store = [&](void* to, int64_t ld, int at, const float_pair (&v)[4]) {
-      store_piece<RING>(static_cast<uint16_t*>(to) + row * ld, 8 * at, f.cols, pair_pack<BF16>(v));
+    const auto store = [&](int o, bool alike, void* to, int64_t ld, int at, const float_pair (&v)[4]) {
+      if constexpr (CUT)
+        ring_store(sh, o, odd, alike, static_cast<uint16_t*>(to) + row * ld, start + 8 * at, f.cols, pair_pack<BF16>(v));
+      else
+        row_pieces(to, row, ld)[at] = pair_pack<BF16>(v);
     };
-    uint4 early[PER][GATE_MAX_OPS];  // (not RING)
-    if constexpr (!RING) {
-      const int ops[GATE_MAX_OPS] = {0, 1, p.dh ? 2 : -1, p.dv ? op_dv : -1, GATE == GATE_FULL ? op_gate : -1};
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int first = 8 * static_cast<int>(threadIdx.x + i * blockDim.x);
-        if (inside_row(first, f.cols)) {
-          ShiftedPiece words[GATE_MAX_OPS];
-#pragma unroll
-          for (int o = 0; o < GATE_MAX_OPS; ++o)
-            if (ops[o] >= 0)
-              words[o] = load_words(static_cast<const uint16_t*>(f.ring.src[ops[o]]) + row * f.ring.ld[ops[o]] + first);
-#pragma unroll
-          for (int o = 0; o < GATE_MAX_OPS; ++o)
-            if (ops[o] >= 0) early[i][o] = shifted(words[o]);
-        } else if (first < f.cols) {
-#pragma unroll
-          for (int o = 0; o < GATE_MAX_OPS; ++o)
-            if (ops[o] >= 0)
-              early[i][o] = load_elements(static_cast<const uint16_t*>(f.ring.src[ops[o]]) + row * f.ring.ld[ops[o]],
-                                          first, f.cols);
-        }
-      }
-    }
     // piece i of y, x, dh, dv or the gate
     const auto operand = [&](int op, int i) {
-      if constexpr (!RING) return early[i][op];
-      const int slot = op <= 2 ? op : op == 3 ? op_dv : op_gate;
-      return reinterpret_cast<const uint4*>(stage + slot * row_bytes)[threadIdx.x + i * blockDim.x];
+      return ring_piece<CUT>(stage + slot_of(op) * row_bytes, threadIdx.x + i * blockDim.x, apart[op]);
     };
     uint4 yv[PER], gv[PER];
 #pragma unroll
@@ -649,10 +811,6 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
       if (threadIdx.x + i * blockDim.x >= pieces) continue;
       yv[i] = operand(0, i);
       if (GATE == GATE_FULL) gv[i] = operand(4, i);
-    }
-    if (BLOCK && !RING) {
-      s1[0] = square_sum([&](int i) { return yv[i]; });
-      block_sums<1>(s1, s_sum[odd][0]);
     }
     const float r1 = BLOCK ? reciprocal_rms(s1[0], inv_cols, f.eps) : 1.0f;
     const float_pair gr1 = pair_of(gr * r1), r1p = pair_of(r1);
@@ -681,7 +839,13 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
       }
     }
     float s2[2] = {sum_of(sq), sum_of(dot)};
+    if constexpr (CUT) {  // (of the row fetched a row ago, into the stage before this one)
+      if (n > 0) ends_store(f, sh, n - 1 + f.ring.stages, ring_data + (s == 0 ? f.ring.stages - 1 : s - 1) * stage_bytes, end);
+    }
     block_sums<2>(s2, s_sum[odd][1]);
+    if constexpr (CUT) {
+      if (n > 0) ends_write(sh, OUTS, n - 1, odd ^ 1);
+    }
     const float r2 = reciprocal_rms(s2[0], inv_cols, f.eps);
     const float m2 = s2[1] * r2 * inv_cols;
     const float_pair r2p = pair_of(r2), back = pair_of(-(r2 * m2)), grp = pair_of(gr);
@@ -728,21 +892,26 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
         dot = fma2(e, gw[i][c], dot);
         dh[c] = mul2(alpha, h[i][c]);
       }
-      store(p.dx, p.lddx, at, dh);
-      if (GATE == GATE_FULL) store(p.dgate, p.lddg, at, dg);
+      store(0, dx_alike, p.dx, p.lddx, at, dh);
+      if (GATE == GATE_FULL) store(2, dg_alike, p.dgate, p.lddg, at, dg);
     }
     const int later = s + 1 == f.ring.stages ? 0 : s + 1;
     const uint32_t later_phase = later == 0 ? phase ^ 1u : phase;
     float s3[3] = {sum_of(dot), sum_of(row_dg), 0.0f};
-    if (RING && row + gridDim.x < f.rows) {
+    if (row + gridDim.x < f.rows) {
       ok = ok && wait_bounded_lazy(bar0 + 8 * later, later_phase, ctl, WAIT_MMA_FULL);
       landed += ok;
-      if (BLOCK) s3[2] = staged_sum(later);
+      if (BLOCK) s3[2] = square_sum(later);
     }
     block_sums<3>(s3, s_sum[odd][2]);
     s1[0] = s3[2];
     // (the stage has been read; into a place whose last copy has landed, no other)
-    if (RING && threadIdx.x == 0 && ok) ring_fetch(f, n + f.ring.stages, s, bar0, data0, policy);
+    if constexpr (!CUT) {
+      if (threadIdx.x == 0 && ok) ring_fetch(f, n + f.ring.stages, s, bar0, data0, policy);
+    } else {
+      if (threadIdx.x < 32 && __all_sync(0xffffffffu, ok)) ring_fetch_cut(f, sh, n + f.ring.stages, s, bar0, data0, policy);
+      ends_load(f, sh, n + f.ring.stages, end);
+    }
     if (GATE == GATE_ROWS && threadIdx.x == 0) store_kind(p.dgate, row, s3[1], p.out_kind);
     const float_pair back1 = pair_of(-(s3[0] * inv_cols * r1 * r1));
 #pragma unroll
@@ -759,13 +928,17 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
         if (GATE == GATE_FULL) d = mul2(d, g[c]);
         h[i][c] = BLOCK ? fma2(y[c], back1, d) : d;
       }
-      store(p.dy, p.lddy, at, h[i]);
+      store(1, dy_alike, p.dy, p.lddy, at, h[i]);
     }
     s = later;
     phase = later_phase;
   }
   grid_launch_dependents();
-  if (RING && threadIdx.x == 0 && !ok) ring_drain(f, landed, bar0);
+  if constexpr (CUT) {
+    __syncthreads();
+    ends_write(sh, OUTS, n - 1, odd ^ 1);
+  }
+  if (threadIdx.x == 0 && !ok) ring_drain(f, landed, bar0);
   const int64_t plane = static_cast<int64_t>(gridDim.x) * f.cols;
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * f.cols;
 #pragma unroll
@@ -780,18 +953,18 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
         v[2 * c] = a.x;
         v[2 * c + 1] = a.y;
       }
-      if constexpr (RING) {
+      if constexpr (!CUT) {
 #pragma unroll
         for (int c = 0; c < 8; c += 4)
           *reinterpret_cast<float4*>(to + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
       } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          if (8 * at + c < f.cols) to[c] = v[c];
+          if (start + 8 * at + c >= 0 && start + 8 * at + c < f.cols) to[c] = v[c];
       }
     };
-    sums_out(part + 8 * at, sum_w2[i]);
-    if (BLOCK || GATE == GATE_COLS) sums_out(part + plane + 8 * at, sum_e[i]);
+    sums_out(part + start + 8 * at, sum_w2[i]);
+    if (BLOCK || GATE == GATE_COLS) sums_out(part + plane + start + 8 * at, sum_e[i]);
   }
 }
 

@@ -4,19 +4,19 @@
 
 namespace sptg {
 
-template <bool BLOCK, bool RING>
+template <bool BLOCK, bool CUT>
 const void* gate_norm_grad_of(int gate_kind) {
   switch (gate_kind) {
-    case GATE_COLS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_COLS, BLOCK, RING>);
-    case GATE_ROWS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_ROWS, BLOCK, RING>);
-    case GATE_FULL: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_FULL, BLOCK, RING>);
-    default: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_NONE, BLOCK, RING>);
+    case GATE_COLS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_COLS, BLOCK, CUT>);
+    case GATE_ROWS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_ROWS, BLOCK, CUT>);
+    case GATE_FULL: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_FULL, BLOCK, CUT>);
+    default: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<true, 2, GATE_NONE, BLOCK, CUT>);
   }
 }
 
-const void* gate_norm_grad_bf16(int gate_kind, bool block, bool ring) {
-  if (block) return ring ? gate_norm_grad_of<true, true>(gate_kind) : gate_norm_grad_of<true, false>(gate_kind);
-  return ring ? gate_norm_grad_of<false, true>(gate_kind) : gate_norm_grad_of<false, false>(gate_kind);
+const void* gate_norm_grad_bf16(int gate_kind, bool block, bool cut) {
+  if (block) return cut ? gate_norm_grad_of<true, true>(gate_kind) : gate_norm_grad_of<true, false>(gate_kind);
+  return cut ? gate_norm_grad_of<false, true>(gate_kind) : gate_norm_grad_of<false, false>(gate_kind);
 }
 
 }  // namespace sptg

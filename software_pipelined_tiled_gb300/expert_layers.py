@@ -294,7 +294,7 @@ def combine_rows(y, places, weights=None, base=None, out=None, stream=None):
     Sums are 32 bits, rounded once.  Returns out, T x C (it may be base).
 
     Differentiable by y, weights and base (combine_rows_grad); places then has to
-    name every row of y once.
+    name every row of y once (where y has more rows than T * top: none twice).
     """
     if ((y.requires_grad or (weights is not None and weights.requires_grad)
          or (base is not None and base.requires_grad)) and _grad_enabled()):
@@ -309,7 +309,8 @@ def combine_rows_grad(dout, y, places, weights=None, dy=None, dweights=None, nee
     ``dy[places[t, j]] = weights[t, j] * dout[t]``, of y's type, and
     ``dweights[t, j] = <y[places[t, j]], dout[t]>``, float32 (None where weights is
     None or need_weights is false; y is then not read).  places has to name every
-    row of y once, as dispatch_rows returns them.
+    row of y once, as dispatch_rows returns them; only where y has another number of
+    rows than T * top, those without a place are 0 (in a given dy: left as they were).
     """
     code = _row_type(y, "y")
     if places.dim() != 2:
@@ -323,6 +324,9 @@ def combine_rows_grad(dout, y, places, weights=None, dy=None, dweights=None, nee
         _dense(weights, (rows, top), _F32, device, "weights")
     if dy is None:
         dy, lddy = _like(y, stream), cols
+        if y_rows != rows * top:  # rows without a place
+            with torch.cuda.stream(_stream(stream, on)):
+                dy.zero_()
     else:
         lddy = _pitch(dy, y_rows, cols, dtype, device, "dy")
     if weights is None or not need_weights:

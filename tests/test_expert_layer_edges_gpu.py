@@ -143,6 +143,43 @@ def test_gate_norm_by_each_of_its_kernels(rows, cols, forward, backward, kind, d
     assert_within(v, ref["v"][0], (cols / 128 + 128) * UNIT * ref["v"][1])
 
 
+@pytest.mark.parametrize("kind", ["none", "cols", "rows", "full"])
+@pytest.mark.parametrize("rows,cols,forward", [
+    (3000, 4097, SHIFTED), (8000, 1001, SHIFTED), (2000, 5003, SHIFTED), (1000, 8189, SHIFTED), (480, 12289, SHIFTED),
+    (470, 16377, ANY), (5000, 1, SHIFTED), (5000, 7, SHIFTED), (5000, 9, SHIFTED), (5000, 21, SHIFTED), (9000, 129, SHIFTED),
+    (700, 8190, SHIFTED)])
+def test_gate_norm_of_many_rows_off_16_byte_boundaries(rows, cols, forward, kind):
+    g = gen(rows * 3 + cols)
+    w2, gate = 1 + rand(g, cols, std=0.2), gate_of(g, kind, rows, cols, BF16)
+    for pitches in ((0, 0, 0, 0), (3, 0, 6, 1)):  # all rows a shift alike; each operand with its own
+        y, x, dh, dv = (rand(g, rows, cols + k + (k > 3))[:, k:cols + k] for k in pitches)
+        for w1 in (rand(g, cols), None):
+            check_gate_norm(y, x, w2, w1, gate, dh=dh, dv=dv)
+            assert chosen()["kind"] == forward
+            sptg.gate_add_rms_norm_grad(dh, dv, y, x, w2, w1, gate)
+            assert chosen()["kind"] == (GRAD_SHIFTED if cols <= 8192 else GRAD_ANY)
+        check_gate_norm(y, x, w2, w2, gate, dv=dv)
+        wide = rand(g, rows, cols + 5)
+        inside, ref = wide[:, 2:cols + 2], gate_norm_reference(y, wide[:, 2:cols + 2], w2, w2, gate, 0.75, 1e-5)
+        before = wide.clone()
+        h, v = sptg.gate_add_rms_norm(y, inside, w2, w2, gate, alpha=0.75, eps=1e-5, h=inside)  # in place
+        assert_within(h, ref["h"][0], (cols / 128 + 128) * UNIT * ref["h"][1])
+        assert_within(v, ref["v"][0], (cols / 128 + 128) * UNIT * ref["v"][1])
+        assert torch.equal(wide[:, :2], before[:, :2]) and torch.equal(wide[:, cols + 2:], before[:, cols + 2:])
+
+
+def test_gate_norm_waits_for_cut_rows_that_run_out_are_reported():
+    g = gen(77)
+    y, x, w = rand(g, 3000, 4097), rand(g, 3000, 4097), rand(g, 4097)
+    cfg = sptg.Config()
+    cfg.timeout_ms, cfg.inject_stall = 100, 1
+    sptg.gate_add_rms_norm_grad(y, x, y, x, w, w, config=cfg)
+    assert chosen()["kind"] == GRAD_SHIFTED
+    assert sptg.device_error() == -5
+    assert sptg.device_error() == 0
+    check_gate_norm(y, x, w, w, None, dh=x, dv=y)
+
+
 def test_gate_norm_waits_that_run_out_are_reported_and_the_context_survives():
     # each block's second row never arrives: its wait runs out after 100 ms, nothing is copied behind
     # it, and what was in flight lands before the block leaves
@@ -385,6 +422,25 @@ def test_gradients_of_some_inputs_and_odd_gradients():
     grad, = torch.autograd.grad(weights, leaf, ones, create_graph=True)
     with pytest.raises(RuntimeError):  # the gradient has no derivative of its own
         grad.sum().backward()
+
+
+def test_rows_without_a_place_get_no_gradient():
+    g = gen(95)
+    places = torch.randperm(40, device="cuda", generator=g)[:24].to(I32).reshape(8, 3)
+    weights = torch.rand(8, 3, device="cuda", generator=g)
+    for cols in (64, 65):
+        y, dout = rand(g, 40, cols), rand(g, 8, cols)
+        torch.full_like(y, 3.0)  # (what the allocator hands out next)
+        leaf = y.clone().requires_grad_()
+        dy, = torch.autograd.grad(sptg.combine_rows(leaf, places, weights), leaf, dout)
+        want = torch.zeros(40, cols, dtype=torch.float64, device="cuda")
+        want[places.flatten().long()] = (weights[:, :, None].double() * dout[:, None].double()).reshape(24, cols)
+        assert_within(dy, want, UNIT * want.abs())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        on_side = sptg.combine_rows_grad(dout, y, places, weights, stream=side)[0]
+        side.synchronize()
+        assert torch.equal(on_side, dy)
 
 
 def test_python_refusals_on_the_gpu():
