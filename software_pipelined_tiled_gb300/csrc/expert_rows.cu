@@ -27,10 +27,10 @@ const void* combine_rows_variant(bool bf16, bool aligned) {
 
 const void* combine_rows_grad_variant(bool bf16, bool aligned) {
   if (bf16)
-    return aligned ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<true, true>)
-                   : reinterpret_cast<const void*>(&combine_rows_grad_kernel<true, false>);
-  return aligned ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<false, true>)
-                 : reinterpret_cast<const void*>(&combine_rows_grad_kernel<false, false>);
+    return aligned ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<true>)
+                   : reinterpret_cast<const void*>(&combine_rows_grad_cut_kernel<true>);
+  return aligned ? reinterpret_cast<const void*>(&combine_rows_grad_kernel<false>)
+                 : reinterpret_cast<const void*>(&combine_rows_grad_cut_kernel<false>);
 }
 
 }  // namespace sptg

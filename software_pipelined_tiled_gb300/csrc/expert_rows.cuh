@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) combine_rows_kernel(const __grid
 
 // Gradients of the sum by y and by the weights, a block to a row: a piece of
 // dout is multiplied by each weight for dy, and by each row of y for dw.
-template <bool BF16, bool ALIGNED>
+template <bool BF16>
 __global__ void __launch_bounds__(ROWS_THREADS) combine_rows_grad_kernel(const __grid_constant__ RowsParams p) {
   __shared__ float s_sum[ROWS_THREADS / 32][ROWS_AT_ONCE];
   const int64_t row = blockIdx.x;
@@ -431,42 +431,18 @@ __global__ void __launch_bounds__(ROWS_THREADS) combine_rows_grad_kernel(const _
         for (int k = 0; k < 8; ++k) dot[j] += d[k] * f[k];
       }
     };
-    if constexpr (ALIGNED) {
-      for (int c = 8 * threadIdx.x; c < p.cols; c += 8 * ROWS_THREADS) {
-        float d[8];
-        unpack_piece<BF16>(*reinterpret_cast<const uint4*>(dout + c), d);
-        uint4 v[ROWS_AT_ONCE];
-        if (p.dweights) {
-#pragma unroll
-          for (int j = 0; j < ROWS_AT_ONCE; ++j)
-            if (at[j] >= 0) v[j] = *reinterpret_cast<const uint4*>(row_of(p.x, at[j], p.ldx) + c);
-        }
+    for (int c = 8 * threadIdx.x; c < p.cols; c += 8 * ROWS_THREADS) {
+      float d[8];
+      unpack_piece<BF16>(*reinterpret_cast<const uint4*>(dout + c), d);
+      uint4 v[ROWS_AT_ONCE];
+      if (p.dweights) {
 #pragma unroll
         for (int j = 0; j < ROWS_AT_ONCE; ++j)
-          if (at[j] >= 0) piece(j, row_of(p.out, at[j], p.ldo) + c, d, v[j]);
+          if (at[j] >= 0) v[j] = *reinterpret_cast<const uint4*>(row_of(p.x, at[j], p.ldx) + c);
       }
-    } else {  // cut by each row of dy; dout from L1 for all but the first
 #pragma unroll
-      for (int j = 0; j < ROWS_AT_ONCE; ++j) {
-        if (at[j] < 0) continue;
-        uint16_t* dy = row_of(p.out, at[j], p.ldo);
-        // (without dw y is not read, and may not be there)
-        const uint16_t* y = p.dweights ? row_of(p.x, at[j], p.ldx) : dout;
-        const CutRow cut(dy, p.cols);
-#pragma unroll 2
-        for (int c = cut.body + 8 * threadIdx.x; c < cut.tail; c += 8 * ROWS_THREADS) {
-          const ShiftedPiece a = load_words(dout + c), b = load_words(y + c);
-          float d[8];
-          unpack_piece<BF16>(shifted(a), d);
-          piece(j, dy + c, d, shifted(b));
-        }
-        for (int i = threadIdx.x; i < cut.ends; i += ROWS_THREADS) {
-          const int c = cut.end(i);
-          const float d = to_float<BF16>(dout[c]);
-          dot[j] += d * to_float<BF16>(y[c]);
-          dy[c] = from_float<BF16>(d * w[j]);
-        }
-      }
+      for (int j = 0; j < ROWS_AT_ONCE; ++j)
+        if (at[j] >= 0) piece(j, row_of(p.out, at[j], p.ldo) + c, d, v[j]);
     }
     if (p.dweights) {
 #pragma unroll
@@ -482,6 +458,89 @@ __global__ void __launch_bounds__(ROWS_THREADS) combine_rows_grad_kernel(const _
         p.dweights[row * p.top + j0 + threadIdx.x] = sum;
       }
       __syncthreads();
+    }
+  }
+  grid_launch_dependents();
+}
+
+// The same for rows off 16-byte boundaries: a warp to an entry (several, each with a part of the
+// columns, where there are fewer entries than warps), since each row of dy is cut elsewhere and
+// takes dout in pieces of its own (from L1 for all but the first). Bound by latency: 16384
+// rows of 4001 from 8 places take 420 us with two pieces at once and 8 blocks an SM, 443 us with
+// four and 4, 500 us with one and 10; a block that goes through its entries in turn 530 us.
+template <bool BF16>
+__global__ void __launch_bounds__(ROWS_THREADS, 8) combine_rows_grad_cut_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int WARPS = ROWS_THREADS / 32, AT_ONCE = 2;  // pieces of a lane whose loads are in flight together
+  __shared__ float s_sum[WARPS];
+  const int64_t row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = p.top == 1 ? WARPS : p.top == 2 ? WARPS / 2 : 1, entries = WARPS / parts;
+  const int part = warp / entries;
+  grid_dependency_wait();
+  const uint16_t* dout = row_of(p.dout, row, p.ldd);
+  const int32_t* places = p.places + row * p.top;
+  const float* weights = p.weights ? p.weights + row * p.top : nullptr;
+  for (int j = warp % entries; j < p.top; j += entries) {
+    const int64_t at = places[j];
+    float dot = 0.0f;
+    if (at >= 0 && at < p.x_rows) {
+      const float w = weights ? weights[j] : 1.0f;
+      uint16_t* dy = row_of(p.out, at, p.ldo);
+      // (without dw y is not read, and may not be there)
+      const uint16_t* y = p.dweights ? row_of(p.x, at, p.ldx) : dout;
+      const CutRow cut(dy, p.cols);
+      const int end = part == 0 && lane < cut.ends ? cut.end(lane) : -1;
+      uint16_t end_d = 0, end_y = 0;
+      if (end >= 0) {
+        end_d = dout[end];
+        end_y = y[end];
+      }
+      for (int c0 = cut.body + 8 * (32 * part + lane); c0 < cut.tail; c0 += 8 * 32 * AT_ONCE * parts) {
+        ShiftedPiece a[AT_ONCE], b[AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+          const int c = c0 + 8 * 32 * parts * k;
+          if (c >= cut.tail) continue;
+          b[k] = load_words(y + c);
+          a[k] = load_words(dout + c);
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+          const int c = c0 + 8 * 32 * parts * k;
+          if (c >= cut.tail) continue;
+          float d[8], f[8];
+          unpack_piece<BF16>(shifted(a[k]), d);
+          unpack_piece<BF16>(shifted(b[k]), f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot += d[i] * f[i];
+            f[i] = d[i] * w;
+          }
+          *reinterpret_cast<uint4*>(dy + c) = pack_piece<BF16>(f);
+        }
+      }
+      if (end >= 0) {
+        const float d = to_float<BF16>(end_d);
+        dot += d * to_float<BF16>(end_y);
+        dy[end] = from_float<BF16>(d * w);
+      }
+    }
+    if (p.dweights) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (parts == 1) {
+        if (lane == 0) p.dweights[row * p.top + j] = dot;
+      } else if (lane == 0) {
+        s_sum[warp] = dot;
+      }
+    }
+  }
+  if (p.dweights && parts > 1) {  // (one entry a warp)
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < entries) {
+      float sum = 0.0f;
+      for (int k = 0; k < parts; ++k) sum += s_sum[k * entries + threadIdx.x];
+      p.dweights[row * p.top + threadIdx.x] = sum;
     }
   }
   grid_launch_dependents();
