@@ -26,7 +26,7 @@ UNITS = ["sptgemm.cu", "square_f16_f16.cu", "square_f16_f32.cu", "square_bf16_bf
          "grouped_y_bf16.cu", "grouped_y_f16.cu", "grouped_dx_bf16.cu", "grouped_dx_f16.cu",
          "grouped_dw_bf16.cu", "grouped_dw_f16.cu",
          "route_experts.cu", "expert_rows.cu", "gate_norm.cu", "gate_norm_grad_bf16.cu",
-         "gate_norm_grad_f16.cu"]
+         "gate_norm_grad_f16.cu", "gate_norm_grad_wide.cu"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,

@@ -562,8 +562,9 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
                        in_pieces(w2, 0) && in_pieces(dh, lddh) && in_pieces(dv, lddv) && in_pieces(dy, lddy) &&
                        in_pieces(dx, lddx) && (!by_col || in_pieces(gate, 0)) &&
                        (!full || (in_pieces(gate, ldg) && in_pieces(dgate, lddg)));
-  enum { GATE_GRAD_RING, GATE_GRAD_CUT, GATE_GRAD_ANY };
-  int kind = GATE_GRAD_ANY, threads = GATE_ANY_THREADS;
+  // by width and alignment; beyond 8192 columns by a cluster, or element by element
+  enum { GATE_GRAD_RING, GATE_GRAD_CUT, GATE_GRAD_WIDE };
+  int kind = GATE_GRAD_WIDE, parts = 1, threads = GATE_ANY_THREADS;
   int64_t blocks = 2 * di.sm_count;
   int smem = 0, stages = 0;
   const void* fn = gate_norm_grad_any_variant(bf16);
@@ -581,6 +582,19 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
     if (!rc) rc = residency(res, dev, fn, threads, smem);
     if (rc) return rc;
     blocks = static_cast<int64_t>(res.blocks) * di.sm_count;
+  }
+  int64_t part_cols = cols;
+  if (cols > 8192 && cols <= 8192 * GATE_MAX_PARTS && vectors) {
+    // the fewest CTAs that hold a row, and as many clusters as the SMs make
+    while (part_cols > 8192) part_cols = ceil_div(cols / 8, parts *= 2) * 8;
+    fn = gate_norm_grad_wide_variant(bf16, gate_kind, w1 != nullptr);
+    const int ops = 2 + (dh != nullptr) + (dv != nullptr) + full;
+    threads = row_threads(part_cols / 8, 2);
+    stages = 2;
+    smem = gate_ring_smem(static_cast<int>(part_cols), ops, stages, false);
+    rc = ensure_smem(dev, fn, gate_ring_most(true));
+    if (rc) return rc;
+    blocks = di.sm_count / parts;
   }
   blocks = std::min({rows, blocks, gate_grad_blocks(cols)});
   if (kind == GATE_GRAD_CUT && blocks < rows) blocks = std::max<int64_t>(8, blocks / 8 * 8);  // (see RowCut)
@@ -601,10 +615,12 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
   p.dgate = dgate;
   p.lddg = lddg;
   p.out_kind = out_kind;
+  p.parts = parts;
+  p.part_cols = static_cast<int>(part_cols);
   p.part = static_cast<float*>(workspace);
   void* args[] = {&p};
-  cudaError_t e = launch_op(fn, dim3(static_cast<unsigned>(blocks)), threads, smem,
-                            1, stream, args);
+  cudaError_t e = launch_op(fn, dim3(static_cast<unsigned>(blocks * parts)), threads, smem,
+                            parts, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "gate_add_rms_norm_grad launch");
   ColumnSumParams c;
   c.part = static_cast<const float*>(workspace);
@@ -620,7 +636,8 @@ int gate_norm_grad(int64_t rows, int64_t cols, int type, const void* dh, int64_t
   e = launch_op(gate_norm_columns_variant(bf16), dim3(static_cast<unsigned>(ceil_div(cols, 32)), by_col || w1 ? 2 : 1),
                 1024, 0, 1, stream, column_args);
   if (e != cudaSuccess) return cuda_fail(e, "gate_add_rms_norm_grad columns launch");
-  set_config("kernel=gate_norm_grad type=%s kind=%lld threads=%lld grid=%lld stages=%lld", name, {kind, threads, blocks, stages});
+  set_config("kernel=gate_norm_grad type=%s kind=%lld threads=%lld grid=%lld stages=%lld parts=%lld", name,
+             {kind, threads, blocks, stages, parts});
   return SPTG_OK;
 }
 

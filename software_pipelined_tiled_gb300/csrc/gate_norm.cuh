@@ -80,6 +80,8 @@ struct GateNormGradParams {
   void* dgate;       // ROWS, FULL
   int64_t lddg;
   int out_kind;      // of ROWS' dgate: OUT_F32 or the rows' type
+  int parts;         // CTAs of a cluster that share a row (1: none do)
+  int part_cols;     // columns of each, a multiple of 8 (the last: what is left)
   float* part;       // [2][blocks][cols]: sums of dv hn, and of e
 };
 
@@ -112,6 +114,31 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float4* s) {
 #pragma unroll 4
   for (int w = 0; w < warps; ++w) {
     const float4 a = s[w];
+    const float part[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += part[i];
+  }
+}
+
+// Sums over a row, of a block or (WIDE) of a cluster whose CTAs share it: the blocks' sums go
+// to all of them, and are added up by rank.
+constexpr int GATE_MAX_PARTS = 8;
+template <bool WIDE, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float4* s, float4* of_parts, int parts, int rank) {
+  block_sums<N>(v, s);
+  if constexpr (!WIDE) return;
+  if (static_cast<int>(threadIdx.x) < parts) {
+    const uint32_t to = map_to_cta(smem_addr(of_parts + rank), threadIdx.x);
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[0]), "f"(N > 1 ? v[N > 1 ? 1 : 0] : 0.0f),
+                 "f"(N > 2 ? v[N > 2 ? 2 : 0] : 0.0f), "f"(0.0f)
+                 : "memory");
+  }
+  __syncwarp();
+  cluster_sync();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  for (int r = 0; r < parts; ++r) {
+    const float4 a = of_parts[r];
     const float part[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += part[i];
@@ -375,18 +402,22 @@ __device__ __forceinline__ const uint16_t* ring_src(const GateRing& r, int o, in
   return static_cast<const uint16_t*>(r.src[o]) + row * r.ld[o];
 }
 
-// Starts the copies of the block's row i into its stage (one thread).
-__device__ __forceinline__ void ring_fetch(const GateNormParams& p, int64_t i, int s, uint32_t bar0,
-                                           uint32_t data0, uint64_t policy) {
-  const int64_t row = blockIdx.x + i * gridDim.x;
+// Starts the copies of the block's row i into its stage (one thread). WIDE: of the
+// columns from col0 on, by the clusters' numbers.
+template <bool WIDE = false>
+__device__ __forceinline__ void ring_fetch(const GateNormParams& p, int64_t i, int s, uint32_t bar0, uint32_t data0,
+                                           uint64_t policy, unsigned group = 0, unsigned groups = 0, int col0 = 0,
+                                           int part_cols = 0) {
+  const int64_t row = WIDE ? group + i * groups : blockIdx.x + i * gridDim.x;
   if (row >= p.rows || (p.ring.inject_stall && i == 1)) return;
-  const uint32_t row_bytes = gate_row_bytes(p.cols, false), bytes = 2u * p.cols;
+  const int cols = WIDE ? part_cols : p.cols;
+  const uint32_t row_bytes = gate_row_bytes(cols, false), bytes = 2u * cols;
   uint32_t dst = data0 + s * p.ring.ops * row_bytes;
   mbar_arrive_expect_tx(bar0 + 8 * s, p.ring.ops * bytes);
 #pragma unroll
   for (int o = 0; o < GATE_MAX_OPS; ++o)
     if (o < p.ring.ops) {
-      bulk_load_1d(dst, ring_src(p.ring, o, row), bytes, bar0 + 8 * s, policy);
+      bulk_load_1d(dst, ring_src(p.ring, o, row) + (WIDE ? col0 : 0), bytes, bar0 + 8 * s, policy);
       dst += row_bytes;
     }
 }
@@ -551,8 +582,8 @@ __device__ __forceinline__ uint4 ring_piece(const uint8_t* row, int at, int apar
 
 // Lets the copies in flight land before the block leaves: those up to a ring past
 // the rows that have.
-__device__ __forceinline__ void ring_drain(const GateNormParams& p, int64_t landed, uint32_t bar0) {
-  for (int64_t i = landed; i < landed + p.ring.stages && blockIdx.x + i * gridDim.x < p.rows; ++i) {
+__device__ __forceinline__ void ring_drain(const GateNormParams& p, unsigned first, unsigned step, int64_t landed, uint32_t bar0) {
+  for (int64_t i = landed; i < landed + p.ring.stages && first + i * step < p.rows; ++i) {
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar0 + 8 * static_cast<uint32_t>(i % p.ring.stages),
                           static_cast<uint32_t>(i / p.ring.stages) & 1u) &&
@@ -682,13 +713,17 @@ __global__ void __launch_bounds__(512) gate_norm_ring_kernel(const __grid_consta
     phase = later_phase;
   }
   grid_launch_dependents();
-  if (threadIdx.x == 0 && !ok) ring_drain(p, landed, bar0);
+  if (threadIdx.x == 0 && !ok) ring_drain(p, blockIdx.x, gridDim.x, landed, bar0);
 }
 
 // Backwards: a fixed number of blocks, PER pieces of 8 elements a thread, whose sums
-// over rows stay in registers. CUT: rows off 16-byte boundaries.
-template <bool BF16, int PER, int GATE, bool BLOCK, bool CUT>
+// over rows stay in registers. GRAD_CUT: rows off 16-byte boundaries. GRAD_WIDE: rows that
+// one block cannot hold, shared by the CTAs of a cluster, each with a part of the columns.
+enum GradForm { GRAD_WHOLE, GRAD_CUT, GRAD_WIDE };
+
+template <bool BF16, int PER, int GATE, bool BLOCK, int FORM>
 __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_constant__ GateNormGradParams p) {
+  constexpr bool CUT = FORM == GRAD_CUT, WIDE = FORM == GRAD_WIDE;
   extern __shared__ __align__(128) uint8_t ring_data[];
   // (alternating, so that a fast warp's next row leaves a slow one's sums alone)
   __shared__ float4 s_sum[2][3][32];
@@ -696,15 +731,19 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
   __shared__ int abort_word;
   __shared__ typename std::conditional<CUT, RingCutShared, RingWholeShared>::type sh;
   const GateNormParams& f = p.f;
+  __shared__ float4 s_parts[WIDE ? 2 : 1][3][WIDE ? GATE_MAX_PARTS : 1];
+  const unsigned parts = WIDE ? p.parts : 1, rank = WIDE ? blockIdx.x % parts : 0;
+  const unsigned group = WIDE ? blockIdx.x / parts : blockIdx.x, groups = WIDE ? gridDim.x / parts : gridDim.x;
+  const int col0 = WIDE ? static_cast<int>(rank) * p.part_cols : 0, cols = WIDE ? min(p.part_cols, f.cols - col0) : f.cols;
   int start = CUT ? -shift_of(static_cast<const uint16_t*>(p.dx) + blockIdx.x * p.lddx) : 0;
   // (rows that fill the block to the last piece leave no room for one more: stores in parts)
-  if (CUT && (f.cols - start + 7) >> 3 > PER * static_cast<int>(blockDim.x)) start = 0;
-  const int pieces = (f.cols - start + 7) >> 3;
+  if (CUT && (cols - start + 7) >> 3 > PER * static_cast<int>(blockDim.x)) start = 0;
+  const int pieces = (cols - start + 7) >> 3;
   const uint4 none = make_uint4(0, 0, 0, 0);
   const float inv_cols = 1.0f / static_cast<float>(f.cols);
   const int op_dv = p.dh ? 3 : 2, op_gate = f.ring.ops - 1;
   const uint32_t bar0 = smem_addr(bars), data0 = smem_addr(ring_data);
-  const int row_bytes = gate_row_bytes(f.cols, CUT), stage_bytes = f.ring.ops * row_bytes;
+  const int row_bytes = gate_row_bytes(cols, CUT), stage_bytes = f.ring.ops * row_bytes;
   const uint64_t policy = policy_evict_first();  // read once
   if (threadIdx.x == 0) {
     for (int s = 0; s < f.ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -726,12 +765,15 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     if (GATE == GATE_FULL) dg_alike = ring_output(f, sh, 2, p.dgate, p.lddg, start);
   }
   constexpr int OUTS = GATE == GATE_FULL ? 3 : 2;
-  __syncthreads();
+  if constexpr (WIDE)
+    cluster_sync();  // (all CTAs are there)
+  else
+    __syncthreads();
   grid_dependency_wait();
   uint16_t end = 0;
   if constexpr (!CUT) {
     if (threadIdx.x == 0)
-      for (int i = 0; i < f.ring.stages; ++i) ring_fetch(f, i, i, bar0, data0, policy);
+      for (int i = 0; i < f.ring.stages; ++i) ring_fetch<WIDE>(f, i, i, bar0, data0, policy, group, groups, col0, cols);
   } else {
     if (threadIdx.x < 32)
       for (int i = 0; i < f.ring.stages; ++i) ring_fetch_cut(f, sh, i, i, bar0, data0, policy);
@@ -751,6 +793,7 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     const int at = threadIdx.x + i * blockDim.x;
     const bool in = at < pieces;
     const auto column = [&](const void* w) {
+      if constexpr (WIDE) return in ? static_cast<const uint4*>(w)[(col0 >> 3) + at] : none;
       return in ? load_piece<!CUT>(static_cast<const uint16_t*>(w), start + 8 * at, f.cols) : none;
     };
     w2[i] = column(f.w2);
@@ -790,16 +833,16 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
   float s1[1] = {0.0f};
   if (BLOCK) {
     s1[0] = square_sum(0);
-    block_sums<1>(s1, s_sum[1][0]);
+    row_sums<WIDE>(s1, s_sum[1][0], s_parts[WIDE][0], parts, rank);
   }
-  for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x, ++n, odd ^= 1) {
+  for (int64_t row = group; row < f.rows; row += groups, ++n, odd ^= 1) {
     const float gr = GATE == GATE_ROWS ? gate_load<BF16>(f.gate, row * f.ldg) : 1.0f;
     const uint8_t* stage = ring_data + s * stage_bytes;
     const auto store = [&](int o, bool alike, void* to, int64_t ld, int at, const float_pair (&v)[4]) {
       if constexpr (CUT)
         ring_store(sh, o, odd, alike, static_cast<uint16_t*>(to) + row * ld, start + 8 * at, f.cols, pair_pack<BF16>(v));
       else
-        row_pieces(to, row, ld)[at] = pair_pack<BF16>(v);
+        row_pieces(to, row, ld)[(col0 >> 3) + at] = pair_pack<BF16>(v);
     };
     // piece i of y, x, dh, dv or the gate
     const auto operand = [&](int op, int i) {
@@ -842,7 +885,7 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     if constexpr (CUT) {  // (of the row fetched a row ago, into the stage before this one)
       if (n > 0) ends_store(f, sh, n - 1 + f.ring.stages, ring_data + (s == 0 ? f.ring.stages - 1 : s - 1) * stage_bytes, end);
     }
-    block_sums<2>(s2, s_sum[odd][1]);
+    row_sums<WIDE>(s2, s_sum[odd][1], s_parts[WIDE ? odd : 0][1], parts, rank);
     if constexpr (CUT) {
       if (n > 0) ends_write(sh, OUTS, n - 1, odd ^ 1);
     }
@@ -898,21 +941,21 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     const int later = s + 1 == f.ring.stages ? 0 : s + 1;
     const uint32_t later_phase = later == 0 ? phase ^ 1u : phase;
     float s3[3] = {sum_of(dot), sum_of(row_dg), 0.0f};
-    if (row + gridDim.x < f.rows) {
+    if (row + groups < f.rows) {
       ok = ok && wait_bounded_lazy(bar0 + 8 * later, later_phase, ctl, WAIT_MMA_FULL);
       landed += ok;
       if (BLOCK) s3[2] = square_sum(later);
     }
-    block_sums<3>(s3, s_sum[odd][2]);
+    row_sums<WIDE>(s3, s_sum[odd][2], s_parts[WIDE ? odd : 0][2], parts, rank);
     s1[0] = s3[2];
     // (the stage has been read; into a place whose last copy has landed, no other)
     if constexpr (!CUT) {
-      if (threadIdx.x == 0 && ok) ring_fetch(f, n + f.ring.stages, s, bar0, data0, policy);
+      if (threadIdx.x == 0 && ok) ring_fetch<WIDE>(f, n + f.ring.stages, s, bar0, data0, policy, group, groups, col0, cols);
     } else {
       if (threadIdx.x < 32 && __all_sync(0xffffffffu, ok)) ring_fetch_cut(f, sh, n + f.ring.stages, s, bar0, data0, policy);
       ends_load(f, sh, n + f.ring.stages, end);
     }
-    if (GATE == GATE_ROWS && threadIdx.x == 0) store_kind(p.dgate, row, s3[1], p.out_kind);
+    if (GATE == GATE_ROWS && threadIdx.x == 0 && rank == 0) store_kind(p.dgate, row, s3[1], p.out_kind);
     const float_pair back1 = pair_of(-(s3[0] * inv_cols * r1 * r1));
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -938,9 +981,9 @@ __global__ void __launch_bounds__(512) gate_norm_grad_kernel(const __grid_consta
     __syncthreads();
     ends_write(sh, OUTS, n - 1, odd ^ 1);
   }
-  if (threadIdx.x == 0 && !ok) ring_drain(f, landed, bar0);
-  const int64_t plane = static_cast<int64_t>(gridDim.x) * f.cols;
-  float* part = p.part + static_cast<int64_t>(blockIdx.x) * f.cols;
+  if (threadIdx.x == 0 && !ok) ring_drain(f, group, groups, landed, bar0);
+  const int64_t plane = static_cast<int64_t>(groups) * f.cols;
+  float* part = p.part + static_cast<int64_t>(group) * f.cols + col0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int at = threadIdx.x + i * blockDim.x;

@@ -4,19 +4,20 @@
 
 namespace sptg {
 
-template <bool BLOCK, bool CUT>
+template <bool BLOCK, int FORM>
 const void* gate_norm_grad_of(int gate_kind) {
   switch (gate_kind) {
-    case GATE_COLS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_COLS, BLOCK, CUT>);
-    case GATE_ROWS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_ROWS, BLOCK, CUT>);
-    case GATE_FULL: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_FULL, BLOCK, CUT>);
-    default: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_NONE, BLOCK, CUT>);
+    case GATE_COLS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_COLS, BLOCK, FORM>);
+    case GATE_ROWS: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_ROWS, BLOCK, FORM>);
+    case GATE_FULL: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_FULL, BLOCK, FORM>);
+    default: return reinterpret_cast<const void*>(&gate_norm_grad_kernel<false, 2, GATE_NONE, BLOCK, FORM>);
   }
 }
 
 const void* gate_norm_grad_f16(int gate_kind, bool block, bool cut) {
-  if (block) return cut ? gate_norm_grad_of<true, true>(gate_kind) : gate_norm_grad_of<true, false>(gate_kind);
-  return cut ? gate_norm_grad_of<false, true>(gate_kind) : gate_norm_grad_of<false, false>(gate_kind);
+  if (block)
+    return cut ? gate_norm_grad_of<true, GRAD_CUT>(gate_kind) : gate_norm_grad_of<true, GRAD_WHOLE>(gate_kind);
+  return cut ? gate_norm_grad_of<false, GRAD_CUT>(gate_kind) : gate_norm_grad_of<false, GRAD_WHOLE>(gate_kind);
 }
 
 }  // namespace sptg

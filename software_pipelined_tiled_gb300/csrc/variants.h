@@ -96,11 +96,13 @@ const void* combine_rows_grad_variant(bool bf16, bool aligned);
 // Gate, scaled residual and norms: a row to a block with one or two pieces of 8
 // elements a thread; rows through rings of blocks; rows off 16-byte boundaries; rows of
 // any width. Backwards by the kind of gate, whether the block's output is normalised,
-// and whether rows are cut by 16-byte boundaries; or rows of any width; the sums over the blocks.
+// and whether rows are cut by 16-byte boundaries; rows that a cluster shares; rows of any
+// width; the sums over the blocks.
 enum GateNormKind : int { GATE_NORM_1, GATE_NORM_2, GATE_NORM_RING, GATE_NORM_SHIFTED, GATE_NORM_ANY };
 const void* gate_norm_variant(bool bf16, int kind);
 const void* gate_norm_grad_bf16(int gate_kind, bool block, bool cut);
 const void* gate_norm_grad_f16(int gate_kind, bool block, bool cut);
+const void* gate_norm_grad_wide_variant(bool bf16, int gate_kind, bool block);
 const void* gate_norm_grad_any_variant(bool bf16);
 const void* gate_norm_columns_variant(bool bf16);
 

@@ -168,13 +168,33 @@ def test_gate_norm_of_many_rows_off_16_byte_boundaries(rows, cols, forward, kind
         assert torch.equal(wide[:, :2], before[:, :2]) and torch.equal(wide[:, cols + 2:], before[:, cols + 2:])
 
 
-def test_gate_norm_waits_for_cut_rows_that_run_out_are_reported():
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("kind", ["none", "cols", "rows", "full"])
+@pytest.mark.parametrize("rows,cols,parts", [(1, 8200, 2), (2, 16384, 2), (300, 16384, 2), (3, 16392, 4), (160, 32768, 4),
+                                             (5, 32776, 8), (40, 65536, 8), (3, 65544, 1), (3, 16385, 1)])
+def test_gate_norm_gradients_of_rows_that_a_cluster_shares(rows, cols, parts, kind, dtype):
+    g = gen(rows + cols)
+    y, x = rand(g, rows, cols, dtype=dtype), rand(g, rows, cols, dtype=dtype, std=2.0)
+    w2, gate = 1 + rand(g, cols, dtype=dtype, std=0.2), gate_of(g, kind, rows, cols, dtype)
+    dh, dv = rand(g, rows, cols, dtype=dtype), rand(g, rows, cols, dtype=dtype)
+    for w1 in (rand(g, cols, dtype=dtype), None):
+        check_gate_norm(y, x, w2, w1, gate, dh=dh, dv=dv)
+        check_gate_norm(y, x, w2, w1, gate, dv=dv, out_dtype=dtype)
+        check_gate_norm(y, x, w2, w1, gate, dh=dh)
+        first = sptg.gate_add_rms_norm_grad(dh, dv, y, x, w2, w1, gate)
+        assert chosen()["kind"] == GRAD_ANY and chosen()["parts"] == parts
+        again = sptg.gate_add_rms_norm_grad(dh, dv, y, x, w2, w1, gate)
+        assert all(a is b or torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("rows,cols,kind", [(3000, 4097, GRAD_SHIFTED), (500, 16384, GRAD_ANY), (200, 40000, GRAD_ANY)])
+def test_gate_norm_gradients_waits_that_run_out_are_reported(rows, cols, kind):
     g = gen(77)
-    y, x, w = rand(g, 3000, 4097), rand(g, 3000, 4097), rand(g, 4097)
+    y, x, w = rand(g, rows, cols), rand(g, rows, cols), rand(g, cols)
     cfg = sptg.Config()
     cfg.timeout_ms, cfg.inject_stall = 100, 1
     sptg.gate_add_rms_norm_grad(y, x, y, x, w, w, config=cfg)
-    assert chosen()["kind"] == GRAD_SHIFTED
+    assert chosen()["kind"] == kind
     assert sptg.device_error() == -5
     assert sptg.device_error() == 0
     check_gate_norm(y, x, w, w, None, dh=x, dv=y)
