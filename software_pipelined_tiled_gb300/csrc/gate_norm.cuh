@@ -261,6 +261,9 @@ __global__ void __launch_bounds__(1024) gate_norm_kernel(const __grid_constant__
   const bool by_column = p.gate_kind == GATE_COLS || p.gate_kind == GATE_FULL;
   const uint16_t* gate = static_cast<const uint16_t*>(p.gate) + (p.gate_kind == GATE_FULL ? row * p.ldg : 0);
   const int start = ALIGNED ? 0 : -shift_of(h_row);
+  // Rows of dense tensors lie alike, and need no shifts (16384 rows of 4097: 156 us, with
+  // shifts 193 us; a ring of such rows, in which fewer warps run, 230 us).
+  const bool alike = shift_of(y) + start == 0 && shift_of(x) + start == 0;
   const auto first = [&](int i) { return start + 8 * static_cast<int>(threadIdx.x + i * blockDim.x); };
   const auto load = [&](const uint16_t* from, int i) {
     return first(i) < p.cols ? load_piece<ALIGNED>(from, first(i), p.cols) : none;
@@ -279,9 +282,14 @@ __global__ void __launch_bounds__(1024) gate_norm_kernel(const __grid_constant__
   for (int i = 0; i < PER; ++i) {
     if (!ALIGNED) {
       if (inside_row(first(i), p.cols)) {
-        const ShiftedPiece a = load_words(y + first(i)), b = load_words(x + first(i));
-        yv[i] = shifted(a);
-        xv[i] = shifted(b);
+        if (alike) {
+          yv[i] = *reinterpret_cast<const uint4*>(y + first(i));
+          xv[i] = *reinterpret_cast<const uint4*>(x + first(i));
+        } else {
+          const ShiftedPiece a = load_words(y + first(i)), b = load_words(x + first(i));
+          yv[i] = shifted(a);
+          xv[i] = shifted(b);
+        }
       } else {
         // (the row's ends: all loads in one branch, so that they are in flight together)
         const bool in = first(i) < p.cols;
