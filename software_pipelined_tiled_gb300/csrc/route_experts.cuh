@@ -127,10 +127,10 @@ __device__ __forceinline__ float logistic(float l) {
   return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
 
-// The larger of two, NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest of three, NaN if any is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
   return m;
 }
 
@@ -382,8 +382,9 @@ __device__ __noinline__ int route_careful(const RouteParams& p, int64_t row, int
   return mine;
 }
 
+// (Seven blocks an SM: 32768 rows of 256 experts, 8 groups 37.2 us, six 38.3 us, eight 37.7 us.)
 template <int TYPE, int LANES, int PER>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, PER == 8 ? 7 : 1)
     route_experts_kernel(const __grid_constant__ RouteParams p) {
   constexpr int N = TYPE == ROUTE_F32 ? 4 : 8;  // logits in 16 bytes
   constexpr uint32_t PLACE = PER - 1;           // a key's lowest bits: PER - 1 - place in the lane
@@ -465,9 +466,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       for (int j = 0; j < PER; ++j)
         l[j] = j < count ? route_load<TYPE>(p.logits, row * p.ld + first + j) : -INFINITY;
     }
-    float m = l[0];
+    float m = max_nan(l[0], l[1], l[2]);
 #pragma unroll
-    for (int j = 1; j < PER; ++j) m = max_nan(m, l[j]);
+    for (int j = 3; j + 1 < PER; j += 2) m = max_nan(m, l[j], l[j + 1]);
+    m = max_nan(m, m, l[PER - 1]);
     bool bad = b_nan || m != m || (!p.sigmoid && m == INFINITY);
     bad = (__ballot_sync(ALL, bad) & mask) != 0;
     uint32_t k[PER];
@@ -524,10 +526,12 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
         score = order_bits(from_order_bits(t1 & ~PLACE) + from_order_bits(t2 & ~PLACE) + 0.0f);
       // (groups after the last have lanes of count 0: score 0, behind all others)
       int rank = 0;
-      for (int o = 0; o < p.groups; ++o) {
+      for (int o0 = 0; o0 < p.groups; o0 += 1 << p.lanes_log2) {  // (each lane of a group looks at others)
+        const int o = o0 + q;
         const uint32_t other = __shfl_sync(ALL, score, o << p.lanes_log2, LANES);
-        rank += other > score || (other == score && o < g);
+        rank += o < p.groups && (other > score || (other == score && o < g));
       }
+      for (int o = 1; o < (1 << p.lanes_log2); o <<= 1) rank += __shfl_xor_sync(ALL, rank, o);
       bool kept = rank < p.top_groups;
       if (!exact) {
         const float w = from_order_bits(~route_max<LANES>(kept ? ~score : 0u));
@@ -724,7 +728,11 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
     own = (own + 2) | (unsettled ? 1 << 16 : 0);
     const int source = (my_row & (AT_ONCE - 1)) * LANES + my_slot;
     const int got = __shfl_sync(ALL, own, source);
-    const float got_m = __shfl_sync(ALL, m, source), got_rz = __shfl_sync(ALL, rz, source);
+    float got_m = 0.0f, got_rz = 1.0f;
+    if (!p.renorm) {
+      got_m = __shfl_sync(ALL, m, source);
+      got_rz = __shfl_sync(ALL, rz, source);
+    }
     if (my_row / AT_ONCE == turn) {
       pick = my_slot < p.top ? (got & 0xffff) - 2 : -1;
       doubt = (got >> 16) != 0;
