@@ -70,10 +70,12 @@ def test_route_of_logits_from_a_product_just_launched(dtype):
 
 
 # ------------------------------------------------- rows to experts and back
-@pytest.mark.parametrize("rows,top,e,kernel", [(256, 8, 64, "dispatch_small"), (257, 8, 64, "dispatch"),
-                                               (4096, 1, 1024, "dispatch"), (4097, 1, 1024, "dispatch"),
+@pytest.mark.parametrize("rows,top,e,kernel", [(256, 8, 64, "dispatch_small"), (512, 8, 64, "dispatch_small"),
+                                               (513, 8, 64, "dispatch"), (257, 8, 64, "dispatch_small"),
+                                               (4096, 1, 1024, "dispatch_small"), (4097, 1, 1024, "dispatch"),
                                                (70001, 3, 200, "dispatch"), (2048, 1, 1024, "dispatch_small"),
-                                               (1, 2048, 33, "dispatch_small"), (3, 5000, 7, "dispatch")])
+                                               (1, 2048, 33, "dispatch_small"), (1, 4096, 33, "dispatch_small"),
+                                               (3, 5000, 7, "dispatch")])
 def test_dispatch_by_each_of_its_kernels(rows, top, e, kernel):
     g = gen(rows + top)
     experts = torch.randint(-1, e + 1, (rows, top), device="cuda", generator=g, dtype=I32)
