@@ -411,9 +411,9 @@ int sptg_grouped_gemm_dw(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype 
  * copies to the host, graph capture, the same bits on every call. Rows of
  * SPTG_T_F16 or SPTG_T_BF16 take any width, pitch and element-aligned pointer; they
  * are read in 16-byte pieces when the width and every pitch are multiples of 8
- * and every pointer is 16-byte aligned, else in pairs of words shifted together (up to
- * 16376 columns; the gradients of the norms up to 8192). cols <= 2^30. Outputs overlap
- * nothing unless said.
+ * and every pointer is 16-byte aligned, else in words shifted together (the norms up to
+ * 16376 columns, their gradients up to 8192; beyond, element by element). cols <= 2^30.
+ * Outputs overlap nothing unless said.
  */
 
 /*

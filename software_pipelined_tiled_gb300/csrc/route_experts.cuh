@@ -25,7 +25,8 @@
 // is a minimum and a maximum), so the next pick is the largest of the lanes' first
 // keys, and the two best of a group are at hand.
 //
-// Bound by the issue of instructions, so whatever one row needs in a few lanes
+// Bound by the issue of instructions (32768 rows of 256 f32 logits, bias, 8 groups, 8 picks:
+// 37 us, of which memory needs 5; two thirds of the issue slots are taken), so whatever one row needs in a few lanes
 // only is done for several at once: a warp makes the choices of up to 4 rows first
 // (8 places each; with more than 8 picks 2 of 16), then looks for doubts and
 // works out the weights of all of them, one place to a lane.
