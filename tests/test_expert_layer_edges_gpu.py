@@ -446,6 +446,36 @@ def test_gradients_of_some_inputs_and_odd_gradients():
         grad.sum().backward()
 
 
+@pytest.mark.parametrize("rows,cols", [(700, 4097), (200, 16384)])
+def test_gradients_of_cut_and_of_shared_rows_in_a_graph(rows, cols):
+    """Captured, replayed with new inputs, and beside the same call on another stream."""
+    g = gen(96)
+    w = rand(g, cols)
+    y, x, dh, dv = (rand(g, rows, cols) for _ in range(4))
+    places = torch.randperm(2 * rows, device="cuda", generator=g).to(I32).reshape(rows, 2)
+    weights, sorted_rows = torch.rand(rows, 2, device="cuda", generator=g), rand(g, 2 * rows, cols)
+
+    def calls(**kw):
+        return (*sptg.gate_add_rms_norm_grad(dh, dv, y, x, w, w, w, out_dtype=F32, **kw),
+                *sptg.combine_rows_grad(dh, sorted_rows, places, weights, **kw))
+
+    calls()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = calls()
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        for t in (y, x, dh, dv):
+            t.copy_(rand(g, rows, cols))
+        torch.cuda.synchronize()
+        graph.replay()
+        beside = calls(stream=side)
+        torch.cuda.synchronize()
+        want = calls()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(out, want, beside))
+
+
 def test_rows_without_a_place_get_no_gradient():
     g = gen(95)
     places = torch.randperm(40, device="cuda", generator=g)[:24].to(I32).reshape(8, 3)
