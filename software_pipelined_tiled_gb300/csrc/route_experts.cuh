@@ -11,12 +11,15 @@
 // The choice is the one that exact arithmetic makes (ties: the lowest index),
 // which 32 bits cannot always tell. Where no bias takes part and groups go by
 // their best expert, experts are compared by their logits, which order them as
-// their scores do. Otherwise keys are computed in 32 bits with a known error; where
-// two that decide lie closer than that, those in doubt are computed anew in 44 bits
-// (Pair) and ranked, and if that does not settle it, the row goes through
-// route_careful(), in 64. Two experts of the same logit and the same bias
-// are a tie and decided as such: with 16-bit logits and biases that move in
-// steps, that is the common case.
+// their scores do. Otherwise keys are computed in 32 bits with a known error, and what
+// decides where two lie closer than that is:
+// - without a bias, logits for experts, and for sums of two scores their difference, formed so
+//   that scores of any size count (route_by_logits);
+// - with a bias, the keys in 44 bits (Pair), and if that does not settle it, in 64
+//   (route_careful). Keys, or sums of two, that differ by less than 2^-42 of their size and the
+//   largest bias's may count as equal.
+// Two experts of the same logit and the same bias are a tie and decided as such: with 16-bit
+// logits and biases that move in steps, that is the common case.
 //
 // A row is the work of LANES lanes of a warp, each with up to PER neighbouring
 // experts in registers (a group's experts in lanes of their own). A lane's key is
@@ -135,7 +138,7 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   return m;
 }
 
-// Sums and maxima of LANES neighbouring lanes; all of a warp take part. (Reductions
+// Sums and maxima of LANES neighbouring lanes; all of a warp take part, or those of the mask. (Reductions
 // and votes with a mask of their own for each part of a warp run part by part: 32768
 // rows of 128 experts, two to a warp, 23 us.)
 template <int LANES>
@@ -145,10 +148,10 @@ __device__ __forceinline__ float route_sum(float v) {
   return v;
 }
 template <int LANES>
-__device__ __forceinline__ uint32_t route_max(uint32_t v) {
+__device__ __forceinline__ uint32_t route_max(uint32_t v, uint32_t mask = 0xffffffffu) {
   if constexpr (LANES == 32) return __reduce_max_sync(0xffffffffu, v);
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(mask, v, o));
   return v;
 }
 
@@ -183,12 +186,13 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
 // b_most, s its size with the bias's: relative to s the score is off by 2^-21 and
 // by its logit's (or its distance from the largest logit) times 2^-23, which is
 // no more than -log2(s) where that counts; the place's bits take 2^-20 (8 experts
-// a lane). A softmax's sum adds 2^-20. (NaN for s = 0: nothing is certain.)
+// a lane). A softmax's sum adds 2^-20. (Below 2^-100 nothing is certain: scores that
+// small lose bits.)
 template <int PER>
 __device__ __forceinline__ float route_apart(float key, float b_most, bool sigmoid) {
   const float APART = PER / 8 * (sigmoid ? 1.9073486e-06f : 3.814697265625e-06f);  // 2^-19, 2^-18
   const float s = fabsf(key) + b_most;
-  return APART * s * (1.0f + 0.0625f * fmaxf(0.0f, -__log2f(s)));
+  return s > 0x1p-100f ? APART * s * (1.0f + 0.0625f * fmaxf(0.0f, -__log2f(s))) : INFINITY;
 }
 
 // Numbers as unevaluated sums of two floats, with error-free sums and products
@@ -258,15 +262,8 @@ __device__ __forceinline__ Pair pair_exp(Pair x) {
   return {v.hi * scale, v.lo * scale};
 }
 
-// A key for the comparison of two experts whose scores lie close: the logit itself
-// where logits stand for the keys; else the score, with a bias if there is one. z: with
-// a bias the softmax's sum, of exponentials from the largest logit m on. Scores without a
-// bias are only compared with one another, and are all multiplied by exp(-m) if m
-// < 0, so that none is too small.
-enum RouteKey : int { KEY_LOGIT, KEY_SCORE, KEY_BIASED };
-static __device__ __noinline__ Pair pair_key(float l, float b, float m, Pair z, int kind, bool sigmoid) {
-  if (kind == KEY_LOGIT) return {l, 0.0f};
-  const float from = kind == KEY_BIASED ? 0.0f : fminf(m, 0.0f);
+// The score with its bias. z: the softmax's sum, of exponentials from the largest logit m on.
+static __device__ __noinline__ Pair pair_key(float l, float b, float m, Pair z, bool sigmoid) {
   // exp(l - m); exp(-l), or exp(l)
   const Pair e = pair_exp(!sigmoid ? pair_sum(l, -m) : Pair{-fabsf(l), 0.0f});
   const Pair one = {1.0f, 0.0f};
@@ -274,11 +271,8 @@ static __device__ __noinline__ Pair pair_key(float l, float b, float m, Pair z, 
   if (sigmoid) {
     below = one + e;
     if (l > 0.0f) above = one;
-    if (from < 0.0f) above = pair_exp(pair_sum(l, -from));
   }
-  Pair s = over(above, below);
-  if (kind == KEY_BIASED) s = s + Pair{b, 0.0f};
-  return s;
+  return over(above, below) + Pair{b, 0.0f};
 }
 
 __device__ __forceinline__ Pair pair_lane(Pair r, uint32_t mask, int lane) {
@@ -293,24 +287,141 @@ __device__ __noinline__ Pair route_pair_z(const RouteParams& p, int64_t row, int
 #pragma unroll 1
   for (int j = 0; j < count; ++j) {
     const float l = route_load<TYPE>(p.logits, row * p.ld + first + j);
-    z = z + pair_key(l, 0.0f, m, {1.0f, 0.0f}, KEY_SCORE, false);
+    z = z + pair_exp(pair_sum(l, -m));
   }
   for (int o = LANES / 2; o > 0; o >>= 1) z = z + pair_lane(z, mask, static_cast<int>(lane_id()) ^ o);
   return z;
 }
 
-// Whether a differs from b by more than the Pairs' errors (2^-40 of the keys' size).
+// Whether a differs from b by more than the Pairs' errors (2^-40 of the keys' size, where
+// that is not so small that Pairs lose bits).
 __device__ __forceinline__ bool pairs_apart(Pair a, Pair b, float b_most) {
-  return fabsf((a.hi - b.hi) + (a.lo - b.lo)) > 9.094947e-13f * (fabsf(a.hi) + b_most);
+  const float size = fmaxf(fabsf(a.hi), fabsf(b.hi)) + b_most;
+  return size > 0x1p-70f && fabsf((a.hi - b.hi) + (a.lo - b.lo)) > 0x1p-40f * size;
+}
+
+// Which of two groups has the larger sum of its two best scores, by their logits a1 >= a2
+// and b1 >= b2 (-infinity: none): 1 the first, -1 the second, 0 neither. Scores f rise with
+// their logits, so that only a1 > b1 >= b2 > a2 (or the reverse) is a question: whether
+// f(a1) - f(b1) > f(b2) - f(a2). Both differences are products of positive factors,
+//
+//   softmax:  f(x) - f(y) = exp(x) (1 - exp(y - x))             (the row's sum left out)
+//   sigmoid:  f(x) - f(y) = f(x) f(-y) (1 - exp(y - x)),   f(x) = exp(min(x, 0)) / (1 + exp(-|x|))
+//
+// and the logarithm of their quotient, the powers of e put together, is compared with 0: no
+// score is too small for it, and none too near 1. In 32 bits if it is far enough from 0, else in
+// 64. (32 bits: 22 roundings of 2^-24 in the quotient, and in the powers and the logarithm,
+// which cancel, five of their size.)
+template <typename F>
+__device__ __forceinline__ F sums_quotient(F a1, F a2, F b1, F b2, bool sigmoid, F& size) {
+  const F zero = 0, one = 1;
+  F power = a1 - b2, quotient = expm1(b1 - a1) / expm1(a2 - b2);
+  size = power;
+  if (sigmoid) {
+    const F up = fmin(a1, zero) - fmin(b2, zero), down = fmax(b1, zero) - fmax(a2, zero);  // (both >= 0)
+    power = up - down;
+    size = up + down;
+    quotient *= ((one + exp(-fabs(b2))) * (one + exp(-fabs(a2)))) / ((one + exp(-fabs(a1))) * (one + exp(-fabs(b1))));
+  }
+  return power + log(quotient);
+}
+static __device__ __noinline__ int compare_sums(float a1, float a2, float b1, float b2, bool sigmoid) {
+  if (a1 == b1) return (a2 > b2) - (a2 < b2);
+  int sign = 1;
+  if (a1 < b1) {
+    const float t1 = a1, t2 = a2;
+    a1 = b1;
+    a2 = b2;
+    b1 = t1;
+    b2 = t2;
+    sign = -1;
+  }
+  if (a2 >= b2) return sign;
+  float size;
+  const float near = sums_quotient<float>(a1, a2, b1, b2, sigmoid, size);
+  if (fabsf(near) > 0x1p-18f + 0x1p-20f * size && fabsf(near) < INFINITY) return near > 0.0f ? sign : -sign;
+  double size64;
+  const double exact = sums_quotient<double>(a1, a2, b1, b2, sigmoid, size64);
+  return exact > 0.0 ? sign : exact < 0.0 ? -sign : 0;
+}
+
+// The choice of one row in doubt without a bias, by the row's lanes: this lane's pick (lane i has
+// the i-th), or -1. It reads its logits anew, as route_careful does.
+template <int TYPE, int LANES, int PER>
+__device__ __noinline__ int route_by_logits(const RouteParams& p, int64_t row, int first, int count, uint32_t mask) {
+  const int sub = static_cast<int>(lane_id()) & (LANES - 1), g = sub >> p.lanes_log2;
+  float l[PER], l1 = -INFINITY, l2 = -INFINITY;  // the group's two best
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    l[j] = j < count && !(p.bias && p.bias[first + j] == -INFINITY)
+               ? route_load<TYPE>(p.logits, row * p.ld + first + j) : -INFINITY;
+    l2 = fmaxf(l2, fminf(l1, l[j]));
+    l1 = fmaxf(l1, l[j]);
+  }
+  bool kept = true;
+  if (p.groups > 1) {
+    for (int o = 1; o < (1 << p.lanes_log2); o <<= 1) {
+      const float a1 = __shfl_xor_sync(mask, l1, o), a2 = __shfl_xor_sync(mask, l2, o);
+      l2 = fmaxf(fminf(l1, a1), fmaxf(l2, a2));
+      l1 = fmaxf(l1, a1);
+    }
+    if (p.group_best == 1) l2 = -INFINITY;
+    // most sums lie far enough apart for 32 bits: a softmax's scores from the row's best on
+    const float m = from_order_bits(route_max<LANES>(order_bits(l1 + 0.0f), mask));
+    const auto score = [&](float v) { return p.sigmoid ? logistic(v) : v > -INFINITY ? expf(v - m) : 0.0f; };
+    const float sum = score(l1) + score(l2);
+    int rank = 0;
+#pragma unroll 1
+    for (int o = 0; o < p.groups; ++o) {
+      const float o1 = __shfl_sync(mask, l1, o << p.lanes_log2, LANES);
+      const float o2 = __shfl_sync(mask, l2, o << p.lanes_log2, LANES);
+      const float other = __shfl_sync(mask, sum, o << p.lanes_log2, LANES), most = fmaxf(sum, other);
+      int sign = other > sum ? 1 : -1;
+      if (!(most > 0x1p-100f && fabsf(other - sum) > 0x1p-16f * most))
+        sign = compare_sums(o1, o2, l1, l2, p.sigmoid);
+      rank += sign > 0 || (sign == 0 && o < g);
+    }
+    kept = rank < p.top_groups;
+  }
+  int mine = -1;
+  uint32_t taken = 0, taken2 = 0;  // the lane's experts that were picked
+#pragma unroll 1
+  for (int i = 0; i < p.top; ++i) {
+    float best = -INFINITY;
+    int at = -1;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const bool free = kept && !(((j < 32 ? taken : taken2) >> (j & 31)) & 1u);
+      if (free && l[j] > best) {
+        best = l[j];
+        at = j;
+      }
+    }
+    // (of equal ones the first lane's, whose experts come first)
+    const uint32_t key = at >= 0 ? order_bits(best + 0.0f) : 0u;
+    const uint32_t most = route_max<LANES>(key, mask);
+    if (most == 0) break;
+    const uint32_t having = __ballot_sync(mask, key == most);
+    const int from = __ffs(having) - 1;
+    const int expert = __shfl_sync(mask, first + at, from);
+    if (sub == i) mine = expert;
+    if (static_cast<int>(lane_id()) == from) {
+      if (at < 32)
+        taken |= 1u << at;
+      else
+        taken2 |= 1u << (at & 31);
+    }
+  }
+  return mine;
 }
 
 // The choice of one row in 64 bits, by the row's lanes: this lane's pick (lane i
-// has the i-th), or -1. For the rows that even Pairs do not settle (and that have more
-// than 16 experts a lane). It reads its inputs anew and holds nothing in the fast
-// path's registers. Without a bias, experts are compared by their logits.
+// has the i-th), or -1. For the rows with a bias that even Pairs do not settle (and that have
+// more than 16 experts a lane). It reads its inputs anew and holds nothing in the fast
+// path's registers.
 template <int TYPE, int LANES, int PER>
 __device__ __noinline__ int route_careful(const RouteParams& p, int64_t row, int first, int count,
-                                          bool biased, bool direct, uint32_t mask) {
+                                          uint32_t mask) {
   const int sub = static_cast<int>(lane_id()) & (LANES - 1);
   const int g = sub >> p.lanes_log2;
   double key[PER];
@@ -322,7 +433,7 @@ __device__ __noinline__ int route_careful(const RouteParams& p, int64_t row, int
   }
   for (int o = LANES / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(mask, m, o));
   double z = 1.0;
-  if (!p.sigmoid && biased) {
+  if (!p.sigmoid) {
     z = 0.0;
 #pragma unroll 1
     for (int j = 0; j < PER; ++j)
@@ -333,14 +444,13 @@ __device__ __noinline__ int route_careful(const RouteParams& p, int64_t row, int
 #pragma unroll 1
   for (int j = 0; j < PER; ++j) {
     if (!(key[j] > -INFINITY)) continue;
-    const float b = p.bias ? p.bias[first + j] : 0.0f;
+    const float b = p.bias[first + j];
     if (b == -INFINITY) {
       key[j] = -INFINITY;
       continue;
     }
-    double k = key[j];
-    if (!direct) k = p.sigmoid ? 1.0 / (1.0 + exp(-k)) : exp(k - m) / z;
-    if (biased) key[j] = k = k + static_cast<double>(b);
+    const double k = (p.sigmoid ? 1.0 / (1.0 + exp(-key[j])) : exp(key[j] - m) / z) + static_cast<double>(b);
+    key[j] = k;
     t2 = fmax(t2, fmin(t1, k));
     t1 = fmax(t1, k);
   }
@@ -504,7 +614,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER == 8 ? 7 : 1)
     bool unsettled = false;
     // what scores are divided by, as a Pair: a softmax's sum beside a bias, once it has been needed
     Pair z2 = {1.0f, 0.0f};
-    bool summed = p.sigmoid || !biased;
+    bool summed = p.sigmoid;
     if (p.groups > 1) {
       uint32_t t1 = 0, t2 = 0;
       if constexpr (SORTED) {
@@ -539,14 +649,13 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER == 8 ? 7 : 1)
         const uint32_t next = route_max<LANES>(kept ? 0u : score);
         const bool near = next != 0 && !(w - from_order_bits(next) >
                                          2.0f * route_apart<PER>(w, 4.0f * b_most, p.sigmoid));
-        if (near) {
+        if (near && (!biased || !SORTED)) {
+          unsettled = true;
+        } else if (near) {
           if constexpr (SORTED) {
             // the groups' sums anew, from each lane's two best keys
-            const int kind = direct ? KEY_LOGIT : biased ? KEY_BIASED : KEY_SCORE;
             if (!summed) z2 = route_pair_z<TYPE, LANES>(p, row, first, count, m, mask);
             summed = true;
-            float most_l = m;  // (a sigmoid's m is the lane's so far)
-            for (int o = LANES / 2; o > 0; o >>= 1) most_l = fmaxf(most_l, __shfl_xor_sync(mask, most_l, o));
             Pair d[2];
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
@@ -554,7 +663,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER == 8 ? 7 : 1)
               const int e = first + static_cast<int>(PLACE - (c & PLACE));
               const float el = c ? route_load<TYPE>(p.logits, row * p.ld + e) : 0.0f;
               const float eb = c && p.bias ? p.bias[e] : 0.0f;
-              const Pair v = pair_key(el, eb, most_l, z2, kind, p.sigmoid);
+              const Pair v = pair_key(el, eb, m, z2, p.sigmoid);
               (i ? d[1] : d[0]) = c ? v : Pair{-INFINITY, 0.0f};
             }
             // A lane's third key near its second might be its second, unless it is a tie with it.
@@ -590,13 +699,12 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER == 8 ? 7 : 1)
               // (of the same two keys: a tie, as between groups of a row of zeros)
               const Pair other1 = pair_lane(d[0], mask, at), other2 = pair_lane(d[1], mask, at);
               const bool tie = other1 == d[0] && other2 == d[1];
-              if (kind != KEY_LOGIT && o != g && g < p.groups && sum.hi > -INFINITY && !tie &&
+              // (a sum past the largest float is infinite or NaN, and settles nothing)
+              if (o != g && g < p.groups && sum.hi != -INFINITY && other.hi != -INFINITY && !tie &&
                   !pairs_apart(sum, other, 4.0f * b_most))
                 unsettled = true;
             }
             kept = rank < p.top_groups;
-          } else {
-            unsettled = true;
           }
         }
       }
@@ -677,25 +785,24 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER == 8 ? 7 : 1)
           }
         const bool rank = __ballot_sync(mask, near || differs || others_differ) != 0;
         // (ranked is one expert a lane beside the picks, and none of unsorted keys)
-        unsettled = unsettled || (rank && (others || !SORTED));
-        if (SORTED && rank) {
+        unsettled = unsettled || (rank && (others || !SORTED || !biased));
+        if (SORTED && rank && biased) {
           // The picks and the extra ones, ranked by Pairs.
-          const int kind = biased ? KEY_BIASED : KEY_LOGIT;  // (without a bias logits order the scores)
           if (!summed) z2 = route_pair_z<TYPE, LANES>(p, row, first, count, m, mask);
           const Pair none = {-INFINITY, 0.0f};
-          Pair a = pair_key(ol, ob, m, z2, kind, p.sigmoid), c = none;
+          Pair a = pair_key(ol, ob, m, z2, p.sigmoid), c = none;
           if (own < 0) a = none;
           const uint32_t extras = __ballot_sync(mask, extra);
-          if (extras != 0) c = pair_key(el, eb, m, z2, kind, p.sigmoid);
+          if (extras != 0) c = pair_key(el, eb, m, z2, p.sigmoid);
           if (!extra) c = none;
           int rank_a = 0, rank_c = 0;
           const auto against = [&](Pair v, int e, float vl, float vb) {
             if (e < 0) return;
             rank_a += v > a || (v == a && e < own);
             rank_c += v > c || (v == c && e < mine_e);
-            if (own >= 0 && e != own && kind == KEY_BIASED && !pairs_apart(v, a, b_most) && (vl != ol || vb != ob))
+            if (own >= 0 && e != own && !pairs_apart(v, a, b_most) && (vl != ol || vb != ob))
               unsettled = true;
-            if (extra && e != mine_e && kind == KEY_BIASED && !pairs_apart(v, c, b_most) && (vl != el || vb != eb))
+            if (extra && e != mine_e && !pairs_apart(v, c, b_most) && (vl != el || vb != eb))
               unsettled = true;
           };
 #pragma unroll 1
@@ -750,7 +857,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER == 8 ? 7 : 1)
     for (int r = 0; doubts != 0 && r < 32 >> p.slots_log2; ++r) {
       if (((doubts >> (r << p.slots_log2)) & ((1u << slots) - 1u)) == 0) continue;
       // (with fewer lanes a row than a warp has, all of the warp's parts do the same)
-      const int careful = route_careful<TYPE, LANES, PER>(p, row0 + r, first, count, biased, direct, mask);
+      const int careful = biased ? route_careful<TYPE, LANES, PER>(p, row0 + r, first, count, mask)
+                                 : route_by_logits<TYPE, LANES, PER>(p, row0 + r, first, count, mask);
       const int found = __shfl_sync(ALL, careful, my_slot);
       if (my_row == r) {
         pick = my_slot < p.top ? found : -1;

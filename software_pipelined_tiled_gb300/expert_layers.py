@@ -132,7 +132,8 @@ def route_experts(logits, top: int, bias=None, scores: str = "softmax", groups: 
     or None) are chosen, largest first, of equal ones the lowest index.  With
     ``groups`` > 1 (equal groups of neighbouring experts) only those of the
     ``top_groups`` groups count whose ``group_best`` (1 or 2) best experts have
-    the largest sum.  Keys are compared as exact arithmetic would compare them.
+    the largest sum.  Keys are compared as exact arithmetic would compare them
+    (without a bias for scores of any size, with one to 2^-42 of keys and biases).
     weights (float32): the chosen scores, without the bias, times ``scale``;
     with ``renormalize`` divided by their sum.  experts: int32.
 
