@@ -470,10 +470,10 @@ int sptg_route_experts_dlogits(int64_t rows, int64_t E, int top, sptg_type type,
  * Its gradients:  dy[places[t, j]] = weights[t, j] * dout[t],
  *                 dweights[t, j] = <y[places[t, j]], dout[t]>
  *
- * (base's is dout). places has to name each row of y once, as sptg_dispatch_rows
- * writes it: a row of dy that none names is left as it was, one that several name
- * gets the value of one of them. A place outside [0, y_rows) has dweights 0.
- * dweights may be NULL (then y is not read).
+ * (base's is dout). places has to name no row of y twice (one that several name gets
+ * the value of one of them). A row of dy that none names is left as it was, or, in
+ * sptg_combine_rows_grad_ex with zero_unnamed = 1, written with zeros. A place outside [0, y_rows)
+ * has dweights 0. dweights may be NULL (then y is not read).
  */
 int sptg_dispatch_rows(int64_t rows, int64_t cols, int top, int64_t E, sptg_type type, const void* x,
                        int64_t ldx, const int32_t* experts, void* sorted, int64_t lds, int32_t* places,
@@ -484,6 +484,10 @@ int sptg_combine_rows(int64_t rows, int64_t cols, int top, int64_t y_rows, sptg_
 int sptg_combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, sptg_type type,
                            const void* dout, int64_t ldd, const void* y, int64_t ldy, const int32_t* places,
                            const float* weights, void* dy, int64_t lddy, float* dweights, void* stream);
+int sptg_combine_rows_grad_ex(int64_t rows, int64_t cols, int top, int64_t y_rows, sptg_type type,
+                              const void* dout, int64_t ldd, const void* y, int64_t ldy,
+                              const int32_t* places, const float* weights, void* dy, int64_t lddy,
+                              float* dweights, int zero_unnamed, void* stream);
 
 /* What a gate multiplies: nothing, a column (cols values), a row (rows values,
  * ldg apart), or an element (rows x cols, row pitch ldg). */

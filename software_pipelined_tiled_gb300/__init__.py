@@ -45,7 +45,7 @@ EXPORTS = ("sptg_gemm", "sptg_gemm_ex", "sptg_gemm_strided", "sptg_gemm_host",
            "sptg_add_rms_norm_ex", "sptg_gemm_w4",
            "sptg_grouped_gemm", "sptg_grouped_gemm_dx", "sptg_grouped_gemm_dw",
            "sptg_route_experts", "sptg_route_experts_dlogits", "sptg_dispatch_rows",
-           "sptg_combine_rows", "sptg_combine_rows_grad", "sptg_gate_add_rms_norm",
+           "sptg_combine_rows", "sptg_combine_rows_grad", "sptg_combine_rows_grad_ex", "sptg_gate_add_rms_norm",
            "sptg_gate_add_rms_norm_grad_workspace", "sptg_gate_add_rms_norm_grad")
 
 
@@ -130,6 +130,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.sptg_dispatch_rows.argtypes = [i64, i64, i, i64, i, vp, i64, vp, vp, i64, vp, vp, vp]
         lib.sptg_combine_rows.argtypes = [i64, i64, i, i64, i, vp, i64, vp, vp, vp, i64, vp, i64, vp]
         lib.sptg_combine_rows_grad.argtypes = [i64, i64, i, i64, i, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]
+        lib.sptg_combine_rows_grad_ex.argtypes = (lib.sptg_combine_rows_grad.argtypes[:-1] + [i, vp])
         lib.sptg_gate_add_rms_norm.argtypes = [i64, i64, i, vp, i64, vp, i64, vp, vp, i, i64, fl, vp, fl,
                                                vp, i64, vp, i64, vp, ctypes.POINTER(Config)]
         lib.sptg_gate_add_rms_norm_grad.argtypes = [i64, i64, i, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
@@ -138,7 +139,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.sptg_gate_add_rms_norm_grad_workspace.argtypes = [i64, i64]
         lib.sptg_gate_add_rms_norm_grad_workspace.restype = i64
         for f in (lib.sptg_route_experts, lib.sptg_route_experts_dlogits, lib.sptg_dispatch_rows,
-                  lib.sptg_combine_rows, lib.sptg_combine_rows_grad, lib.sptg_gate_add_rms_norm,
+                  lib.sptg_combine_rows, lib.sptg_combine_rows_grad, lib.sptg_combine_rows_grad_ex,
+                  lib.sptg_gate_add_rms_norm,
                   lib.sptg_gate_add_rms_norm_grad):
             f.restype = ctypes.c_int
         lib.sptg_version.argtypes = []

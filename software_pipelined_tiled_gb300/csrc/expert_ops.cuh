@@ -330,21 +330,24 @@ int combine_rows(int64_t rows, int64_t cols, int top, int64_t y_rows, int type, 
 
 int combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, int type, const void* dout,
                       int64_t ldd, const void* y, int64_t ldy, const int32_t* places, const float* weights,
-                      void* dy, int64_t lddy, float* dweights, cudaStream_t stream) {
+                      void* dy, int64_t lddy, float* dweights, int zero_unnamed, cudaStream_t stream) {
   bool bf16;
   const char* name;
   if (!row_type(type, bf16, name)) return refuse(SPTG_ERR_ARG, "rows are f16 or bf16");
   int rc = rows_sizes(rows, cols, top);
   if (rc) return rc;
   if (y_rows < 0 || y_rows > kMaxDim) return refuse(SPTG_ERR_ARG, kDimText);
-  if (rows == 0 || (cols == 0 && !dweights)) {
+  if (zero_unnamed != 0 && zero_unnamed != 1) return refuse(SPTG_ERR_ARG, "zero_unnamed must be 0 or 1");
+  const bool zeros = zero_unnamed && y_rows > 0 && cols > 0;
+  if ((rows == 0 && !zeros) || (cols == 0 && !dweights)) {
     set_config("kernel=none type=%s (empty output)", name, {});
     return SPTG_OK;
   }
-  if (!places || (cols > 0 && (!dout || (y_rows > 0 && (!dy || (dweights && !y))))))
+  if ((rows > 0 && (!places || (cols > 0 && (!dout || (y_rows > 0 && dweights && !y))))) ||
+      (cols > 0 && y_rows > 0 && !dy))
     return refuse(SPTG_ERR_ARG, "null pointer");
   if (dweights && !weights) return refuse(SPTG_ERR_ARG, "dweights belong to weights");
-  if (cols > 0 && (ldd < cols || (y_rows > 0 && (lddy < cols || (dweights && ldy < cols)))))
+  if (cols > 0 && ((rows > 0 && ldd < cols) || (y_rows > 0 && (lddy < cols || (dweights && ldy < cols)))))
     return refuse(SPTG_ERR_ARG, "row pitches must be at least the row lengths");
   if (off_by(dout, 2) || off_by(dy, 2) || off_by(y, 2) || off_by(places, 4) || off_by(weights, 4) ||
       off_by(dweights, 4))
@@ -368,11 +371,38 @@ int combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, int t
   p.dweights = dweights;
   p.cols = static_cast<int>(cols);
   p.top = top;
+  p.entries = rows * top;
+  // Rows of dy that no place names. With as many rows as places only entries that were dropped
+  // leave some, for blocks of the same launch to find, where what these read is at most as
+  // much as zeros for all rows would write, and rows are wide enough for the call to take longer
+  // than they do (16384 rows of 8 places and 512 columns: 75 us, zeros first 112). Else zeros for all
+  // rows go first.
+  if (zeros) {
+    const int64_t window = std::min<int64_t>(
+        aligned ? ZERO_MAX_WINDOW : ZERO_CUT_WINDOW,
+        std::max<int64_t>(ZERO_MIN_WINDOW, ceil_div(ceil_div(y_rows, 32), 32) * 32));
+    const int64_t blocks = std::min<int64_t>(ZERO_MAX_BLOCKS, ceil_div(y_rows, window));
+    if (y_rows == p.entries && cols >= 512 && 2 * ceil_div(y_rows, window) <= cols) {
+      p.zero_blocks = static_cast<int>(blocks);
+      p.zero_window = static_cast<int>(window);
+    } else {
+      const size_t width = static_cast<size_t>(cols) * 2;
+      const cudaError_t e = lddy == cols || y_rows == 1
+                                ? cudaMemsetAsync(dy, 0, width * static_cast<size_t>(y_rows), stream)
+                                : cudaMemset2DAsync(dy, static_cast<size_t>(lddy) * 2, 0, width,
+                                                    static_cast<size_t>(y_rows), stream);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (rows == 0) {
+      set_config("kernel=zero-fill type=%s", name, {});
+      return SPTG_OK;
+    }
+  }
   void* args[] = {&p};
-  const cudaError_t e = launch_op(combine_rows_grad_variant(bf16, aligned), dim3(static_cast<unsigned>(rows)),
-                                  ROWS_THREADS, 0, 1, stream, args);
+  const cudaError_t e = launch_op(combine_rows_grad_variant(bf16, aligned),
+                                  dim3(static_cast<unsigned>(rows + p.zero_blocks)), ROWS_THREADS, 0, 1, stream, args);
   if (e != cudaSuccess) return cuda_fail(e, "combine_rows_grad launch");
-  set_config("kernel=combine_grad type=%s aligned=%lld", name, {aligned});
+  set_config("kernel=combine_grad type=%s aligned=%lld zero_blocks=%lld", name, {aligned, p.zero_blocks});
   return SPTG_OK;
 }
 
@@ -683,7 +713,17 @@ int sptg_combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, 
                            const float* weights, void* dy, int64_t lddy, float* dweights, void* stream) {
   return guarded([&] {
     return combine_rows_grad(rows, cols, top, y_rows, type, dout, ldd, y, ldy, places, weights, dy, lddy,
-                             dweights, static_cast<cudaStream_t>(stream));
+                             dweights, 0, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int sptg_combine_rows_grad_ex(int64_t rows, int64_t cols, int top, int64_t y_rows, sptg_type type,
+                              const void* dout, int64_t ldd, const void* y, int64_t ldy, const int32_t* places,
+                              const float* weights, void* dy, int64_t lddy, float* dweights, int zero_unnamed,
+                              void* stream) {
+  return guarded([&] {
+    return combine_rows_grad(rows, cols, top, y_rows, type, dout, ldd, y, ldy, places, weights, dy, lddy,
+                             dweights, zero_unnamed, static_cast<cudaStream_t>(stream));
   });
 }
 

@@ -25,7 +25,7 @@ from .layers import _16BIT, _F32, _I32, _call, _dense, _empty, _matrix, _pitch, 
 _lib = _pkg.load()
 _route, _route_grad = _lib.sptg_route_experts, _lib.sptg_route_experts_dlogits
 _dispatch, _combine, _combine_grad = (_lib.sptg_dispatch_rows, _lib.sptg_combine_rows,
-                                      _lib.sptg_combine_rows_grad)
+                                      _lib.sptg_combine_rows_grad_ex)
 _gate_norm, _gate_norm_grad = _lib.sptg_gate_add_rms_norm, _lib.sptg_gate_add_rms_norm_grad
 _workspace = _lib.sptg_gate_add_rms_norm_grad_workspace
 
@@ -295,7 +295,7 @@ def combine_rows(y, places, weights=None, base=None, out=None, stream=None):
     Sums are 32 bits, rounded once.  Returns out, T x C (it may be base).
 
     Differentiable by y, weights and base (combine_rows_grad); places then has to
-    name every row of y once (where y has more rows than T * top: none twice).
+    name no row of y twice.  Rows that none names have gradient 0.
     """
     if ((y.requires_grad or (weights is not None and weights.requires_grad)
          or (base is not None and base.requires_grad)) and _grad_enabled()):
@@ -309,9 +309,8 @@ def combine_rows_grad(dout, y, places, weights=None, dy=None, dweights=None, nee
 
     ``dy[places[t, j]] = weights[t, j] * dout[t]``, of y's type, and
     ``dweights[t, j] = <y[places[t, j]], dout[t]>``, float32 (None where weights is
-    None or need_weights is false; y is then not read).  places has to name every
-    row of y once, as dispatch_rows returns them; only where y has another number of
-    rows than T * top, those without a place are 0 (in a given dy: left as they were).
+    None or need_weights is false; y is then not read).  places has to name no row of
+    y twice; rows that none names are 0 (in a given dy: left as they were).
     """
     code = _row_type(y, "y")
     if places.dim() != 2:
@@ -323,11 +322,9 @@ def combine_rows_grad(dout, y, places, weights=None, dy=None, dweights=None, nee
     _dense(places, (rows, top), _I32, device, "places")
     if weights is not None:
         _dense(weights, (rows, top), _F32, device, "weights")
-    if dy is None:
+    zeros = dy is None
+    if zeros:
         dy, lddy = _like(y, stream), cols
-        if y_rows != rows * top:  # rows without a place
-            with torch.cuda.stream(_stream(stream, on)):
-                dy.zero_()
     else:
         lddy = _pitch(dy, y_rows, cols, dtype, device, "dy")
     if weights is None or not need_weights:
@@ -340,7 +337,8 @@ def combine_rows_grad(dout, y, places, weights=None, dy=None, dweights=None, nee
     _call(_combine_grad, device, stream, (
         rows, cols, top, y_rows, code, dout.data_ptr(), ldd, y.data_ptr(), ldy, places.data_ptr(),
         None if weights is None else weights.data_ptr(), dy.data_ptr(), lddy,
-        None if dweights is None else dweights.data_ptr()), (dout, y, places, weights, dy, dweights))
+        None if dweights is None else dweights.data_ptr(), 1 if zeros else 0),
+        (dout, y, places, weights, dy, dweights))
     return dy, dweights
 
 

@@ -1,0 +1,130 @@
+"""Gradients of the operators around an expert layer in calls that a training run may make: entries that were dropped."""
+import pytest
+import torch
+
+import software_pipelined_tiled_gb300 as sptg
+from test_expert_layer_gpu import BF16, F16, I32, NAN, UNIT, assert_within, gen, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    torch.cuda.synchronize()
+    assert sptg.device_error() == 0
+
+
+# ------------------------------------------------------- entries that were dropped
+def dropped_places(g, rows, top, share, y_rows=None):
+    """A permutation's first places, some of them outside of y's rows."""
+    y_rows = rows * top if y_rows is None else y_rows
+    places = torch.randperm(max(y_rows, rows * top), device="cuda", generator=g)[:rows * top].to(I32).reshape(rows, top)
+    outside = torch.tensor([-1, -(1 << 31), y_rows, (1 << 31) - 1], dtype=torch.int64, device="cuda").to(I32)
+    some = outside[torch.randint(0, 4, (rows, top), device="cuda", generator=g)]
+    return torch.where(torch.rand(rows, top, device="cuda", generator=g) < share, some, places)
+
+
+def dy_reference(dout, places, weights, y_rows):
+    """(One product of 32 bits a value; rows without a place are 0.)"""
+    want = torch.zeros(y_rows, dout.shape[1], dtype=torch.float64, device="cuda")
+    t, j = ((places >= 0) & (places < y_rows)).nonzero(as_tuple=True)
+    w = 1.0 if weights is None else weights[t, j, None].double()
+    want[places[t, j].long()] = dout[t].double() * w
+    return want
+
+
+def poison(*likes):
+    """What the allocator hands out next for tensors like these."""
+    for t in [torch.full_like(x, NAN) for x in likes]:
+        del t
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,top,cols", [(1, 1, 8), (8, 3, 64), (8, 3, 65), (40, 2, 1024), (531, 6, 2056), (333, 1, 1031),
+                                           (1500, 8, 1025), (2600, 7, 1152), (9000, 2, 520), (20011, 3, 16)])
+@pytest.mark.parametrize("share", [0.0, 0.05, 0.6, 1.0])
+def test_rows_of_dropped_entries_get_no_gradient(share, rows, top, cols, dtype):
+    g = gen(rows + top)
+    y, dout = rand(g, rows * top, cols, dtype=dtype), rand(g, rows, cols, dtype=dtype)
+    places = dropped_places(g, rows, top, share)
+    for weights in (torch.rand(rows, top, device="cuda", generator=g), None):
+        want = dy_reference(dout, places, weights, rows * top)
+        leaf = y.clone().requires_grad_()
+        out = sptg.combine_rows(leaf, places, weights)
+        poison(y)
+        dy, = torch.autograd.grad(out, leaf, dout)
+        assert_within(dy, want, UNIT * want.abs())
+        poison(y)
+        dy, dweights = sptg.combine_rows_grad(dout, y, places, weights)
+        assert_within(dy, want, UNIT * want.abs())
+        if weights is not None:
+            assert not dweights[(places < 0) | (places >= rows * top)].any()
+            poison(y)
+            assert torch.equal(sptg.combine_rows_grad(dout, y, places, weights, need_weights=False)[0], dy)
+        given = torch.full_like(y, 7.0)  # a given dy's rows without a place are left as they were
+        sptg.combine_rows_grad(dout, y, places, weights, dy=given)
+        named = torch.zeros(rows * top, dtype=torch.bool, device="cuda")
+        named[places[(places >= 0) & (places < rows * top)].long()] = True
+        assert (given[~named] == 7.0).all() and torch.equal(given[named], dy[named])
+
+
+@pytest.mark.parametrize("y_rows", [5000, 7000, 90000])
+@pytest.mark.parametrize("cols", [1024, 2049, 24])
+def test_rows_without_a_place_beside_dropped_entries(cols, y_rows):
+    g = gen(cols + y_rows)
+    places = dropped_places(g, 1500, 4, 0.1, y_rows)
+    y, dout = rand(g, y_rows, cols), rand(g, 1500, cols)
+    weights = torch.rand(1500, 4, device="cuda", generator=g)
+    poison(y)
+    dy, _ = sptg.combine_rows_grad(dout, y, places, weights)
+    want = dy_reference(dout, places, weights, y_rows)
+    assert_within(dy, want, UNIT * want.abs())
+    poison(y[:300])
+    none, _ = sptg.combine_rows_grad(dout[:0], y[:300], places[:0], weights[:0])  # no rows at all
+    assert none.shape == (300, cols) and not none.any()
+
+
+@pytest.mark.parametrize("rows,cols", [(600, 1024), (600, 1027), (600, 80)])
+def test_dropped_entries_in_a_graph_and_on_another_stream(rows, cols):
+    g = gen(21)
+    y, dout, weights = rand(g, rows * 4, cols), rand(g, rows, cols), torch.rand(rows, 4, device="cuda", generator=g)
+    places = dropped_places(g, rows, 4, 0.2)
+
+    def calls(**kw):
+        return sptg.combine_rows_grad(dout, y, places, weights, **kw)
+
+    calls()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = calls()
+    side = torch.cuda.Stream()
+    for seed in range(3):
+        places.copy_(dropped_places(gen(seed), rows, 4, 0.3 * seed))
+        out[0].fill_(NAN)
+        torch.cuda.synchronize()
+        graph.replay()
+        beside = calls(stream=side)
+        torch.cuda.synchronize()
+        want = dy_reference(dout, places, weights, rows * 4)
+        assert_within(out[0], want, UNIT * want.abs())
+        assert torch.equal(beside[0], out[0]) and torch.equal(beside[1], out[1])
+
+
+@pytest.mark.parametrize("off,cols", [(0, 1024), (8, 96), (3, 1024), (0, 97)])
+def test_zeros_in_a_gradient_of_strided_rows(off, cols):
+    """By the C entry, which takes dy: rows without a place get zeros, what lies beside the rows is left as it was."""
+    g = gen(22)
+    rows, top = 300, 4
+    wide = torch.full((rows * top, 1100), 7.0, dtype=BF16, device="cuda")
+    y, dout = rand(g, rows * top, cols), rand(g, rows, cols)
+    weights, places = torch.rand(rows, top, device="cuda", generator=g), dropped_places(g, rows, top, 0.3)
+    want = dy_reference(dout, places, weights, rows * top)
+    dy = wide[:, off:off + cols]
+    rc = sptg.load().sptg_combine_rows_grad_ex(
+        rows, cols, top, rows * top, 1, dout.data_ptr(), cols, y.data_ptr(), cols, places.data_ptr(), weights.data_ptr(),
+        dy.data_ptr(), 1100, None, 1, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    assert_within(dy, want, UNIT * want.abs())
+    assert (wide[:, :off] == 7.0).all() and (wide[:, off + cols:] == 7.0).all()
