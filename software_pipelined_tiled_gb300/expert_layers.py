@@ -393,21 +393,24 @@ def _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, st
 
 class _GateAddRmsNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, y, residual, weight, block_weight, gate, alpha, eps):
+    def forward(ctx, y, residual, weight, block_weight, gate, alpha, eps, config):
         ctx.save_for_backward(y, residual, weight, block_weight, gate)
         ctx.how = (alpha, eps)
+        # (backward has what forward was given, whatever becomes of the caller's object)
+        ctx.config = None if config is None else type(config).from_buffer_copy(config)
         ctx.set_materialize_grads(False)
-        return _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, None, None, None)
+        return _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, None, None, None, config)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dv):
         if dh is None and dv is None:
-            return (None,) * 7
+            return (None,) * 8
         y, residual, weight, block_weight, gate = ctx.saved_tensors
         dh, dv = (None if t is None else _as_rows(t, y.dtype) for t in (dh, dv))
-        grads = gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight, gate, *ctx.how)
-        return tuple(g if n else None for g, n in zip(grads, ctx.needs_input_grad)) + (None, None)
+        grads = gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight, gate, *ctx.how,
+                                       config=ctx.config)
+        return tuple(g if n else None for g, n in zip(grads, ctx.needs_input_grad)) + (None,) * 3
 
 
 def gate_add_rms_norm(y, residual, weight, block_weight=None, gate=None, alpha: float = 1.0,
@@ -421,13 +424,13 @@ def gate_add_rms_norm(y, residual, weight, block_weight=None, gate=None, alpha: 
     values; gate: None, C values (or 1 x C), T x 1 or T x C, all of y's type.
     config: a Config, for its timeout_ms and inject_stall.
 
-    Differentiable by all tensors (gate_add_rms_norm_grad).
+    Differentiable by all tensors (gate_add_rms_norm_grad, with the same config).
     """
     if ((y.requires_grad or residual.requires_grad or weight.requires_grad
          or (block_weight is not None and block_weight.requires_grad)
          or (gate is not None and gate.requires_grad)) and _grad_enabled()):
         return _differentiated(_GateAddRmsNorm, stream, y.device,
-                               (y, residual, weight, block_weight, gate, alpha, eps), (h, v))
+                               (y, residual, weight, block_weight, gate, alpha, eps, config), (h, v))
     return _run_gate_norm(y, residual, weight, block_weight, gate, alpha, eps, h, v, stream, config)
 
 

@@ -1,9 +1,11 @@
-"""Gradients of the operators around an expert layer in calls that a training run may make: entries that were dropped."""
+"""Gradients of the operators around an expert layer in calls that a training run may make: entries that were dropped,
+a configuration."""
 import pytest
 import torch
 
 import software_pipelined_tiled_gb300 as sptg
 from test_expert_layer_gpu import BF16, F16, I32, NAN, UNIT, assert_within, gen, rand
+from test_layer_ops_edges_gpu import chosen
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +130,26 @@ def test_zeros_in_a_gradient_of_strided_rows(off, cols):
     assert rc == 0
     assert_within(dy, want, UNIT * want.abs())
     assert (wide[:, :off] == 7.0).all() and (wide[:, off + cols:] == 7.0).all()
+
+
+# ------------------------------------------------------- a configuration
+def test_a_configuration_holds_where_gradients_are_asked_for():
+    g = gen(31)
+    y, x, w = rand(g, 2500, 4096), rand(g, 2500, 4096), rand(g, 4096)
+    leaf = y.clone().requires_grad_()
+    bad = sptg.Config()
+    bad.timeout_ms = -1
+    with pytest.raises(sptg.SptgError):
+        sptg.gate_add_rms_norm(leaf, x, w, w, config=bad)
+    # (as in test_expert_layer_edges_gpu: each block's second row never arrives, and the waits for it run out)
+    cfg = sptg.Config()
+    cfg.timeout_ms, cfg.inject_stall = 100, 1
+    h, v = sptg.gate_add_rms_norm(leaf, x, w, w, config=cfg)
+    assert chosen()["kind"] == 2 and sptg.device_error() == -5
+    cfg.inject_stall = 0  # the backward call has what the forward call was given
+    torch.autograd.grad((h, v), leaf, (x, y))
+    assert sptg.device_error() == -5  # (reported by a thread of automatic differentiation's, to the same word)
+    fine = sptg.Config()
+    fine.timeout_ms = 1000
+    got = torch.autograd.grad(sptg.gate_add_rms_norm(leaf, x, w, w, config=fine), leaf, (x, y))[0]
+    assert torch.equal(got, sptg.gate_add_rms_norm_grad(x, y, y, x, w, w)[0])
