@@ -7,7 +7,8 @@ checks holds here too.
 ``route_experts``, ``dispatch_rows``, ``combine_rows`` and ``gate_add_rms_norm``
 take part in PyTorch's automatic differentiation: where an input requires a
 gradient (and none of the outputs is given), backward runs the functions that
-compute the gradients, which can also be called by themselves.  All of them can
+compute the gradients, which can also be called by themselves (tensors that carry
+tangents of the forward mode are refused).  All of them can
 be captured in a CUDA graph; a backward pass only while no other graph of the
 same leaves is alive (PyTorch's rule: a leaf's node keeps to the stream that it was
 made on, which may not join the capture).
@@ -20,7 +21,8 @@ import torch
 
 import software_pipelined_tiled_gb300 as _pkg
 
-from .layers import _16BIT, _F32, _I32, _call, _dense, _empty, _matrix, _pitch, _refuse, _stream
+from .layers import (_16BIT, _F32, _I32, _call, _dense, _empty, _forward, _matrix, _pitch, _refuse,
+                     _refuse_tangents, _stream)
 
 _lib = _pkg.load()
 _route, _route_grad = _lib.sptg_route_experts, _lib.sptg_route_experts_dlogits
@@ -143,6 +145,8 @@ def route_experts(logits, top: int, bias=None, scores: str = "softmax", groups: 
 
     weights is differentiable by the logits (route_experts_dlogits).
     """
+    if _forward._current_level >= 0:
+        _refuse_tangents(logits)
     if logits.requires_grad and _grad_enabled():
         return _differentiated(_RouteExperts, stream, logits.device,
                                (logits, top, bias, scores, groups, top_groups, group_best, renormalize,
@@ -234,6 +238,8 @@ def dispatch_rows(x, experts, num_experts: int, out=None, places=None, offsets=N
 
     rows is differentiable by x (dispatch_rows_dx).
     """
+    if _forward._current_level >= 0:
+        _refuse_tangents(x)
     if x.requires_grad and _grad_enabled():
         return _differentiated(_DispatchRows, stream, x.device, (x, experts, num_experts),
                                (out, places, offsets))
@@ -297,6 +303,8 @@ def combine_rows(y, places, weights=None, base=None, out=None, stream=None):
     Differentiable by y, weights and base (combine_rows_grad); places then has to
     name no row of y twice.  Rows that none names have gradient 0.
     """
+    if _forward._current_level >= 0:
+        _refuse_tangents(y, weights, base)
     if ((y.requires_grad or (weights is not None and weights.requires_grad)
          or (base is not None and base.requires_grad)) and _grad_enabled()):
         return _differentiated(_CombineRows, stream, y.device, (y, places, weights, base), (out,))
@@ -426,6 +434,8 @@ def gate_add_rms_norm(y, residual, weight, block_weight=None, gate=None, alpha: 
 
     Differentiable by all tensors (gate_add_rms_norm_grad, with the same config).
     """
+    if _forward._current_level >= 0:
+        _refuse_tangents(y, residual, weight, block_weight, gate)
     if ((y.requires_grad or residual.requires_grad or weight.requires_grad
          or (block_weight is not None and block_weight.requires_grad)
          or (gate is not None and gate.requires_grad)) and _grad_enabled()):

@@ -10,8 +10,9 @@ on another stream has to be waited for first (``stream.wait_stream``), as has th
 call itself before its results are used elsewhere.  The tensors passed may be
 dropped as soon as the call returns: the allocator learns that the stream uses them.
 
-``grouped_gemm`` takes part in PyTorch's automatic differentiation; the other
-calls, like ``gemm``, return tensors without a history.
+``grouped_gemm`` takes part in PyTorch's automatic differentiation (backwards;
+tensors that carry tangents of its forward mode are refused); the other calls,
+like ``gemm``, return tensors without a history.
 
 A decoding step makes these calls for every layer and token, so the checks are
 written for little time: each looks at attributes only, and what a message
@@ -22,6 +23,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 import software_pipelined_tiled_gb300 as _pkg
 
@@ -63,6 +65,13 @@ def _pitch(t, rows: int, cols: int, dtype, device: int, name: str) -> int:
 def _dense(t, shape, dtype, device: int, name: str):
     if not (t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()):
         _refuse(name, t, f"a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {device}")
+
+
+def _refuse_tangents(*tensors):
+    """For calls that are differentiated backwards only, inside of a level of forward mode."""
+    for t in tensors:
+        if t is not None and _forward.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("there is no derivative in forward mode: a tensor carries a tangent")
 
 
 def _matrix(t, name: str):
@@ -259,6 +268,8 @@ def grouped_gemm(X, W, offsets, out=None, out_dtype=None, stream=None):
     grouped_gemm_dw on Y's gradient in the operands' type, and gives gradients of
     that type; ``out`` is then refused.
     """
+    if _forward._current_level >= 0:
+        _refuse_tangents(X, W)
     if (X.requires_grad or W.requires_grad) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where X or W requires a gradient")

@@ -1,10 +1,11 @@
 """Gradients of the operators around an expert layer in calls that a training run may make: entries that were dropped,
-a configuration."""
+a configuration, tangents."""
 import pytest
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 import software_pipelined_tiled_gb300 as sptg
-from test_expert_layer_gpu import BF16, F16, I32, NAN, UNIT, assert_within, gen, rand
+from test_expert_layer_gpu import BF16, F16, F32, I32, NAN, UNIT, assert_within, gen, rand
 from test_layer_ops_edges_gpu import chosen
 
 pytestmark = pytest.mark.gpu
@@ -153,3 +154,30 @@ def test_a_configuration_holds_where_gradients_are_asked_for():
     fine.timeout_ms = 1000
     got = torch.autograd.grad(sptg.gate_add_rms_norm(leaf, x, w, w, config=fine), leaf, (x, y))[0]
     assert torch.equal(got, sptg.gate_add_rms_norm_grad(x, y, y, x, w, w)[0])
+
+
+# ------------------------------------------------------- forward mode
+def test_tangents_are_refused_not_dropped():
+    g = gen(41)
+    x, residual, w, gate = rand(g, 8, 16), rand(g, 8, 16), rand(g, 16), rand(g, 8, 1)
+    logits, weights = rand(g, 8, 4, dtype=F32), torch.rand(8, 2, device="cuda", generator=g)
+    _, ids = sptg.route_experts(logits, 2)
+    y, places, offsets = sptg.dispatch_rows(x, ids, 4)
+    W = rand(g, 4, 24, 16)
+    calls = ((lambda l: sptg.route_experts(l, 2), (logits,)), (lambda x: sptg.dispatch_rows(x, ids, 4), (x,)),
+             (lambda y, w, b: sptg.combine_rows(y, places, w, base=b), (y, weights, x)),
+             (lambda *t: sptg.gate_add_rms_norm(*t), (x, residual, w, w, gate)),
+             (lambda X, W: sptg.grouped_gemm(X, W, offsets), (y, W)))
+    for call, tensors in calls:
+        plain = call(*tensors)
+        for i, t in enumerate(tensors):
+            with forward_ad.dual_level():
+                dual = forward_ad.make_dual(t, torch.ones_like(t))
+                mixed = tensors[:i] + (dual,) + tensors[i + 1:]
+                with pytest.raises(NotImplementedError):
+                    call(*mixed)
+                with torch.no_grad(), pytest.raises(NotImplementedError):
+                    call(*mixed)
+                again = call(*tensors)  # tensors without tangents pass
+        for a, b in zip(again if isinstance(again, tuple) else (again,), plain if isinstance(plain, tuple) else (plain,)):
+            assert torch.equal(a, b)
