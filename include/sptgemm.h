@@ -510,7 +510,9 @@ typedef enum {
  *   v = t * weight / sqrt(mean(t^2) + eps)           rounded to the rows' type
  *
  * h may be y or residual (same pointer and pitch). A row whose sum of squares
- * passes the fp32 range is normalised to 0.
+ * passes the fp32 range is normalised to 0. The kernel goes by rows, cols and alignment, and
+ * kernels multiply and add in orders of their own: the same row may differ in its last
+ * bits between calls of another number of rows, pitch or alignment (not between equal calls).
  *
  * The gradients of y, residual, gate, weight and block_weight from dh and dv
  * (either may be NULL: 0). dy, dresidual and an element-wise dgate are of the rows'

@@ -429,7 +429,8 @@ def gate_add_rms_norm(y, residual, weight, block_weight=None, gate=None, alpha: 
     ``h = alpha * residual + gate * u`` (the new residual stream; may be y or
     residual itself), ``v = h * weight / sqrt(mean(h^2) + eps)``, in 32 bits, h
     and v rounded once each.  y, residual: T x C, float16 or bfloat16; weights: C
-    values; gate: None, C values (or 1 x C), T x 1 or T x C, all of y's type.
+    values; gate: None, C values (or 1 x C, where T is not 1), T x 1 or T x C, all of y's
+    type.  A row's last bits may depend on T, which chooses among kernels.
     config: a Config, for its timeout_ms and inject_stall.
 
     Differentiable by all tensors (gate_add_rms_norm_grad, with the same config).
@@ -451,7 +452,8 @@ def gate_add_rms_norm_grad(dh, dv, y, residual, weight, block_weight=None, gate=
     dh, dv: gradients of h and v (T x C of y's type; either may be None).
     ``out_dtype``: of the gradients that are sums over rows or columns (weight,
     block_weight, a gate that is broadcast): y's type (default) or float32.
-    Those of inputs that are None are None.
+    Those of inputs that are None are None.  With one row, a gate of 1 x C is T x C: its
+    gradient is no sum and of y's type (that of a gate of C values is of out_dtype always).
     """
     code = _row_type(y, "y")
     rows, cols = y.shape

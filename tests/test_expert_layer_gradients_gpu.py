@@ -1,5 +1,5 @@
 """Gradients of the operators around an expert layer in calls that a training run may make: entries that were dropped,
-a configuration, tangents."""
+a configuration, tangents, one row."""
 import pytest
 import torch
 import torch.autograd.forward_ad as forward_ad
@@ -181,3 +181,17 @@ def test_tangents_are_refused_not_dropped():
                 again = call(*tensors)  # tensors without tangents pass
         for a, b in zip(again if isinstance(again, tuple) else (again,), plain if isinstance(plain, tuple) else (plain,)):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------- types
+def test_type_of_a_column_gates_gradient():
+    """Of C values: out_dtype for any number of rows.  1 x C with one row is the gate with a value an element."""
+    g = gen(51)
+    w = rand(g, 64)
+    for rows in (1, 2):
+        y, x = rand(g, rows, 64), rand(g, rows, 64)
+        grads = sptg.gate_add_rms_norm_grad(x, y, y, x, w, w, w, out_dtype=F32)
+        assert grads[4].dtype == F32 and grads[4].shape == (64,)
+        wide = sptg.gate_add_rms_norm_grad(x, y, y, x, w, w, w[None], out_dtype=F32)[4]
+        assert wide.shape == (1, 64) and wide.dtype == (BF16 if rows == 1 else F32)
+        assert torch.equal(wide[0].to(BF16), grads[4].to(BF16))
