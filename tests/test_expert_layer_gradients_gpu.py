@@ -1,11 +1,11 @@
 """Gradients of the operators around an expert layer in calls that a training run may make: entries that were dropped,
-a configuration, tangents, one row."""
+a configuration, tangents, one row, and a million rows."""
 import pytest
 import torch
 import torch.autograd.forward_ad as forward_ad
 
 import software_pipelined_tiled_gb300 as sptg
-from test_expert_layer_gpu import BF16, F16, F32, I32, NAN, UNIT, assert_within, gen, rand
+from test_expert_layer_gpu import BF16, F16, F32, I32, NAN, UNIT, assert_within, gate_norm_reference, gen, rand
 from test_layer_ops_edges_gpu import chosen
 
 pytestmark = pytest.mark.gpu
@@ -195,3 +195,32 @@ def test_type_of_a_column_gates_gradient():
         wide = sptg.gate_add_rms_norm_grad(x, y, y, x, w, w, w[None], out_dtype=F32)[4]
         assert wide.shape == (1, 64) and wide.dtype == (BF16 if rows == 1 else F32)
         assert torch.equal(wide[0].to(BF16), grads[4].to(BF16))
+
+
+def test_gate_norm_sums_past_32_bits_of_elements():
+    """1.1 million rows: the sums over all of them against 64 bits, chunk by chunk.  Nothing cancels (inputs are positive) and
+    gradients grow with the row, so that rows left out, taken twice or taken for others would show.  The bound counts an
+    addition in 32 bits for each row of a block (at least 152 blocks) and for each block, and check_gate_norm's roundings
+    of a term: 1e-3 of the sum of magnitudes."""
+    g = gen(52)
+    rows, cols = 1_100_000, 4096
+    y, x, dh, dv = (rand(g, rows, cols).abs_() for _ in range(4))
+    w2, w1, gate = (rand(g, cols).abs_() for _ in range(3))
+    by_row = (1 + torch.arange(rows, device="cuda") * 8 // rows).to(BF16)[:, None]
+    dh.mul_(by_row)
+    dv.mul_(by_row)
+    grads = sptg.gate_add_rms_norm_grad(dh, dv, y, x, w2, w1, gate, out_dtype=F32)[2:]
+    assert y.numel() > 2 ** 32
+    names = ("weight", "block_weight", "gate")
+    sums = {k: [torch.zeros(cols, dtype=torch.float64, device="cuda") for _ in range(2)] for k in names}
+    for at in range(0, rows, 20000):
+        s = slice(at, min(rows, at + 20000))
+        ref = gate_norm_reference(y[s], x[s], w2, w1, gate, 1.0, 1e-6, dh[s], dv[s])
+        for k in names:
+            for total, part in zip(sums[k], ref[k]):
+                total += part
+        del ref
+    for k, got in zip(names, grads):
+        want, mag = sums[k]
+        assert want.abs().sum() > 0.2 * mag.sum()
+        assert_within(got, want, (cols / 128 + 128 + rows / 152 + 456) * UNIT * mag)
