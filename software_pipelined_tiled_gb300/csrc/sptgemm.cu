@@ -8,7 +8,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
