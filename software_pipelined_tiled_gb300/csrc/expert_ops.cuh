@@ -381,8 +381,8 @@ int combine_rows_grad(int64_t rows, int64_t cols, int top, int64_t y_rows, int t
     const int64_t window = std::min<int64_t>(
         aligned ? ZERO_MAX_WINDOW : ZERO_CUT_WINDOW,
         std::max<int64_t>(ZERO_MIN_WINDOW, ceil_div(ceil_div(y_rows, 32), 32) * 32));
-    const int64_t blocks = std::min<int64_t>(ZERO_MAX_BLOCKS, ceil_div(y_rows, window));
-    if (y_rows == p.entries && (aligned || cols >= 384) && 2 * ceil_div(y_rows, window) <= cols) {
+    const int64_t blocks = ceil_div(y_rows, window);
+    if (y_rows == p.entries && (aligned || cols >= 384) && 2 * blocks <= cols && blocks <= ZERO_MAX_BLOCKS) {
       p.zero_blocks = static_cast<int>(blocks);
       p.zero_window = static_cast<int>(window);
     } else {

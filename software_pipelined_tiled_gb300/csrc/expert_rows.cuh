@@ -410,62 +410,57 @@ __global__ void __launch_bounds__(ROWS_THREADS) combine_rows_kernel(const __grid
 // for a window of rows through all places, while the other blocks work. (16384 rows of 8
 // places: 32 blocks of 4096 rows, which read 16 MB from L2; no time that can be measured beside
 // the 335 us of rows of 4096, where zeros for all rows first take 150 us. A call of a few rows
-// takes 0.2 to 0.8 us longer. Cut rows have windows of 1 KB, since they live from L1: 16384
-// rows of 4001 432 us, without this 426.)
-constexpr int ZERO_MIN_WINDOW = 1024, ZERO_MAX_WINDOW = 32768, ZERO_MAX_BLOCKS = 2048;
+// takes 0.3 to 0.5 us longer. Blocks for cut rows, which live from L1, keep 1 KB of it for this.)
+constexpr int ZERO_MIN_WINDOW = 1024, ZERO_MAX_WINDOW = 32768, ZERO_CUT_WINDOW = 8192, ZERO_MAX_BLOCKS = 2048;
 
-constexpr int ZERO_CUT_WINDOW = 8192;
 template <bool ALIGNED>
 __device__ __forceinline__ void zero_unnamed_rows(const RowsParams& p) {
   __shared__ uint32_t s_named[(ALIGNED ? ZERO_MAX_WINDOW : ZERO_CUT_WINDOW) / 32];
   constexpr int AT_ONCE = 8;  // words of places of a thread whose loads are in flight together
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, words = p.zero_window / 32;
-  const int64_t step = static_cast<int64_t>(p.zero_blocks) * p.zero_window;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.zero_window; first < p.x_rows; first += step) {
-    for (int w = threadIdx.x; w < words; w += ROWS_THREADS) s_named[w] = 0;
-    __syncthreads();
-    const auto name = [&](int place) {
-      const int64_t at = place - first;
-      if (at >= 0 && at < p.zero_window) atomicOr(&s_named[at >> 5], 1u << (at & 31));
-    };
-    // whole 16-byte words of places, and the few before and behind them
-    const int64_t head = min(p.entries, static_cast<int64_t>(((16 - (reinterpret_cast<uintptr_t>(p.places) & 15)) & 15) >> 2));
-    const int4* of4 = reinterpret_cast<const int4*>(p.places + head);
-    const int64_t n4 = (p.entries - head) >> 2;
-    for (int64_t i0 = threadIdx.x; i0 < n4; i0 += AT_ONCE * ROWS_THREADS) {
-      int4 v[AT_ONCE];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.zero_window;
+  for (int w = threadIdx.x; w < words; w += ROWS_THREADS) s_named[w] = 0;
+  __syncthreads();
+  const auto name = [&](int place) {
+    const int64_t at = place - first;
+    if (at >= 0 && at < p.zero_window) atomicOr(&s_named[at >> 5], 1u << (at & 31));
+  };
+  // whole 16-byte words of places, and the few before and behind them
+  const int64_t head = min(p.entries, static_cast<int64_t>(((16 - (reinterpret_cast<uintptr_t>(p.places) & 15)) & 15) >> 2));
+  const int4* of4 = reinterpret_cast<const int4*>(p.places + head);
+  const int64_t n4 = (p.entries - head) >> 2;
+  for (int64_t i0 = threadIdx.x; i0 < n4; i0 += AT_ONCE * ROWS_THREADS) {
+    int4 v[AT_ONCE];
 #pragma unroll
-      for (int k = 0; k < AT_ONCE; ++k) {
-        const int64_t i = i0 + k * ROWS_THREADS;
-        v[k] = i < n4 ? of4[i] : make_int4(-1, -1, -1, -1);
-      }
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int64_t i = i0 + k * ROWS_THREADS;
+      v[k] = i < n4 ? of4[i] : make_int4(-1, -1, -1, -1);
+    }
 #pragma unroll
-      for (int k = 0; k < AT_ONCE; ++k) {
-        name(v[k].x);
-        name(v[k].y);
-        name(v[k].z);
-        name(v[k].w);
+    for (int k = 0; k < AT_ONCE; ++k) {
+      name(v[k].x);
+      name(v[k].y);
+      name(v[k].z);
+      name(v[k].w);
+    }
+  }
+  if (threadIdx.x < head) name(p.places[threadIdx.x]);
+  if (head + 4 * n4 + threadIdx.x < p.entries) name(p.places[head + 4 * n4 + threadIdx.x]);
+  __syncthreads();
+  for (int w = warp; w < words; w += ROWS_THREADS / 32) {  // a row to a warp
+    for (uint32_t rest = ~s_named[w]; rest != 0; rest &= rest - 1) {
+      const int64_t row = first + 32 * w + __ffs(rest) - 1;
+      if (row >= p.x_rows) break;
+      uint16_t* out = row_of(p.out, row, p.ldo);
+      const uint4 zeros = make_uint4(0, 0, 0, 0);
+      if constexpr (ALIGNED) {
+        for (int c = 8 * lane; c < p.cols; c += 8 * 32) *reinterpret_cast<uint4*>(out + c) = zeros;
+      } else {
+        const CutRow cut(out, p.cols);
+        for (int c = cut.body + 8 * lane; c < cut.tail; c += 8 * 32) *reinterpret_cast<uint4*>(out + c) = zeros;
+        if (lane < cut.ends) out[cut.end(lane)] = 0;
       }
     }
-    if (threadIdx.x < head) name(p.places[threadIdx.x]);
-    if (head + 4 * n4 + threadIdx.x < p.entries) name(p.places[head + 4 * n4 + threadIdx.x]);
-    __syncthreads();
-    for (int w = warp; w < words; w += ROWS_THREADS / 32) {  // a row to a warp
-      for (uint32_t rest = ~s_named[w]; rest != 0; rest &= rest - 1) {
-        const int64_t row = first + 32 * w + __ffs(rest) - 1;
-        if (row >= p.x_rows) break;
-        uint16_t* out = row_of(p.out, row, p.ldo);
-        const uint4 zeros = make_uint4(0, 0, 0, 0);
-        if constexpr (ALIGNED) {
-          for (int c = 8 * lane; c < p.cols; c += 8 * 32) *reinterpret_cast<uint4*>(out + c) = zeros;
-        } else {
-          const CutRow cut(out, p.cols);
-          for (int c = cut.body + 8 * lane; c < cut.tail; c += 8 * 32) *reinterpret_cast<uint4*>(out + c) = zeros;
-          if (lane < cut.ends) out[cut.end(lane)] = 0;
-        }
-      }
-    }
-    __syncthreads();  // (before the next window's words)
   }
 }
 

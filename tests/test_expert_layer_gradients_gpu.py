@@ -133,6 +133,18 @@ def test_zeros_in_a_gradient_of_strided_rows(off, cols):
     assert (wide[:, :off] == 7.0).all() and (wide[:, off + cols:] == 7.0).all()
 
 
+@pytest.mark.parametrize("rows,top,cols", [(1, 1, 8), (1, 3, 1024), (700, 3, 1024), (701, 3, 1031), (2051, 1, 512)])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_dropped_entries_of_places_at_any_address(at, rows, top, cols):
+    g = gen(23 + rows)
+    y, dout = rand(g, rows * top, cols), rand(g, rows, cols)
+    places = torch.zeros(rows * top + 8, dtype=I32, device="cuda")[at:at + rows * top].view(rows, top)
+    places.copy_(dropped_places(g, rows, top, 0.2))
+    want = dy_reference(dout, places, None, rows * top)
+    poison(y)
+    assert_within(sptg.combine_rows_grad(dout, y, places)[0], want, UNIT * want.abs())
+
+
 # ------------------------------------------------------- a configuration
 def test_a_configuration_holds_where_gradients_are_asked_for():
     g = gen(31)
