@@ -431,9 +431,9 @@ int sptg_grouped_gemm_dw(int64_t E, int64_t T, int64_t N, int64_t K, sptg_dtype 
  * 32 do not settle a choice); equal ones in the order of their experts, as are
  * groups. Without a bias (or with one of zeros) that holds for scores of any size: logits
  * stand for them. With one, keys or sums of two that differ by less than 2^-42 of the
- * larger and the largest bias may count as equal. An expert whose logit or bias is -infinity is never chosen:
- * a row with fewer than `top` experts left has -1 with weight 0 in its last
- * places. A row that holds a NaN (or, with a softmax, +infinity) gets experts 0 ... top
+ * larger and the largest bias may count as equal. An expert whose logit or bias is
+ * -infinity is never chosen: a row with fewer than `top` experts left has -1 with
+ * weight 0 in its last places. A row that holds a NaN (or, with a softmax, +infinity) gets experts 0 ... top
  * - 1 with weights NaN.
  *
  * logits: rows x E of SPTG_T_F16, SPTG_T_BF16 or SPTG_T_F32, row pitch ld;

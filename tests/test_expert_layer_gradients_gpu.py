@@ -88,7 +88,7 @@ def test_rows_without_a_place_beside_dropped_entries(cols, y_rows):
     assert none.shape == (300, cols) and not none.any()
 
 
-@pytest.mark.parametrize("rows,cols", [(600, 1024), (600, 1027), (600, 80)])
+@pytest.mark.parametrize("rows,cols", [(600, 1024), (600, 1027), (600, 80), (600, 81)])
 def test_dropped_entries_in_a_graph_and_on_another_stream(rows, cols):
     g = gen(21)
     y, dout, weights = rand(g, rows * 4, cols), rand(g, rows, cols), torch.rand(rows, 4, device="cuda", generator=g)
